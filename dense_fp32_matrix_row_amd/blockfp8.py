@@ -1,0 +1,261 @@
+"""8-bit block-scaled products (ctypes binding of include/blockfp8.h): the
+quantiser, the product, and a linear layer's forward and backward made of them.
+
+hip_fp8_quantize and hip_fp8_gemm carry the C ABI's names and argument order
+and return its status codes; matrix and stream arguments are as in `sgemm`.
+quantize, quantize_transposed, quantize_both, gemm, linear_forward and
+linear_backward take and return torch device tensors, run on torch's current
+stream of the tensors' device and raise on errors.  Every operation runs in the
+library's HIP kernels; there is no fallback.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+from typing import Optional, Tuple
+
+from . import sgemm as _sgemm
+
+EXPORTS = ("hip_fp8_quantize", "hip_fp8_gemm", "hip_fp8_quantize_status_string",
+           "hip_fp8_gemm_status_string")
+
+F32, BF16, F16 = 0, 1, 2
+SCALE_F32, SCALE_E8M0 = 0, 1
+BLOCK = 128
+MAX_LD = 1 << 23
+
+_bound = None
+
+
+def load():
+    """The library with this header's functions declared."""
+    global _bound
+    lib = _sgemm.load()
+    if lib is not _bound:
+        i32, i64, f32, vp = ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_void_p
+        lib.hip_fp8_quantize.restype = i32
+        lib.hip_fp8_quantize.argtypes = [i32, i32, vp, i32, i32, i32, i32, vp, i32, vp, i64, i64,
+                                         vp, i32, vp, i64, i64, vp]
+        lib.hip_fp8_gemm.restype = i32
+        lib.hip_fp8_gemm.argtypes = [i32, i32, i32, f32, vp, i32, vp, i64, i64, i32,
+                                     vp, i32, vp, i64, i64, i32, i32, f32, vp, i32, vp, i32, i32, vp]
+        for name in ("hip_fp8_quantize_status_string", "hip_fp8_gemm_status_string"):
+            getattr(lib, name).restype = ctypes.c_char_p
+            getattr(lib, name).argtypes = [i32]
+        _bound = lib
+    return lib
+
+
+def hip_fp8_quantize(rows, cols, X, x_type, ldx, block_rows, scale_type, Q, ldq, S, s_row, s_col,
+                     QT, ldqt, ST, st_row, st_col, stream=None) -> int:
+    """Codes and scales of X and / or of its transpose; returns the status code (0 = enqueued)."""
+    a, s = _sgemm._addr, _sgemm._stream
+    return int(load().hip_fp8_quantize(int(rows), int(cols), a(X), int(x_type), int(ldx), int(block_rows),
+                                       int(scale_type), a(Q), int(ldq), a(S), int(s_row), int(s_col),
+                                       a(QT), int(ldqt), a(ST), int(st_row), int(st_col), s(stream)))
+
+
+def hip_fp8_gemm(M, N, K, alpha, A, lda, SA, sa_row, sa_col, a_block_rows, B, ldb, SB, sb_row, sb_col,
+                 b_block_rows, scale_type, beta, C, ldc, D, ldd, c_type, stream=None) -> int:
+    """D <- alpha*A@B^T + beta*C of quantised A and B; returns the status code."""
+    a, s = _sgemm._addr, _sgemm._stream
+    return int(load().hip_fp8_gemm(int(M), int(N), int(K), float(alpha), a(A), int(lda), a(SA), int(sa_row),
+                                   int(sa_col), int(a_block_rows), a(B), int(ldb), a(SB), int(sb_row),
+                                   int(sb_col), int(b_block_rows), int(scale_type), float(beta), a(C),
+                                   int(ldc), a(D), int(ldd), int(c_type), s(stream)))
+
+
+def hip_fp8_quantize_status_string(status) -> str:
+    return load().hip_fp8_quantize_status_string(int(status)).decode()
+
+
+def hip_fp8_gemm_status_string(status) -> str:
+    return load().hip_fp8_gemm_status_string(int(status)).decode()
+
+
+@dataclasses.dataclass(frozen=True)
+class BlockFp8:
+    """A quantised matrix: q, its e4m3 codes (rows x cols, columns side by
+    side), and s, a scale for each block of block_rows x 128 (float32, or
+    float8_e8m0fnu for powers of two)."""
+
+    q: "torch.Tensor"  # noqa: F821
+    s: "torch.Tensor"  # noqa: F821
+    block_rows: int = 1
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+
+def _types():
+    import torch
+    return {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _scale_type(dtype) -> int:
+    import torch
+    if dtype == torch.float32:
+        return SCALE_F32
+    if dtype == torch.float8_e8m0fnu:
+        return SCALE_E8M0
+    raise TypeError(f"scales are float32 or float8_e8m0fnu, not {dtype}")
+
+
+def _ceil(a, b):
+    return -(-a // b)
+
+
+def _matrix(name, t):
+    """The row stride of a 2-D view whose columns lie side by side."""
+    if not t.is_cuda:
+        raise TypeError(f"{name} must live on the GPU")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.shape[0] > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D row-major view with unit column stride")
+    if max(t.shape) >= 1 << 31:
+        raise ValueError(f"{name} has a side of 2^31 or more")
+    if t.shape[0] <= 1:
+        return max(t.shape[1], 1)
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows overlap")
+    if t.stride(0) >= 1 << 31:
+        raise ValueError(f"{name}'s row stride is 2^31 or more")
+    return max(t.stride(0), 1)
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _check(status, what):
+    if status != 0:
+        raise _sgemm.SgemmError(status, what(status))
+
+
+def _empty(rows, cols, block_rows, scale, device):
+    """Room for a quantised matrix: rows of a multiple of 16 bytes, the scales
+    of one block column side by side."""
+    import torch
+    ld = max(_ceil(cols, 16) * 16, 16)
+    q = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
+    s = torch.empty((_ceil(cols, BLOCK), _ceil(rows, block_rows)), dtype=scale, device=device).T
+    return BlockFp8(q, s, block_rows), ld
+
+
+def _quantize(x, block_rows, scale, as_is, transposed):
+    import torch
+    ldx = _matrix("x", x)
+    if x.dtype not in _types():
+        raise TypeError(f"x is float32, bfloat16 or float16, not {x.dtype}")
+    if block_rows not in (1, BLOCK):
+        raise ValueError(f"block_rows is 1 or 128, not {block_rows}")
+    scale = torch.float32 if scale is None else scale
+    kind = _scale_type(scale)
+    rows, cols = x.shape
+    with torch.cuda.device(x.device):
+        n, ldn = _empty(rows, cols, block_rows, scale, x.device) if as_is else (None, 0)
+        t, ldt = _empty(cols, rows, block_rows, scale, x.device) if transposed else (None, 0)
+        if rows and cols:
+            args = []
+            for o, ld in ((n, ldn), (t, ldt)):
+                args += [o.q, ld, o.s, o.s.stride(0), o.s.stride(1)] if o is not None else [None, 0, None, 0, 0]
+            _check(hip_fp8_quantize(rows, cols, x, _types()[x.dtype], ldx, block_rows, kind, *args),
+                   hip_fp8_quantize_status_string)
+    return n, t
+
+
+def quantize(x, block_rows: int = 1, scale=None) -> BlockFp8:
+    """x (2-D, rows may be strided) in blocks of block_rows x 128; `scale` is
+    torch.float32 (default) or torch.float8_e8m0fnu."""
+    return _quantize(x, block_rows, scale, True, False)[0]
+
+
+def quantize_transposed(x, block_rows: int = 1, scale=None) -> BlockFp8:
+    """x's transpose, in blocks of block_rows x 128 of the transpose."""
+    return _quantize(x, block_rows, scale, False, True)[1]
+
+
+def quantize_both(x, block_rows: int = 1, scale=None) -> Tuple[BlockFp8, BlockFp8]:
+    """quantize(x) and quantize_transposed(x) from one read of x."""
+    return _quantize(x, block_rows, scale, True, True)
+
+
+def _operand(name, o, K):
+    ld = _matrix(name, o.q)
+    if o.q.element_size() != 1:
+        raise TypeError(f"{name}'s codes are one byte each, not {o.q.dtype}")
+    if o.q.shape[0] <= 1 or K == 0:
+        ld = max(_ceil(ld, 16) * 16, 16)
+    want = (_ceil(o.q.shape[0], o.block_rows), _ceil(K, BLOCK)) if o.block_rows in (1, BLOCK) else None
+    if want is None:
+        raise ValueError(f"{name}'s block_rows is 1 or 128, not {o.block_rows}")
+    if tuple(o.s.shape) != want:
+        raise ValueError(f"{name}'s scales are {tuple(o.s.shape)}, not {want}")
+    if not o.s.is_cuda:
+        raise TypeError(f"{name}'s scales must live on the GPU")
+    if o.q.shape[0] and K and ld % 16 == 0:  # the last row is read up to a multiple of 16 bytes
+        end = o.q.storage_offset() + (o.q.shape[0] - 1) * ld + _ceil(K, 16) * 16
+        if end > o.q.untyped_storage().nbytes():
+            raise ValueError(f"{name}'s storage ends within the last row's padding to a multiple of 16 bytes")
+    return [o.q, ld, o.s, o.s.stride(0), o.s.stride(1), o.block_rows]
+
+
+def gemm(a: BlockFp8, b: BlockFp8, c=None, alpha: float = 1.0, beta: float = 0.0, out=None, out_dtype=None):
+    """alpha * a @ b^T + beta * c as a new tensor, or in `out` (which may be c).
+
+    The result's type is out's, c's, or out_dtype (default bfloat16)."""
+    import torch
+    M, K = a.q.shape
+    N = b.q.shape[0]
+    if b.q.shape[1] != K:
+        raise ValueError(f"shape mismatch: a {tuple(a.q.shape)}, b {tuple(b.q.shape)}")
+    if a.s.dtype != b.s.dtype:
+        raise TypeError(f"scales of two types: {a.s.dtype} and {b.s.dtype}")
+    kind = _scale_type(a.s.dtype)
+    left, right = _operand("a", a, K), _operand("b", b, K)
+    if beta == 0.0:
+        c = None
+    elif c is None:
+        raise ValueError("beta is not 0 but there is no c")
+    dtype = out.dtype if out is not None else c.dtype if c is not None else out_dtype or torch.bfloat16
+    if dtype not in _types():
+        raise TypeError(f"the result is float32, bfloat16 or float16, not {dtype}")
+    if out_dtype is not None and out_dtype != dtype:
+        raise TypeError(f"out_dtype is {out_dtype}, but the result is {dtype}")
+    for name, t in (("c", c), ("out", out)):
+        if t is not None and (tuple(t.shape) != (M, N) or t.dtype != dtype):
+            raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {(M, N)} {dtype}")
+    _same_device(a.q, a.s, b.q, b.s, c, out)
+    with torch.cuda.device(a.q.device):
+        if out is None:
+            out = torch.empty((M, N), dtype=dtype, device=a.q.device)
+        ldc = _matrix("c", c) if c is not None else 0
+        _check(hip_fp8_gemm(M, N, K, alpha, *left, *right, kind, beta, c, ldc, out, _matrix("out", out),
+                            _types()[dtype]), hip_fp8_gemm_status_string)
+    return out
+
+
+def linear_forward(x, w: BlockFp8, out_dtype=None):
+    """y = x w^T of tokens x (T x I) and a quantised weight w (O x I).
+
+    Returns y (T x O, of x's type by default) and x^T quantised (I x T), which
+    linear_backward takes.  x is read once."""
+    xq, xt = quantize_both(x, 1, w.s.dtype)
+    return gemm(xq, w, out_dtype=out_dtype or x.dtype), xt
+
+
+def linear_backward(dy, xt: BlockFp8, wt: BlockFp8, dw=None, out_dtype=None):
+    """The gradients of linear_forward: dx = dy w (T x I) and dw = dy^T x (O x I).
+
+    dy: T x O; xt: x^T as linear_forward returned it; wt: w^T quantised (I x O).
+    dx has dy's type by default.  dw is float32, a new tensor, or added to the
+    tensor given, in place."""
+    import torch
+    dyq, dyt = quantize_both(dy, 1, wt.s.dtype)
+    dx = gemm(dyq, wt, out_dtype=out_dtype or dy.dtype)
+    if dw is None:
+        return dx, gemm(dyt, xt, out_dtype=torch.float32)
+    return dx, gemm(dyt, xt, c=dw, beta=1.0, out=dw)

@@ -1,0 +1,410 @@
+// nt_tile.h -- the tile kernel that the block-scaled 8-bit product
+// (fp8_gemm.hip) and the orthogonalised update (orthogonal.hip) share:
+// D = A * B^T over operands whose rows are contiguous along K.
+//
+// Both operands are rows of bytes, taken 128 bytes a step: 128 e4m3 codes, or
+// 32 numbers as halfs hi and lo (64 bytes each).  A step is eight 16-byte
+// chunks of a row; lane group g = lane / 16 of a wavefront takes chunks g and
+// 4 + g of row lane % 16.  For the 8-bit matrix instruction that is some
+// permutation of the block's 128 k, the same one on both sides, which leaves
+// the sum's terms as they are.
+//
+// B's rows go in as the instruction's first operand, A's as its second, so that
+// a lane ends up with D[m][n .. n+3], m = lane % 16, n = 4 (lane / 16): four
+// neighbours in a row of D, stored at once.
+//
+// LDS: row r of a panel at 128 r, chunk c in slot c ^ ((r / 2) % 8).  The 16
+// rows that a lane group reads at one c then lie in 16 different 16-byte slots
+// of 256 bytes, which is what a 128-bit read needs to be free of conflicts.
+// The loads that go straight from memory to LDS place lane l at 16 l behind a
+// wavefront-wide base, so the permutation is in the address that they read:
+// 8 lanes still read 128 bytes of one row.
+#pragma once
+
+#include "sgemm_internal.h"
+
+namespace sgemm {
+namespace nt {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+constexpr int kStep = 128;  // bytes of a row per step
+
+// One operand: `rows` rows of K bytes, ld bytes apart (a multiple of 16, as
+// the base), and a scale for each 1 << shift rows of each step.
+struct Side {
+  const uint8_t* p;
+  int64_t ld;
+  int rows;
+  const void* s;
+  int64_t s_row, s_col;
+  int shift;
+  int64_t batch;  // bytes between the matrices of a batch
+};
+
+struct Frag {
+  v4i lo, hi;  // chunks g and 4 + g
+};
+
+// Tile: BM rows of A by BN rows of B, over WM x WN wavefronts.
+template <int BM_, int BN_, int WM_, int WN_, int WPS_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int WPS = WPS_;  // wavefronts per SIMD the registers must allow
+  static constexpr int threads = 64 * WM * WN;
+  static constexpr int TM = BM / WM, TN = BN / WN;
+  static constexpr int MT = TM / 16, NT = TN / 16;
+};
+
+// Where a block's tile lies in D.
+struct Place {
+  int tm, tn;
+};
+
+// Blocks in the order of their ids within an XCD walk columns of tiles `group`
+// high, so that the tiles an XCD runs together share A and B panels in its L2.
+__device__ __forceinline__ Place place_of(int64_t id, int tiles_m, int tiles_n, int group) {
+  const int64_t per = int64_t(group) * tiles_n;
+  const int first = static_cast<int>(id / per) * group;
+  const int high = min(group, tiles_m - first);
+  const int64_t in = id % per;
+  return Place{first + static_cast<int>(in % high), static_cast<int>(in / high)};
+}
+
+// The chunks of a panel of ROWS rows, split over the wavefronts of the block.
+template <int ROWS, int WAVES>
+struct Panel {
+  static constexpr int kLoads = ROWS / 8 / WAVES;  // 1 KB loads per wavefront
+  static_assert(ROWS % (8 * WAVES) == 0, "every wavefront takes whole loads");
+  uint32_t off[kLoads];
+  uint32_t chunk;  // of this lane, bytes into the step (the same for all its loads but for bit 6)
+
+  // Rows past the end repeat the last one: in bounds, and their sums are not stored.
+  __device__ __forceinline__ void init(int wave, int lane, int rows_left, int64_t ld) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = (wave * kLoads + i) * 8 + lane / 8;
+      const int slot = lane % 8;
+      const int c = slot ^ ((row / 2) % 8);
+      off[i] = static_cast<uint32_t>(min(row, rows_left - 1)) * static_cast<uint32_t>(ld) + 16 * c;
+    }
+  }
+  __device__ __forceinline__ void load(const uint8_t* base, uint8_t* lds, int wave) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      __builtin_amdgcn_global_load_lds(base + off[i],
+                                       (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + i) * 1024),
+                                       16, 0, 0);
+  }
+  // The last, partial step: chunks past K's end (`left` bytes from base) repeat the last one.
+  __device__ __forceinline__ void load_last(const uint8_t* base, uint8_t* lds, int wave, int lane, int left) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = (wave * kLoads + i) * 8 + lane / 8;
+      const uint32_t c = 16 * ((lane % 8) ^ ((row / 2) % 8));
+      const uint32_t last = static_cast<uint32_t>(left - 1) / 16 * 16;
+      __builtin_amdgcn_global_load_lds(base + (off[i] - c + min(c, last)),
+                                       (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + i) * 1024),
+                                       16, 0, 0);
+    }
+  }
+};
+
+__device__ __forceinline__ Frag read_frag(const uint8_t* panel, int row, int g) {
+  const int x = (row / 2) % 8;
+  Frag f;
+  f.lo = *reinterpret_cast<const v4i*>(panel + row * kStep + 16 * (g ^ x));
+  f.hi = *reinterpret_cast<const v4i*>(panel + row * kStep + 16 * ((4 + g) ^ x));
+  return f;
+}
+
+// Zeroes the bytes of a chunk from byte `keep` on.
+__device__ __forceinline__ v4i mask_chunk(v4i v, int keep) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int k = keep - 4 * w;
+    v[w] = k >= 4 ? v[w] : k <= 0 ? 0 : v[w] & ((1 << (8 * k)) - 1);
+  }
+  return v;
+}
+
+__device__ __forceinline__ Frag mask_frag(Frag f, int g, int left) {
+  f.lo = mask_chunk(f.lo, left - 16 * g);
+  f.hi = mask_chunk(f.hi, left - 16 * (4 + g));
+  return f;
+}
+
+// --- what a step does with two fragments -----------------------------------
+//
+// A policy's Op is a fragment as its matrix instructions take it; mac adds the
+// product of B's fragment n and A's fragment m; kScaleBytes is what a scale has
+// in memory, kRowScales whether mac takes the scales of the four D columns
+// (floats, in sn) or B's row's own (bits, in sn[0]).
+
+__device__ __forceinline__ v8i join(const Frag& f) {
+  return __builtin_shufflevector(f.lo, f.hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// A scale as float: its bits, or 2^(e - 127) of an e8m0 byte (255 is NaN, 0 is
+// subnormal).
+template <int BYTES>
+__device__ __forceinline__ float scale_value(uint32_t s) {
+  if constexpr (BYTES == 4) return __uint_as_float(s);
+  return __uint_as_float(s == 255 ? 0x7fc00000u : s == 0 ? 0x00400000u : s << 23);
+}
+
+// The 8-bit matrix instruction, as its rounding was measured: the products of
+// eight neighbours along k are lined up with the largest of them and cut 13
+// bits below it, and only the sums of eight are added as floats.  On normal
+// data that is 1.5e-5 of the result, far below the half step of a 16-bit
+// result (2^-9, 2^-12), and far above a float's: float results use Widened.
+
+// Float scales: a block of 128 is summed from zero and added times its scales'
+// product (the matrix instruction can apply powers of two only).  UNIFORM: all
+// B rows of a wavefront share a scale.
+template <bool UNIFORM>
+struct Fp8F32 {
+  static constexpr int kScaleBytes = 4;
+  static constexpr bool kUniform = UNIFORM, kRowScales = true;
+  using Acc = v4f;
+  using Op = v8i;
+  static __device__ __forceinline__ Op prepare(const Frag& f) { return join(f); }
+  static __device__ __forceinline__ void zero(Acc& a) { a = v4f{0, 0, 0, 0}; }
+  static __device__ __forceinline__ void mac(Acc& acc, const Op& n, const Op& m, v4f sn, float sm) {
+    const v4f z = {0, 0, 0, 0};
+    add(acc, __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(n, m, z, 0, 0, 0, 0, 0, 0), sn, sm);
+  }
+  static __device__ __forceinline__ void add(Acc& acc, v4f t, v4f sn, float sm) {
+    if constexpr (UNIFORM) {
+      const float s = sm * sn[0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(t[i], s, acc[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(t[i], sm * sn[i], acc[i]);
+    }
+  }
+  static __device__ __forceinline__ v4f value(const Acc& a) { return a; }
+};
+
+// Power-of-two scales, which the matrix instruction applies: lane l gives the
+// scale of row l % 16, the same for all of the block's 128 k.
+struct Fp8E8M0 {
+  static constexpr int kScaleBytes = 1;
+  static constexpr bool kUniform = false, kRowScales = false;
+  using Acc = v4f;
+  using Op = v8i;
+  static __device__ __forceinline__ Op prepare(const Frag& f) { return join(f); }
+  static __device__ __forceinline__ void zero(Acc& a) { a = v4f{0, 0, 0, 0}; }
+  static __device__ __forceinline__ void mac(Acc& acc, const Op& n, const Op& m, uint32_t sn, uint32_t sm) {
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(n, m, acc, 0, 0, 0, sn, 0, sm);
+  }
+  static __device__ __forceinline__ v4f value(const Acc& a) { return a; }
+};
+
+// The codes widened to halfs, which is exact, and multiplied by the half
+// instruction, whose sums keep a float's bits: half the 8-bit rate.
+template <bool UNIFORM, int BYTES>
+struct Widened {
+  static constexpr int kScaleBytes = BYTES;
+  static constexpr bool kUniform = UNIFORM, kRowScales = true;
+  using Acc = v4f;
+  struct Op {
+    v8h k[4];
+  };
+  static __device__ __forceinline__ Op prepare(const Frag& f) {
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    Op o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const uint32_t c = static_cast<uint32_t>(q < 2 ? f.lo[2 * q + w] : f.hi[2 * (q - 2) + w]);
+        const v2h x = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, false));
+        const v2h y = __builtin_bit_cast(v2h, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, 1.0f, true));
+        o.k[q][4 * w] = x[0];
+        o.k[q][4 * w + 1] = x[1];
+        o.k[q][4 * w + 2] = y[0];
+        o.k[q][4 * w + 3] = y[1];
+      }
+    return o;
+  }
+  static __device__ __forceinline__ void zero(Acc& a) { a = v4f{0, 0, 0, 0}; }
+  static __device__ __forceinline__ void mac(Acc& acc, const Op& n, const Op& m, v4f sn, float sm) {
+    v4f t = {0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(n.k[q], m.k[q], t, 0, 0, 0);
+    Fp8F32<UNIFORM>::add(acc, t, sn, sm);
+  }
+  static __device__ __forceinline__ v4f value(const Acc& a) { return a; }
+};
+
+// Pairs of halfs, x = hi + lo 2^-11: hi hi' in one sum, hi lo' + lo hi' in
+// another that is 2^11 larger; lo lo' (2^-22 of the product) is left out, as
+// small as the pair's own rounding.
+struct HalfPair {
+  static constexpr int kScaleBytes = 0;
+  static constexpr bool kUniform = false, kRowScales = false;
+  struct Acc {
+    v4f hh, x;
+  };
+  using Op = Frag;
+  static __device__ __forceinline__ Op prepare(const Frag& f) { return f; }
+  static __device__ __forceinline__ void zero(Acc& a) { a.hh = a.x = v4f{0, 0, 0, 0}; }
+  static __device__ __forceinline__ void mac(Acc& acc, const Op& n, const Op& m, uint32_t, uint32_t) {
+    const v8h nh = __builtin_bit_cast(v8h, n.lo), nl = __builtin_bit_cast(v8h, n.hi);
+    const v8h mh = __builtin_bit_cast(v8h, m.lo), ml = __builtin_bit_cast(v8h, m.hi);
+    acc.hh = __builtin_amdgcn_mfma_f32_16x16x32_f16(nh, mh, acc.hh, 0, 0, 0);
+    acc.x = __builtin_amdgcn_mfma_f32_16x16x32_f16(nh, ml, acc.x, 0, 0, 0);
+    acc.x = __builtin_amdgcn_mfma_f32_16x16x32_f16(nl, mh, acc.x, 0, 0, 0);
+  }
+  static __device__ __forceinline__ v4f value(const Acc& a) {
+    v4f r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = fmaf(a.x[i], 0x1p-11f, a.hh[i]);
+    return r;
+  }
+};
+
+// --- the tile -------------------------------------------------------------
+
+template <class P, class T>
+struct Shared {
+  static constexpr int kScales = P::kScaleBytes ? T::BM + T::BN : 0;
+  alignas(16) uint8_t a[2][T::BM * kStep];
+  alignas(16) uint8_t b[2][T::BN * kStep];
+  uint32_t s[2][kScales ? kScales : 1];
+};
+
+// A wavefront's sums.
+template <class P, class T>
+struct Sums {
+  typename P::Acc v[T::NT][T::MT];
+};
+
+// The scale of row `row` (clamped) of a side at step k, as 32 bits.
+template <int BYTES>
+__device__ __forceinline__ uint32_t load_scale(const Side& o, int row, int k) {
+  const int64_t at = int64_t(min(row, o.rows - 1) >> o.shift) * o.s_row + int64_t(k) * o.s_col;
+  if constexpr (BYTES == 4) return static_cast<const uint32_t*>(o.s)[at];
+  return static_cast<const uint8_t*>(o.s)[at];
+}
+
+// Sums the tile at rows m0 of A and n0 of B over steps [k0, k1) of K bytes
+// (the last of which may be partial) into acc.
+template <class P, class T>
+struct TileOp {
+static __device__ __forceinline__ void sum(Shared<P, T>& sh, const Side& A, const Side& B, int m0, int n0, int K,
+                                         int k0, int k1, Sums<P, T>& acc) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  const int wm = wave % T::WM, wn = wave / T::WM;
+  const int row = lane % 16, g = lane / 16;
+
+#pragma unroll
+  for (int j = 0; j < T::NT; ++j)
+#pragma unroll
+    for (int i = 0; i < T::MT; ++i) P::zero(acc.v[j][i]);
+  if (k0 >= k1) return;
+
+  Panel<T::BM, T::WM * T::WN> pa;
+  Panel<T::BN, T::WM * T::WN> pb;
+  pa.init(wave, lane, A.rows - m0, A.ld);
+  pb.init(wave, lane, B.rows - n0, B.ld);
+  const uint8_t* ga = A.p + int64_t(m0) * A.ld;
+  const uint8_t* gb = B.p + int64_t(n0) * B.ld;
+
+  constexpr int kScales = Shared<P, T>::kScales;
+  constexpr int kPer = (kScales + T::threads - 1) / T::threads;
+  uint32_t sc[kPer ? kPer : 1];
+
+  auto fetch = [&](int k, int buf) {
+    const int left = K - k * kStep;
+    if (left >= kStep) {
+      pa.load(ga + int64_t(k) * kStep, sh.a[buf], wave);
+      pb.load(gb + int64_t(k) * kStep, sh.b[buf], wave);
+    } else {
+      pa.load_last(ga + int64_t(k) * kStep, sh.a[buf], wave, lane, left);
+      pb.load_last(gb + int64_t(k) * kStep, sh.b[buf], wave, lane, left);
+    }
+    if constexpr (kScales > 0) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int r = threadIdx.x + i * T::threads;
+        if (r < T::BM) sc[i] = load_scale<P::kScaleBytes>(A, m0 + r, k);
+        else if (r < kScales) sc[i] = load_scale<P::kScaleBytes>(B, n0 + r - T::BM, k);
+      }
+    }
+  };
+  auto place_scales = [&](int buf) {
+    if constexpr (kScales > 0) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int r = threadIdx.x + i * T::threads;
+        if (r < kScales) sh.s[buf][r] = sc[i];
+      }
+    }
+  };
+  auto step = [&](int buf, bool partial, int left) {
+    typename P::Op mo[T::MT];
+    uint32_t sm[T::MT];
+#pragma unroll
+    for (int i = 0; i < T::MT; ++i) {
+      Frag f = read_frag(sh.a[buf], wm * T::TM + 16 * i + row, g);
+      if (partial) f = mask_frag(f, g, left);
+      mo[i] = P::prepare(f);
+      sm[i] = 0;
+      if constexpr (kScales > 0) sm[i] = sh.s[buf][wm * T::TM + 16 * i + row];
+    }
+#pragma unroll
+    for (int j = 0; j < T::NT; ++j) {
+      Frag f = read_frag(sh.b[buf], wn * T::TN + 16 * j + row, g);
+      if (partial) f = mask_frag(f, g, left);
+      const typename P::Op no = P::prepare(f);
+      if constexpr (P::kRowScales) {
+        v4f sn;
+        const uint32_t* s = &sh.s[buf][T::BM + wn * T::TN + (P::kUniform ? 0 : 16 * j + 4 * g)];
+#pragma unroll
+        for (int i = 0; i < (P::kUniform ? 1 : 4); ++i) sn[i] = scale_value<P::kScaleBytes>(s[i]);
+#pragma unroll
+        for (int i = 0; i < T::MT; ++i) P::mac(acc.v[j][i], no, mo[i], sn, scale_value<P::kScaleBytes>(sm[i]));
+      } else {
+        uint32_t sn = 0;
+        if constexpr (kScales > 0) sn = sh.s[buf][T::BM + wn * T::TN + 16 * j + row];
+#pragma unroll
+        for (int i = 0; i < T::MT; ++i) P::mac(acc.v[j][i], no, mo[i], sn, sm[i]);
+      }
+    }
+  };
+
+  fetch(k0, 0);
+  place_scales(0);
+  for (int k = k0; k < k1; ++k) {
+    const int buf = (k - k0) & 1;
+    __syncthreads();  // this step's panels have arrived, and the other buffer has been read
+    if (k + 1 < k1) fetch(k + 1, buf ^ 1);
+    const int left = K - k * kStep;
+    if (left >= kStep) step(buf, false, kStep);
+    else step(buf, true, left);
+    if (k + 1 < k1) place_scales(buf ^ 1);
+  }
+}
+
+// Calls epi(m, n, v) for every four neighbours D[m][n .. n+3] that the lane
+// holds, also past D's edges.
+template <class E>
+static __device__ __forceinline__ void out(const Sums<P, T>& acc, int m0, int n0, const E& epi) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  const int wm = wave % T::WM, wn = wave / T::WM;
+#pragma unroll
+  for (int i = 0; i < T::MT; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NT; ++j)
+      epi(m0 + wm * T::TM + 16 * i + lane % 16, n0 + wn * T::TN + 16 * j + 4 * (lane / 16), P::value(acc.v[j][i]));
+}
+};
+
+}  // namespace nt
+}  // namespace sgemm

@@ -1,0 +1,423 @@
+// orthogonal.hip -- hip_orthogonalize: Newton-Schulz products on the matrix
+// cores with operands as pairs of halfs.
+//
+// A number x of the iterate is kept as hi + lo 2^-11 with halfs hi = RN(s x),
+// lo = RN(2^11 (s x - hi)) for a fixed power of two s: 22 significant bits
+// while |s x| is between 2^-14 and 65504, an absolute 2^-36 below.  The sums
+// are float.  Three half products an element (hi hi', hi lo', lo hi') run at a
+// third of the half rate, five times the float matrix rate, and err no more
+// than float products do.
+//
+// Per step, with m <= n the sides of the iterate X and X^T kept beside it, all
+// operands have their K side contiguous:
+//   S = X X^T               (m x m, K = n; symmetric: the lower tiles, mirrored)
+//   P = b S + c S S         (m x m, K = m; S is its own transpose; symmetric)
+//   X' = a X + P X          (m x n, K = m; X^T is the other operand), written
+//                           as X' (in place: a block reads what it writes) and
+//                           as X'^T into the other of two buffers.
+#include "../../include/orthogonal.h"
+#include "lowp.h"
+#include "nt_tile.h"
+
+namespace sgemm {
+namespace {
+
+using nt::Side;
+using nt::v4f;
+
+constexpr float kScaleX = 0x1p12f;  // |X| < 16
+constexpr float kScaleS = 0x1p8f;   // |S|, |P| < 255
+constexpr int kNormBlocks = 256;
+
+__host__ __device__ inline int64_t pad32(int64_t n) { return (n + 31) / 32 * 32; }
+
+// A matrix of pairs: row r, element k at r * ld + (k / 32) * 128 + 2 (k % 32),
+// hi there and lo 64 bytes on; rows padded to 32 elements with zeros.
+struct Pairs {
+  uint8_t* p;
+  int64_t ld;     // bytes
+  int64_t batch;  // bytes between matrices
+};
+
+__device__ __forceinline__ int64_t pair_at(int64_t k) { return k / 32 * 128 + 2 * (k % 32); }
+
+__device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
+  hi = static_cast<_Float16>(v);
+  lo = static_cast<_Float16>((v - static_cast<float>(hi)) * 2048.0f);
+}
+
+__device__ __forceinline__ void store_pair(uint8_t* row, int64_t k, float v) {
+  _Float16 hi, lo;
+  split(v, hi, lo);
+  uint8_t* at = row + pair_at(k);
+  *reinterpret_cast<_Float16*>(at) = hi;
+  *reinterpret_cast<_Float16*>(at + 64) = lo;
+}
+
+// Four neighbours from k, a multiple of 4.
+__device__ __forceinline__ void store_pairs(uint8_t* row, int64_t k, v4f v) {
+  Pack<4, _Float16> hi, lo;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split(v[i], hi.v[i], lo.v[i]);
+  uint8_t* at = row + pair_at(k);
+  *reinterpret_cast<uint2*>(at) = __builtin_bit_cast(uint2, hi);
+  *reinterpret_cast<uint2*>(at + 64) = __builtin_bit_cast(uint2, lo);
+}
+
+__device__ __forceinline__ v4f load_pairs(const uint8_t* row, int64_t k) {
+  const uint8_t* at = row + pair_at(k);
+  const auto hi = __builtin_bit_cast(Pack<4, _Float16>, *reinterpret_cast<const uint2*>(at));
+  const auto lo = __builtin_bit_cast(Pack<4, _Float16>, *reinterpret_cast<const uint2*>(at + 64));
+  v4f v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = fmaf(static_cast<float>(lo.v[i]), 0x1p-11f, static_cast<float>(hi.v[i]));
+  return v;
+}
+
+struct Source {
+  const void* g;
+  int64_t ld, batch;
+  int rows, cols;
+};
+
+// The sum of squares of a matrix, in doubles: every block a part, in a fixed
+// order (no atomics).
+template <class T>
+__global__ __launch_bounds__(256) void k_norm(Source src, double* part, int parts) {
+  const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
+  const int groups = static_cast<int>(ceil_div(src.cols, 4));
+  const int64_t items = int64_t(src.rows) * groups;
+  double sum = 0;
+  for (int64_t it = int64_t(blockIdx.x) * 256 + threadIdx.x; it < items; it += int64_t(parts) * 256) {
+    const int64_t row = it / groups;
+    const int col = static_cast<int>(it % groups) * 4;
+    const T* p = g + row * src.ld + col;
+    if (col + 4 <= src.cols) {
+      const Pack<4, T> v = load_pack<4>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const double x = to_float(v.v[i]);
+        sum = fma(x, x, sum);
+      }
+    } else {
+      for (int i = 0; i < src.cols - col; ++i) {
+        const double x = to_float(p[i]);
+        sum = fma(x, x, sum);
+      }
+    }
+  }
+  __shared__ double s[256];
+  s[threadIdx.x] = sum;
+  __syncthreads();
+  for (int d = 128; d > 0; d /= 2) {
+    if (static_cast<int>(threadIdx.x) < d) s[threadIdx.x] += s[threadIdx.x + d];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) part[int64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = s[0];
+}
+
+// |G|_F + eps from the parts; all threads of a 256-thread block call it.
+__device__ __forceinline__ float divisor(const double* part, int parts, float eps, double* s) {
+  s[threadIdx.x] = static_cast<int>(threadIdx.x) < parts ? part[int64_t(blockIdx.y) * kNormBlocks + threadIdx.x] : 0.0;
+  __syncthreads();
+  for (int d = 128; d > 0; d /= 2) {
+    if (static_cast<int>(threadIdx.x) < d) s[threadIdx.x] += s[threadIdx.x + d];
+    __syncthreads();
+  }
+  return static_cast<float>(sqrt(s[0])) + eps;
+}
+
+// X_0 as pairs, as G lies (`direct`: rows of G) and transposed (`across`), a
+// 64 x 64 tile a block through LDS; both padded with zeros.
+template <class T>
+__global__ __launch_bounds__(256) void k_start(Source src, const double* part, int parts, float eps, Pairs direct,
+                                               Pairs across, int tiles_c) {
+  __shared__ double s[256];
+  __shared__ float t[64][65];
+  const float div = divisor(part, parts, eps, s);
+  const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
+  const int r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
+#pragma unroll
+  for (int p = 0; p < 16; ++p) {
+    const int r = p * 4 + threadIdx.x / 64, c = threadIdx.x % 64;
+    float v = 0.0f;
+    if (r0 + r < src.rows && c0 + c < src.cols) v = to_float(g[(r0 + r) * src.ld + c0 + c]) / div;
+    t[r][c] = v * kScaleX;
+  }
+  __syncthreads();
+  uint8_t* dp = direct.p + blockIdx.y * direct.batch;
+  uint8_t* ap = across.p + blockIdx.y * across.batch;
+  const int64_t dpad = pad32(src.cols), apad = pad32(src.rows);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int r = p * 16 + threadIdx.x / 16, c = threadIdx.x % 16 * 4;
+    if (r0 + r < src.rows && c0 + c < dpad)
+      store_pairs(dp + (r0 + r) * direct.ld, c0 + c, v4f{t[r][c], t[r][c + 1], t[r][c + 2], t[r][c + 3]});
+    if (c0 + r < src.cols && r0 + c < apad)
+      store_pairs(ap + (c0 + r) * across.ld, r0 + c, v4f{t[c][r], t[c + 1][r], t[c + 2][r], t[c + 3][r]});
+  }
+}
+
+// steps == 0: G / (|G|_F + eps).
+template <class T>
+__global__ __launch_bounds__(256) void k_divide(Source src, const double* part, int parts, float eps, T* x,
+                                                int64_t ldx, int64_t batch_x) {
+  __shared__ double s[256];
+  const float div = divisor(part, parts, eps, s);
+  const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
+  const int64_t items = int64_t(src.rows) * src.cols;
+  for (int64_t it = int64_t(blockIdx.x) * 256 + threadIdx.x; it < items; it += int64_t(gridDim.x) * 256) {
+    const int64_t r = it / src.cols, c = it % src.cols;
+    from_float(to_float(g[r * src.ld + c]) / div, x[blockIdx.y * batch_x + r * ldx + c]);
+  }
+}
+
+// A symmetric m x m matrix of pairs: value(m, n, v) of the sums, written at its
+// place and, off the diagonal tiles, mirrored.  Both indexes run on past m to
+// the padding, where zeros go.
+struct SymmetricOut {
+  Pairs out, add;  // add: the matrix that is added times `b`, or none
+  int m;
+  float scale, b;
+  int batch;
+  bool mirror;
+  __device__ __forceinline__ void operator()(int r, int c, v4f v) const {
+    if (r >= pad32(m) || c >= pad32(m)) return;
+    uint8_t* base = out.p + batch * out.batch;
+    v4f x = {0, 0, 0, 0};
+    if (r < m) {
+      const v4f old = add.p ? load_pairs(add.p + batch * add.batch + r * add.ld, c) : x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = c + i < m ? fmaf(v[i], scale, b * old[i]) : 0.0f;
+      store_pairs(base + r * out.ld, c, x);
+    }
+    if (mirror) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < m) store_pair(base + (c + i) * out.ld, r, x[i]);
+    }
+  }
+};
+
+// a X + P X: as pairs in place and transposed, or at the last step as the result.
+template <class T>
+struct IterateOut {
+  Pairs x, xt;
+  T* out;  // not NULL at the last step
+  int64_t ldo, batch_o;
+  int m, n;
+  float a;
+  int batch;
+  bool tall;
+  __device__ __forceinline__ void operator()(int r, int c, v4f v) const {
+    if (r >= pad32(m) || c >= pad32(n)) return;
+    uint8_t* row = x.p + batch * x.batch + r * x.ld;
+    v4f y = {0, 0, 0, 0};
+    if (r < m) {
+      const v4f old = load_pairs(row, c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = c + i < n ? fmaf(a, old[i], v[i] * (1.0f / kScaleS)) : 0.0f;
+    }
+    if (out) {
+      if (r >= m) return;
+      T* o = out + batch * batch_o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < n) from_float(y[i] * (1.0f / kScaleX), tall ? o[(c + i) * ldo + r] : o[r * ldo + c + i]);
+    } else {
+      if (r < m) store_pairs(row, c, y);
+      uint8_t* t = xt.p + batch * xt.batch;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < n) store_pair(t + (c + i) * xt.ld, r, y[i]);
+    }
+  }
+};
+
+using Tile = nt::Tile<64, 64, 2, 2, 2>;
+
+// The lower triangle's tiles, row by row.
+__device__ __forceinline__ nt::Place triangle(int id) {
+  int i = static_cast<int>((sqrtf(8.0f * id + 1.0f) - 1.0f) * 0.5f);
+  while ((i + 1) * (i + 2) / 2 <= id) ++i;
+  while (i * (i + 1) / 2 > id) --i;
+  return nt::Place{i, id - i * (i + 1) / 2};
+}
+
+template <class T>
+__global__ __launch_bounds__(T::threads, T::WPS) void k_symmetric(Side A, int K, SymmetricOut out) {
+  __shared__ nt::Shared<nt::HalfPair, T> sh;
+  out.batch = blockIdx.y;
+  A.p += blockIdx.y * A.batch;
+  const nt::Place at = triangle(blockIdx.x);
+  out.mirror = at.tm != at.tn;
+  nt::Sums<nt::HalfPair, T> acc;
+  nt::TileOp<nt::HalfPair, T>::sum(sh, A, A, at.tm * T::BM, at.tn * T::BN, K * 4, 0, K / 32, acc);
+  nt::TileOp<nt::HalfPair, T>::out(acc, at.tm * T::BM, at.tn * T::BN, out);
+}
+
+template <class T, class O>
+__global__ __launch_bounds__(T::threads, T::WPS) void k_iterate(Side A, Side B, int K, IterateOut<O> out, int tiles_m,
+                                                                int tiles_n) {
+  __shared__ nt::Shared<nt::HalfPair, T> sh;
+  out.batch = blockIdx.y;
+  A.p += blockIdx.y * A.batch;
+  B.p += blockIdx.y * B.batch;
+  const nt::Place at = nt::place_of(xcd_contiguous(blockIdx.x, gridDim.x), tiles_m, tiles_n, 8);
+  nt::Sums<nt::HalfPair, T> acc;
+  nt::TileOp<nt::HalfPair, T>::sum(sh, A, B, at.tm * T::BM, at.tn * T::BN, K * 4, 0, K / 32, acc);
+  nt::TileOp<nt::HalfPair, T>::out(acc, at.tm * T::BM, at.tn * T::BN, out);
+}
+
+// The workspace: per-block parts of the norms, then X, X^T twice, S and P.
+struct Layout {
+  int m, n;
+  int64_t part, x, xt[2], s, p, bytes;
+  int64_t ldx, ldm;  // bytes of a row of X, and of the others
+};
+
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+Layout layout_of(int batch, int rows, int cols) {
+  Layout l;
+  l.m = rows < cols ? rows : cols;
+  l.n = rows < cols ? cols : rows;
+  l.ldx = pad32(l.n) * 4;
+  l.ldm = pad32(l.m) * 4;
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += up256(bytes);
+    return here;
+  };
+  l.part = take(int64_t(batch) * kNormBlocks * 8);
+  l.x = take(batch * (l.m * l.ldx));
+  l.xt[0] = take(batch * (l.n * l.ldm));
+  l.xt[1] = take(batch * (l.n * l.ldm));
+  l.s = take(batch * (l.m * l.ldm));
+  l.p = take(batch * (l.m * l.ldm));
+  l.bytes = at;
+  return l;
+}
+
+int check_sizes(int batch, int rows, int cols, int type) {
+  if (batch < 0 || batch > 65535) return -1;
+  if (rows < 0 || rows > HIP_ORTHOGONAL_MAX_SIZE) return -2;
+  if (cols < 0 || cols > HIP_ORTHOGONAL_MAX_SIZE) return -3;
+  if (type != HIP_ORTHOGONAL_F32 && type != HIP_ORTHOGONAL_BF16 && type != HIP_ORTHOGONAL_F16) return -4;
+  return 0;
+}
+
+template <class T>
+hipError_t launch(int batch, const Source& src, int steps, const float* co, float eps, T* x, int64_t ldx,
+                  int64_t batch_x, uint8_t* ws, hipStream_t stream) {
+  const Layout l = layout_of(batch, src.rows, src.cols);
+  double* part = reinterpret_cast<double*>(ws + l.part);
+  const int64_t groups = int64_t(src.rows) * ceil_div(src.cols, 4);
+  const int parts = static_cast<int>(ceil_div(groups, 1024) < kNormBlocks ? ceil_div(groups, 1024) : kNormBlocks);
+  hipLaunchKernelGGL((k_norm<T>), dim3(parts, batch), dim3(256), 0, stream, src, part, parts);
+  if (steps == 0) {
+    const int64_t blocks = ceil_div(int64_t(src.rows) * src.cols, 256);
+    hipLaunchKernelGGL((k_divide<T>), dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), batch), dim3(256), 0,
+                       stream, src, part, parts, eps, x, ldx, batch_x);
+    return hipGetLastError();
+  }
+  const bool tall = src.rows > src.cols;
+  const Pairs X{ws + l.x, l.ldx, l.m * l.ldx};
+  Pairs XT{ws + l.xt[0], l.ldm, l.n * l.ldm}, XT2{ws + l.xt[1], l.ldm, l.n * l.ldm};
+  const Pairs S{ws + l.s, l.ldm, l.m * l.ldm}, P{ws + l.p, l.ldm, l.m * l.ldm};
+  // 64-wide tiles: both paddings (to 32) lie inside them
+  const int64_t tr = ceil_div(src.rows, 64), tc = ceil_div(src.cols, 64);
+  hipLaunchKernelGGL((k_start<T>), dim3(static_cast<unsigned>(tr * tc), batch), dim3(256), 0, stream, src, part, parts,
+                     eps, tall ? XT : X, tall ? X : XT, static_cast<int>(tc));
+  const auto side = [](const Pairs& p, int rows) { return Side{p.p, p.ld, rows, nullptr, 0, 0, 0, p.batch}; };
+  const int km = static_cast<int>(pad32(l.m)), kn = static_cast<int>(pad32(l.n));
+  const unsigned tm = static_cast<unsigned>(ceil_div(l.m, Tile::BM)), tn = static_cast<unsigned>(ceil_div(l.n, Tile::BN));
+  for (int i = 0; i < steps; ++i) {
+    const float a = co[3 * i], b = co[3 * i + 1], c = co[3 * i + 2];
+    hipLaunchKernelGGL((k_symmetric<Tile>), dim3(tm * (tm + 1) / 2, batch), dim3(Tile::threads), 0, stream,
+                       side(X, l.m), kn,
+                       SymmetricOut{S, Pairs{nullptr, 0, 0}, l.m, kScaleS / (kScaleX * kScaleX), 0.0f, 0, false});
+    hipLaunchKernelGGL((k_symmetric<Tile>), dim3(tm * (tm + 1) / 2, batch), dim3(Tile::threads), 0, stream,
+                       side(S, l.m), km, SymmetricOut{P, S, l.m, c / kScaleS, b, 0, false});
+    const bool last = i + 1 == steps;
+    hipLaunchKernelGGL((k_iterate<Tile, T>), dim3(tm * tn, batch), dim3(Tile::threads), 0, stream, side(P, l.m),
+                       side(XT, l.n), km,
+                       IterateOut<T>{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, a, 0, tall},
+                       static_cast<int>(tm), static_cast<int>(tn));
+    const Pairs t = XT;
+    XT = XT2;
+    XT2 = t;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" {
+
+int hip_orthogonalize_workspace(int batch, int rows, int cols, int type, long long* bytes) {
+  const int bad = check_sizes(batch, rows, cols, type);
+  if (bad) return bad;
+  if (bytes) *bytes = layout_of(batch, rows, cols).bytes;
+  return 0;
+}
+
+int hip_orthogonalize(int batch, int rows, int cols, int type, const void* G, int ldg, long long stride_g, int steps,
+                      const float* coefficients, float eps, void* X, int ldx, long long stride_x, void* workspace,
+                      long long workspace_bytes, hipStream_t stream) {
+  const int bad = check_sizes(batch, rows, cols, type);
+  if (bad) return bad;
+  const bool some = batch > 0 && rows > 0 && cols > 0;
+  if (some && G == nullptr) return -5;
+  if (ldg < (cols > 1 ? cols : 1)) return -6;
+  if (stride_g < 0) return -7;
+  if (steps < 0 || steps > HIP_ORTHOGONAL_MAX_STEPS) return -8;
+  if (some && steps > 0 && coefficients == nullptr) return -9;
+  if (!(eps >= 0.0f)) return -10;
+  if (some && X == nullptr) return -11;
+  if (ldx < (cols > 1 ? cols : 1)) return -12;
+  if (stride_x < 0 || (batch > 1 && stride_x < int64_t(rows) * ldx)) return -13;
+  if (!some) return 0;
+  if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return -14;
+  if (workspace_bytes < layout_of(batch, rows, cols).bytes) return -15;
+  const Source src{G, ldg, stride_g, rows, cols};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  hipError_t e;
+  if (type == HIP_ORTHOGONAL_F32)
+    e = launch(batch, src, steps, coefficients, eps, static_cast<float*>(X), ldx, stride_x, ws, stream);
+  else if (type == HIP_ORTHOGONAL_BF16)
+    e = launch(batch, src, steps, coefficients, eps, static_cast<bf16*>(X), ldx, stride_x, ws, stream);
+  else
+    e = launch(batch, src, steps, coefficients, eps, static_cast<_Float16*>(X), ldx, stride_x, ws, stream);
+  return static_cast<int>(e);
+}
+
+const char* hip_orthogonalize_status_string(int status) {
+  switch (status) {
+    case 0: return "success";
+    case -1: return "argument 1 (batch) is negative or above 65535";
+    case -2: return "argument 2 (rows) is negative or above HIP_ORTHOGONAL_MAX_SIZE";
+    case -3: return "argument 3 (cols) is negative or above HIP_ORTHOGONAL_MAX_SIZE";
+    case -4: return "argument 4 (type) is not a known type";
+    case -5: return "argument 5 (G) is NULL";
+    case -6: return "argument 6 (ldg) is smaller than max(1, cols)";
+    case -7: return "argument 7 (stride_g) is negative";
+    case -8: return "argument 8 (steps) is negative or above HIP_ORTHOGONAL_MAX_STEPS";
+    case -9: return "argument 9 (coefficients) is NULL";
+    case -10: return "argument 10 (eps) is negative or NaN";
+    case -11: return "argument 11 (X) is NULL";
+    case -12: return "argument 12 (ldx) is smaller than max(1, cols)";
+    case -13: return "argument 13 (stride_x) is negative or lets the batch's matrices overlap";
+    case -14: return "argument 14 (workspace) is NULL or not 256-byte aligned";
+    case -15: return "argument 15 (workspace_bytes) is smaller than hip_orthogonalize_workspace says";
+    default: break;
+  }
+  if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));
+  return "unknown status";
+}
+
+}  // extern "C"
