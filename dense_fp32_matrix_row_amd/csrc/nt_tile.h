@@ -383,6 +383,7 @@ static __device__ __forceinline__ void sum(Shared<P, T>& sh, const Side& A, cons
   place_scales(0);
   for (int k = k0; k < k1; ++k) {
     const int buf = (k - k0) & 1;
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the barrier alone need not wait for loads to LDS
     __syncthreads();  // this step's panels have arrived, and the other buffer has been read
     if (k + 1 < k1) fetch(k + 1, buf ^ 1);
     const int left = K - k * kStep;
