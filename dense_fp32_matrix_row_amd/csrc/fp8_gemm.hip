@@ -2,7 +2,7 @@
 // a scale for each block of 128 along K.
 #include "../../include/blockfp8.h"
 #include "lowp.h"
-#include "nt_tile.h"
+#include "nt_loop.h"
 
 namespace sgemm {
 namespace {
@@ -17,28 +17,47 @@ struct Out {
   int64_t ldd, ldc;
   int M, N;
   float alpha, beta;
-  __device__ __forceinline__ void operator()(int m, int n, v4f v) const {
-    if (m >= M || n >= N) return;
-    O* d0 = d + m * ldd + n;
-    const O* c0 = c + m * ldc + n;
-    if (n + 4 <= N) {
-      Pack<4, O> r, o;
-      if (beta != 0.0f) o = load_pack<4>(c0);
+  template <bool ADD>
+  __device__ __forceinline__ Pack<4, O> value(v4f v, const Pack<4, O>& o) const {
+    Pack<4, O> r;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x = alpha * v[i];
-        if (beta != 0.0f) x = fmaf(beta, to_float(o.v[i]), x);
-        from_float(x, r.v[i]);
-      }
-      store_pack(d0, r);
+    for (int i = 0; i < 4; ++i) {
+      float x = alpha * v[i];
+      if (ADD) x = fmaf(beta, to_float(o.v[i]), x);
+      from_float(x, r.v[i]);
+    }
+    return r;
+  }
+  // Four neighbours inside D, or across its edge.
+  template <bool ADD>
+  __device__ __forceinline__ void inside(int m, int n, v4f v) const {
+    Pack<4, O> o{};
+    if (ADD) o = load_pack<4>(c + m * ldc + n);
+    store_pack(d + m * ldd + n, value<ADD>(v, o));
+  }
+  template <bool ADD>
+  __device__ __forceinline__ void edge(int m, int n, v4f v) const {
+    if (m >= M) return;
+    Pack<4, O> o{};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (ADD && n + i < N) o.v[i] = c[m * ldc + n + i];
+    const Pack<4, O> r = value<ADD>(v, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < N) d[m * ldd + n + i] = r.v[i];
+  }
+  // each: calls its argument with (m, n, v) for all that a thread holds of the
+  // rows x cols tile at m0, n0.
+  template <class F>
+  __device__ __forceinline__ void tile(int m0, int n0, int rows, int cols, const F& each) const {
+    const bool whole = m0 + rows <= M && n0 + cols <= N;
+    if (beta == 0.0f) {
+      if (whole) each([&](int m, int n, v4f v) { inside<false>(m, n, v); });
+      else each([&](int m, int n, v4f v) { edge<false>(m, n, v); });
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < N) {
-          float x = alpha * v[i];
-          if (beta != 0.0f) x = fmaf(beta, to_float(c0[i]), x);
-          from_float(x, d0[i]);
-        }
+      if (whole) each([&](int m, int n, v4f v) { inside<true>(m, n, v); });
+      else each([&](int m, int n, v4f v) { edge<true>(m, n, v); });
     }
   }
 };
@@ -51,7 +70,8 @@ __global__ __launch_bounds__(T::threads, T::WPS) void k_gemm(Side A, Side B, int
     const nt::Place at = nt::place_of(xcd_contiguous(t, tiles), tiles_m, tiles_n, 8);
     nt::Sums<P, T> acc;
     nt::TileOp<P, T>::sum(sh, A, B, at.tm * T::BM, at.tn * T::BN, K, 0, static_cast<int>(ceil_div(K, nt::kStep)), acc);
-    nt::TileOp<P, T>::out(acc, at.tm * T::BM, at.tn * T::BN, out);
+    const int m0 = at.tm * T::BM, n0 = at.tn * T::BN;
+    out.tile(m0, n0, T::BM, T::BN, [&](const auto& epi) { nt::TileOp<P, T>::out(acc, m0, n0, epi); });
     __syncthreads();  // the next tile writes the same LDS
   }
 }
@@ -64,12 +84,37 @@ void launch_tile(const Side& A, const Side& B, int K, const Out<O>& out, hipStre
                      s, A, B, K, out, static_cast<int>(tm), static_cast<int>(tn), tiles);
 }
 
+template <class L, class O>
+__global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, Out<O> out, int tiles_m, int tiles_n) {
+  __shared__ alignas(16) uint8_t smem[L::kLds];
+  const nt::Place at = nt::place_of(xcd_contiguous(blockIdx.x, gridDim.x), tiles_m, tiles_n, 8);
+  const int m0 = at.tm * L::BM, n0 = at.tn * L::BN;
+  nt::v16f acc[L::kAcc];
+  nt::loop_sum<L>(smem, A, B, m0, n0, K, acc);
+  out.tile(m0, n0, L::BM, L::BN, [&](const auto& epi) { nt::loop_out<L>(acc, m0, n0, epi); });
+}
+
+template <class L, class O>
+void launch_loop(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
+  const int64_t tm = ceil_div(out.M, L::BM), tn = ceil_div(out.N, L::BN);
+  hipLaunchKernelGGL((k_loop<L, O>), dim3(static_cast<unsigned>(tm * tn)), dim3(L::threads), 0, s, A, B, K, out,
+                     static_cast<int>(tm), static_cast<int>(tn));
+}
+
 template <class P, class O>
 void launch_policy(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
   using Small = nt::Tile<64, 64, 2, 2, 2>;
   using Large = nt::Tile<128, 128, 2, 2, 2>;
   if (ceil_div(out.M, 128) * ceil_div(out.N, 128) >= 256) launch_tile<P, Large>(A, B, K, out, s);
   else launch_tile<P, Small>(A, B, K, out, s);
+}
+
+template <class P, nt::Kind KIND, class O>
+void launch_16(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
+  using L = nt::Loop<KIND, 8, 4, 2, 4>;
+  if (K > 0 && L::fits(A) && L::fits(B) && ceil_div(out.M, 128) * ceil_div(out.N, 128) >= 256)
+    launch_loop<L>(A, B, K, out, s);
+  else launch_policy<P>(A, B, K, out, s);
 }
 
 template <class O>
@@ -83,9 +128,9 @@ void launch_out(const Side& A, const Side& B, int K, int scale_type, const Out<O
       if (B.shift) launch_policy<nt::Widened<true, 4>>(A, B, K, out, s);
       else launch_policy<nt::Widened<false, 4>>(A, B, K, out, s);
     }
-  } else if (scale_type == HIP_FP8_SCALE_E8M0) launch_policy<nt::Fp8E8M0>(A, B, K, out, s);
-  else if (B.shift) launch_policy<nt::Fp8F32<true>>(A, B, K, out, s);
-  else launch_policy<nt::Fp8F32<false>>(A, B, K, out, s);
+  } else if (scale_type == HIP_FP8_SCALE_E8M0) launch_16<nt::Fp8E8M0, nt::Kind::kE8M0>(A, B, K, out, s);
+  else if (B.shift) launch_16<nt::Fp8F32<true>, nt::Kind::kF32Uniform>(A, B, K, out, s);
+  else launch_16<nt::Fp8F32<false>, nt::Kind::kF32Rows>(A, B, K, out, s);
 }
 
 bool bad_ld(int ld, int K) { return ld < (K > 1 ? K : 1) || ld % 16 != 0 || ld > HIP_FP8_MAX_LD; }

@@ -1,0 +1,142 @@
+// nt_loop.h -- the large tiles of the block-scaled 8-bit product and the
+// orthogonalised update: D = A * B^T over operands whose rows are contiguous
+// along K (nt_tile.h has the operands' form), with the K loop in assembly
+// (nt_loop.inc, written by gen_nt_loop.py).
+#pragma once
+
+#include "nt_loop.inc"
+#include "nt_tile.h"
+
+namespace sgemm {
+namespace nt {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+enum class Kind { kE8M0, kF32Uniform, kF32Rows, kPair };
+
+// Block tile of WM x WN wavefronts of 16 MT x 16 NT, 256 registers each.
+template <Kind KIND_, int MT_, int NT_, int WM_, int WN_>
+struct Loop {
+  static constexpr Kind KIND = KIND_;
+  static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_;
+  static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, waves = WM * WN, threads = 64 * waves;
+  static constexpr bool kScaled = KIND != Kind::kPair;
+  static constexpr int kScaleBytes = KIND == Kind::kE8M0 ? 1 : 4;
+  static constexpr int kStages = (BM + BN) * kStep <= 32768 ? 32768 : 65536;  // bytes from one to the next
+  static constexpr int kScaleLoads = kScaled ? ((BM + BN) / 64 + waves - 1) / waves : 0;
+  static constexpr int kLds = 2 * kStages + 2 * 256 * waves * kScaleLoads;
+  static constexpr int kA = BM / 8 / waves, kB = BN / 8 / waves;  // loads a wavefront and step
+  static constexpr int kAcc = MT * NT / 4;
+  static_assert(kA == 4 && (kB == 4 || kB == 2) && kScaleLoads <= 1, "the operands below");
+
+  // Whether every scale of a tile lies within 32 bits of the first.
+  static bool fits(const Side& o) { return !kScaled || o.s_row <= (int64_t(1) << 30) / 256 / kScaleBytes; }
+};
+
+#define NT_LOOP_RUN(NAME, SUMS, MORE, MASKS)                                                                  \
+  asm volatile(NT_LOOP_##NAME                                                                                 \
+               : SUMS, "+{s[60:63]}"(ra), "+{s[64:67]}"(rb), [steps] "+s"(steps), [aLo] "+v"(aLo),            \
+                 [aHi] "+v"(aHi), [bLo] "+v"(bLo), [bHi] "+v"(bHi) MORE                                       \
+               : [aEven] "v"(aEven), [aOdd] "v"(aOdd), [bEven] "v"(bEven), [bOdd] "v"(bOdd),                  \
+                 [ldsA] "s"(lds_a), [ldsB] "s"(lds_b), [oA0] "s"(oa[0]), [oA1] "s"(oa[1]), [oA2] "s"(oa[2]),  \
+                 [oA3] "s"(oa[3]), [oB0] "s"(ob[0]), [oB1] "s"(ob[1]), [oB2] "s"(ob[2]), [oB3] "s"(ob[3]) MASKS                                                                 \
+               : NT_CLOBBERS_##NAME, "memory", "scc")
+#define NT_SUMS_8                                                                                             \
+  "=&{v[0:15]}"(acc[0]), "=&{v[16:31]}"(acc[1]), "=&{v[32:47]}"(acc[2]), "=&{v[48:63]}"(acc[3]),              \
+      "=&{v[64:79]}"(acc[4]), "=&{v[80:95]}"(acc[5]), "=&{v[96:111]}"(acc[6]), "=&{v[112:127]}"(acc[7])
+#define NT_SCALES , "+{s[68:69]}"(sp), [aS] "+v"(aS), [bS] "+v"(bS)
+#define NT_MASKS                                                                                              \
+  , "{s[70:71]}"(ss), [ldsS] "s"(lds_s), [gS0] "v"(gs), [partial] "s"(partial), [maskLo0] "v"(mask[0]),       \
+      [maskLo1] "v"(mask[1]), [maskLo2] "v"(mask[2]), [maskLo3] "v"(mask[3]), [maskHi0] "v"(mask[4]),         \
+      [maskHi1] "v"(mask[5]), [maskHi2] "v"(mask[6]), [maskHi3] "v"(mask[7])
+#define NT_NONE
+
+// A value that all lanes of a wavefront share, in a scalar register.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(static_cast<int>(v)); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return uniform(static_cast<uint32_t>(v)) | static_cast<uint64_t>(uniform(static_cast<uint32_t>(v >> 32))) << 32;
+}
+
+// Sums the tile at rows m0 of A and n0 of B over K > 0 bytes.  LDS (L::kLds
+// bytes) must not be in use.
+template <class L>
+__device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Side& B, int m0, int n0, int K,
+                                         v16f (&acc)[L::kAcc]) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  const int wm = wave % L::WM, wn = wave / L::WM, row = lane % 16, g = lane / 16;
+  const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)smem));
+
+  // The panels end with their last row: what lies past it, or past the last row's end, is read as zeros.
+  const auto resource = [&](const Side& o, int row0, int rows) {
+    const uint64_t at = reinterpret_cast<uint64_t>(o.p + row0 * o.ld);
+    const uint32_t bytes = static_cast<uint32_t>(min(o.rows - row0, rows) - 1) * static_cast<uint32_t>(o.ld) + (K + 15) / 16 * 16;
+    return v4i{static_cast<int>(uniform(static_cast<uint32_t>(at))),
+               static_cast<int>(uniform(static_cast<uint32_t>(at >> 32) & 0xffff)), static_cast<int>(uniform(bytes)), 0x00020000};
+  };
+  v4i ra = resource(A, m0, L::BM), rb = resource(B, n0, L::BN);
+  // Load i of a wavefront takes rows (wave kA + i) 8 ..: every other one has its chunks 64 bytes off.
+  const uint32_t lda = static_cast<uint32_t>(A.ld), ldb = static_cast<uint32_t>(B.ld);
+  const uint32_t chunk = 16 * ((lane % 8) ^ (lane / 16));
+  const uint32_t aEven = lane / 8 * lda + chunk, aOdd = lane / 8 * lda + (chunk ^ 64);
+  const uint32_t bEven = lane / 8 * ldb + chunk, bOdd = lane / 8 * ldb + (chunk ^ 64);
+  uint32_t oa[4], ob[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    oa[i] = uniform((wave * L::kA + i) * 8 * lda);
+    ob[i] = uniform((wave * L::kB + i) * 8 * ldb);
+  }
+  const uint32_t lds_a = uniform(lds + wave * L::kA * 1024), lds_b = uniform(lds + wave * L::kB * 1024);
+
+  const uint32_t at = row * kStep + 16 * (g ^ ((row / 2) % 8));
+  uint32_t aLo = lds + wm * L::MT * 16 * kStep + at, aHi = aLo ^ 64;
+  uint32_t bLo = lds + (L::BM + wn * L::NT * 16) * kStep + at, bHi = bLo ^ 64;
+  uint32_t steps = uniform(static_cast<uint32_t>(K - 1) / kStep + 1);
+
+  if constexpr (L::kScaled) {
+    // A wavefront loads 64 rows' scales, all of one side; the wavefronts past the last row's repeat it.
+    const bool left = wave * 64 < L::BM;
+    const Side& o = left ? A : B;
+    const int row0 = left ? m0 : n0, r = min(left ? wave * 64 + lane : wave * 64 - L::BM + lane, (left ? L::BM : L::BN) - 1);
+    const uint64_t s0 = reinterpret_cast<uint64_t>(o.s) + (row0 >> o.shift) * o.s_row * L::kScaleBytes;
+    uint64_t sp = uniform(s0);
+    const uint64_t ss = uniform(static_cast<uint64_t>(o.s_col * L::kScaleBytes));
+    const uint32_t gs = static_cast<uint32_t>(((min(row0 + r, o.rows - 1) >> o.shift) - (row0 >> o.shift)) * o.s_row * L::kScaleBytes);
+    const uint32_t lds_s = uniform(lds + wave * 256);
+    const uint32_t s = lds + 2 * L::kStages;
+    uint32_t aS = s + 4 * (wm * L::MT * 16 + row);
+    uint32_t bS = s + 4 * (L::BM + wn * L::NT * 16 + (L::KIND == Kind::kE8M0 ? row : L::KIND == Kind::kF32Rows ? 4 * g : 0));
+    const int last = K - (static_cast<int>(steps) - 1) * kStep;  // bytes of the last step
+    const uint32_t partial = uniform(static_cast<uint32_t>(last < kStep));
+    int mask[8];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const int keep = last - 16 * (w < 4 ? g : 4 + g) - 4 * (w % 4);
+      mask[w] = keep >= 4 ? -1 : keep <= 0 ? 0 : (1 << (8 * keep)) - 1;
+    }
+    if constexpr (L::KIND == Kind::kE8M0) NT_LOOP_RUN(e8m0_256x256, NT_SUMS_8, NT_SCALES, NT_MASKS);
+    else if constexpr (L::KIND == Kind::kF32Uniform) NT_LOOP_RUN(f32u_256x256, NT_SUMS_8, NT_SCALES, NT_MASKS);
+    else NT_LOOP_RUN(f32n_256x256, NT_SUMS_8, NT_SCALES, NT_MASKS);
+  } else {
+    NT_LOOP_RUN(pair_256x256, NT_SUMS_8, NT_NONE, NT_NONE);
+  }
+}
+
+// Calls epi(m, n, v) for every four neighbours D[m][n .. n+3] that the lane
+// holds, also past D's edges.
+template <class L, class E>
+__device__ __forceinline__ void loop_out(const v16f (&acc)[L::kAcc], int m0, int n0, const E& epi) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  const int wm = wave % L::WM, wn = wave / L::WM;
+#pragma unroll
+  for (int i = 0; i < L::MT; ++i)
+#pragma unroll
+    for (int j = 0; j < L::NT; ++j) {
+      const int at = j * L::MT + i;
+      const v16f& a = acc[at / 4];
+      epi(m0 + (wm * L::MT + i) * 16 + lane % 16, n0 + (wn * L::NT + j) * 16 + 4 * (lane / 16),
+          v4f{a[at % 4 * 4], a[at % 4 * 4 + 1], a[at % 4 * 4 + 2], a[at % 4 * 4 + 3]});
+    }
+}
+
+}  // namespace nt
+}  // namespace sgemm

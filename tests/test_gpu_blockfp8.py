@@ -186,6 +186,23 @@ def test_gemm_against_the_definition(M, N, K, a_block, b_block, scale):
 
 
 @pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("b_block", (1, 128))
+@pytest.mark.parametrize("kind", ("bf16", "f32"))
+@pytest.mark.parametrize("K", (1, 128, 200, 384, 505, 640, 1023))
+def test_gemm_large_tiles(K, kind, b_block, scale):
+    """Enough rows and columns for the large tiles, ragged on both sides; one to eight steps along K."""
+    M, N = 2049, 2085
+    a, da = operand(M, K, 1, scale, 13)
+    b, db = operand(N, K, b_block, scale, 14)
+    c = values(M, N, TYPES[kind], 15)
+    want = da @ db.T
+    tol = tolerance(da, db, K, scale, TYPES[kind], want)
+    close(blockfp8.gemm(a, b, out_dtype=TYPES[kind]), want, tol)
+    want = 0.5 * want - c.double()
+    close(blockfp8.gemm(a, b, c=c.cuda(), alpha=0.5, beta=-1.0), want, tolerance(da, db, K, scale, TYPES[kind], want, c.double(), 0.5))
+
+
+@pytest.mark.parametrize("scale", SCALES)
 @pytest.mark.parametrize("kind", TYPES)
 @pytest.mark.parametrize("alpha,beta", [(1.0, 0.0), (0.5, 1.0), (-2.0, 3.0), (1.0, -1.0)])
 def test_gemm_types_and_scaling(alpha, beta, kind, scale):
