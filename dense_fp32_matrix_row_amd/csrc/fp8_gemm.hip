@@ -109,9 +109,8 @@ void launch_policy(const Side& A, const Side& B, int K, const Out<O>& out, hipSt
   else launch_tile<P, Small>(A, B, K, out, s);
 }
 
-template <class P, nt::Kind KIND, class O>
-void launch_16(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
-  using L = nt::Loop<KIND, 8, 4, 2, 4>;
+template <class P, class L, class O>
+void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
   if (K > 0 && L::fits(A) && L::fits(B) && ceil_div(out.M, 128) * ceil_div(out.N, 128) >= 256)
     launch_loop<L>(A, B, K, out, s);
   else launch_policy<P>(A, B, K, out, s);
@@ -119,18 +118,19 @@ void launch_16(const Side& A, const Side& B, int K, const Out<O>& out, hipStream
 
 template <class O>
 void launch_out(const Side& A, const Side& B, int K, int scale_type, const Out<O>& out, hipStream_t s) {
+  using nt::Kind;
   if constexpr (sizeof(O) == 4) {
     // a float result: sums with a float's bits
     if (scale_type == HIP_FP8_SCALE_E8M0) {
-      if (B.shift) launch_policy<nt::Widened<true, 1>>(A, B, K, out, s);
-      else launch_policy<nt::Widened<false, 1>>(A, B, K, out, s);
+      if (B.shift) launch<nt::Widened<true, 1>, nt::Loop<Kind::kWideE8M0Uniform, 4, 4, 4, 2>>(A, B, K, out, s);
+      else launch<nt::Widened<false, 1>, nt::Loop<Kind::kWideE8M0Rows, 4, 4, 4, 2>>(A, B, K, out, s);
     } else {
-      if (B.shift) launch_policy<nt::Widened<true, 4>>(A, B, K, out, s);
-      else launch_policy<nt::Widened<false, 4>>(A, B, K, out, s);
+      if (B.shift) launch<nt::Widened<true, 4>, nt::Loop<Kind::kWideF32Uniform, 4, 4, 4, 2>>(A, B, K, out, s);
+      else launch<nt::Widened<false, 4>, nt::Loop<Kind::kWideF32Rows, 4, 4, 4, 2>>(A, B, K, out, s);
     }
-  } else if (scale_type == HIP_FP8_SCALE_E8M0) launch_16<nt::Fp8E8M0, nt::Kind::kE8M0>(A, B, K, out, s);
-  else if (B.shift) launch_16<nt::Fp8F32<true>, nt::Kind::kF32Uniform>(A, B, K, out, s);
-  else launch_16<nt::Fp8F32<false>, nt::Kind::kF32Rows>(A, B, K, out, s);
+  } else if (scale_type == HIP_FP8_SCALE_E8M0) launch<nt::Fp8E8M0, nt::Loop<Kind::kE8M0, 8, 4, 2, 4>>(A, B, K, out, s);
+  else if (B.shift) launch<nt::Fp8F32<true>, nt::Loop<Kind::kF32Uniform, 8, 4, 2, 4>>(A, B, K, out, s);
+  else launch<nt::Fp8F32<false>, nt::Loop<Kind::kF32Rows, 8, 4, 2, 4>>(A, B, K, out, s);
 }
 
 bool bad_ld(int ld, int K) { return ld < (K > 1 ? K : 1) || ld % 16 != 0 || ld > HIP_FP8_MAX_LD; }

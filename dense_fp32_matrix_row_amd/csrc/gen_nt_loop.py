@@ -25,8 +25,17 @@ Kinds:
          row's scale and the one scale of the wavefront's B rows
   f32n   the same with a scale for each of B's rows
   pair   numbers as pairs of halfs (64 bytes hi, 64 bytes lo), three products
+  w32u, w32n, w8u, w8n
+         8-bit codes widened to halfs, four products, scaled afterwards as f32u
+         and f32n; the scales floats (w32) or bytes (w8), which a thread each
+         turns into floats on their way to LDS
 Products that are scaled afterwards lie in a ring of four results, and each is
-added after three more have been issued, when it has arrived.
+added when enough more have been issued for it to have arrived.
+
+Widening takes as many vector instructions as scaling does, so fragments are
+widened once a step: a half of A and all of B stay widened, and the codes of one
+half of each side are on their way.  Those of a step have all been read after
+its second quarter, where the barrier is then.
 
 Run as a script to rewrite nt_loop.inc; a test checks that the committed file
 is what this writes.
@@ -41,36 +50,46 @@ OUT = os.path.join(os.path.dirname(os.path.abspath(__file__)), "nt_loop.inc")
 
 class Loop:
     """One loop's text.  Registers: v[0:..] the sums, (j MT + i) 4; then the
-    fragments of A and B, the ring of results, A's and B's scales."""
+    fragments of A and B, the widened ones, the ring of results, A's and B's
+    scales."""
 
     def __init__(self, kind, mt, nt, wm, wn):
-        self.kind, self.mt, self.nt = kind, mt, nt
+        self.kind, self.mt, self.nt, self.wm, self.wn = kind, mt, nt, wm, wn
         self.hm, self.hn = mt // 2, nt // 2
         self.waves = wm * wn
         self.bm, self.bn = 16 * mt * wm, 16 * nt * wn
         self.la, self.lb = self.bm // 8 // self.waves, self.bn // 8 // self.waves
         self.stride = 1 << (128 * (self.bm + self.bn) - 1).bit_length()
         self.scaled = kind != "pair"
-        self.after = kind in ("f32u", "f32n")
-        self.scale_waves = (self.bm + self.bn) // 64
+        self.wide = kind[0] == "w"
+        self.after = self.wide or kind[0] == "f"
+        self.uniform = self.after and kind[-1] == "u"
+        self.rows = self.after and kind[-1] == "n"
+        self.bytes = kind.startswith("w8")
+        # loads of 64 scales a wavefront
+        self.scale_loads = -(-((self.bm + self.bn) // 64) // self.waves) if self.scaled else 0
         self.scale_stage = 256 * self.waves * self.scale_loads
-        self.lines = []
+        # products after which a result has arrived, and the first of a quarter
+        # after which no scales of the quarter before are wanted
+        self.age = 5 if self.wide else 3
+        self.settled = 6 if self.wide else 2
         at = 4 * mt * nt
-        # as many slots for A as registers allow: half of MT, each reused when its products are issued, or all
-        self.slots = mt if mt <= 4 else mt // 2
+        # slots for A: all of MT, or half of it, each used again when its products are issued
+        self.slots = mt if mt <= 4 and not self.wide else self.hm
         self.a0, at = at, at + 8 * self.slots
-        self.b0, at = at, at + 8 * nt
+        self.b0, at = at, at + 8 * (self.hn if self.wide else nt)
+        self.wa0, at = at, at + (16 * self.hm if self.wide else 0)
+        self.wb0, at = at, at + (16 * nt if self.wide else 0)
         self.t0, at = at, at + (16 if self.after else 0)
         self.sm0, at = at, at + (mt if self.scaled else 0)
-        self.sn0, at = at, at + {"e8m0": nt, "f32u": 2, "f32n": 4 * nt, "pair": 0}[kind]
+        self.sn0, at = at, at + (4 * nt if self.rows else 2 if self.uniform else nt if self.scaled else 0)
+        self.sv, at = at, at + (1 if self.bytes else 0)
         self.registers = at
-        self.reads = []    # LDS reads under way, oldest first: the registers' names
-        self.pending = []  # products not yet added: (result, j, i), oldest first
-
-    @property
-    def scale_loads(self):
-        """Loads of 64 scales a wavefront."""
-        return -(-((self.bm + self.bn) // 64) // self.waves) if self.scaled else 0
+        self.lines = []
+        self.reads = []    # LDS reads under way, oldest first: what arrives
+        self.pending = []  # products not yet added: (result, j, i, issued)
+        self.count = 0     # products (of a sum of their own) so far
+        self.issued = 0    # matrix instructions so far
 
     # -- text
 
@@ -85,7 +104,15 @@ class Loop:
         return self._frag(self.a0 + 8 * (i % self.slots), part)
 
     def fb(self, j, part=None):
-        return self._frag(self.b0 + 8 * j, part)
+        return self._frag(self.b0 + 8 * (j % self.hn if self.wide else j), part)
+
+    def wa(self, i, q):
+        at = self.wa0 + 16 * (i % self.hm) + 4 * q
+        return f"v[{at}:{at + 3}]"
+
+    def wb(self, j, q):
+        at = self.wb0 + 16 * j + 4 * q
+        return f"v[{at}:{at + 3}]"
 
     @staticmethod
     def _frag(at, part):
@@ -97,7 +124,7 @@ class Loop:
         return f"v{self.sm0 + i}"
 
     def sn(self, j, r=0):
-        return f"v{self.sn0 + (4 * j + r if self.kind == 'f32n' else j)}"
+        return f"v{self.sn0 + (4 * j + r if self.rows else j)}"
 
     # -- LDS reads; `name` says what arrives with them
 
@@ -112,28 +139,28 @@ class Loop:
             self.emit(f"s_waitcnt lgkmcnt({min(len(self.reads) - 1 - last, 15)})")
             self.reads = self.reads[last + 1:]
 
-    # The scales of results still in the ring must stay until these are added, which
-    # is after the third product of the next quarter: from then on new ones may come.
-    SETTLED = 2
-
     def a_reads(self, i):
         yield lambda: self.read(f"ds_read_b128 {self.fa(i, 0)}, %[aLo] offset:{2048 * i}", ("a", i))
         yield lambda: self.read(f"ds_read_b128 {self.fa(i, 1)}, %[aHi] offset:{2048 * i}", ("a", i))
+
+    def a_scale(self, i):
         if self.scaled:
             yield lambda: self.read(f"ds_read_b32 {self.sm(i)}, %[aS] offset:{64 * i}", ("sa", i))
 
     def b_reads(self, j):
         yield lambda: self.read(f"ds_read_b128 {self.fb(j, 0)}, %[bLo] offset:{2048 * j}", ("b", j))
         yield lambda: self.read(f"ds_read_b128 {self.fb(j, 1)}, %[bHi] offset:{2048 * j}", ("b", j))
+
+    def b_scale(self, j):
         if self.kind == "e8m0":
             yield lambda: self.read(f"ds_read_b32 {self.sn(j)}, %[bS] offset:{64 * j}", ("sb", j))
-        elif self.kind == "f32n":
+        elif self.rows:
             at = self.sn0 + 4 * j
             yield lambda: self.read(f"ds_read_b128 v[{at}:{at + 3}], %[bS] offset:{64 * j}", ("sb", j))
 
     def uniform_read(self, stage):
         """The wavefront's one scale of B, of the step in `stage`."""
-        if self.kind == "f32u":
+        if self.uniform:
             yield lambda: self.read(f"ds_read_b32 {self.sn(stage)}, %[bS]", ("su", stage))
 
     # -- loads to LDS
@@ -149,12 +176,15 @@ class Loop:
                 def one(side=side, k=k, base=base, lane=lane, rs=rs):
                     self.emit(f"s_add_u32 m0, %[lds{side}], {stage * self.stride + base + 1024 * k}")
                     self.emit("s_nop 0")
-                    self.emit(f"buffer_load_dwordx4 {lane}, {rs}, %[o{side}{k}] offen lds")
+                    self.emit(f"buffer_load_dwordx4 {lane}, {rs}, s{(72 if side == 'A' else 72 + self.la) + k} offen lds")
                 yield one
             elif n < self.loads:
                 k = n - self.la - self.lb
 
                 def one(k=k):
+                    if self.bytes:
+                        self.emit(f"global_load_ubyte v{self.sv}, %[gS{k}], s[68:69]")
+                        return
                     size = "ubyte" if self.kind == "e8m0" else "dword"
                     at = 2 * self.stride + stage * self.scale_stage + 256 * self.waves * k
                     self.emit(f"s_add_u32 m0, %[ldsS], {at}")
@@ -182,9 +212,9 @@ class Loop:
 
     def add(self, entry):
         """A result that has arrived into its sum, times its scales."""
-        t, j, i = entry
+        t, j, i, _ = entry
         at = 4 * (j * self.mt + i)
-        if self.kind == "f32n":
+        if self.rows:
             self.need([("sa", i), ("sb", j)])
             for r in range(4):
                 self.emit(f"v_mul_f32 v{t + r}, v{t + r}, {self.sm(i)}")
@@ -194,63 +224,103 @@ class Loop:
             for r in range(4):
                 self.emit(f"v_fmac_f32 v{at + r}, v{t + r}, {self.sm(i)}")
 
-    def masks(self, names):
-        """Zero what lies past K's end of fragments that have arrived."""
-        for side, n in names:
-            at = (self.a0 + 8 * (n % self.slots)) if side == "a" else self.b0 + 8 * n
-            for r in range(8):
-                self.emit(f"v_and_b32 v{at + r}, v{at + r}, %[mask{'Lo' if r < 4 else 'Hi'}{r % 4}]")
-        if names:
-            self.emit("s_nop 1")
+    def add_arrived(self):
+        while self.pending and self.issued - self.pending[0][3] >= self.age:
+            self.add(self.pending.pop(0))
+
+    def mask(self, at):
+        """Zero what lies past K's end of a fragment that has arrived."""
+        for r in range(8):
+            self.emit(f"v_and_b32 v{at + r}, v{at + r}, %[mask{'Lo' if r < 4 else 'Hi'}{r % 4}]")
+
+    def widen(self, side, n, masked):
+        """Side entries that widen a fragment, in fours."""
+        raw = self.a0 + 8 * (n % self.hm) if side == "a" else self.b0 + 8 * (n % self.hn)
+        to = self.wa0 + 16 * (n % self.hm) if side == "a" else self.wb0 + 16 * n
+
+        def some(k):
+            self.need([(side, n)])
+            if k == 0 and masked:
+                self.mask(raw)
+            for r in (2 * k, 2 * k + 1):
+                for high in (0, 1):
+                    self.emit(f"v_cvt_scalef32_pk_f16_fp8 v{to + 2 * r + high}, v{raw + r}, 1.0"
+                              + (" op_sel:[1,0,0]" if high else ""))
+        return [lambda k=k: some(k) for k in range(4)]
 
     def quarter(self, ih, jh, stage, side, masked=()):
         """The products of halves ih of A and jh of B; `side`: what to issue
-        between them, entries (first, f): f after product number `first` or later."""
+        between them, entries (first, f, tag): f after matrix instruction number
+        `first` or later, and before the first that wants what `tag` names."""
         side = list(side)
-        group = 2 if self.kind == "pair" else 1
         order = []
-        for i0 in range(0, self.hm, group):
-            for term in range(3 if self.kind == "pair" else 1):
-                for i in range(i0, min(i0 + group, self.hm)):
-                    for j in range(self.hn):
-                        order.append((ih * self.hm + i, jh * self.hn + j, term))
-        # evenly over the products, none before its time
+        if self.kind == "pair":  # the terms of a sum lie four apart
+            for i0 in range(0, self.hm, 2):
+                order += [(i, j, term) for term in range(3) for i in range(i0, min(i0 + 2, self.hm)) for j in range(self.hn)]
+        elif self.wide:
+            order = [(i, j, q) for i in range(self.hm) for q in range(4) for j in range(self.hn)]
+        else:
+            order = [(i, j, 0) for i in range(self.hm) for j in range(self.hn)]
+        order = [(ih * self.hm + i, jh * self.hn + j, part) for i, j, part in order]
         total = len(order)
         fresh = set(masked)
-        for n, (i, j, term) in enumerate(order):
-            self.need([("a", i), ("b", j)] + ([("sa", i), ("sb", j)] if self.kind == "e8m0" else []))
-            now = [x for x in (("a", i), ("b", j)) if x in fresh]
-            if now:
-                fresh -= set(now)
-                self.masks(now)
-            a, b = self.fa(i), self.fb(j)
-            if self.kind == "e8m0":
-                self.emit(f"v_mfma_scale_f32_16x16x128_f8f6f4 {self.acc(j, i)}, {b}, {a}, {self.acc(j, i)}, "
-                          f"{self.sn(j)}, {self.sm(i)} op_sel_hi:[0,0,0]")
-            elif self.kind == "pair":
-                self.emit(f"v_mfma_f32_16x16x32_f16 {self.acc(j, i)}, {self.fb(j, int(term == 2))}, "
-                          f"{self.fa(i, int(term == 1))}, {self.acc(j, i)}")
+        result = {}
+        for n, (i, j, part) in enumerate(order):
+            wanted = [("a", i), ("b", j)]
+            while any(e[2] in wanted for e in side):
+                side.pop(0)[1]()
+            if self.wide:
+                if part == 0:
+                    result[j] = self.t0 + 4 * (self.count % 4)
+                    self.count += 1
+                t = result[j]
+                c = f"v[{t}:{t + 3}]" if part else "0"
+                self.emit(f"v_mfma_f32_16x16x32_f16 v[{t}:{t + 3}], {self.wb(j, part)}, {self.wa(i, part)}, {c}")
             else:
-                t = self.t0 + 4 * (self.count % 4)
-                self.count += 1
-                self.emit(f"v_mfma_f32_16x16x128_f8f6f4 v[{t}:{t + 3}], {b}, {a}, 0")
-                if self.kind == "f32u" and (ih, jh) in ((0, stage), (1, 1 - stage)) and j == jh * self.hn:
+                self.need(wanted + ([("sa", i), ("sb", j)] if self.kind == "e8m0" else []))
+                now = [x for x in wanted if x in fresh]
+                fresh -= set(now)
+                for name, k in now:
+                    self.mask(self.a0 + 8 * (k % self.slots) if name == "a" else self.b0 + 8 * k)
+                if now:
+                    self.emit("s_nop 1")
+                a, b = self.fa(i), self.fb(j)
+                if self.kind == "e8m0":
+                    self.emit(f"v_mfma_scale_f32_16x16x128_f8f6f4 {self.acc(j, i)}, {b}, {a}, {self.acc(j, i)}, "
+                              f"{self.sn(j)}, {self.sm(i)} op_sel_hi:[0,0,0]")
+                elif self.kind == "pair":
+                    self.emit(f"v_mfma_f32_16x16x32_f16 {self.acc(j, i)}, {self.fb(j, int(part == 2))}, "
+                              f"{self.fa(i, int(part == 1))}, {self.acc(j, i)}")
+                else:
+                    t = self.t0 + 4 * (self.count % 4)
+                    self.count += 1
+                    self.emit(f"v_mfma_f32_16x16x128_f8f6f4 v[{t}:{t + 3}], {b}, {a}, 0")
+            self.issued += 1
+            if self.after and part == (3 if self.wide else 0):
+                if self.uniform and (ih, jh) in ((0, stage), (1, 1 - stage)) and j == jh * self.hn:
                     # this half's first quarter: A's scale becomes the product of both
                     self.need([("sa", i), ("su", stage)])
                     self.emit(f"v_mul_f32 {self.sm(i)}, {self.sm(i)}, {self.sn(stage)}")
-                self.pending.append((t, j, i))
-                if len(self.pending) > 3:
-                    self.add(self.pending.pop(0))
+                self.pending.append((t, j, i, self.issued))
+            self.add_arrived()
+            # the side evenly over the products, none before its time
             left = total - n - 1
-            due = [s for s in side if s[0] <= n]
-            later = len(side) - len(due)
-            take = -(-len(due) // max(1, left - (later > 0) + 1)) if left else len(side)
-            for s in (due if left else list(side))[:take]:
-                side.remove(s)
-                s[1]()
+            due = [e for e in side if e[0] <= n]
+            take = -(-len(due) // (left + (len(due) == len(side)))) if left else len(side)
+            for e in (due if left else list(side))[:take]:
+                side.remove(e)
+                e[1]()
         assert not side
 
     def meet(self):
+        if self.bytes:  # this thread's scale: 2^(e - 127); 0 is subnormal, 255 NaN
+            self.emit("s_waitcnt vmcnt(0)")
+            self.emit(f"v_add_u32 %[tmp], 1, v{self.sv}")
+            self.emit("v_and_b32 %[tmp], 0xff, %[tmp]")
+            self.emit("v_cmp_gt_u32 vcc, 2, %[tmp]")
+            self.emit("v_cndmask_b32 %[tmp], 0, %[half], vcc")
+            self.emit(f"v_lshl_or_b32 %[tmp], v{self.sv}, 23, %[tmp]")
+            self.emit(f"ds_write_b32 %[wS], %[tmp] offset:{self.write_stage * self.scale_stage}")
         self.emit("s_waitcnt vmcnt(0) lgkmcnt(0)")
         self.reads = []
         self.emit("s_barrier")
@@ -264,117 +334,185 @@ class Loop:
             for n in ("aS", "bS"):
                 self.emit(f"v_add_u32 %[{n}], {sign * self.scale_stage}, %[{n}]")
 
-    def step(self, x, still, masked=False):
-        """A step out of stage x, whose first halves have been read; still: how
-        many steps follow, 2 for more."""
-        y = 1 - x
-        split = (self.loads * 5 + 8) // 9
-        halves = lambda side, h: [(side, h * n + k) for n in [self.hm if side == "a" else self.hn] for k in range(n)]  # noqa: E731
-        m = lambda names: names if masked else ()  # noqa: E731
-        per = self.hn * (3 if self.kind == "pair" else 1)  # products a fragment of A has in a quarter
-        group = 2 if self.kind == "pair" else 1
-
-        side = self.b_side(y)
-        if self.slots == self.mt:  # room beside the first half
-            side += [(self.SETTLED if self.after else 0, f) for i in range(self.hm) for f in self.a_reads(self.hm + i)]
-        if still > 0:
-            side = self.merged(side, [(0, f) for f in self.dma(y, range(split, self.loads + 1))])
-        self.quarter(0, x, x, side, m(halves("a", 0) + halves("b", x)))
-
-        side = []
-        if self.slots < self.mt:
-            for i in range(self.hm):
-                done = per * (i // group * group + group) - 1
-                side += [(done, f) for f in self.a_reads(self.hm + i)]
-        self.quarter(0, y, x, side, m(halves("b", y)))
-        self.quarter(1, y, x, [], m(halves("a", 1)))
-        side = []
-        if still > 0:
-            self.meet()
-            self.turn(y)
-            side += self.b_side(y)
-            side += [(0, f) for f in self.uniform_read(y)]
-            for i in range(self.hm):
-                done = 0 if self.slots == self.mt else per * (i // group * group + group) - 1
-                side += [(done, f) for f in self.a_reads(i)]
-        if still > 1:
-            side = self.merged(side, [(0, f) for f in self.dma(x, range(split))])
-        self.quarter(1, x, x, side)
-
-    def b_side(self, half):
-        """The reads of a half of B, as a quarter's side entries."""
-        late = self.SETTLED if self.kind == "f32n" else 0
-        reads = [list(self.b_reads(half * self.hn + j)) for j in range(self.hn)]
-        return [(0, f) for r in reads for f in r[:2]] + [(late, f) for r in reads for f in r[2:]]
+    @staticmethod
+    def entries(first, fs, tag=None):
+        return [(first, f, tag) for f in fs]
 
     @staticmethod
     def merged(reads, loads):
         """Loads evenly among the reads."""
         out, n = [], len(loads)
+        loads = list(loads)
         for k, entry in enumerate(reads):
             out.append(entry)
             while loads and (n - len(loads)) * len(reads) <= k * n:
                 out.append(loads.pop(0))
         return out + loads
 
+    def split(self):
+        """How many of a step's loads go first."""
+        return (self.loads * 5 + 8) // 9
+
+    def step(self, x, still, masked=False):
+        """A step out of stage x, whose first halves have been read; still: how
+        many steps follow, 2 for more.  masked: it is the last and ends early."""
+        if self.wide:
+            return self.wide_step(x, still, masked)
+        y = 1 - x
+        split = self.split()
+        m = lambda side, h: [(side, h * n + k) for n in [self.hm if side == "a" else self.hn] for k in range(n)] if masked else []  # noqa: E731
+        per = self.hn * (3 if self.kind == "pair" else 1)  # matrix instructions a fragment of A has in a quarter
+        group = 2 if self.kind == "pair" else 1
+        done = lambda i: per * min(i // group * group + group, self.hm) - 1  # noqa: E731  the last of them
+        late = self.settled if self.after else 0
+
+        def b_side(half):
+            js = [half * self.hn + j for j in range(self.hn)]
+            return ([e for j in js for e in self.entries(0, self.b_reads(j))]
+                    + [e for j in js for e in self.entries(late, self.b_scale(j))])
+
+        def a_side(half, at):
+            out = []
+            for i in range(self.hm):
+                first = at(i)
+                out += self.entries(first, self.a_reads(half * self.hm + i))
+                out += self.entries(max(first, late), self.a_scale(half * self.hm + i))
+            return out
+
+        side = b_side(y)
+        if self.slots == self.mt:  # room beside the first half
+            side += a_side(1, lambda i: 0)
+        if still > 0:
+            side = self.merged(side, self.entries(0, self.dma(y, range(split, self.loads + 1))))
+        self.quarter(0, x, x, side, m("a", 0) + m("b", x))
+        self.quarter(0, y, x, a_side(1, done) if self.slots < self.mt else [], m("b", y))
+        self.quarter(1, y, x, [], m("a", 1))
+        side = []
+        if still > 0:
+            self.write_stage = y
+            self.meet()
+            self.turn(y)
+            side = b_side(y) + self.entries(0, self.uniform_read(y))
+            side += a_side(0, done if self.slots < self.mt else lambda i: 0)
+        if still > 1:
+            side = self.merged(side, self.entries(0, self.dma(x, range(split))))
+        self.quarter(1, x, x, side)
+
+    def wide_step(self, x, still, masked):
+        """At its begin the first half of B and A's first fragment are widened,
+        the rest of A's first half has been read."""
+        y = 1 - x
+        split = self.split()
+        half = 4 * self.hn  # matrix instructions a fragment of A has in a quarter
+        assert self.hm == 2
+        bs = lambda h: [h * self.hn + j for j in range(self.hn)]  # noqa: E731
+
+        side = self.entries(0, self.widen("a", 1, masked), ("a", 1))
+        for j in bs(y):
+            side += self.entries(0, self.b_reads(j))
+        side += self.entries(0, self.a_reads(2)) + self.entries(0, self.a_reads(3))
+        for i in (2, 3):
+            side += self.entries(self.settled, self.a_scale(i))
+        for j in bs(y):
+            side += self.entries(self.settled, self.b_scale(j))
+        if still > 0:
+            side = self.merged(side, self.entries(0, self.dma(y, range(split, self.loads + 1))))
+        for j in bs(y):
+            side += self.entries(half, self.widen("b", j, masked), ("b", j))
+        self.quarter(0, x, x, side)
+        self.quarter(0, y, x, self.entries(half - 1, self.widen("a", 2, masked), ("a", 2)))
+        side = self.entries(0, self.widen("a", 3, masked), ("a", 3))
+        if still > 0:
+            self.write_stage = y
+            self.meet()
+            self.turn(y)
+            side += self.entries(0, self.a_reads(0)) + [e for j in bs(y) for e in self.entries(0, self.b_reads(j))]
+            side += self.entries(0, self.a_reads(1)) + self.entries(0, self.uniform_read(y))
+            for i in (0, 1):
+                side += self.entries(self.settled, self.a_scale(i))
+        if still > 1:
+            side = self.merged(side, self.entries(0, self.dma(x, range(split))))
+        self.quarter(1, y, x, side)
+        side = []
+        if still > 0:
+            last = masked_next = self.next_masked
+            for j in bs(y):
+                side += self.entries(0, self.widen("b", j, masked_next), ("b", j))
+                side += self.entries(self.settled, self.b_scale(j))
+            side += self.entries(half - 1, self.widen("a", 0, last), ("a", 0))
+        self.quarter(1, x, x, side)
+
     def start(self, x):
         """The first step into stage x."""
         for f in self.dma(x, range(self.loads + 1)):
             f()
-        for n in range(4 * self.mt * self.nt):
+        for n in list(range(4 * self.mt * self.nt)) + list(range(self.t0, self.sv)):
             self.emit(f"v_mov_b32 v{n}, 0")
-        for n in range(self.t0, self.registers):
-            self.emit(f"v_mov_b32 v{n}, 0")
+        self.write_stage = x
         self.meet()
         if x == 1:
             self.turn(1)
         for f in self.uniform_read(x):
             f()
         for i in range(self.hm):
-            for f in self.a_reads(i):
+            for f in list(self.a_reads(i)) + list(self.a_scale(i)):
                 f()
-        for j in range(self.hn):
-            for f in self.b_reads(x * self.hn + j):
+        for j in range(x * self.hn, (x + 1) * self.hn):
+            for f in list(self.b_reads(j)) + list(self.b_scale(j)):
                 f()
         self.emit("s_waitcnt lgkmcnt(0)")
         self.reads = []
 
+    def prime(self, x, masked):
+        """What of the first step is widened where it begins."""
+        if self.wide:
+            for f in [f for j in range(x * self.hn, (x + 1) * self.hn) for f in self.widen("b", j, masked)] + self.widen("a", 0, masked):
+                f()
+
     def first_part(self, x):
-        for f in self.dma(x, range((self.loads * 5 + 8) // 9)):
+        for f in self.dma(x, range(self.split())):
             f()
+
+    def state(self):
+        """What is under way and pending, counted from here."""
+        return list(self.reads), [(t, j, i, n - self.issued) for t, j, i, n in self.pending], self.count % 4
+
+    def enter(self, state):
+        self.reads, self.pending, self.count = list(state[0]), list(state[1]), state[2]
+        self.issued = 0
 
     def text(self):
         """The whole loop; %[steps] >= 1, the last step in stage 1."""
         # what is under way and pending where a step begins: as the step before leaves it
-        probe = Loop(self.kind, self.mt, self.nt, self.waves, 1)
-        probe.__dict__.update({k: v for k, v in self.__dict__.items() if k not in ("lines", "reads", "pending")})
-        probe.lines, probe.reads, probe.pending, probe.count = [], [], [], 0
+        self.next_masked = False
+        probe = Loop(self.kind, self.mt, self.nt, self.wm, self.wn)
+        probe.next_masked = False
         begin = {}
         for x in (0, 1, 0, 1, 0, 1):
-            begin[x] = (list(probe.reads), list(probe.pending), probe.count % 4)
+            begin[x] = probe.state()
             probe.step(x, 2)
-        assert begin[0] == (probe.reads, probe.pending, probe.count % 4)
+        assert begin[0] == probe.state()
 
-        def enter(x):
-            reads, pending, count = begin[x]
-            self.reads, self.pending, self.count = list(reads), list(pending), count
-
-        def check(x):
-            assert (self.reads, self.pending, self.count % 4) == begin[x], (x, self.reads, begin[x])
-
-        self.count = 0
+        self.emit("s_mov_b32 s72, %[oA]")
+        for k in range(1, self.la):
+            self.emit(f"s_add_u32 s{72 + k}, s{71 + k}, %[eA]")
+        self.emit(f"s_mov_b32 s{72 + self.la}, %[oB]")
+        for k in range(1, self.lb):
+            self.emit(f"s_add_u32 s{72 + self.la + k}, s{71 + self.la + k}, %[eB]")
         self.emit("s_bitcmp1_b32 %[steps], 0")
         self.emit("s_cbranch_scc1 .Lnt_odd_%=")
         self.start(0)
+        self.prime(0, False)
         self.emit("s_branch .Lnt_even_%=")
         self.emit(".Lnt_odd_%=:")
         self.start(1)
         self.emit("s_cmp_eq_u32 %[steps], 1")
-        self.emit("s_cbranch_scc1 .Lnt_last_%=")
+        self.emit("s_cbranch_scc1 .Lnt_single_%=")
+        self.prime(1, False)
         self.first_part(0)
-        enter(1)
+        self.enter(begin[1])
         self.step(1, 2)
-        check(0)
+        assert self.state() == begin[0]
         self.emit("s_branch .Lnt_pairs_%=")
         self.emit(".Lnt_even_%=:")
         self.first_part(1)
@@ -384,29 +522,33 @@ class Loop:
         self.emit("s_cmp_eq_u32 %[steps], 0")
         self.emit("s_cbranch_scc1 .Lnt_next_%=")
         self.emit(".Lnt_loop_%=:")
-        enter(0)
+        self.enter(begin[0])
         self.step(0, 2)
-        check(1)
+        assert self.state() == begin[1]
         self.step(1, 2)
-        check(0)
+        assert self.state() == begin[0]
         self.emit("s_sub_u32 %[steps], %[steps], 1")
         self.emit("s_cmp_lg_u32 %[steps], 0")
         self.emit("s_cbranch_scc1 .Lnt_loop_%=")
         self.emit(".Lnt_next_%=:")
-        enter(0)
+        self.enter(begin[0])
+        self.next_masked = True
         self.step(0, 1)
-        check(1)
+        assert self.state() == begin[1]
+        self.emit("s_branch .Lnt_last_%=")
+        self.emit(".Lnt_single_%=:")
+        self.prime(1, True)
         self.emit(".Lnt_last_%=:")
-        if self.scaled:
+        if self.scaled and not self.wide:
             self.emit("s_cmp_lg_u32 %[partial], 0")
             self.emit("s_cbranch_scc1 .Lnt_masked_%=")
-        enter(1)
-        self.step(1, 0)
+        self.enter(begin[1])
+        self.step(1, 0, masked=self.wide)
         self.drain()
-        if self.scaled:
+        if self.scaled and not self.wide:
             self.emit("s_branch .Lnt_end_%=")
             self.emit(".Lnt_masked_%=:")
-            enter(1)
+            self.enter(begin[1])
             self.step(1, 0, masked=True)
             self.drain()
             self.emit(".Lnt_end_%=:")
@@ -426,7 +568,9 @@ class Loop:
 
 
 LOOPS = [
-    ("e8m0", 8, 4, 2, 4), ("f32u", 8, 4, 2, 4), ("f32n", 8, 4, 2, 4), ("pair", 8, 4, 2, 4),
+    ("e8m0", 8, 4, 2, 4), ("f32u", 8, 4, 2, 4), ("f32n", 8, 4, 2, 4),
+    ("w32u", 4, 4, 4, 2), ("w32n", 4, 4, 4, 2), ("w8u", 4, 4, 4, 2), ("w8n", 4, 4, 4, 2),
+    ("pair", 8, 4, 2, 4), ("pair", 6, 6, 2, 2), ("pair", 4, 4, 2, 2),
 ]
 
 
@@ -434,14 +578,14 @@ def generate() -> str:
     out = ["// Generated by gen_nt_loop.py (the K loops of nt_loop.h); do not edit."]
     for args in LOOPS:
         loop = Loop(*args)
-        loop.count = 0
         name = loop.name()
         text = loop.text()
         out.append(f"#define NT_LOOP_{name} \\")
         out += [f'  "{line}\\n" \\' for line in text]
         out.append('  ""')
         spare = range(4 * loop.mt * loop.nt, loop.registers)
-        out.append(f"#define NT_CLOBBERS_{name} " + ", ".join(f'"v{n}"' for n in spare))
+        out.append(f"#define NT_CLOBBERS_{name} " + ", ".join(f'"v{n}"' for n in spare)
+                   + ", " + ", ".join(f'"s{72 + n}"' for n in range(loop.la + loop.lb)) + (', "vcc"' if loop.bytes else ""))
     return "\n".join(out) + "\n"
 
 

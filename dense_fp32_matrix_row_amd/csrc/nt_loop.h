@@ -12,43 +12,52 @@ namespace nt {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-enum class Kind { kE8M0, kF32Uniform, kF32Rows, kPair };
+// What a loop multiplies and how it scales (gen_nt_loop.py).
+enum class Kind { kE8M0, kF32Uniform, kF32Rows, kWideF32Uniform, kWideF32Rows, kWideE8M0Uniform, kWideE8M0Rows, kPair };
 
-// Block tile of WM x WN wavefronts of 16 MT x 16 NT, 256 registers each.
+// Block tile of WM x WN wavefronts of 16 MT x 16 NT, at most 256 registers each.
 template <Kind KIND_, int MT_, int NT_, int WM_, int WN_>
 struct Loop {
   static constexpr Kind KIND = KIND_;
   static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_;
   static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, waves = WM * WN, threads = 64 * waves;
   static constexpr bool kScaled = KIND != Kind::kPair;
-  static constexpr int kScaleBytes = KIND == Kind::kE8M0 ? 1 : 4;
+  static constexpr bool kBytes = KIND == Kind::kWideE8M0Uniform || KIND == Kind::kWideE8M0Rows;
+  static constexpr bool kUniform =
+      KIND == Kind::kF32Uniform || KIND == Kind::kWideF32Uniform || KIND == Kind::kWideE8M0Uniform;
+  static constexpr int kScaleBytes = KIND == Kind::kE8M0 || kBytes ? 1 : 4;
   static constexpr int kStages = (BM + BN) * kStep <= 32768 ? 32768 : 65536;  // bytes from one to the next
   static constexpr int kScaleLoads = kScaled ? ((BM + BN) / 64 + waves - 1) / waves : 0;
   static constexpr int kLds = 2 * kStages + 2 * 256 * waves * kScaleLoads;
   static constexpr int kA = BM / 8 / waves, kB = BN / 8 / waves;  // loads a wavefront and step
   static constexpr int kAcc = MT * NT / 4;
-  static_assert(kA == 4 && (kB == 4 || kB == 2) && kScaleLoads <= 1, "the operands below");
+  static_assert(kScaleLoads <= 1 && kA % 2 == 0 && kB % 2 == 0, "one scale a thread, rows of chunks in turn");
 
   // Whether every scale of a tile lies within 32 bits of the first.
   static bool fits(const Side& o) { return !kScaled || o.s_row <= (int64_t(1) << 30) / 256 / kScaleBytes; }
 };
 
-#define NT_LOOP_RUN(NAME, SUMS, MORE, MASKS)                                                                  \
-  asm volatile(NT_LOOP_##NAME                                                                                 \
-               : SUMS, "+{s[60:63]}"(ra), "+{s[64:67]}"(rb), [steps] "+s"(steps), [aLo] "+v"(aLo),            \
-                 [aHi] "+v"(aHi), [bLo] "+v"(bLo), [bHi] "+v"(bHi) MORE                                       \
-               : [aEven] "v"(aEven), [aOdd] "v"(aOdd), [bEven] "v"(bEven), [bOdd] "v"(bOdd),                  \
-                 [ldsA] "s"(lds_a), [ldsB] "s"(lds_b), [oA0] "s"(oa[0]), [oA1] "s"(oa[1]), [oA2] "s"(oa[2]),  \
-                 [oA3] "s"(oa[3]), [oB0] "s"(ob[0]), [oB1] "s"(ob[1]), [oB2] "s"(ob[2]), [oB3] "s"(ob[3]) MASKS                                                                 \
+#define NT_LOOP_RUN(NAME, SUMS, MORE_OUT, MORE_IN)                                                                 \
+  asm volatile(NT_LOOP_##NAME                                                                                      \
+               : SUMS, "+{s[60:63]}"(ra), "+{s[64:67]}"(rb), [steps] "+s"(steps), [aLo] "+v"(aLo),                 \
+                 [aHi] "+v"(aHi), [bLo] "+v"(bLo), [bHi] "+v"(bHi) MORE_OUT                                        \
+               : [aEven] "v"(aEven), [aOdd] "v"(aOdd), [bEven] "v"(bEven), [bOdd] "v"(bOdd), [ldsA] "s"(lds_a),    \
+                 [ldsB] "s"(lds_b), [oA] "s"(oa), [eA] "s"(ea), [oB] "s"(ob), [eB] "s"(eb) MORE_IN                 \
                : NT_CLOBBERS_##NAME, "memory", "scc")
-#define NT_SUMS_8                                                                                             \
-  "=&{v[0:15]}"(acc[0]), "=&{v[16:31]}"(acc[1]), "=&{v[32:47]}"(acc[2]), "=&{v[48:63]}"(acc[3]),              \
-      "=&{v[64:79]}"(acc[4]), "=&{v[80:95]}"(acc[5]), "=&{v[96:111]}"(acc[6]), "=&{v[112:127]}"(acc[7])
-#define NT_SCALES , "+{s[68:69]}"(sp), [aS] "+v"(aS), [bS] "+v"(bS)
-#define NT_MASKS                                                                                              \
-  , "{s[70:71]}"(ss), [ldsS] "s"(lds_s), [gS0] "v"(gs), [partial] "s"(partial), [maskLo0] "v"(mask[0]),       \
-      [maskLo1] "v"(mask[1]), [maskLo2] "v"(mask[2]), [maskLo3] "v"(mask[3]), [maskHi0] "v"(mask[4]),         \
-      [maskHi1] "v"(mask[5]), [maskHi2] "v"(mask[6]), [maskHi3] "v"(mask[7])
+#define NT_SUMS_4                                                                                                  \
+  "=&{v[0:15]}"(acc[0]), "=&{v[16:31]}"(acc[1]), "=&{v[32:47]}"(acc[2]), "=&{v[48:63]}"(acc[3])
+#define NT_SUMS_8                                                                                                  \
+  NT_SUMS_4, "=&{v[64:79]}"(acc[4]), "=&{v[80:95]}"(acc[5]), "=&{v[96:111]}"(acc[6]), "=&{v[112:127]}"(acc[7])
+#define NT_SUMS_9 NT_SUMS_8, "=&{v[128:143]}"(acc[8])
+#define NT_SCALES_OUT , "+{s[68:69]}"(sp), [aS] "+v"(aS), [bS] "+v"(bS)
+#define NT_SCALES_IN                                                                                               \
+  , "{s[70:71]}"(ss), [gS0] "v"(gs), [maskLo0] "v"(mask[0]), [maskLo1] "v"(mask[1]), [maskLo2] "v"(mask[2]),       \
+      [maskLo3] "v"(mask[3]), [maskHi0] "v"(mask[4]), [maskHi1] "v"(mask[5]), [maskHi2] "v"(mask[6]),              \
+      [maskHi3] "v"(mask[7])
+#define NT_DIRECT_IN NT_SCALES_IN, [ldsS] "s"(lds_s)
+#define NT_PARTIAL_IN NT_DIRECT_IN, [partial] "s"(partial)
+#define NT_BYTES_OUT NT_SCALES_OUT, [tmp] "=&v"(tmp)
+#define NT_BYTES_IN NT_SCALES_IN, [wS] "v"(wS), [half] "v"(0x400000)
 #define NT_NONE
 
 // A value that all lanes of a wavefront share, in a scalar register.
@@ -79,12 +88,8 @@ __device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Sid
   const uint32_t chunk = 16 * ((lane % 8) ^ (lane / 16));
   const uint32_t aEven = lane / 8 * lda + chunk, aOdd = lane / 8 * lda + (chunk ^ 64);
   const uint32_t bEven = lane / 8 * ldb + chunk, bOdd = lane / 8 * ldb + (chunk ^ 64);
-  uint32_t oa[4], ob[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    oa[i] = uniform((wave * L::kA + i) * 8 * lda);
-    ob[i] = uniform((wave * L::kB + i) * 8 * ldb);
-  }
+  const uint32_t ea = uniform(8 * lda), eb = uniform(8 * ldb);
+  const uint32_t oa = uniform(wave * L::kA * 8 * lda), ob = uniform(wave * L::kB * 8 * ldb);
   const uint32_t lds_a = uniform(lds + wave * L::kA * 1024), lds_b = uniform(lds + wave * L::kB * 1024);
 
   const uint32_t at = row * kStep + 16 * (g ^ ((row / 2) % 8));
@@ -104,7 +109,7 @@ __device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Sid
     const uint32_t lds_s = uniform(lds + wave * 256);
     const uint32_t s = lds + 2 * L::kStages;
     uint32_t aS = s + 4 * (wm * L::MT * 16 + row);
-    uint32_t bS = s + 4 * (L::BM + wn * L::NT * 16 + (L::KIND == Kind::kE8M0 ? row : L::KIND == Kind::kF32Rows ? 4 * g : 0));
+    uint32_t bS = s + 4 * (L::BM + wn * L::NT * 16 + (L::KIND == Kind::kE8M0 ? row : L::kUniform ? 0 : 4 * g));
     const int last = K - (static_cast<int>(steps) - 1) * kStep;  // bytes of the last step
     const uint32_t partial = uniform(static_cast<uint32_t>(last < kStep));
     int mask[8];
@@ -113,11 +118,21 @@ __device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Sid
       const int keep = last - 16 * (w < 4 ? g : 4 + g) - 4 * (w % 4);
       mask[w] = keep >= 4 ? -1 : keep <= 0 ? 0 : (1 << (8 * keep)) - 1;
     }
-    if constexpr (L::KIND == Kind::kE8M0) NT_LOOP_RUN(e8m0_256x256, NT_SUMS_8, NT_SCALES, NT_MASKS);
-    else if constexpr (L::KIND == Kind::kF32Uniform) NT_LOOP_RUN(f32u_256x256, NT_SUMS_8, NT_SCALES, NT_MASKS);
-    else NT_LOOP_RUN(f32n_256x256, NT_SUMS_8, NT_SCALES, NT_MASKS);
-  } else {
+    uint32_t tmp;
+    const uint32_t wS = s + 4 * threadIdx.x;
+    if constexpr (L::KIND == Kind::kE8M0) NT_LOOP_RUN(e8m0_256x256, NT_SUMS_8, NT_SCALES_OUT, NT_PARTIAL_IN);
+    else if constexpr (L::KIND == Kind::kF32Uniform) NT_LOOP_RUN(f32u_256x256, NT_SUMS_8, NT_SCALES_OUT, NT_PARTIAL_IN);
+    else if constexpr (L::KIND == Kind::kF32Rows) NT_LOOP_RUN(f32n_256x256, NT_SUMS_8, NT_SCALES_OUT, NT_PARTIAL_IN);
+    else if constexpr (L::KIND == Kind::kWideF32Uniform) NT_LOOP_RUN(w32u_256x128, NT_SUMS_4, NT_SCALES_OUT, NT_DIRECT_IN);
+    else if constexpr (L::KIND == Kind::kWideF32Rows) NT_LOOP_RUN(w32n_256x128, NT_SUMS_4, NT_SCALES_OUT, NT_DIRECT_IN);
+    else if constexpr (L::KIND == Kind::kWideE8M0Uniform) NT_LOOP_RUN(w8u_256x128, NT_SUMS_4, NT_BYTES_OUT, NT_BYTES_IN);
+    else NT_LOOP_RUN(w8n_256x128, NT_SUMS_4, NT_BYTES_OUT, NT_BYTES_IN);
+  } else if constexpr (L::BM == 256) {
     NT_LOOP_RUN(pair_256x256, NT_SUMS_8, NT_NONE, NT_NONE);
+  } else if constexpr (L::BM == 192) {
+    NT_LOOP_RUN(pair_192x192, NT_SUMS_9, NT_NONE, NT_NONE);
+  } else {
+    NT_LOOP_RUN(pair_128x128, NT_SUMS_4, NT_NONE, NT_NONE);
   }
 }
 

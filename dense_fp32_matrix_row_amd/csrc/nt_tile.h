@@ -242,31 +242,23 @@ struct Widened {
   static __device__ __forceinline__ v4f value(const Acc& a) { return a; }
 };
 
-// Pairs of halfs, x = hi + lo 2^-11: hi hi' in one sum, hi lo' + lo hi' in
-// another that is 2^11 larger; lo lo' (2^-22 of the product) is left out, as
-// small as the pair's own rounding.
+// Pairs of halfs, x = hi + lo: hi hi' + hi lo' + lo hi'; lo lo' (2^-22 of the
+// product) is left out, as small as the pair's own rounding.
 struct HalfPair {
   static constexpr int kScaleBytes = 0;
   static constexpr bool kUniform = false, kRowScales = false;
-  struct Acc {
-    v4f hh, x;
-  };
+  using Acc = v4f;
   using Op = Frag;
   static __device__ __forceinline__ Op prepare(const Frag& f) { return f; }
-  static __device__ __forceinline__ void zero(Acc& a) { a.hh = a.x = v4f{0, 0, 0, 0}; }
+  static __device__ __forceinline__ void zero(Acc& a) { a = v4f{0, 0, 0, 0}; }
   static __device__ __forceinline__ void mac(Acc& acc, const Op& n, const Op& m, uint32_t, uint32_t) {
     const v8h nh = __builtin_bit_cast(v8h, n.lo), nl = __builtin_bit_cast(v8h, n.hi);
     const v8h mh = __builtin_bit_cast(v8h, m.lo), ml = __builtin_bit_cast(v8h, m.hi);
-    acc.hh = __builtin_amdgcn_mfma_f32_16x16x32_f16(nh, mh, acc.hh, 0, 0, 0);
-    acc.x = __builtin_amdgcn_mfma_f32_16x16x32_f16(nh, ml, acc.x, 0, 0, 0);
-    acc.x = __builtin_amdgcn_mfma_f32_16x16x32_f16(nl, mh, acc.x, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(nh, mh, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(nh, ml, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(nl, mh, acc, 0, 0, 0);
   }
-  static __device__ __forceinline__ v4f value(const Acc& a) {
-    v4f r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = fmaf(a.x[i], 0x1p-11f, a.hh[i]);
-    return r;
-  }
+  static __device__ __forceinline__ v4f value(const Acc& a) { return a; }
 };
 
 // --- the tile -------------------------------------------------------------

@@ -1,10 +1,11 @@
 // orthogonal.hip -- hip_orthogonalize: Newton-Schulz products on the matrix
 // cores with operands as pairs of halfs.
 //
-// A number x of the iterate is kept as hi + lo 2^-11 with halfs hi = RN(s x),
-// lo = RN(2^11 (s x - hi)) for a fixed power of two s: 22 significant bits
-// while |s x| is between 2^-14 and 65504, an absolute 2^-36 below.  The sums
-// are float.  Three half products an element (hi hi', hi lo', lo hi') run at a
+// A number x of the iterate is kept as hi + lo with halfs hi = RN(s x), lo =
+// RN(s x - hi) for a fixed power of two s: 22 significant bits while |s x| is
+// between 2^-3 and 65504, an absolute 2^-25 below (a half's least step is
+// 2^-24).  That is 2^-37 of |X_0|_F = 1, whose elements are 2^-12 in the mean for
+// 4096 x 4096.  The sums are float.  Three half products an element (hi hi', hi lo', lo hi') run at a
 // third of the half rate, five times the float matrix rate, and err no more
 // than float products do.
 //
@@ -17,7 +18,7 @@
 //                           as X'^T into the other of two buffers.
 #include "../../include/orthogonal.h"
 #include "lowp.h"
-#include "nt_tile.h"
+#include "nt_loop.h"
 
 namespace sgemm {
 namespace {
@@ -43,7 +44,7 @@ __device__ __forceinline__ int64_t pair_at(int64_t k) { return k / 32 * 128 + 2 
 
 __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
   hi = static_cast<_Float16>(v);
-  lo = static_cast<_Float16>((v - static_cast<float>(hi)) * 2048.0f);
+  lo = static_cast<_Float16>(v - static_cast<float>(hi));
 }
 
 __device__ __forceinline__ void store_pair(uint8_t* row, int64_t k, float v) {
@@ -70,7 +71,7 @@ __device__ __forceinline__ v4f load_pairs(const uint8_t* row, int64_t k) {
   const auto lo = __builtin_bit_cast(Pack<4, _Float16>, *reinterpret_cast<const uint2*>(at + 64));
   v4f v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = fmaf(static_cast<float>(lo.v[i]), 0x1p-11f, static_cast<float>(hi.v[i]));
+  for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(hi.v[i]) + static_cast<float>(lo.v[i]);
   return v;
 }
 
@@ -234,8 +235,6 @@ struct IterateOut {
   }
 };
 
-using Tile = nt::Tile<64, 64, 2, 2, 2>;
-
 // The lower triangle's tiles, row by row.
 __device__ __forceinline__ nt::Place triangle(int id) {
   int i = static_cast<int>((sqrtf(8.0f * id + 1.0f) - 1.0f) * 0.5f);
@@ -244,29 +243,69 @@ __device__ __forceinline__ nt::Place triangle(int id) {
   return nt::Place{i, id - i * (i + 1) / 2};
 }
 
+// Small tiles, compiled.
+struct Compiled : nt::Tile<64, 64, 2, 2, 2> {
+  static constexpr int kMinWaves = 2;
+};
+// Large ones, with their loop in assembly; several wavefronts a SIMD where registers allow.
+template <int MT, int NT, int WM, int WN>
+struct Assembled : nt::Loop<nt::Kind::kPair, MT, NT, WM, WN> {
+  static constexpr int kMinWaves = 2;
+};
+
+template <class T, class E>
+__device__ __forceinline__ void product(const Side& A, const Side& B, int m0, int n0, int K, const E& epi) {
+  if constexpr (std::is_same_v<T, Compiled>) {
+    using P = nt::HalfPair;
+    __shared__ nt::Shared<P, T> sh;
+    nt::Sums<P, T> acc;
+    nt::TileOp<P, T>::sum(sh, A, B, m0, n0, K * 4, 0, K / 32, acc);
+    nt::TileOp<P, T>::out(acc, m0, n0, epi);
+  } else {
+    __shared__ alignas(16) uint8_t smem[T::kLds];
+    nt::v16f acc[T::kAcc];
+    nt::loop_sum<T>(smem, A, B, m0, n0, K * 4, acc);
+    nt::loop_out<T>(acc, m0, n0, epi);
+  }
+}
+
 template <class T>
-__global__ __launch_bounds__(T::threads, T::WPS) void k_symmetric(Side A, int K, SymmetricOut out) {
-  __shared__ nt::Shared<nt::HalfPair, T> sh;
+__global__ __launch_bounds__(T::threads, T::kMinWaves) void k_symmetric(Side A, int K, SymmetricOut out) {
   out.batch = blockIdx.y;
   A.p += blockIdx.y * A.batch;
-  const nt::Place at = triangle(blockIdx.x);
+  const nt::Place at = triangle(static_cast<int>(xcd_contiguous(blockIdx.x, gridDim.x)));
   out.mirror = at.tm != at.tn;
-  nt::Sums<nt::HalfPair, T> acc;
-  nt::TileOp<nt::HalfPair, T>::sum(sh, A, A, at.tm * T::BM, at.tn * T::BN, K * 4, 0, K / 32, acc);
-  nt::TileOp<nt::HalfPair, T>::out(acc, at.tm * T::BM, at.tn * T::BN, out);
+  product<T>(A, A, at.tm * T::BM, at.tn * T::BN, K, out);
 }
 
 template <class T, class O>
-__global__ __launch_bounds__(T::threads, T::WPS) void k_iterate(Side A, Side B, int K, IterateOut<O> out, int tiles_m,
-                                                                int tiles_n) {
-  __shared__ nt::Shared<nt::HalfPair, T> sh;
+__global__ __launch_bounds__(T::threads, T::kMinWaves) void k_iterate(Side A, Side B, int K, IterateOut<O> out,
+                                                                      int tiles_m, int tiles_n) {
   out.batch = blockIdx.y;
   A.p += blockIdx.y * A.batch;
   B.p += blockIdx.y * B.batch;
   const nt::Place at = nt::place_of(xcd_contiguous(blockIdx.x, gridDim.x), tiles_m, tiles_n, 8);
-  nt::Sums<nt::HalfPair, T> acc;
-  nt::TileOp<nt::HalfPair, T>::sum(sh, A, B, at.tm * T::BM, at.tn * T::BN, K * 4, 0, K / 32, acc);
-  nt::TileOp<nt::HalfPair, T>::out(acc, at.tm * T::BM, at.tn * T::BN, out);
+  product<T>(A, B, at.tm * T::BM, at.tn * T::BN, K, out);
+}
+
+// Calls f with the tile that takes the products of `batch` matrices of rows x
+// cols soonest: rounds over the CUs times what a round takes, by the measured
+// rates of the tiles at full occupancy.
+template <class F>
+void pick_tile(int batch, int rows, int cols, bool symmetric, const F& f) {
+  const auto cost = [&](int tile, int per_cu, double us) {
+    const int64_t tm = ceil_div(rows, tile), tn = ceil_div(cols, tile);
+    const int64_t tiles = batch * (symmetric ? tm * (tm + 1) / 2 : tm * tn), at_once = int64_t(256) * per_cu;
+    // the last round may fill the CUs in part
+    const int64_t rest = tiles % at_once;
+    return us * (tiles / at_once * per_cu + (rest ? ceil_div(rest, 256) : 0));
+  };
+  // relative times of a tile's product alone on its CU
+  const double c256 = cost(256, 1, 4.0), c192 = cost(192, 1, 2.4), c128 = cost(128, 2, 1.1), c64 = cost(64, 4, 0.45);
+  if (c256 <= c192 && c256 <= c128 && c256 <= c64) f(Assembled<8, 4, 2, 4>{});
+  else if (c192 <= c128 && c192 <= c64) f(Assembled<6, 6, 2, 2>{});
+  else if (c128 <= c64) f(Assembled<4, 4, 2, 2>{});
+  else f(Compiled{});
 }
 
 // The workspace: per-block parts of the norms, then X, X^T twice, S and P.
@@ -332,19 +371,27 @@ hipError_t launch(int batch, const Source& src, int steps, const float* co, floa
                      eps, tall ? XT : X, tall ? X : XT, static_cast<int>(tc));
   const auto side = [](const Pairs& p, int rows) { return Side{p.p, p.ld, rows, nullptr, 0, 0, 0, p.batch}; };
   const int km = static_cast<int>(pad32(l.m)), kn = static_cast<int>(pad32(l.n));
-  const unsigned tm = static_cast<unsigned>(ceil_div(l.m, Tile::BM)), tn = static_cast<unsigned>(ceil_div(l.n, Tile::BN));
+  const auto symmetric = [&](const Side& a, int K, const SymmetricOut& out) {
+    pick_tile(batch, l.m, l.m, true, [&](auto tile) {
+      using Tile = decltype(tile);
+      const unsigned t = static_cast<unsigned>(ceil_div(l.m, Tile::BM));
+      hipLaunchKernelGGL((k_symmetric<Tile>), dim3(t * (t + 1) / 2, batch), dim3(Tile::threads), 0, stream, a, K, out);
+    });
+  };
   for (int i = 0; i < steps; ++i) {
     const float a = co[3 * i], b = co[3 * i + 1], c = co[3 * i + 2];
-    hipLaunchKernelGGL((k_symmetric<Tile>), dim3(tm * (tm + 1) / 2, batch), dim3(Tile::threads), 0, stream,
-                       side(X, l.m), kn,
-                       SymmetricOut{S, Pairs{nullptr, 0, 0}, l.m, kScaleS / (kScaleX * kScaleX), 0.0f, 0, false});
-    hipLaunchKernelGGL((k_symmetric<Tile>), dim3(tm * (tm + 1) / 2, batch), dim3(Tile::threads), 0, stream,
-                       side(S, l.m), km, SymmetricOut{P, S, l.m, c / kScaleS, b, 0, false});
+    symmetric(side(X, l.m), kn,
+              SymmetricOut{S, Pairs{nullptr, 0, 0}, l.m, kScaleS / (kScaleX * kScaleX), 0.0f, 0, false});
+    symmetric(side(S, l.m), km, SymmetricOut{P, S, l.m, c / kScaleS, b, 0, false});
     const bool last = i + 1 == steps;
-    hipLaunchKernelGGL((k_iterate<Tile, T>), dim3(tm * tn, batch), dim3(Tile::threads), 0, stream, side(P, l.m),
-                       side(XT, l.n), km,
-                       IterateOut<T>{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, a, 0, tall},
-                       static_cast<int>(tm), static_cast<int>(tn));
+    pick_tile(batch, l.m, l.n, false, [&](auto tile) {
+      using Tile = decltype(tile);
+      const unsigned tm = static_cast<unsigned>(ceil_div(l.m, Tile::BM)), tn = static_cast<unsigned>(ceil_div(l.n, Tile::BN));
+      hipLaunchKernelGGL((k_iterate<Tile, T>), dim3(tm * tn, batch), dim3(Tile::threads), 0, stream, side(P, l.m),
+                         side(XT, l.n), km,
+                         IterateOut<T>{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, a, 0, tall},
+                         static_cast<int>(tm), static_cast<int>(tn));
+    });
     const Pairs t = XT;
     XT = XT2;
     XT2 = t;

@@ -50,6 +50,19 @@ def test_against_the_definition(shape, kind):
     assert far(got, ref.orthogonalize(g, co, 1e-7)) <= tolerance(co, TYPES[kind])
 
 
+@pytest.mark.parametrize("shape", [(1100, 1300), (1500, 1021), (2, 900, 1500), (2100, 2200), (2800, 2750)])
+def test_large_tiles(shape):
+    """Enough for each of the large tiles, ragged on both sides."""
+    g = matrix(shape, torch.float32, seed=3)
+    co = [orthogonal.QUINTIC] * 2
+    got = orthogonal.orthogonalize(g.cuda(), steps=2)
+    assert far(got, ref.orthogonalize(g, co, 1e-7)) <= tolerance(co, torch.float32)
+    # a block of a few rows by itself: an error there would not show in the whole's norm
+    want = ref.orthogonalize(g, co, 1e-7)
+    d = (got.cpu().double() - want).flatten(0, -2)
+    assert (d.norm(dim=-1) <= 4 * tolerance(co, torch.float32) * want.flatten(0, -2).norm(dim=-1)).all()
+
+
 @pytest.mark.parametrize("steps", (0, 1, 2, 3, 8))
 @pytest.mark.parametrize("shape", [(40, 70), (3, 70, 40)])
 def test_steps_and_batches(steps, shape):

@@ -59,5 +59,6 @@ def test_registers_of_reads_under_way_are_not_touched(args):
         if line == "s_barrier":
             assert lines[n - 1] == "s_waitcnt vmcnt(0) lgkmcnt(0)"
     # the loads of a turn: two whole steps' into each stage, each once
-    loads = [(lines[n - 2], line) for n, line in enumerate(lines) if begin < n < end and "lds" in line and "load" in line]
+    loads = [(lines[n - 2], line) for n, line in enumerate(lines) if begin < n < end and "load" in line and line.endswith("lds")]
+    loads += [("scales", n) for n, line in enumerate(body) if "load" in line and not line.endswith("offen lds")]
     assert len(loads) == 2 * loop.loads and len(set(loads)) == len(loads)
