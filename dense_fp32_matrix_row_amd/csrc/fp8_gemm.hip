@@ -2,6 +2,7 @@
 // a scale for each block of 128 along K.
 #include "../../include/blockfp8.h"
 #include "lowp.h"
+#include "nt_direct.h"
 #include "nt_loop.h"
 
 namespace sgemm {
@@ -17,72 +18,57 @@ struct Out {
   int64_t ldd, ldc;
   int M, N;
   float alpha, beta;
-  template <bool ADD>
-  __device__ __forceinline__ Pack<4, O> value(v4f v, const Pack<4, O>& o) const {
-    Pack<4, O> r;
+  // COUNT neighbours of row m from column n, those inside D; WHOLE: all are.
+  template <bool WHOLE, bool ADD, int COUNT>
+  __device__ __forceinline__ void row(int m, int n, const float (&v)[COUNT]) const {
+    if (!WHOLE && (m >= M || n >= N)) return;
+    O* const to = d + m * ldd + n;
+    const O* const from = c + m * ldc + n;
+    const bool whole = WHOLE || n + COUNT <= N;
+    Pack<COUNT, O> r, o{};
+    if (ADD) {
+      if (whole) {
+        o = load_pack<COUNT>(from);
+      } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < COUNT; ++i)
+          if (n + i < N) o.v[i] = from[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
       float x = alpha * v[i];
       if (ADD) x = fmaf(beta, to_float(o.v[i]), x);
       from_float(x, r.v[i]);
     }
-    return r;
-  }
-  // Four neighbours inside D, or across its edge.
-  template <bool ADD>
-  __device__ __forceinline__ void inside(int m, int n, v4f v) const {
-    Pack<4, O> o{};
-    if (ADD) o = load_pack<4>(c + m * ldc + n);
-    store_pack(d + m * ldd + n, value<ADD>(v, o));
-  }
-  template <bool ADD>
-  __device__ __forceinline__ void edge(int m, int n, v4f v) const {
-    if (m >= M) return;
-    Pack<4, O> o{};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (ADD && n + i < N) o.v[i] = c[m * ldc + n + i];
-    const Pack<4, O> r = value<ADD>(v, o);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < N) d[m * ldd + n + i] = r.v[i];
-  }
-  // each: calls its argument with (m, n, v) for all that a thread holds of the
-  // rows x cols tile at m0, n0.
-  template <class F>
-  __device__ __forceinline__ void tile(int m0, int n0, int rows, int cols, const F& each) const {
-    const bool whole = m0 + rows <= M && n0 + cols <= N;
-    if (beta == 0.0f) {
-      if (whole) each([&](int m, int n, v4f v) { inside<false>(m, n, v); });
-      else each([&](int m, int n, v4f v) { edge<false>(m, n, v); });
+    if (whole) {
+      store_pack(to, r);
     } else {
-      if (whole) each([&](int m, int n, v4f v) { inside<true>(m, n, v); });
-      else each([&](int m, int n, v4f v) { edge<true>(m, n, v); });
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i)
+        if (n + i < N) to[i] = r.v[i];
+    }
+  }
+  __device__ __forceinline__ void operator()(int m, int n, v4f v) const {
+    const float x[4] = {v[0], v[1], v[2], v[3]};
+    if (beta == 0.0f) row<false, false>(m, n, x);
+    else row<false, true>(m, n, x);
+  }
+  // f with what of a rows x cols tile at m0, n0 is known beforehand.
+  template <class F>
+  __device__ __forceinline__ void tile(int m0, int n0, int rows, int cols, const F& f) const {
+    const bool whole = m0 + rows <= M && n0 + cols <= N;
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    if (beta == 0.0f) {
+      if (whole) f(yes, no);
+      else f(no, no);
+    } else {
+      if (whole) f(yes, yes);
+      else f(no, yes);
     }
   }
 };
-
-template <class P, class T, class O>
-__global__ __launch_bounds__(T::threads, T::WPS) void k_gemm(Side A, Side B, int K, Out<O> out, int tiles_m,
-                                                             int tiles_n, int64_t tiles) {
-  __shared__ nt::Shared<P, T> sh;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const nt::Place at = nt::place_of(xcd_contiguous(t, tiles), tiles_m, tiles_n, 8);
-    nt::Sums<P, T> acc;
-    nt::TileOp<P, T>::sum(sh, A, B, at.tm * T::BM, at.tn * T::BN, K, 0, static_cast<int>(ceil_div(K, nt::kStep)), acc);
-    const int m0 = at.tm * T::BM, n0 = at.tn * T::BN;
-    out.tile(m0, n0, T::BM, T::BN, [&](const auto& epi) { nt::TileOp<P, T>::out(acc, m0, n0, epi); });
-    __syncthreads();  // the next tile writes the same LDS
-  }
-}
-
-template <class P, class T, class O>
-void launch_tile(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
-  const int64_t tm = ceil_div(out.M, T::BM), tn = ceil_div(out.N, T::BN), tiles = tm * tn;
-  const int64_t cap = kMaxWorkItems / T::threads;
-  hipLaunchKernelGGL((k_gemm<P, T, O>), dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)), dim3(T::threads), 0,
-                     s, A, B, K, out, static_cast<int>(tm), static_cast<int>(tn), tiles);
-}
 
 template <class L, class O>
 __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, Out<O> out, int tiles_m, int tiles_n) {
@@ -91,7 +77,26 @@ __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, O
   const int m0 = at.tm * L::BM, n0 = at.tn * L::BN;
   nt::v16f acc[L::kAcc];
   nt::loop_sum<L>(smem, A, B, m0, n0, K, acc);
-  out.tile(m0, n0, L::BM, L::BN, [&](const auto& epi) { nt::loop_out<L>(acc, m0, n0, epi); });
+  if constexpr (sizeof(O) == 4) {  // four neighbours are 16 bytes, four lanes 64
+    out.tile(m0, n0, L::BM, L::BN, [&](auto whole, auto add) {
+      nt::loop_out<L>(acc, m0, n0, [&](int m, int n, v4f v) {
+        const float x[4] = {v[0], v[1], v[2], v[3]};
+        out.template row<whole.value, add.value>(m, n, x);
+      });
+    });
+  } else {  // by way of LDS, so that 16-byte stores fill whole lines: 61 -> 60 us at 4096^3
+    using Sheet = nt::Sheet<L::BN>;
+    static_assert(sizeof(Sheet) <= L::kLds, "a sheet fits");
+    Sheet& sheet = *reinterpret_cast<Sheet*>(smem);
+    __syncthreads();  // all wavefronts have left the loop
+    out.tile(m0, n0, L::BM, L::BN, [&](auto whole, auto add) {
+      nt::loop_sheets<L>(sheet, acc, [&](int top) {
+        sheet.template out<L::threads>(
+            false, [&](int r, int c, float (&v)[8]) { out.template row<whole.value, add.value>(m0 + top + r, n0 + c, v); },
+            [](int, int, const float (&)[8]) {});
+      });
+    });
+  }
 }
 
 template <class L, class O>
@@ -101,36 +106,129 @@ void launch_loop(const Side& A, const Side& B, int K, const Out<O>& out, hipStre
                      static_cast<int>(tm), static_cast<int>(tn));
 }
 
-template <class P, class O>
-void launch_policy(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
-  using Small = nt::Tile<64, 64, 2, 2, 2>;
-  using Large = nt::Tile<128, 128, 2, 2, 2>;
-  if (ceil_div(out.M, 128) * ceil_div(out.N, 128) >= 256) launch_tile<P, Large>(A, B, K, out, s);
-  else launch_tile<P, Small>(A, B, K, out, s);
+template <class D, class O>
+__global__ __launch_bounds__(D::threads, 2) void k_direct(Side A, Side B, int K, Out<O> out, int tiles_m, int64_t tiles) {
+  __shared__ typename D::Meet meet;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int64_t id = xcd_contiguous(t, tiles);
+    const int m0 = static_cast<int>(id % tiles_m) * D::BM, n0 = static_cast<int>(id / tiles_m) * D::BN;
+    D::run(meet, A, B, m0, n0, K, out);
+    __syncthreads();  // the next tile writes the same LDS
+  }
 }
 
-template <class P, class L, class O>
-void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
-  if (K > 0 && L::fits(A) && L::fits(B) && ceil_div(out.M, 128) * ceil_div(out.N, 128) >= 256)
-    launch_loop<L>(A, B, K, out, s);
-  else launch_policy<P>(A, B, K, out, s);
+template <class D, class O>
+void launch_direct(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
+  const int64_t tm = ceil_div(out.M, D::BM), tiles = tm * ceil_div(out.N, D::BN);
+  const int64_t cap = kMaxWorkItems / D::threads;
+  hipLaunchKernelGGL((k_direct<D, O>), dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)), dim3(D::threads), 0, s,
+                     A, B, K, out, static_cast<int>(tm), tiles);
+}
+
+// Which tile takes a product, by estimates of the time in us: of a small tile
+// (16, 32 or 64 square) what a launch takes, what one of its wavefronts' steps
+// takes alone, and what a step of one block takes among many; of a large one
+// what a step takes alone and in a full round over the 256 CUs.  Measured over
+// 28 sizes from 1 x 4096 x 4096 to 4096^3 of each kind, which they meet within
+// a quarter.  16-bit results; float ones, whose codes are widened.
+enum class Way { kSmall16, kSmall32, kSmall64, kLoop128, kLoop256, kRows, kColumns };
+struct Choice {
+  Way way;
+  int at;  // kRows, kColumns: where D is cut in two
+  double us;
+};
+
+Choice choose(int M, int N, int K, bool wide, bool loops, int cuts) {
+  const double steps = static_cast<double>(ceil_div(K, nt::kStep)), each = static_cast<double>(ceil_div(K, 8 * nt::kStep));
+  const auto small = [&](int t, double base, double alone, double among) {
+    const double blocks = static_cast<double>(ceil_div(M, t) * ceil_div(N, t));
+    return base + each * (alone > among * blocks ? alone : among * blocks);
+  };
+  const auto loop = [&](int bn, double base, double alone, double full) {
+    const int64_t tiles = ceil_div(M, 256) * ceil_div(N, bn), rest = tiles % 256;
+    return base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0));
+  };
+  Choice best{Way::kSmall16, 0, small(16, 3.0, 0.5, 0.0035)};
+  const auto offer = [&](Way w, int at, double us) {
+    if (us < best.us) best = Choice{w, at, us};
+  };
+  offer(Way::kSmall32, 0, small(32, 2.3, 1.5, wide ? 0.0085 : 0.007));
+  offer(Way::kSmall64, 0, wide ? small(64, 2.0, 4.9, 0.027) : small(64, 3.5, 2.5, 0.0167));
+  if (!loops) return best;
+  offer(Way::kLoop128, 0, wide ? loop(128, 7.0, 1.45, 2.0) : loop(128, 6.0, 0.65, 0.98));
+  if (!wide) offer(Way::kLoop256, 0, loop(256, 7.0, 1.0, 1.6));
+  // rows or columns that hardly fill their tiles apart from the rest
+  for (int t = 128; cuts > 0 && t <= 256; t *= 2) {
+    if (N > t && N % t) {
+      const int at = N - N % t;
+      offer(Way::kColumns, at, choose(M, at, K, wide, loops, cuts - 1).us + choose(M, N - at, K, wide, loops, 0).us);
+    }
+    if (t == 256 && M > t && M % t) {
+      const int at = M - M % t;
+      offer(Way::kRows, at, choose(at, N, K, wide, loops, cuts - 1).us + choose(M - at, N, K, wide, loops, 0).us);
+    }
+  }
+  return best;
+}
+
+Side from_row(Side o, int row, int scale_bytes) {  // row: a multiple of 128
+  o.p += row * o.ld;
+  o.s = static_cast<const uint8_t*>(o.s) + (row >> o.shift) * o.s_row * scale_bytes;
+  o.rows -= row;
+  return o;
+}
+
+template <class P, nt::Kind KIND, class O>
+void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s, int cuts = 2) {
+  using Loop128 = nt::Loop<KIND, 4, 4, 4, 2, 3>;
+  constexpr bool wide = sizeof(O) == 4;
+  const Choice c = choose(out.M, out.N, K, wide, K > 0 && Loop128::fits(A) && Loop128::fits(B), cuts);
+  switch (c.way) {
+    case Way::kSmall16: return launch_direct<nt::Direct<P, 1, 1, 8>>(A, B, K, out, s);
+    case Way::kSmall32: return launch_direct<nt::Direct<P, 2, 2, 8>>(A, B, K, out, s);
+    case Way::kSmall64: return launch_direct<nt::Direct<P, 4, 4, 8>>(A, B, K, out, s);
+    case Way::kLoop128: return launch_loop<Loop128>(A, B, K, out, s);
+    case Way::kLoop256:
+      if constexpr (!wide) launch_loop<nt::Loop<KIND, 8, 4, 2, 4, 2>>(A, B, K, out, s);
+      return;
+    case Way::kRows: {
+      Out<O> first = out, rest = out;
+      first.M = c.at;
+      rest.M -= c.at;
+      rest.d += c.at * out.ldd;
+      if (out.beta != 0.0f) rest.c += c.at * out.ldc;
+      launch<P, KIND>(A, B, K, first, s, cuts - 1);
+      return launch<P, KIND>(from_row(A, c.at, P::kScaleBytes), B, K, rest, s, 0);
+    }
+    case Way::kColumns: {
+      Out<O> first = out, rest = out;
+      first.N = c.at;
+      rest.N -= c.at;
+      rest.d += c.at;
+      if (out.beta != 0.0f) rest.c += c.at;
+      launch<P, KIND>(A, B, K, first, s, cuts - 1);
+      return launch<P, KIND>(A, from_row(B, c.at, P::kScaleBytes), K, rest, s, 0);
+    }
+  }
 }
 
 template <class O>
 void launch_out(const Side& A, const Side& B, int K, int scale_type, const Out<O>& out, hipStream_t s) {
   using nt::Kind;
+  const bool bytes = scale_type == HIP_FP8_SCALE_E8M0, uniform = B.shift != 0;
   if constexpr (sizeof(O) == 4) {
     // a float result: sums with a float's bits
-    if (scale_type == HIP_FP8_SCALE_E8M0) {
-      if (B.shift) launch<nt::Widened<true, 1>, nt::Loop<Kind::kWideE8M0Uniform, 4, 4, 4, 2>>(A, B, K, out, s);
-      else launch<nt::Widened<false, 1>, nt::Loop<Kind::kWideE8M0Rows, 4, 4, 4, 2>>(A, B, K, out, s);
-    } else {
-      if (B.shift) launch<nt::Widened<true, 4>, nt::Loop<Kind::kWideF32Uniform, 4, 4, 4, 2>>(A, B, K, out, s);
-      else launch<nt::Widened<false, 4>, nt::Loop<Kind::kWideF32Rows, 4, 4, 4, 2>>(A, B, K, out, s);
-    }
-  } else if (scale_type == HIP_FP8_SCALE_E8M0) launch<nt::Fp8E8M0, nt::Loop<Kind::kE8M0, 8, 4, 2, 4>>(A, B, K, out, s);
-  else if (B.shift) launch<nt::Fp8F32<true>, nt::Loop<Kind::kF32Uniform, 8, 4, 2, 4>>(A, B, K, out, s);
-  else launch<nt::Fp8F32<false>, nt::Loop<Kind::kF32Rows, 8, 4, 2, 4>>(A, B, K, out, s);
+    if (bytes && uniform) launch<nt::Widened<true, 1>, Kind::kWideE8M0Uniform>(A, B, K, out, s);
+    else if (bytes) launch<nt::Widened<false, 1>, Kind::kWideE8M0Rows>(A, B, K, out, s);
+    else if (uniform) launch<nt::Widened<true, 4>, Kind::kWideF32Uniform>(A, B, K, out, s);
+    else launch<nt::Widened<false, 4>, Kind::kWideF32Rows>(A, B, K, out, s);
+  } else if (bytes) {
+    launch<nt::Fp8E8M0, Kind::kE8M0>(A, B, K, out, s);
+  } else if (uniform) {
+    launch<nt::Fp8F32<true>, Kind::kF32Uniform>(A, B, K, out, s);
+  } else {
+    launch<nt::Fp8F32<false>, Kind::kF32Rows>(A, B, K, out, s);
+  }
 }
 
 bool bad_ld(int ld, int K) { return ld < (K > 1 ? K : 1) || ld % 16 != 0 || ld > HIP_FP8_MAX_LD; }

@@ -7,17 +7,24 @@ and prefetches of a 128 x 64 wavefront tile within 256 registers nor keeps the
 products between the reads that they hide.
 
 A loop sums a block tile of 16 MT WM x 16 NT WN over steps of 128 bytes of K.
-Two stages lie in LDS, a power of two apart; a stage is A's panel, B's panel
-(rows of 128 bytes, 16-byte chunk c of row r in slot c ^ ((r / 2) % 8)) and,
-behind both stages, the scales of the stage's rows (4 bytes each).
+Two to four stages lie in LDS; a stage is A's panel and B's (rows of 128 bytes,
+16-byte chunk c of row r in slot c ^ ((r / 2) % 8)), and behind all stages lie
+the scales of each one's rows (4 bytes each).
 
 A step's MT x NT products are taken in four quarters, two halves of A by two of
-B, in the order (0, x) (0, y) (1, y) (1, x), with x = 0, y = 1 in stage 0 and
-the reverse in stage 1: each quarter but the first of a step changes one half
-only, and what it needs is read during the quarter before it, over the step's
-end too.  The loads of the step after next go to the stage whose last reads all
-wavefronts have made by the end of the third quarter, where the step's only
-barrier is.
+B, in the order (0, x) (0, y) (1, y) (1, x), with x = 0, y = 1 in every other
+step and the reverse in between: each quarter but the first of a step changes
+one half only, and what it needs is read during the quarter before it, over the
+step's end too.  The step's only barrier is at the end of the third quarter, when
+all wavefronts have made their last reads of its stage and the next step's loads
+have arrived; behind it the loads into that stage start, as many steps ahead as
+there are stages.
+
+The loop is unrolled over the stages and both orders (2, 4 or 6 positions) and
+entered where it has to be for the last step to be in the last position.  Loads
+of steps that do not exist go through descriptors of zero bytes: they touch no
+memory, so all steps are alike.  The last step, where K may end within the 128
+bytes, and the one before it have code of their own.
 
 Kinds:
   e8m0   8-bit products, power-of-two scales applied by the instruction
@@ -53,13 +60,14 @@ class Loop:
     fragments of A and B, the widened ones, the ring of results, A's and B's
     scales."""
 
-    def __init__(self, kind, mt, nt, wm, wn):
-        self.kind, self.mt, self.nt, self.wm, self.wn = kind, mt, nt, wm, wn
+    def __init__(self, kind, mt, nt, wm, wn, stages):
+        self.kind, self.mt, self.nt, self.wm, self.wn, self.stages = kind, mt, nt, wm, wn, stages
+        self.positions = stages if stages % 2 == 0 else 2 * stages
         self.hm, self.hn = mt // 2, nt // 2
         self.waves = wm * wn
         self.bm, self.bn = 16 * mt * wm, 16 * nt * wn
         self.la, self.lb = self.bm // 8 // self.waves, self.bn // 8 // self.waves
-        self.stride = 1 << (128 * (self.bm + self.bn) - 1).bit_length()
+        self.stride = 128 * (self.bm + self.bn)  # bytes from one stage to the next
         self.scaled = kind != "pair"
         self.wide = kind[0] == "w"
         self.after = self.wide or kind[0] == "f"
@@ -83,7 +91,7 @@ class Loop:
         self.t0, at = at, at + (16 if self.after else 0)
         self.sm0, at = at, at + (mt if self.scaled else 0)
         self.sn0, at = at, at + (4 * nt if self.rows else 2 if self.uniform else nt if self.scaled else 0)
-        self.sv, at = at, at + (1 if self.bytes else 0)
+        self.sv, at = at, at + (stages if self.bytes else 0)
         self.registers = at
         self.lines = []
         self.reads = []    # LDS reads under way, oldest first: what arrives
@@ -179,17 +187,13 @@ class Loop:
                     self.emit(f"buffer_load_dwordx4 {lane}, {rs}, s{(72 if side == 'A' else 72 + self.la) + k} offen lds")
                 yield one
             elif n < self.loads:
-                k = n - self.la - self.lb
-
-                def one(k=k):
+                def one():
                     if self.bytes:
-                        self.emit(f"global_load_ubyte v{self.sv}, %[gS{k}], s[68:69]")
+                        self.emit(f"buffer_load_ubyte v{self.sv + stage}, %[gS], s[68:71], 0 offen")
                         return
-                    size = "ubyte" if self.kind == "e8m0" else "dword"
-                    at = 2 * self.stride + stage * self.scale_stage + 256 * self.waves * k
-                    self.emit(f"s_add_u32 m0, %[ldsS], {at}")
+                    self.emit(f"s_add_u32 m0, %[ldsS], {self.stages * self.stride + stage * self.scale_stage}")
                     self.emit("s_nop 0")
-                    self.emit(f"global_load_lds_{size} %[gS{k}], s[68:69]")
+                    self.emit(f"buffer_load_{'ubyte' if self.kind == 'e8m0' else 'dword'} %[gS], s[68:71], 0 offen lds")
                 yield one
             else:
                 yield self.advance
@@ -199,14 +203,18 @@ class Loop:
         return self.la + self.lb + self.scale_loads
 
     def advance(self):
-        """On to the next step's."""
+        """On to the next step's; past the last one's descriptors have no bytes."""
         for lo in (60, 64):
             self.emit(f"s_add_u32 s{lo}, s{lo}, 128")
             self.emit(f"s_addc_u32 s{lo + 1}, s{lo + 1}, 0")
             self.emit(f"s_sub_u32 s{lo + 2}, s{lo + 2}, 128")
         if self.scaled:
-            self.emit("s_add_u32 s68, s68, s70")
-            self.emit("s_addc_u32 s69, s69, s71")
+            self.emit("s_add_u32 s68, s68, s86")
+            self.emit("s_addc_u32 s69, s69, s87")
+        self.emit("s_sub_u32 %[left], %[left], 1")
+        self.emit("s_cmp_gt_i32 %[left], 0")
+        for hi in (62, 66) + ((70,) if self.scaled else ()):
+            self.emit(f"s_cselect_b32 s{hi}, s{hi}, 0")
 
     # -- products
 
@@ -312,27 +320,30 @@ class Loop:
                 e[1]()
         assert not side
 
-    def meet(self):
+    def meet(self, stage, under_way):
+        """Loads but the newest `under_way` have arrived, those of `stage` among
+        them, and all this wavefront's reads; then all wavefronts'."""
         if self.bytes:  # this thread's scale: 2^(e - 127); 0 is subnormal, 255 NaN
-            self.emit("s_waitcnt vmcnt(0)")
-            self.emit(f"v_add_u32 %[tmp], 1, v{self.sv}")
+            sv = f"v{self.sv + stage}"
+            self.emit(f"s_waitcnt vmcnt({under_way})")
+            self.emit(f"v_add_u32 %[tmp], 1, {sv}")
             self.emit("v_and_b32 %[tmp], 0xff, %[tmp]")
             self.emit("v_cmp_gt_u32 vcc, 2, %[tmp]")
             self.emit("v_cndmask_b32 %[tmp], 0, %[half], vcc")
-            self.emit(f"v_lshl_or_b32 %[tmp], v{self.sv}, 23, %[tmp]")
-            self.emit(f"ds_write_b32 %[wS], %[tmp] offset:{self.write_stage * self.scale_stage}")
-        self.emit("s_waitcnt vmcnt(0) lgkmcnt(0)")
+            self.emit(f"v_lshl_or_b32 %[tmp], {sv}, 23, %[tmp]")
+            self.emit(f"ds_write_b32 %[wS], %[tmp] offset:{stage * self.scale_stage}")
+        self.emit(f"s_waitcnt vmcnt({under_way}) lgkmcnt(0)")
         self.reads = []
         self.emit("s_barrier")
 
     def turn(self, stage):
-        """The reads' places move to `stage`."""
-        sign = 1 if stage else -1
+        """The reads' places move to `stage` from the one before it."""
+        by = 1 if stage else 1 - self.stages
         for n in ("aLo", "aHi", "bLo", "bHi"):
-            self.emit(f"v_add_u32 %[{n}], {sign * self.stride}, %[{n}]")
+            self.emit(f"v_add_u32 %[{n}], {by * self.stride}, %[{n}]")
         if self.scaled:
             for n in ("aS", "bS"):
-                self.emit(f"v_add_u32 %[{n}], {sign * self.scale_stage}, %[{n}]")
+                self.emit(f"v_add_u32 %[{n}], {by * self.scale_stage}, %[{n}]")
 
     @staticmethod
     def entries(first, fs, tag=None):
@@ -350,15 +361,17 @@ class Loop:
         return out + loads
 
     def split(self):
-        """How many of a step's loads go first."""
+        """How many of a step's loads start before the next step does."""
         return (self.loads * 5 + 8) // 9
 
-    def step(self, x, still, masked=False):
-        """A step out of stage x, whose first halves have been read; still: how
-        many steps follow, 2 for more.  masked: it is the last and ends early."""
+    def step(self, position, last=False, masked=False):
+        """A step, whose first halves have been read; last: none follows.
+        masked: zero what lies past K's end, of the last step."""
         if self.wide:
-            return self.wide_step(x, still, masked)
-        y = 1 - x
+            return self.wide_step(position, last, masked)
+        x, y = position % 2, 1 - position % 2
+        stage, after = position % self.stages, (position + 1) % self.stages
+        before = (position - 1) % self.stages
         split = self.split()
         m = lambda side, h: [(side, h * n + k) for n in [self.hm if side == "a" else self.hn] for k in range(n)] if masked else []  # noqa: E731
         per = self.hn * (3 if self.kind == "pair" else 1)  # matrix instructions a fragment of A has in a quarter
@@ -382,32 +395,33 @@ class Loop:
         side = b_side(y)
         if self.slots == self.mt:  # room beside the first half
             side += a_side(1, lambda i: 0)
-        if still > 0:
-            side = self.merged(side, self.entries(0, self.dma(y, range(split, self.loads + 1))))
+        if not last:
+            side = self.merged(side, self.entries(0, self.dma(before, range(split, self.loads + 1))))
         self.quarter(0, x, x, side, m("a", 0) + m("b", x))
         self.quarter(0, y, x, a_side(1, done) if self.slots < self.mt else [], m("b", y))
         self.quarter(1, y, x, [], m("a", 1))
         side = []
-        if still > 0:
-            self.write_stage = y
-            self.meet()
-            self.turn(y)
+        if not last:
+            self.meet(after, self.loads * (self.stages - 2))
+            self.turn(after)
             side = b_side(y) + self.entries(0, self.uniform_read(y))
             side += a_side(0, done if self.slots < self.mt else lambda i: 0)
-        if still > 1:
-            side = self.merged(side, self.entries(0, self.dma(x, range(split))))
+            side = self.merged(side, self.entries(0, self.dma(stage, range(split))))
         self.quarter(1, x, x, side)
 
-    def wide_step(self, x, still, masked):
+    def wide_step(self, position, last, masked):
         """At its begin the first half of B and A's first fragment are widened,
-        the rest of A's first half has been read."""
-        y = 1 - x
+        the rest of A's first half has been read.  masked: the last step is this
+        one, or the next (what is widened here of it)."""
+        x, y = position % 2, 1 - position % 2
+        stage, after = position % self.stages, (position + 1) % self.stages
+        before = (position - 1) % self.stages
         split = self.split()
         half = 4 * self.hn  # matrix instructions a fragment of A has in a quarter
         assert self.hm == 2
         bs = lambda h: [h * self.hn + j for j in range(self.hn)]  # noqa: E731
 
-        side = self.entries(0, self.widen("a", 1, masked), ("a", 1))
+        side = self.entries(0, self.widen("a", 1, masked and last), ("a", 1))
         for j in bs(y):
             side += self.entries(0, self.b_reads(j))
         side += self.entries(0, self.a_reads(2)) + self.entries(0, self.a_reads(3))
@@ -415,43 +429,40 @@ class Loop:
             side += self.entries(self.settled, self.a_scale(i))
         for j in bs(y):
             side += self.entries(self.settled, self.b_scale(j))
-        if still > 0:
-            side = self.merged(side, self.entries(0, self.dma(y, range(split, self.loads + 1))))
+        if not last:
+            side = self.merged(side, self.entries(0, self.dma(before, range(split, self.loads + 1))))
         for j in bs(y):
-            side += self.entries(half, self.widen("b", j, masked), ("b", j))
+            side += self.entries(half, self.widen("b", j, masked and last), ("b", j))
         self.quarter(0, x, x, side)
-        self.quarter(0, y, x, self.entries(half - 1, self.widen("a", 2, masked), ("a", 2)))
-        side = self.entries(0, self.widen("a", 3, masked), ("a", 3))
-        if still > 0:
-            self.write_stage = y
-            self.meet()
-            self.turn(y)
+        self.quarter(0, y, x, self.entries(half - 1, self.widen("a", 2, masked and last), ("a", 2)))
+        side = self.entries(0, self.widen("a", 3, masked and last), ("a", 3))
+        if not last:
+            self.meet(after, self.loads * (self.stages - 2))
+            self.turn(after)
             side += self.entries(0, self.a_reads(0)) + [e for j in bs(y) for e in self.entries(0, self.b_reads(j))]
             side += self.entries(0, self.a_reads(1)) + self.entries(0, self.uniform_read(y))
             for i in (0, 1):
                 side += self.entries(self.settled, self.a_scale(i))
-        if still > 1:
-            side = self.merged(side, self.entries(0, self.dma(x, range(split))))
+            side = self.merged(side, self.entries(0, self.dma(stage, range(split))))
         self.quarter(1, y, x, side)
         side = []
-        if still > 0:
-            last = masked_next = self.next_masked
+        if not last:
             for j in bs(y):
-                side += self.entries(0, self.widen("b", j, masked_next), ("b", j))
+                side += self.entries(0, self.widen("b", j, masked), ("b", j))
                 side += self.entries(self.settled, self.b_scale(j))
-            side += self.entries(half - 1, self.widen("a", 0, last), ("a", 0))
+            side += self.entries(half - 1, self.widen("a", 0, masked), ("a", 0))
         self.quarter(1, x, x, side)
 
-    def start(self, x):
-        """The first step into stage x."""
-        for f in self.dma(x, range(self.loads + 1)):
+    def start(self, position):
+        """The loads of the first steps, the very first in `position`."""
+        for ahead in range(self.stages - 1):
+            for f in self.dma((position + ahead) % self.stages, range(self.loads + 1)):
+                f()
+        for f in self.dma((position - 1) % self.stages, range(self.split())):
             f()
-        for n in list(range(4 * self.mt * self.nt)) + list(range(self.t0, self.sv)):
-            self.emit(f"v_mov_b32 v{n}, 0")
-        self.write_stage = x
-        self.meet()
-        if x == 1:
-            self.turn(1)
+        self.first_meet = (position % self.stages, self.loads * (self.stages - 2) + self.split())
+
+    def first_reads(self, x):
         for f in self.uniform_read(x):
             f()
         for i in range(self.hm):
@@ -469,10 +480,6 @@ class Loop:
             for f in [f for j in range(x * self.hn, (x + 1) * self.hn) for f in self.widen("b", j, masked)] + self.widen("a", 0, masked):
                 f()
 
-    def first_part(self, x):
-        for f in self.dma(x, range(self.split())):
-            f()
-
     def state(self):
         """What is under way and pending, counted from here."""
         return list(self.reads), [(t, j, i, n - self.issued) for t, j, i, n in self.pending], self.count % 4
@@ -482,16 +489,25 @@ class Loop:
         self.issued = 0
 
     def text(self):
-        """The whole loop; %[steps] >= 1, the last step in stage 1."""
+        """The whole loop: %[first] the position of the first step, %[turns] the
+        times that the last position but one is passed before the last two
+        steps, %[left] the number of steps."""
         # what is under way and pending where a step begins: as the step before leaves it
-        self.next_masked = False
-        probe = Loop(self.kind, self.mt, self.nt, self.wm, self.wn)
-        probe.next_masked = False
+        probe = Loop(self.kind, self.mt, self.nt, self.wm, self.wn, self.stages)
         begin = {}
-        for x in (0, 1, 0, 1, 0, 1):
-            begin[x] = probe.state()
-            probe.step(x, 2)
-        assert begin[0] == probe.state()
+        for position in list(range(self.positions)) * 2:
+            state = probe.state()
+            assert position not in begin or position == 0 or begin[position] == state
+            begin[position] = state
+            probe.step(position)
+        assert begin[0] == probe.state() and all(begin[p] == begin[p % 2] for p in begin)
+        top = self.positions - 1
+
+        def take(position, label, **how):
+            self.emit(f".Lnt_{label}_%=:")
+            self.enter(begin[position])
+            self.step(position, **how)
+            assert how.get("last") or self.state() == begin[(position + 1) % 2]
 
         self.emit("s_mov_b32 s72, %[oA]")
         for k in range(1, self.la):
@@ -499,42 +515,52 @@ class Loop:
         self.emit(f"s_mov_b32 s{72 + self.la}, %[oB]")
         for k in range(1, self.lb):
             self.emit(f"s_add_u32 s{72 + self.la + k}, s{71 + self.la + k}, %[eB]")
-        self.emit("s_bitcmp1_b32 %[steps], 0")
+        for stage in range(1, self.stages):
+            for position in range(stage, self.positions, self.stages):
+                self.emit(f"s_cmp_eq_u32 %[first], {position}")
+                self.emit(f"s_cbranch_scc1 .Lnt_start{stage}_%=")
+        for stage in range(self.stages):
+            if stage:
+                self.emit(f".Lnt_start{stage}_%=:")
+            self.start(stage)
+            if self.bytes:  # only this place knows which register the bytes are in
+                self.zeros()
+                self.meet(*self.first_meet)
+            if stage < self.stages - 1:
+                self.emit("s_branch .Lnt_started_%=")
+        self.emit(".Lnt_started_%=:")
+        if not self.bytes:
+            self.zeros()
+            self.meet(*self.first_meet)
+        self.emit("s_bitcmp1_b32 %[first], 0")
         self.emit("s_cbranch_scc1 .Lnt_odd_%=")
-        self.start(0)
+        self.first_reads(0)
         self.prime(0, False)
-        self.emit("s_branch .Lnt_even_%=")
+        self.jump(range(0, top - 1, 2))
+        self.emit("s_branch .Lnt_check_%=")
         self.emit(".Lnt_odd_%=:")
-        self.start(1)
-        self.emit("s_cmp_eq_u32 %[steps], 1")
+        self.first_reads(1)
+        self.emit(f"s_cmp_eq_u32 %[first], {top}")
+        self.emit("s_cbranch_scc1 .Lnt_top_%=")
+        self.prime(1, False)
+        self.jump(range(1, top - 1, 2))
+        if self.positions > 2:
+            self.emit("s_branch .Lnt_check_%=")
+        # the first position is the last when there is one step, or one over whole turns
+        self.emit(".Lnt_top_%=:")
+        self.emit("s_cmp_eq_u32 %[single], 1")
         self.emit("s_cbranch_scc1 .Lnt_single_%=")
         self.prime(1, False)
-        self.first_part(0)
-        self.enter(begin[1])
-        self.step(1, 2)
-        assert self.state() == begin[0]
-        self.emit("s_branch .Lnt_pairs_%=")
-        self.emit(".Lnt_even_%=:")
-        self.first_part(1)
-        self.emit(".Lnt_pairs_%=:")
-        self.emit("s_sub_u32 %[steps], %[steps], 2")
-        self.emit("s_lshr_b32 %[steps], %[steps], 1")
-        self.emit("s_cmp_eq_u32 %[steps], 0")
+        take(top, "turn")
+        for position in range(top - 1):
+            take(position, position)
+        self.emit(".Lnt_check_%=:")
+        self.emit("s_cmp_eq_u32 %[turns], 0")
         self.emit("s_cbranch_scc1 .Lnt_next_%=")
-        self.emit(".Lnt_loop_%=:")
-        self.enter(begin[0])
-        self.step(0, 2)
-        assert self.state() == begin[1]
-        self.step(1, 2)
-        assert self.state() == begin[0]
-        self.emit("s_sub_u32 %[steps], %[steps], 1")
-        self.emit("s_cmp_lg_u32 %[steps], 0")
-        self.emit("s_cbranch_scc1 .Lnt_loop_%=")
-        self.emit(".Lnt_next_%=:")
-        self.enter(begin[0])
-        self.next_masked = True
-        self.step(0, 1)
-        assert self.state() == begin[1]
+        self.emit("s_sub_u32 %[turns], %[turns], 1")
+        take(top - 1, "before")
+        self.emit("s_branch .Lnt_turn_%=")
+        take(top - 1, "next", masked=self.wide)
         self.emit("s_branch .Lnt_last_%=")
         self.emit(".Lnt_single_%=:")
         self.prime(1, True)
@@ -542,20 +568,26 @@ class Loop:
         if self.scaled and not self.wide:
             self.emit("s_cmp_lg_u32 %[partial], 0")
             self.emit("s_cbranch_scc1 .Lnt_masked_%=")
-        self.enter(begin[1])
-        self.step(1, 0, masked=self.wide)
+        take(top, "whole", last=True, masked=self.wide)
         self.drain()
         if self.scaled and not self.wide:
             self.emit("s_branch .Lnt_end_%=")
-            self.emit(".Lnt_masked_%=:")
-            self.enter(begin[1])
-            self.step(1, 0, masked=True)
+            take(top, "masked", last=True, masked=True)
             self.drain()
             self.emit(".Lnt_end_%=:")
         return self.lines
 
+    def zeros(self):
+        for n in list(range(4 * self.mt * self.nt)) + list(range(self.t0, self.sv)):
+            self.emit(f"v_mov_b32 v{n}, 0")
+
+    def jump(self, positions):
+        for position in positions:
+            self.emit(f"s_cmp_eq_u32 %[first], {position}")
+            self.emit(f"s_cbranch_scc1 .Lnt_{position}_%=")
+
     def drain(self):
-        self.emit("s_waitcnt lgkmcnt(0)")
+        self.emit("s_waitcnt vmcnt(0) lgkmcnt(0)")
         self.reads = []
         self.emit("s_nop 15")
         self.emit("s_nop 7")
@@ -568,9 +600,10 @@ class Loop:
 
 
 LOOPS = [
-    ("e8m0", 8, 4, 2, 4), ("f32u", 8, 4, 2, 4), ("f32n", 8, 4, 2, 4),
-    ("w32u", 4, 4, 4, 2), ("w32n", 4, 4, 4, 2), ("w8u", 4, 4, 4, 2), ("w8n", 4, 4, 4, 2),
-    ("pair", 8, 4, 2, 4), ("pair", 6, 6, 2, 2), ("pair", 4, 4, 2, 2),
+    ("e8m0", 8, 4, 2, 4, 2), ("f32u", 8, 4, 2, 4, 2), ("f32n", 8, 4, 2, 4, 2),
+    ("e8m0", 4, 4, 4, 2, 3), ("f32u", 4, 4, 4, 2, 3), ("f32n", 4, 4, 4, 2, 3),
+    ("w32u", 4, 4, 4, 2, 3), ("w32n", 4, 4, 4, 2, 3), ("w8u", 4, 4, 4, 2, 3), ("w8n", 4, 4, 4, 2, 3),
+    ("pair", 8, 4, 2, 4, 2), ("pair", 6, 6, 2, 2, 3), ("pair", 4, 2, 2, 4, 4),
 ]
 
 

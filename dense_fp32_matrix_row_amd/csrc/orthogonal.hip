@@ -12,12 +12,13 @@
 // Per step, with m <= n the sides of the iterate X and X^T kept beside it, all
 // operands have their K side contiguous:
 //   S = X X^T               (m x m, K = n; symmetric: the lower tiles, mirrored)
-//   P = b S + c S S         (m x m, K = m; S is its own transpose; symmetric)
-//   X' = a X + P X          (m x n, K = m; X^T is the other operand), written
-//                           as X' (in place: a block reads what it writes) and
-//                           as X'^T into the other of two buffers.
+//   P = a + b S + c S S     (m x m, K = m; S is its own transpose; symmetric)
+//   X' = P X                (m x n, K = m; X^T is the other operand), written
+//                           as X' over X, which is not read, and as X'^T into
+//                           the other of two buffers.
 #include "../../include/orthogonal.h"
 #include "lowp.h"
+#include "nt_direct.h"
 #include "nt_loop.h"
 
 namespace sgemm {
@@ -173,15 +174,30 @@ __global__ __launch_bounds__(256) void k_divide(Source src, const double* part, 
   }
 }
 
-// A symmetric m x m matrix of pairs: value(m, n, v) of the sums, written at its
-// place and, off the diagonal tiles, mirrored.  Both indexes run on past m to
-// the padding, where zeros go.
+// Eight neighbours from k, a multiple of 8: two stores of 16 bytes.
+__device__ __forceinline__ void store_pairs8(uint8_t* row, int64_t k, const float (&v)[8]) {
+  Pack<8, _Float16> hi, lo;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split(v[i], hi.v[i], lo.v[i]);
+  uint8_t* at = row + pair_at(k);
+  *reinterpret_cast<uint4*>(at) = __builtin_bit_cast(uint4, hi);
+  *reinterpret_cast<uint4*>(at + 64) = __builtin_bit_cast(uint4, lo);
+}
+
+// What becomes of the sums of a symmetric m x m matrix: scaled, `b` times `add`
+// added (if there is one) and `diagonal` on the diagonal, written as pairs at
+// its place and, off the diagonal tiles, mirrored.  Both indexes run on past m
+// to the padding, where zeros go.
 struct SymmetricOut {
-  Pairs out, add;  // add: the matrix that is added times `b`, or none
+  Pairs out, add;
   int m;
-  float scale, b;
+  float scale, b, diagonal;
   int batch;
   bool mirror;
+  __device__ __forceinline__ float value(int r, int c, float v, float old) const {
+    return r < m && c < m ? fmaf(v, scale, b * old) + (r == c ? diagonal : 0.0f) : 0.0f;
+  }
+  // four neighbours of a row
   __device__ __forceinline__ void operator()(int r, int c, v4f v) const {
     if (r >= pad32(m) || c >= pad32(m)) return;
     uint8_t* base = out.p + batch * out.batch;
@@ -189,7 +205,7 @@ struct SymmetricOut {
     if (r < m) {
       const v4f old = add.p ? load_pairs(add.p + batch * add.batch + r * add.ld, c) : x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = c + i < m ? fmaf(v[i], scale, b * old[i]) : 0.0f;
+      for (int i = 0; i < 4; ++i) x[i] = value(r, c + i, v[i], old[i]);
       store_pairs(base + r * out.ld, c, x);
     }
     if (mirror) {
@@ -198,27 +214,44 @@ struct SymmetricOut {
         if (c + i < m) store_pair(base + (c + i) * out.ld, r, x[i]);
     }
   }
+  // 64 rows of a tile, from row r0 and column c0
+  template <int THREADS, int COLS>
+  __device__ __forceinline__ void sheet(nt::Sheet<COLS>& s, int r0, int c0) const {
+    uint8_t* base = out.p + batch * out.batch;
+    s.template out<THREADS>(
+        mirror,
+        [&](int r, int c, float (&v)[8]) {
+          r += r0, c += c0;
+          if (c >= pad32(m)) return;
+          v4f old[2] = {};
+          if (add.p && r < m) {
+            old[0] = load_pairs(add.p + batch * add.batch + r * add.ld, c);
+            old[1] = load_pairs(add.p + batch * add.batch + r * add.ld, c + 4);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = value(r, c + i, v[i], old[i / 4][i % 4]);
+          if (r < m) store_pairs8(base + r * out.ld, c, v);
+        },
+        [&](int c, int r, const float (&v)[8]) {
+          if (c0 + c < m && r0 + r < pad32(m)) store_pairs8(base + (c0 + c) * out.ld, r0 + r, v);
+        });
+  }
 };
 
-// a X + P X: as pairs in place and transposed, or at the last step as the result.
+// P X: as pairs and transposed pairs, or at the last step as the result.
 template <class T>
 struct IterateOut {
   Pairs x, xt;
   T* out;  // not NULL at the last step
   int64_t ldo, batch_o;
   int m, n;
-  float a;
   int batch;
   bool tall;
   __device__ __forceinline__ void operator()(int r, int c, v4f v) const {
     if (r >= pad32(m) || c >= pad32(n)) return;
-    uint8_t* row = x.p + batch * x.batch + r * x.ld;
-    v4f y = {0, 0, 0, 0};
-    if (r < m) {
-      const v4f old = load_pairs(row, c);
+    v4f y;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = c + i < n ? fmaf(a, old[i], v[i] * (1.0f / kScaleS)) : 0.0f;
-    }
+    for (int i = 0; i < 4; ++i) y[i] = r < m && c + i < n ? v[i] * (1.0f / kScaleS) : 0.0f;
     if (out) {
       if (r >= m) return;
       T* o = out + batch * batch_o;
@@ -226,12 +259,52 @@ struct IterateOut {
       for (int i = 0; i < 4; ++i)
         if (c + i < n) from_float(y[i] * (1.0f / kScaleX), tall ? o[(c + i) * ldo + r] : o[r * ldo + c + i]);
     } else {
-      if (r < m) store_pairs(row, c, y);
+      if (r < m) store_pairs(x.p + batch * x.batch + r * x.ld, c, y);
       uint8_t* t = xt.p + batch * xt.batch;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (c + i < n) store_pair(t + (c + i) * xt.ld, r, y[i]);
     }
+  }
+  // `count` of eight neighbours of the result, from `at`
+  __device__ __forceinline__ void result(T* at, int count, const float (&v)[8]) const {
+    Pack<8, T> p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) from_float(v[i] * (1.0f / (kScaleS * kScaleX)), p.v[i]);
+    if (count >= 8) {
+      store_pack(at, p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < count) at[i] = p.v[i];
+    }
+  }
+  template <int THREADS, int COLS>
+  __device__ __forceinline__ void sheet(nt::Sheet<COLS>& s, int r0, int c0) const {
+    T* o = out + batch * batch_o;
+    uint8_t *xp = x.p + batch * x.batch, *tp = xt.p + batch * xt.batch;
+    s.template out<THREADS>(
+        !out || tall,
+        [&](int r, int c, float (&v)[8]) {
+          r += r0, c += c0;
+          if (out) {
+            if (!tall && r < m && c < n) result(o + r * ldo + c, n - c, v);
+            return;
+          }
+          if (c >= pad32(n)) return;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = r < m && c + i < n ? v[i] * (1.0f / kScaleS) : 0.0f;
+          if (r < m) store_pairs8(xp + r * x.ld, c, v);
+        },
+        [&](int c, int r, const float (&v)[8]) {
+          r += r0, c += c0;
+          if (c >= n) return;
+          if (!out) {
+            if (r < pad32(m)) store_pairs8(tp + c * xt.ld, r, v);
+          } else if (r < m) {
+            result(o + c * ldo + r, m - r, v);
+          }
+        });
   }
 };
 
@@ -243,29 +316,33 @@ __device__ __forceinline__ nt::Place triangle(int id) {
   return nt::Place{i, id - i * (i + 1) / 2};
 }
 
-// Small tiles, compiled.
-struct Compiled : nt::Tile<64, 64, 2, 2, 2> {
+// Small tiles, K split over the wavefronts.
+template <int T>
+struct Small : nt::Direct<nt::HalfPair, T, T, 8> {
+  static constexpr bool kDirect = true;
   static constexpr int kMinWaves = 2;
 };
 // Large ones, with their loop in assembly; several wavefronts a SIMD where registers allow.
-template <int MT, int NT, int WM, int WN>
-struct Assembled : nt::Loop<nt::Kind::kPair, MT, NT, WM, WN> {
+template <int MT, int NT, int WM, int WN, int STAGES>
+struct Assembled : nt::Loop<nt::Kind::kPair, MT, NT, WM, WN, STAGES> {
+  static constexpr bool kDirect = false;
   static constexpr int kMinWaves = 2;
 };
 
 template <class T, class E>
 __device__ __forceinline__ void product(const Side& A, const Side& B, int m0, int n0, int K, const E& epi) {
-  if constexpr (std::is_same_v<T, Compiled>) {
-    using P = nt::HalfPair;
-    __shared__ nt::Shared<P, T> sh;
-    nt::Sums<P, T> acc;
-    nt::TileOp<P, T>::sum(sh, A, B, m0, n0, K * 4, 0, K / 32, acc);
-    nt::TileOp<P, T>::out(acc, m0, n0, epi);
+  if constexpr (T::kDirect) {
+    __shared__ typename T::Meet meet;
+    T::run(meet, A, B, m0, n0, K * 4, epi);
   } else {
     __shared__ alignas(16) uint8_t smem[T::kLds];
     nt::v16f acc[T::kAcc];
     nt::loop_sum<T>(smem, A, B, m0, n0, K * 4, acc);
-    nt::loop_out<T>(acc, m0, n0, epi);
+    using Sheet = nt::Sheet<T::BN>;
+    static_assert(sizeof(Sheet) <= T::kLds, "a sheet fits");
+    Sheet& sheet = *reinterpret_cast<Sheet*>(smem);
+    __syncthreads();  // all wavefronts have left the loop
+    nt::loop_sheets<T>(sheet, acc, [&](int top) { epi.template sheet<T::threads>(sheet, m0 + top, n0); });
   }
 }
 
@@ -301,11 +378,13 @@ void pick_tile(int batch, int rows, int cols, bool symmetric, const F& f) {
     return us * (tiles / at_once * per_cu + (rest ? ceil_div(rest, 256) : 0));
   };
   // relative times of a tile's product alone on its CU
-  const double c256 = cost(256, 1, 4.0), c192 = cost(192, 1, 2.4), c128 = cost(128, 2, 1.1), c64 = cost(64, 4, 0.45);
-  if (c256 <= c192 && c256 <= c128 && c256 <= c64) f(Assembled<8, 4, 2, 4>{});
-  else if (c192 <= c128 && c192 <= c64) f(Assembled<6, 6, 2, 2>{});
-  else if (c128 <= c64) f(Assembled<4, 4, 2, 2>{});
-  else f(Compiled{});
+  const double c256 = cost(256, 1, 4.0), c192 = cost(192, 1, 2.4), c128 = cost(128, 1, 1.1), c64 = cost(64, 1, 0.8),
+               c32 = cost(32, 1, 0.18);
+  if (c256 <= c192 && c256 <= c128 && c256 <= c64 && c256 <= c32) f(Assembled<8, 4, 2, 4, 2>{});
+  else if (c192 <= c128 && c192 <= c64 && c192 <= c32) f(Assembled<6, 6, 2, 2, 3>{});
+  else if (c128 <= c64 && c128 <= c32) f(Assembled<4, 2, 2, 4, 4>{});
+  else if (c64 <= c32) f(Small<4>{});
+  else f(Small<2>{});
 }
 
 // The workspace: per-block parts of the norms, then X, X^T twice, S and P.
@@ -381,15 +460,15 @@ hipError_t launch(int batch, const Source& src, int steps, const float* co, floa
   for (int i = 0; i < steps; ++i) {
     const float a = co[3 * i], b = co[3 * i + 1], c = co[3 * i + 2];
     symmetric(side(X, l.m), kn,
-              SymmetricOut{S, Pairs{nullptr, 0, 0}, l.m, kScaleS / (kScaleX * kScaleX), 0.0f, 0, false});
-    symmetric(side(S, l.m), km, SymmetricOut{P, S, l.m, c / kScaleS, b, 0, false});
+              SymmetricOut{S, Pairs{nullptr, 0, 0}, l.m, kScaleS / (kScaleX * kScaleX), 0.0f, 0.0f, 0, false});
+    symmetric(side(S, l.m), km, SymmetricOut{P, S, l.m, c / kScaleS, b, a * kScaleS, 0, false});
     const bool last = i + 1 == steps;
     pick_tile(batch, l.m, l.n, false, [&](auto tile) {
       using Tile = decltype(tile);
       const unsigned tm = static_cast<unsigned>(ceil_div(l.m, Tile::BM)), tn = static_cast<unsigned>(ceil_div(l.n, Tile::BN));
       hipLaunchKernelGGL((k_iterate<Tile, T>), dim3(tm * tn, batch), dim3(Tile::threads), 0, stream, side(P, l.m),
                          side(XT, l.n), km,
-                         IterateOut<T>{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, a, 0, tall},
+                         IterateOut<T>{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, 0, tall},
                          static_cast<int>(tm), static_cast<int>(tn));
     });
     const Pairs t = XT;

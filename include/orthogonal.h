@@ -52,7 +52,7 @@ int hip_orthogonalize_workspace(int batch, int rows, int cols, int type, long lo
  * The norm is summed in double.  The iterate and the products' operands are
  * kept as pairs of halfs, 22 significant bits, and multiplied on the
  * matrix cores with float sums; their fixed-point range asks for
- * |X_i| < 16, |S|, |b S + c S^2| < 255 element by element, which every
+ * |X_i| < 16, |S|, |a + b S + c S^2| < 255 element by element, which every
  * convergent polynomial keeps (the singular values of X_0 are at most 1);
  * where a polynomial leaves it the result is infinite or NaN.
  *
