@@ -89,18 +89,29 @@ class BlockFp8:
         return self.q.shape
 
 
+_TYPES = None    # of matrices that are not quantised
+_SCALES = None
+
+
+def _tables():
+    """The type codes by torch's dtypes (torch is imported on first use)."""
+    global _TYPES, _SCALES
+    if _TYPES is None:
+        import torch
+        _SCALES = {torch.float32: SCALE_F32, torch.float8_e8m0fnu: SCALE_E8M0}
+        _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+    return _TYPES, _SCALES
+
+
 def _types():
-    import torch
-    return {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+    return _tables()[0]
 
 
 def _scale_type(dtype) -> int:
-    import torch
-    if dtype == torch.float32:
-        return SCALE_F32
-    if dtype == torch.float8_e8m0fnu:
-        return SCALE_E8M0
-    raise TypeError(f"scales are float32 or float8_e8m0fnu, not {dtype}")
+    kind = _tables()[1].get(dtype)
+    if kind is None:
+        raise TypeError(f"scales are float32 or float8_e8m0fnu, not {dtype}")
+    return kind
 
 
 def _ceil(a, b):
@@ -108,20 +119,24 @@ def _ceil(a, b):
 
 
 def _matrix(name, t):
-    """The row stride of a 2-D view whose columns lie side by side."""
+    """(rows, columns, row stride) of a 2-D view whose columns lie side by side."""
     if not t.is_cuda:
         raise TypeError(f"{name} must live on the GPU")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.shape[0] > 0 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D row-major view with unit column stride")
-    if max(t.shape) >= 1 << 31:
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{name} must be a 2-D row-major view with unit column stride")
+    if rows >= 1 << 31 or cols >= 1 << 31:
         raise ValueError(f"{name} has a side of 2^31 or more")
-    if t.shape[0] <= 1:
-        return max(t.shape[1], 1)
-    if t.stride(0) < t.shape[1]:
+    if rows <= 1:
+        return rows, cols, max(cols, 1)
+    if ld < cols:
         raise ValueError(f"{name}'s rows overlap")
-    if t.stride(0) >= 1 << 31:
+    if ld >= 1 << 31:
         raise ValueError(f"{name}'s row stride is 2^31 or more")
-    return max(t.stride(0), 1)
+    return rows, cols, max(ld, 1)
 
 
 def _same_device(first, *others):
@@ -135,35 +150,48 @@ def _check(status, what):
         raise _sgemm.SgemmError(status, what(status))
 
 
+def _call(device, function, what, *args):
+    """The C function with torch's current stream of the device as its last
+    argument, the device current; raises on errors."""
+    import torch
+    index = device.index
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(device, function, what, *args)
+    _check(function(*args, torch.cuda.current_stream(index).cuda_stream), what)
+
+
 def _empty(rows, cols, block_rows, scale, device):
     """Room for a quantised matrix: rows of a multiple of 16 bytes, the scales
-    of one block column side by side."""
+    of one block column side by side.  And the row stride."""
     import torch
     ld = max(_ceil(cols, 16) * 16, 16)
-    q = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)[:, :cols]
-    s = torch.empty((_ceil(cols, BLOCK), _ceil(rows, block_rows)), dtype=scale, device=device).T
-    return BlockFp8(q, s, block_rows), ld
+    q = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)
+    if ld != cols:
+        q = q[:, :cols]
+    r = _ceil(rows, block_rows)
+    return BlockFp8(q, torch.empty_strided((r, _ceil(cols, BLOCK)), (1, r), dtype=scale, device=device), block_rows), ld
 
 
 def _quantize(x, block_rows, scale, as_is, transposed):
     import torch
-    ldx = _matrix("x", x)
-    if x.dtype not in _types():
+    rows, cols, ldx = _matrix("x", x)
+    x_type = _types().get(x.dtype)
+    if x_type is None:
         raise TypeError(f"x is float32, bfloat16 or float16, not {x.dtype}")
     if block_rows not in (1, BLOCK):
         raise ValueError(f"block_rows is 1 or 128, not {block_rows}")
     scale = torch.float32 if scale is None else scale
     kind = _scale_type(scale)
-    rows, cols = x.shape
-    with torch.cuda.device(x.device):
-        n, ldn = _empty(rows, cols, block_rows, scale, x.device) if as_is else (None, 0)
-        t, ldt = _empty(cols, rows, block_rows, scale, x.device) if transposed else (None, 0)
-        if rows and cols:
-            args = []
-            for o, ld in ((n, ldn), (t, ldt)):
-                args += [o.q, ld, o.s, o.s.stride(0), o.s.stride(1)] if o is not None else [None, 0, None, 0, 0]
-            _check(hip_fp8_quantize(rows, cols, x, _types()[x.dtype], ldx, block_rows, kind, *args),
-                   hip_fp8_quantize_status_string)
+    device = x.device
+    n, ldn = _empty(rows, cols, block_rows, scale, device) if as_is else (None, 0)
+    t, ldt = _empty(cols, rows, block_rows, scale, device) if transposed else (None, 0)
+    if rows and cols:
+        args = []
+        for o, ld in ((n, ldn), (t, ldt)):
+            args += [o.q.data_ptr(), ld, o.s.data_ptr(), *o.s.stride()] if o is not None else [None, 0, None, 0, 0]
+        _call(device, load().hip_fp8_quantize, hip_fp8_quantize_status_string,
+              rows, cols, x.data_ptr(), x_type, ldx, block_rows, kind, *args)
     return n, t
 
 
@@ -183,24 +211,24 @@ def quantize_both(x, block_rows: int = 1, scale=None) -> Tuple[BlockFp8, BlockFp
     return _quantize(x, block_rows, scale, True, True)
 
 
-def _operand(name, o, K):
-    ld = _matrix(name, o.q)
-    if o.q.element_size() != 1:
-        raise TypeError(f"{name}'s codes are one byte each, not {o.q.dtype}")
-    if o.q.shape[0] <= 1 or K == 0:
+def _operand(name, o):
+    """(rows, K, the C function's arguments) of a quantised matrix."""
+    q, s, block_rows = o.q, o.s, o.block_rows
+    rows, K, ld = _matrix(name, q)
+    if q.element_size() != 1:
+        raise TypeError(f"{name}'s codes are one byte each, not {q.dtype}")
+    if rows <= 1 or K == 0:
         ld = max(_ceil(ld, 16) * 16, 16)
-    want = (_ceil(o.q.shape[0], o.block_rows), _ceil(K, BLOCK)) if o.block_rows in (1, BLOCK) else None
-    if want is None:
-        raise ValueError(f"{name}'s block_rows is 1 or 128, not {o.block_rows}")
-    if tuple(o.s.shape) != want:
-        raise ValueError(f"{name}'s scales are {tuple(o.s.shape)}, not {want}")
-    if not o.s.is_cuda:
+    if block_rows not in (1, BLOCK):
+        raise ValueError(f"{name}'s block_rows is 1 or 128, not {block_rows}")
+    if tuple(s.shape) != (_ceil(rows, block_rows), _ceil(K, BLOCK)):
+        raise ValueError(f"{name}'s scales are {tuple(s.shape)}, not {(_ceil(rows, block_rows), _ceil(K, BLOCK))}")
+    if not s.is_cuda:
         raise TypeError(f"{name}'s scales must live on the GPU")
-    if o.q.shape[0] and K and ld % 16 == 0:  # the last row is read up to a multiple of 16 bytes
-        end = o.q.storage_offset() + (o.q.shape[0] - 1) * ld + _ceil(K, 16) * 16
-        if end > o.q.untyped_storage().nbytes():
+    if K % 16 and rows and ld % 16 == 0:  # the last row is read up to a multiple of 16 bytes
+        if q.storage_offset() + (rows - 1) * ld + _ceil(K, 16) * 16 > q.untyped_storage().nbytes():
             raise ValueError(f"{name}'s storage ends within the last row's padding to a multiple of 16 bytes")
-    return [o.q, ld, o.s, o.s.stride(0), o.s.stride(1), o.block_rows]
+    return rows, K, (q.data_ptr(), ld, s.data_ptr(), *s.stride(), block_rows)
 
 
 def gemm(a: BlockFp8, b: BlockFp8, c=None, alpha: float = 1.0, beta: float = 0.0, out=None, out_dtype=None):
@@ -208,20 +236,21 @@ def gemm(a: BlockFp8, b: BlockFp8, c=None, alpha: float = 1.0, beta: float = 0.0
 
     The result's type is out's, c's, or out_dtype (default bfloat16)."""
     import torch
-    M, K = a.q.shape
-    N = b.q.shape[0]
-    if b.q.shape[1] != K:
-        raise ValueError(f"shape mismatch: a {tuple(a.q.shape)}, b {tuple(b.q.shape)}")
-    if a.s.dtype != b.s.dtype:
-        raise TypeError(f"scales of two types: {a.s.dtype} and {b.s.dtype}")
-    kind = _scale_type(a.s.dtype)
-    left, right = _operand("a", a, K), _operand("b", b, K)
+    M, K, left = _operand("a", a)
+    N, L, right = _operand("b", b)
+    if L != K:
+        raise ValueError(f"shape mismatch: a {(M, K)}, b {(N, L)}")
+    scale = a.s.dtype
+    if scale != b.s.dtype:
+        raise TypeError(f"scales of two types: {scale} and {b.s.dtype}")
+    kind = _scale_type(scale)
     if beta == 0.0:
         c = None
     elif c is None:
         raise ValueError("beta is not 0 but there is no c")
     dtype = out.dtype if out is not None else c.dtype if c is not None else out_dtype or torch.bfloat16
-    if dtype not in _types():
+    c_type = _types().get(dtype)
+    if c_type is None:
         raise TypeError(f"the result is float32, bfloat16 or float16, not {dtype}")
     if out_dtype is not None and out_dtype != dtype:
         raise TypeError(f"out_dtype is {out_dtype}, but the result is {dtype}")
@@ -229,12 +258,15 @@ def gemm(a: BlockFp8, b: BlockFp8, c=None, alpha: float = 1.0, beta: float = 0.0
         if t is not None and (tuple(t.shape) != (M, N) or t.dtype != dtype):
             raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {(M, N)} {dtype}")
     _same_device(a.q, a.s, b.q, b.s, c, out)
-    with torch.cuda.device(a.q.device):
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=a.q.device)
-        ldc = _matrix("c", c) if c is not None else 0
-        _check(hip_fp8_gemm(M, N, K, alpha, *left, *right, kind, beta, c, ldc, out, _matrix("out", out),
-                            _types()[dtype]), hip_fp8_gemm_status_string)
+    device = a.q.device
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=device)
+        ldd = max(N, 1)
+    else:
+        ldd = _matrix("out", out)[2]
+    from_c, ldc = (c.data_ptr(), _matrix("c", c)[2]) if c is not None else (None, 0)
+    _call(device, load().hip_fp8_gemm, hip_fp8_gemm_status_string, M, N, K, alpha, *left, *right, kind, beta,
+          from_c, ldc, out.data_ptr(), ldd, c_type)
     return out
 
 

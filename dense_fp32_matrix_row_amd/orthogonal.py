@@ -111,17 +111,20 @@ def orthogonalize(g, steps: int = 5, coefficients: Optional[Sequence] = None, ep
     if len(co) != steps or any(len(v) != 3 for v in co):
         raise ValueError("coefficients are (a, b, c), or one such triple for each step")
     flat = [float(x) for v in co for x in v]
-    with torch.cuda.device(g.device):
-        if out is None:
-            out = torch.empty(g.shape, dtype=g.dtype, device=g.device)
-        if out.shape != g.shape or out.dtype != g.dtype or out.device != g.device:
-            raise ValueError(f"out is {tuple(out.shape)} {out.dtype}, not {tuple(g.shape)} {g.dtype}")
-        _, _, _, ldx, stride_x = _layout("out", out)
-        need = hip_orthogonalize_workspace(batch, rows, cols, types[g.dtype])
-        if workspace is None:
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=g.device)
-        elif workspace.device != g.device or not workspace.is_contiguous():
-            raise ValueError("the workspace must be contiguous and on g's device")
-        _check(hip_orthogonalize(batch, rows, cols, types[g.dtype], g, ldg, stride_g, steps, flat, eps, out, ldx,
-                                 stride_x, workspace, workspace.numel() * workspace.element_size()))
+    device = g.device
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return orthogonalize(g, steps, co, eps, out, workspace)
+    if out is None:
+        out = torch.empty(g.shape, dtype=g.dtype, device=device)
+    if out.shape != g.shape or out.dtype != g.dtype or out.device != device:
+        raise ValueError(f"out is {tuple(out.shape)} {out.dtype}, not {tuple(g.shape)} {g.dtype}")
+    _, _, _, ldx, stride_x = _layout("out", out)
+    kind = types[g.dtype]
+    if workspace is None:
+        workspace = torch.empty(max(hip_orthogonalize_workspace(batch, rows, cols, kind), 1), dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on g's device")
+    _check(hip_orthogonalize(batch, rows, cols, kind, g, ldg, stride_g, steps, flat, eps, out, ldx, stride_x, workspace,
+                             workspace.numel() * workspace.element_size(), torch.cuda.current_stream().cuda_stream))
     return out
