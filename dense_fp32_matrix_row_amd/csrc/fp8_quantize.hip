@@ -14,81 +14,108 @@ constexpr float kE4m3Max = 448.0f;
 constexpr uint32_t kAmaxFloor = (127u - 100u) << 23;  // 2^-100
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// A block's scale: s and 1 / s, for float scales also three units less and more
-// of 1 / s, and what is stored for it.
+// What a block's elements are multiplied by, and m as codes4 has it.
+struct Factor {
+  float f;
+  uint32_t m;
+};
+// That and the bits of the scale that is stored.
 struct Scale {
-  float s, r, less, more;
+  Factor by;
   uint32_t stored;
-  bool bad;  // the block holds an infinity or a NaN
 };
 
-// From the bits of the largest |x|: as unsigned integers magnitudes order like
-// their values, with infinities and then NaNs above, so that neither is lost
-// in the maximum.
-template <int KIND>
-__device__ __forceinline__ Scale make_scale(uint32_t top) {
-  Scale q;
-  q.bad = top >= kInfBits;
-  if (top < kAmaxFloor) top = kAmaxFloor;
-  if constexpr (KIND == HIP_FP8_SCALE_F32) {
-    q.s = __uint_as_float(top) / kE4m3Max;
-    q.r = 1.0f / q.s;
-    q.less = __uint_as_float(__float_as_uint(q.r) - 3);
-    q.more = __uint_as_float(__float_as_uint(q.r) + 3);
-    q.stored = q.bad ? 0x7fc00000u : __float_as_uint(q.s);
-  } else {
-    // a = f 2^p with 1 <= f < 2, 448 = 1.75 2^8: 2^(p-8), or twice that for f > 1.75
-    const uint32_t e = (top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-    q.s = __uint_as_float(e << 23);
-    q.r = __uint_as_float((254 - e) << 23);
-    q.stored = q.bad ? 0xffu : e;
-  }
-  return q;
+__device__ __forceinline__ uint32_t round4(float a, float b, float c, float d) {
+  const int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
 }
 
 // x / s as a float whose rounding to e4m3 is that of the exact quotient.
-template <int KIND>
-__device__ __forceinline__ float quotient(float x, const Scale& q) {
-  float t = x * q.r;
-  if constexpr (KIND == HIP_FP8_SCALE_F32) {
-    // The remainder x - t s is exact (t is within two units of the quotient),
-    // so one correction with it rounds the quotient correctly.  Then the only
-    // wrong roundings left are of quotients that fall on a border between two
-    // codes by their float rounding alone: borders have at most five
-    // significant bits, and the new remainder says to which side to step.
-    t = fmaf(fmaf(-t, q.s, x), q.r, t);
-    const uint32_t b = __float_as_uint(t);
-    if ((b & 0x7ffffu) == 0 && (b << 1) != 0) {
-      const float rem = fmaf(-t, q.s, x);
-      const float out = __uint_as_float(__float_as_uint(rem) ^ (b & 0x80000000u));  // > 0: away from zero
-      t = __uint_as_float(b + (out > 0.0f ? 1 : 0) - (out < 0.0f ? 1 : 0));
-    }
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  // The remainder x - t s is exact (t is within two units of the quotient),
+  // so one correction with it rounds the quotient correctly.  Then the only
+  // wrong roundings left are of quotients that fall on a border between two
+  // codes by their float rounding alone: borders have at most five
+  // significant bits, and the new remainder says to which side to step.
+  float t = x * r;
+  t = fmaf(fmaf(-t, s, x), r, t);
+  const uint32_t b = __float_as_uint(t);
+  if ((b & 0x7ffffu) == 0 && (b << 1) != 0) {
+    const float rem = fmaf(-t, s, x);
+    const float out = __uint_as_float(__float_as_uint(rem) ^ (b & 0x80000000u));  // > 0: away from zero
+    t = __uint_as_float(b + (out > 0.0f ? 1 : 0) - (out < 0.0f ? 1 : 0));
   }
   return t;
 }
 
-__device__ __forceinline__ uint32_t round4(float a, float b, float c, float d) {
-  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true));
+// The codes of four elements x / s, each the exact quotient rounded once.
+//
+// Power-of-two scales: the product with 1 / s is exact.
+//
+// Float scales, 16-bit x: with a the block's largest magnitude, 448 x / a is
+// either a border between two codes (of five bits) or at least 2^-16 of it away,
+// x and a having 11 bits at most.  s = a / 448 (1 + e), |e| <= 2^-24, so the
+// quotients that matter are all off their borders to the same side, by e's
+// sign: f = 1 / s is moved 2^-19 to that side, past all rounding errors
+// (2^-22 together), and the product rounds as the quotient does.  Where e is 0
+// a border is met exactly, and the tie goes to the even code: the product is
+// rounded to 18 bits first, which gives a border that is 2^-22 away itself and
+// keeps all else on its side.  m is the mask of that rounding, or of none.
+// One element in 200 of bf16 data is such a border.
+//
+// Float scales, float x: the exact quotient lies between the products with
+// 1 / s less and more three units (at least 3 x 2^-24 off, x r within 2 x 2^-24),
+// so where both round to the same code that is it.  Elsewhere, one element in
+// 10^5 of ordinary data, the quotient is looked at closely.  m holds s.
+template <int KIND, class X>
+__device__ __forceinline__ uint32_t codes4(X a, X b, X c, X d, Factor q) {
+  const float x[4] = {to_float(a), to_float(b), to_float(c), to_float(d)};
+  if constexpr (KIND == HIP_FP8_SCALE_E8M0) {
+    return round4(x[0] * q.f, x[1] * q.f, x[2] * q.f, x[3] * q.f);
+  } else if constexpr (sizeof(X) == 2) {
+    const uint32_t half = (0u - q.m) >> 1;
+    const auto t = [&](float v) { return __uint_as_float((__float_as_uint(v * q.f) + half) & q.m); };
+    return round4(t(x[0]), t(x[1]), t(x[2]), t(x[3]));
+  } else {
+    const float less = __uint_as_float(__float_as_uint(q.f) - 3), more = __uint_as_float(__float_as_uint(q.f) + 3);
+    uint32_t v = round4(x[0] * less, x[1] * less, x[2] * less, x[3] * less);
+    if (v != round4(x[0] * more, x[1] * more, x[2] * more, x[3] * more)) {
+      const float s = __uint_as_float(q.m);
+      v = round4(quotient(x[0], s, q.f), quotient(x[1], s, q.f), quotient(x[2], s, q.f), quotient(x[3], s, q.f));
+    }
+    return v;
+  }
 }
 
-// The codes of four quotients.  For float scales the exact quotient lies
-// between the products with `less` and `more` (x r is within 2^-24 of it from
-// r's rounding and 2^-24 from its own, three units are 3 x 2^-24 at least), so
-// where both round to the same code that is it.  Elsewhere, one element in
-// 10^5 of ordinary data, the quotient is looked at closely; all together 4
-// instructions an element instead of 12.
-template <int KIND>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, const Scale& q) {
-  uint32_t v;
+// From the bits of the largest |x|: as unsigned integers magnitudes order like
+// their values, with infinities and then NaNs above, so that neither is lost
+// in the maximum.  A block that holds one has a NaN for a factor, which makes
+// every code NaN.
+template <int KIND, class X>
+__device__ __forceinline__ Scale make_scale(uint32_t top) {
+  Scale q;
+  const bool bad = top >= kInfBits;
+  if (top < kAmaxFloor) top = kAmaxFloor;
   if constexpr (KIND == HIP_FP8_SCALE_F32) {
-    v = round4(a * q.less, b * q.less, c * q.less, d * q.less);
-    if (v != round4(a * q.more, b * q.more, c * q.more, d * q.more))
-      v = round4(quotient<KIND>(a, q), quotient<KIND>(b, q), quotient<KIND>(c, q), quotient<KIND>(d, q));
+    const float a = __uint_as_float(top), s = a / kE4m3Max, r = 1.0f / s;
+    if constexpr (sizeof(X) == 2) {
+      const float e = fmaf(-s, kE4m3Max, a);  // exact; > 0: s is less than a / 448, the quotients more
+      q.by.f = e > 0.0f ? r * (1.0f + 0x1p-19f) : e < 0.0f ? r * (1.0f - 0x1p-19f) : r;
+      q.by.m = e == 0.0f ? ~0x3fu : ~0u;
+    } else {
+      q.by.f = r;
+      q.by.m = __float_as_uint(s);
+    }
+    q.stored = bad ? 0x7fc00000u : __float_as_uint(s);
   } else {
-    v = round4(quotient<KIND>(a, q), quotient<KIND>(b, q), quotient<KIND>(c, q), quotient<KIND>(d, q));
+    // a = f 2^p with 1 <= f < 2, 448 = 1.75 2^8: 2^(p-8), or twice that for f > 1.75
+    const uint32_t e = (top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    q.by.f = __uint_as_float((254 - e) << 23);
+    q.by.m = 0;
+    q.stored = bad ? 0xffu : e;
   }
-  return q.bad ? 0x7f7f7f7fu : v;
+  if (bad) q.by.f = __uint_as_float(0x7fc00000u);
+  return q;
 }
 
 template <int KIND>
@@ -101,15 +128,19 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 
 // Eight neighbours of a row from column `col`, zeros past `cols`.
 template <class X>
-__device__ __forceinline__ void load8(const X* row, int col, int cols, float (&v)[8]) {
-  if (col + 8 <= cols) {
-    const Pack<8, X> p = load_pack<8>(row + col);
+__device__ __forceinline__ Pack<8, X> load8(const X* row, int col, int cols) {
+  if (col + 8 <= cols) return load_pack<8>(row + col);
+  Pack<8, X> p{};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float(p.v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? to_float(row[col + i]) : 0.0f;
-  }
+  for (int i = 0; i < 8; ++i)
+    if (col + i < cols) p.v[i] = row[col + i];
+  return p;
+}
+
+// The codes of eight neighbours.
+template <int KIND, class X>
+__device__ __forceinline__ uint2 codes8(const Pack<8, X>& p, Factor q) {
+  return make_uint2(codes4<KIND>(p.v[0], p.v[1], p.v[2], p.v[3], q), codes4<KIND>(p.v[4], p.v[5], p.v[6], p.v[7], q));
 }
 
 // Eight codes of a row from column `col`, none past `cols`.
@@ -120,6 +151,17 @@ __device__ __forceinline__ void store8(uint8_t* row, int col, int cols, uint2 c)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (col + i < cols) row[col + i] = static_cast<uint8_t>((i < 4 ? c.x : c.y) >> (8 * (i % 4)));
+  }
+}
+
+// Makes the compiler forget what it made of the elements so far, lest it keep
+// them as floats beside the halves that they come as: twice the registers.
+template <class X>
+__device__ __forceinline__ void forget(Pack<8, X>& p) {
+  if constexpr (sizeof(X) == 2) {
+    uint4 w = __builtin_bit_cast(uint4, p);
+    asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
+    p = __builtin_bit_cast(Pack<8, X>, w);
   }
 }
 
@@ -136,11 +178,14 @@ struct Args {
   int64_t st_row, st_col;
 };
 
-// Maximum over the 16 lanes of a group.
+// Maximum over the 16 lanes of a group: with the neighbour, the next pair, the
+// other half of eight and of sixteen.
+template <int CONTROL>
+__device__ __forceinline__ uint32_t max_with(uint32_t v) {
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CONTROL, 0xf, 0xf, true)));
+}
 __device__ __forceinline__ uint32_t max16(uint32_t v) {
-#pragma unroll
-  for (int d = 1; d < 16; d *= 2) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), d)));
-  return v;
+  return max_with<0x140>(max_with<0x141>(max_with<0x4e>(max_with<0xb1>(v))));
 }
 
 // Blocks of 1 x 128 as the matrix lies: sixteen lanes a block, eight neighbours
@@ -151,14 +196,12 @@ __global__ __launch_bounds__(256) void k_rows(const X* __restrict__ x, Args a, i
   for (int64_t it = int64_t(blockIdx.x) * 16 + threadIdx.x / 16; it < items; it += int64_t(gridDim.x) * 16) {
     const int64_t row = it / blocks;
     const int kb = static_cast<int>(it % blocks), col = kb * 128 + lane * 8;
-    float v[8];
-    load8(x + row * a.ldx, col, a.cols, v);
+    const Pack<8, X> v = load8(x + row * a.ldx, col, a.cols);
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, magnitude(v[i]));
-    const Scale q = make_scale<KIND>(max16(top));
-    store8(a.q + row * a.ldq, col, a.cols,
-           make_uint2(codes4<KIND>(v[0], v[1], v[2], v[3], q), codes4<KIND>(v[4], v[5], v[6], v[7], q)));
+    for (int i = 0; i < 8; ++i) top = max(top, magnitude(to_float(v.v[i])));
+    const Scale q = make_scale<KIND, X>(max16(top));
+    store8(a.q + row * a.ldq, col, a.cols, codes8<KIND>(v, q.by));
     if (lane == 0) store_scale<KIND>(a.s, row * a.s_row + kb * a.s_col, q);
   }
 }
@@ -166,13 +209,14 @@ __global__ __launch_bounds__(256) void k_rows(const X* __restrict__ x, Args a, i
 // 128 x 128 tiles, a thread holding 8 x 8 of it: rows 8 rg .., columns 8 cg ...
 // Blocks of 128 x 128 have one scale for the tile; blocks of 1 x 128 one for
 // each row (a maximum over 16 lanes) and, transposed, one for each column (a
-// maximum through LDS).  Transposed codes go through LDS too, so that they
+// maximum through LDS); a thread each works out those 256 scales.  Transposed codes go through LDS too, so that they
 // leave in 128-byte rows: column c's eight bytes of row group rg lie in slot
 // rg ^ (c / 8) of 16, which spreads both sides over the banks.
 template <class X, int KIND, int BR, bool AS_IS, bool TRANS>
-__global__ __launch_bounds__(256) void k_tile(const X* __restrict__ x, Args a, int tiles_c, int64_t tiles) {
+__global__ __launch_bounds__(256, 2) void k_tile(const X* __restrict__ x, Args a, int tiles_c, int64_t tiles) {
   __shared__ uint32_t part[16][128];
-  __shared__ Scale cscale[128];
+  __shared__ Factor cscale[128], rscale[128];  // of column 8 c + i at 16 i + c, of rows as they are
+  __shared__ alignas(16) uint32_t row_top[128];
   __shared__ alignas(16) uint8_t tr[TRANS ? 128 * 128 : 16];
   const int cg = threadIdx.x % 16, rg = threadIdx.x / 16;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -182,16 +226,11 @@ __global__ __launch_bounds__(256) void k_tile(const X* __restrict__ x, Args a, i
     const int cols = static_cast<int>(min(int64_t(128), a.cols - c0));
     const int col = cg * 8;
 
-    float v[8][8];
+    Pack<8, X> v[8];
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
       const int row = rg * 8 + p;
-      if (row < rows) {
-        load8(x + (r0 + row) * a.ldx + c0, col, cols, v[p]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
-      }
+      v[p] = row < rows ? load8(x + (r0 + row) * a.ldx + c0, col, cols) : Pack<8, X>{};
     }
 
     uint32_t rtop[8], ctop[8];
@@ -199,10 +238,12 @@ __global__ __launch_bounds__(256) void k_tile(const X* __restrict__ x, Args a, i
     for (int p = 0; p < 8; ++p) {
       rtop[p] = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) rtop[p] = max(rtop[p], magnitude(v[p][i]));
+      for (int i = 0; i < 8; ++i) rtop[p] = max(rtop[p], magnitude(to_float(v[p].v[i])));
     }
 
-    Scale whole;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) forget(v[p]);
+    Factor whole;
     if constexpr (BR == 128) {
       uint32_t top = 0;
 #pragma unroll
@@ -215,55 +256,70 @@ __global__ __launch_bounds__(256) void k_tile(const X* __restrict__ x, Args a, i
       top = max16(top);
       top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
       top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-      whole = make_scale<KIND>(top);
+      const Scale q = make_scale<KIND, X>(top);
+      whole = q.by;
       if (threadIdx.x == 0) {
-        if constexpr (AS_IS) store_scale<KIND>(a.s, tr_i * a.s_row + tc_i * a.s_col, whole);
-        if constexpr (TRANS) store_scale<KIND>(a.st, tc_i * a.st_row + tr_i * a.st_col, whole);
+        if constexpr (AS_IS) store_scale<KIND>(a.s, tr_i * a.s_row + tc_i * a.s_col, q);
+        if constexpr (TRANS) store_scale<KIND>(a.st, tc_i * a.st_row + tr_i * a.st_col, q);
       }
     } else if constexpr (TRANS) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ctop[i] = 0;
 #pragma unroll
-        for (int p = 0; p < 8; ++p) ctop[i] = max(ctop[i], magnitude(v[p][i]));
+        for (int p = 0; p < 8; ++p) ctop[i] = max(ctop[i], magnitude(to_float(v[p].v[i])));
         part[rg][col + i] = ctop[i];
       }
+      if constexpr (AS_IS) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) rtop[p] = max16(rtop[p]);
+        if (cg == 0) {
+          *reinterpret_cast<uint4*>(&row_top[rg * 8]) = make_uint4(rtop[0], rtop[1], rtop[2], rtop[3]);
+          *reinterpret_cast<uint4*>(&row_top[rg * 8 + 4]) = make_uint4(rtop[4], rtop[5], rtop[6], rtop[7]);
+        }
+      }
       __syncthreads();
+      if (AS_IS && threadIdx.x >= 128) {
+        const int row = threadIdx.x - 128;
+        const Scale q = make_scale<KIND, X>(row_top[row]);
+        rscale[row] = q.by;
+        if (row < rows) store_scale<KIND>(a.s, (r0 + row) * a.s_row + tc_i * a.s_col, q);
+      }
       if (threadIdx.x < 128) {
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = max(top, part[i][threadIdx.x]);
-        const Scale q = make_scale<KIND>(top);
-        cscale[threadIdx.x] = q;
+        const Scale q = make_scale<KIND, X>(top);
+        cscale[threadIdx.x % 8 * 16 + threadIdx.x / 8] = q.by;
         if (static_cast<int>(threadIdx.x) < cols)
           store_scale<KIND>(a.st, (c0 + threadIdx.x) * a.st_row + tr_i * a.st_col, q);
       }
       __syncthreads();
     }
 
+#pragma unroll
+    for (int p = 0; p < 8; ++p) forget(v[p]);
     if constexpr (AS_IS) {
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
         const int row = rg * 8 + p;
-        Scale q = whole;
-        if constexpr (BR == 1) {
-          q = make_scale<KIND>(max16(rtop[p]));
-          if (cg == 0 && row < rows) store_scale<KIND>(a.s, (r0 + row) * a.s_row + tc_i * a.s_col, q);
-        }
+        Factor by = whole;
+        if constexpr (BR == 1) by = rscale[row];
         if (row < rows)
-          store8(a.q + (r0 + row) * a.ldq + c0, col, cols,
-                 make_uint2(codes4<KIND>(v[p][0], v[p][1], v[p][2], v[p][3], q),
-                            codes4<KIND>(v[p][4], v[p][5], v[p][6], v[p][7], q)));
+          store8(a.q + (r0 + row) * a.ldq + c0, col, cols, codes8<KIND>(v[p], by));
       }
     }
     if constexpr (TRANS) {
 #pragma unroll
+      for (int p = 0; p < 8; ++p) forget(v[p]);
+#pragma unroll
       for (int i = 0; i < 8; ++i) {
-        Scale q = whole;
-        if constexpr (BR == 1) q = cscale[col + i];
-        const uint2 c = make_uint2(codes4<KIND>(v[0][i], v[1][i], v[2][i], v[3][i], q),
-                                   codes4<KIND>(v[4][i], v[5][i], v[6][i], v[7][i], q));
-        *reinterpret_cast<uint2*>(&tr[(col + i) * 128 + 8 * (rg ^ cg)]) = c;
+        Factor by = whole;
+        if constexpr (BR == 1) by = cscale[16 * i + cg];
+        Pack<8, X> column;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) column.v[p] = v[p].v[i];
+        *reinterpret_cast<uint2*>(&tr[(col + i) * 128 + 8 * (rg ^ cg)]) = codes8<KIND>(column, by);
       }
       __syncthreads();
 #pragma unroll
@@ -304,7 +360,7 @@ void launch_kind(const void* x, const Args& a, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(tiles < cap ? tiles : cap));
   if (a.q && a.qt) hipLaunchKernelGGL((k_tile<X, KIND, BR, true, true>), grid, dim3(256), 0, stream, p, a, blocks, tiles);
   else if (a.qt) hipLaunchKernelGGL((k_tile<X, KIND, BR, false, true>), grid, dim3(256), 0, stream, p, a, blocks, tiles);
-  else hipLaunchKernelGGL((k_tile<X, KIND, BR, true, false>), grid, dim3(256), 0, stream, p, a, blocks, tiles);
+  else if constexpr (BR == 128) hipLaunchKernelGGL((k_tile<X, KIND, BR, true, false>), grid, dim3(256), 0, stream, p, a, blocks, tiles);
 }
 
 template <class X>

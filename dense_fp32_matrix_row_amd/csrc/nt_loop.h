@@ -169,7 +169,7 @@ __device__ __forceinline__ void loop_out(const v16f (&acc)[L::kAcc], int m0, int
 // rows of sums at a time lie in LDS, COLS + 4 floats apart (four columns of 16
 // rows at once, as fragments come, then fall in different banks).
 template <int COLS>
-struct Sheet {
+struct alignas(16) Sheet {
   static constexpr int kLd = COLS + 4;
   float v[64 * kLd];
 

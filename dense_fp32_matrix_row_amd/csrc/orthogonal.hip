@@ -357,40 +357,123 @@ __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_symmetric(Side A, 
 
 template <class T, class O>
 __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_iterate(Side A, Side B, int K, IterateOut<O> out,
-                                                                      int tiles_m, int tiles_n) {
+                                                                      int col0, int tiles_m, int tiles_n) {
   out.batch = blockIdx.y;
   A.p += blockIdx.y * A.batch;
   B.p += blockIdx.y * B.batch;
   const nt::Place at = nt::place_of(xcd_contiguous(blockIdx.x, gridDim.x), tiles_m, tiles_n, 8);
-  product<T>(A, B, at.tm * T::BM, at.tn * T::BN, K, out);
+  product<T>(A, B, at.tm * T::BM, col0 + at.tn * T::BN, K, out);
 }
 
-// Calls f with the tile that takes the products of `batch` matrices of rows x
-// cols soonest: rounds over the CUs times what a round takes, by the measured
-// rates of the tiles at full occupancy.
-template <class F>
-void pick_tile(int batch, int rows, int cols, bool symmetric, const F& f) {
-  const auto cost = [&](int tile, int per_cu, double us) {
-    const int64_t tm = ceil_div(rows, tile), tn = ceil_div(cols, tile);
-    const int64_t tiles = batch * (symmetric ? tm * (tm + 1) / 2 : tm * tn), at_once = int64_t(256) * per_cu;
-    // the last round may fill the CUs in part
-    const int64_t rest = tiles % at_once;
-    return us * (tiles / at_once * per_cu + (rest ? ceil_div(rest, 256) : 0));
+// One of `splits` parts of the K of a symmetric product's tiles: the sums as the
+// wavefronts hold them, 16 bytes a lane side by side.
+template <class T>
+__global__ __launch_bounds__(T::threads, T::kMinWaves) void k_partial(Side A, int K, float* sums, int tiles, int splits) {
+  __shared__ alignas(16) uint8_t smem[T::kLds];
+  const int64_t id = xcd_contiguous(blockIdx.x, gridDim.x);  // an XCD's blocks share a part of K
+  const int tile = static_cast<int>(id % tiles), part = static_cast<int>(id / tiles), steps = K / 32;
+  const int k0 = static_cast<int>(int64_t(steps) * part / splits), k1 = static_cast<int>(int64_t(steps) * (part + 1) / splits);
+  const nt::Place at = triangle(tile);
+  A.p += blockIdx.y * A.batch + int64_t(k0) * nt::kStep;
+  nt::v16f acc[T::kAcc];
+  nt::loop_sum<T>(smem, A, A, at.tm * T::BM, at.tn * T::BN, (k1 - k0) * nt::kStep, acc);
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  float* to = sums + ((int64_t(blockIdx.y) * splits + part) * tiles + tile) * (T::BM * T::BN) + wave * (T::MT * T::NT * 256) + lane * 4;
+#pragma unroll
+  for (int f = 0; f < T::MT * T::NT; ++f)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) to[f * 256 + r] = acc[f / 4][f % 4 * 4 + r];
+}
+
+// The parts added in their order, half a tile (the 64 rows of one wm) a block.
+template <class T>
+__global__ __launch_bounds__(T::threads) void k_finish(const float* sums, int tiles, int splits, SymmetricOut out) {
+  static_assert(T::MT == 4 && T::BM == 128, "64 rows a wavefront");
+  __shared__ nt::Sheet<T::BN> sheet;
+  const int tile = blockIdx.x / 2, wm = blockIdx.x % 2, lane = threadIdx.x % 64;
+  const nt::Place at = triangle(tile);
+  out.batch = blockIdx.y;
+  out.mirror = at.tm != at.tn;
+  constexpr int kFrags = T::MT * T::NT;
+  for (int q = threadIdx.x / 64; q < T::WN * kFrags; q += T::waves) {
+    const int wn = q / kFrags, f = q % kFrags;  // fragment f = j MT + i of wavefront wn WM + wm
+    const float* from = sums + (int64_t(blockIdx.y) * splits * tiles + tile) * (T::BM * T::BN) + ((wn * T::WM + wm) * kFrags + f) * 256 + lane * 4;
+    v4f v = {0, 0, 0, 0};
+    for (int p = 0; p < splits; ++p) v += *reinterpret_cast<const v4f*>(from + int64_t(p) * tiles * (T::BM * T::BN));
+    sheet.put(f % T::MT * 16 + lane % 16, (wn * T::NT + f / T::MT) * 16 + 4 * (lane / 16), v);
+  }
+  out.sheet<T::threads>(sheet, at.tm * T::BM + 64 * wm, at.tn * T::BN);
+}
+
+// Which tile takes the products of `batch` matrices, by estimates of the time in
+// us: of the small ones what a launch, a step of a wavefront alone and a step of
+// one block among many take; of the large ones what a step takes alone and with
+// all 256 CUs at it.  Measured from 256 x 256 to 4096 x 4096, which they meet
+// within a quarter.
+enum class Way { kSmall32, kSmall64, kLoop128, kLoop192, kLoop256, kSplit, kColumns };
+struct Choice {
+  Way way;
+  int at;  // kSplit: parts of K; kColumns: where the result is cut in two
+  double us;
+};
+constexpr int kMaxParts = 16;
+
+Choice choose(int batch, int rows, int cols, int K, bool symmetric, bool cut) {
+  const double steps = K / 32, each = static_cast<double>(ceil_div(K / 32, 8));
+  const auto tiles_of = [&](int t) {
+    const int64_t tm = ceil_div(rows, t), tn = ceil_div(cols, t);
+    return batch * (symmetric ? tm * (tm + 1) / 2 : tm * tn);
   };
-  // relative times of a tile's product alone on its CU
-  const double c256 = cost(256, 1, 4.0), c192 = cost(192, 1, 2.4), c128 = cost(128, 1, 1.1), c64 = cost(64, 1, 0.8),
-               c32 = cost(32, 1, 0.18);
-  if (c256 <= c192 && c256 <= c128 && c256 <= c64 && c256 <= c32) f(Assembled<8, 4, 2, 4, 2>{});
-  else if (c192 <= c128 && c192 <= c64 && c192 <= c32) f(Assembled<6, 6, 2, 2, 3>{});
-  else if (c128 <= c64 && c128 <= c32) f(Assembled<4, 2, 2, 4, 4>{});
-  else if (c64 <= c32) f(Small<4>{});
-  else f(Small<2>{});
+  Choice best{Way::kSmall32, 0, 1e30};
+  const auto offer = [&](Way w, int at, double us) {
+    if (us < best.us) best = Choice{w, at, us};
+  };
+  const auto small = [&](Way w, int t, double base, double alone, double among) {
+    const double blocks = static_cast<double>(tiles_of(t));
+    offer(w, 0, base + each * (alone > among * blocks ? alone : among * blocks));
+  };
+  const auto loop = [&](Way w, int t, double base, double alone, double full) {
+    const int64_t tiles = tiles_of(t), rest = tiles % 256;
+    offer(w, 0, base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0)));
+  };
+  small(Way::kSmall32, 32, 2.5, 1.5, 0.0105);
+  small(Way::kSmall64, 64, 3.5, 4.0, 0.0225);
+  loop(Way::kLoop128, 128, 6.0, 0.6, 0.69);
+  loop(Way::kLoop192, 192, 8.0, 1.0, 1.4);
+  loop(Way::kLoop256, 256, 10.0, 1.45, 2.3);
+  if (symmetric) {
+    const int64_t tiles = tiles_of(128);
+    const int64_t most = steps / 2 < kMaxParts ? static_cast<int64_t>(steps / 2) : kMaxParts;
+    const int64_t parts = 256 / tiles < most ? 256 / tiles : most;
+    if (parts > 1) offer(Way::kSplit, static_cast<int>(parts), 11.0 + static_cast<double>(ceil_div(K / 32, parts)) * 0.65 + 0.016 * tiles * parts);
+  }
+  for (int t = 128; cut && !symmetric && t <= 256; t += 64)  // columns that hardly fill their tiles apart from the rest
+    if (cols > t && cols % t) {
+      const int at = cols - cols % t;
+      offer(Way::kColumns, at, choose(batch, rows, at, K, false, false).us + choose(batch, rows, cols - at, K, false, false).us);
+    }
+  return best;
 }
 
-// The workspace: per-block parts of the norms, then X, X^T twice, S and P.
+using Loop128 = Assembled<4, 2, 2, 4, 4>;
+
+// Calls f with the tile.
+template <class F>
+void with_tile(Way way, const F& f) {
+  switch (way) {
+    case Way::kSmall32: return f(Small<2>{});
+    case Way::kSmall64: return f(Small<4>{});
+    case Way::kLoop128: return f(Loop128{});
+    case Way::kLoop192: return f(Assembled<6, 6, 2, 2, 3>{});
+    default: return f(Assembled<8, 4, 2, 4, 2>{});
+  }
+}
+
+// The workspace: per-block parts of the norms, then X, X^T twice, S and P, and the
+// parts of the symmetric products' sums.
 struct Layout {
   int m, n;
-  int64_t part, x, xt[2], s, p, bytes;
+  int64_t part, x, xt[2], s, p, sums, bytes;
   int64_t ldx, ldm;  // bytes of a row of X, and of the others
 };
 
@@ -414,6 +497,8 @@ Layout layout_of(int batch, int rows, int cols) {
   l.xt[1] = take(batch * (l.n * l.ldm));
   l.s = take(batch * (l.m * l.ldm));
   l.p = take(batch * (l.m * l.ldm));
+  const int64_t t = ceil_div(l.m, Loop128::BM), tiles = batch * (t * (t + 1) / 2);
+  l.sums = take(tiles > 0 && tiles <= 128 ? (256 / tiles < kMaxParts ? 256 / tiles : kMaxParts) * tiles * (Loop128::BM * Loop128::BN * 4) : 0);
   l.bytes = at;
   return l;
 }
@@ -451,10 +536,27 @@ hipError_t launch(int batch, const Source& src, int steps, const float* co, floa
   const auto side = [](const Pairs& p, int rows) { return Side{p.p, p.ld, rows, nullptr, 0, 0, 0, p.batch}; };
   const int km = static_cast<int>(pad32(l.m)), kn = static_cast<int>(pad32(l.n));
   const auto symmetric = [&](const Side& a, int K, const SymmetricOut& out) {
-    pick_tile(batch, l.m, l.m, true, [&](auto tile) {
+    const Choice c = choose(batch, l.m, l.m, K, true, false);
+    if (c.way == Way::kSplit) {
+      const int t = static_cast<int>(ceil_div(l.m, Loop128::BM)), tiles = t * (t + 1) / 2;
+      float* sums = reinterpret_cast<float*>(ws + l.sums);
+      hipLaunchKernelGGL((k_partial<Loop128>), dim3(tiles * c.at, batch), dim3(Loop128::threads), 0, stream, a, K, sums, tiles, c.at);
+      hipLaunchKernelGGL((k_finish<Loop128>), dim3(tiles * 2, batch), dim3(Loop128::threads), 0, stream, sums, tiles, c.at, out);
+      return;
+    }
+    with_tile(c.way, [&](auto tile) {
       using Tile = decltype(tile);
       const unsigned t = static_cast<unsigned>(ceil_div(l.m, Tile::BM));
       hipLaunchKernelGGL((k_symmetric<Tile>), dim3(t * (t + 1) / 2, batch), dim3(Tile::threads), 0, stream, a, K, out);
+    });
+  };
+  // columns col0 .. col0 + cols - 1 of P X
+  const auto iterate = [&](const Side& p, const Side& xt, int col0, int cols, Way way, const IterateOut<T>& out) {
+    with_tile(way, [&](auto tile) {
+      using Tile = decltype(tile);
+      const unsigned tm = static_cast<unsigned>(ceil_div(l.m, Tile::BM)), tn = static_cast<unsigned>(ceil_div(cols, Tile::BN));
+      hipLaunchKernelGGL((k_iterate<Tile, T>), dim3(tm * tn, batch), dim3(Tile::threads), 0, stream, p, xt, km, out, col0,
+                         static_cast<int>(tm), static_cast<int>(tn));
     });
   };
   for (int i = 0; i < steps; ++i) {
@@ -463,14 +565,14 @@ hipError_t launch(int batch, const Source& src, int steps, const float* co, floa
               SymmetricOut{S, Pairs{nullptr, 0, 0}, l.m, kScaleS / (kScaleX * kScaleX), 0.0f, 0.0f, 0, false});
     symmetric(side(S, l.m), km, SymmetricOut{P, S, l.m, c / kScaleS, b, a * kScaleS, 0, false});
     const bool last = i + 1 == steps;
-    pick_tile(batch, l.m, l.n, false, [&](auto tile) {
-      using Tile = decltype(tile);
-      const unsigned tm = static_cast<unsigned>(ceil_div(l.m, Tile::BM)), tn = static_cast<unsigned>(ceil_div(l.n, Tile::BN));
-      hipLaunchKernelGGL((k_iterate<Tile, T>), dim3(tm * tn, batch), dim3(Tile::threads), 0, stream, side(P, l.m),
-                         side(XT, l.n), km,
-                         IterateOut<T>{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, 0, tall},
-                         static_cast<int>(tm), static_cast<int>(tn));
-    });
+    const IterateOut<T> out{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, 0, tall};
+    const Choice way = choose(batch, l.m, l.n, km, false, true);
+    if (way.way == Way::kColumns) {
+      iterate(side(P, l.m), side(XT, l.n), 0, way.at, choose(batch, l.m, way.at, km, false, false).way, out);
+      iterate(side(P, l.m), side(XT, l.n), way.at, l.n - way.at, choose(batch, l.m, l.n - way.at, km, false, false).way, out);
+    } else {
+      iterate(side(P, l.m), side(XT, l.n), 0, l.n, way.way, out);
+    }
     const Pairs t = XT;
     XT = XT2;
     XT2 = t;

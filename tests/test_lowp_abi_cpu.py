@@ -88,6 +88,8 @@ def test_orthogonalize_workspace_grows_with_the_batch_and_holds_the_iterate():
     assert one >= 3 * 100 * 300 * 4 + 2 * 100 * 100 * 4
     assert orthogonal.hip_orthogonalize_workspace(1, 300, 100, 0) == one
     assert orthogonal.hip_orthogonalize_workspace(4, 100, 300, 0) > 3 * one
+    for batch, rows, cols in ((0, 4, 4), (3, 0, 4), (3, 4, 0)):  # nothing to hold
+        assert orthogonal.hip_orthogonalize_workspace(batch, rows, cols, 0) >= 0
     with pytest.raises(sgemm.SgemmError):
         orthogonal.hip_orthogonalize_workspace(-1, 4, 4, 0)
 
