@@ -148,12 +148,12 @@ Choice choose(int M, int N, int K, bool wide, bool loops, int cuts) {
     const int64_t tiles = ceil_div(M, 256) * ceil_div(N, bn), rest = tiles % 256;
     return base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0));
   };
-  Choice best{Way::kSmall16, 0, small(16, 3.0, 0.5, 0.0035)};
+  Choice best{Way::kSmall16, 0, small(16, 2.8, 0.45, 0.003)};
   const auto offer = [&](Way w, int at, double us) {
     if (us < best.us) best = Choice{w, at, us};
   };
-  offer(Way::kSmall32, 0, small(32, 2.3, 1.5, wide ? 0.0085 : 0.007));
-  offer(Way::kSmall64, 0, wide ? small(64, 2.0, 4.9, 0.027) : small(64, 3.5, 2.5, 0.0167));
+  offer(Way::kSmall32, 0, small(32, 2.3, 1.3, wide ? 0.007 : 0.0056));
+  offer(Way::kSmall64, 0, wide ? small(64, 2.0, 4.5, 0.024) : small(64, 3.0, 2.2, 0.0135));
   if (!loops) return best;
   offer(Way::kLoop128, 0, wide ? loop(128, 7.0, 1.45, 2.0) : loop(128, 6.0, 0.65, 0.98));
   if (!wide) offer(Way::kLoop256, 0, loop(256, 7.0, 1.0, 1.6));

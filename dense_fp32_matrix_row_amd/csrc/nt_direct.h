@@ -35,18 +35,24 @@ struct Direct {
     uint32_t sa[MT], sb[NT][kSn ? kSn : 1];
   };
 
-  // Where a lane's rows begin; rows past the end repeat the last one.
+  // Where a lane's rows begin; rows past the end repeat the last one.  Of a step's
+  // 128 bytes of a row a lane takes two times 16, 64 apart.  Where all rows begin
+  // in the same half of the cache's 128-byte lines, odd rows take the second
+  // first, so that a load takes both halves of the lines alike (256 x 1024 x 1024
+  // with rows of 1024 bytes: 4.9 -> 4.1 us).
   struct Reader {
     const uint8_t *a, *b;
     uint32_t ra[MT], rb[NT];
     const uint8_t *sa[MT], *sb[NT][kSn ? kSn : 1];
     int64_t ca, cb;  // bytes from one step's scales to the next's
     uint32_t last;   // the last 16 bytes of a row
+    bool turn_a, turn_b;
     int g;
 
     __device__ __forceinline__ Reader(const Side& A, const Side& B, int m0, int n0, int K, int row, int g_)
         : a(A.p + int64_t(m0) * A.ld), b(B.p + int64_t(n0) * B.ld), ca(A.s_col * P::kScaleBytes),
-          cb(B.s_col * P::kScaleBytes), last(static_cast<uint32_t>(K - 1) / 16 * 16), g(g_) {
+          cb(B.s_col * P::kScaleBytes), last(static_cast<uint32_t>(K - 1) / 16 * 16), turn_a(row % 2 != 0 && A.ld / 64 % 2 == 0),
+          turn_b(row % 2 != 0 && B.ld / 64 % 2 == 0), g(g_) {
       const auto scale = [](const Side& o, int at) {
         return static_cast<const uint8_t*>(o.s) + (int64_t(min(at, o.rows - 1) >> o.shift) * o.s_row) * P::kScaleBytes;
       };
@@ -68,24 +74,40 @@ struct Direct {
       return *p;
     }
     __device__ __forceinline__ void read(Raw& r, int k) const {
-      const uint32_t lo = min(static_cast<uint32_t>(k) * kStep + 16 * g, last);
-      const uint32_t hi = min(static_cast<uint32_t>(k) * kStep + 64 + 16 * g, last);
+      const uint32_t first = static_cast<uint32_t>(k) * kStep + 16 * g, lo = min(first, last), hi = min(first + 64, last);
+      const uint32_t alo = turn_a ? hi : lo, ahi = turn_a ? lo : hi, blo = turn_b ? hi : lo, bhi = turn_b ? lo : hi;
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        r.a[i].lo = *reinterpret_cast<const v4i*>(a + ra[i] + lo);
-        r.a[i].hi = *reinterpret_cast<const v4i*>(a + ra[i] + hi);
+        r.a[i].lo = *reinterpret_cast<const v4i*>(a + ra[i] + alo);
+        r.a[i].hi = *reinterpret_cast<const v4i*>(a + ra[i] + ahi);
         if constexpr (kScaled) r.sa[i] = scale_at(sa[i] + k * ca);
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        r.b[j].lo = *reinterpret_cast<const v4i*>(b + rb[j] + lo);
-        r.b[j].hi = *reinterpret_cast<const v4i*>(b + rb[j] + hi);
+        r.b[j].lo = *reinterpret_cast<const v4i*>(b + rb[j] + blo);
+        r.b[j].hi = *reinterpret_cast<const v4i*>(b + rb[j] + bhi);
         if constexpr (kScaled)
 #pragma unroll
           for (int s = 0; s < kSn; ++s) r.sb[j][s] = scale_at(sb[j][s] + k * cb);
       }
     }
   };
+
+  // What was read the other way round.
+  static __device__ __forceinline__ void turn(Frag& f, bool other) {
+    const v4i lo = f.lo;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      f.lo[w] = other ? f.hi[w] : lo[w];
+      f.hi[w] = other ? lo[w] : f.hi[w];
+    }
+  }
+  static __device__ __forceinline__ void turn(Raw& r, const Reader& rd) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i) turn(r.a[i], rd.turn_a);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) turn(r.b[j], rd.turn_b);
+  }
 
   static __device__ __forceinline__ void mac(typename P::Acc (&acc)[NT][MT], const Raw& r) {
     typename P::Op mo[MT];
@@ -137,9 +159,11 @@ struct Direct {
       int k = wave;
       for (; k + WAVES < steps; k += WAVES) {
         rd.read(next, k + WAVES);
+        turn(now, rd);
         mac(acc, now);
         now = next;
       }
+      turn(now, rd);
       if (K - k * kStep < kStep) mask(now, K - k * kStep, g);
       mac(acc, now);
     }

@@ -1,6 +1,7 @@
-// nt_tile.h -- the tile kernel that the block-scaled 8-bit product
-// (fp8_gemm.hip) and the orthogonalised update (orthogonal.hip) share:
-// D = A * B^T over operands whose rows are contiguous along K.
+// nt_tile.h -- what the tiles of the block-scaled 8-bit product (fp8_gemm.hip)
+// and of the orthogonalised update (orthogonal.hip) share: D = A * B^T over
+// operands whose rows are contiguous along K.  nt_direct.h has the small tiles,
+// nt_loop.h the large ones.
 //
 // Both operands are rows of bytes, taken 128 bytes a step: 128 e4m3 codes, or
 // 32 numbers as halfs hi and lo (64 bytes each).  A step is eight 16-byte
@@ -12,13 +13,6 @@
 // B's rows go in as the instruction's first operand, A's as its second, so that
 // a lane ends up with D[m][n .. n+3], m = lane % 16, n = 4 (lane / 16): four
 // neighbours in a row of D, stored at once.
-//
-// LDS: row r of a panel at 128 r, chunk c in slot c ^ ((r / 2) % 8).  The 16
-// rows that a lane group reads at one c then lie in 16 different 16-byte slots
-// of 256 bytes, which is what a 128-bit read needs to be free of conflicts.
-// The loads that go straight from memory to LDS place lane l at 16 l behind a
-// wavefront-wide base, so the permutation is in the address that they read:
-// 8 lanes still read 128 bytes of one row.
 #pragma once
 
 #include "sgemm_internal.h"
@@ -49,16 +43,6 @@ struct Frag {
   v4i lo, hi;  // chunks g and 4 + g
 };
 
-// Tile: BM rows of A by BN rows of B, over WM x WN wavefronts.
-template <int BM_, int BN_, int WM_, int WN_, int WPS_>
-struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
-  static constexpr int WPS = WPS_;  // wavefronts per SIMD the registers must allow
-  static constexpr int threads = 64 * WM * WN;
-  static constexpr int TM = BM / WM, TN = BN / WN;
-  static constexpr int MT = TM / 16, NT = TN / 16;
-};
-
 // Where a block's tile lies in D.
 struct Place {
   int tm, tn;
@@ -72,53 +56,6 @@ __device__ __forceinline__ Place place_of(int64_t id, int tiles_m, int tiles_n, 
   const int high = min(group, tiles_m - first);
   const int64_t in = id % per;
   return Place{first + static_cast<int>(in % high), static_cast<int>(in / high)};
-}
-
-// The chunks of a panel of ROWS rows, split over the wavefronts of the block.
-template <int ROWS, int WAVES>
-struct Panel {
-  static constexpr int kLoads = ROWS / 8 / WAVES;  // 1 KB loads per wavefront
-  static_assert(ROWS % (8 * WAVES) == 0, "every wavefront takes whole loads");
-  uint32_t off[kLoads];
-  uint32_t chunk;  // of this lane, bytes into the step (the same for all its loads but for bit 6)
-
-  // Rows past the end repeat the last one: in bounds, and their sums are not stored.
-  __device__ __forceinline__ void init(int wave, int lane, int rows_left, int64_t ld) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = (wave * kLoads + i) * 8 + lane / 8;
-      const int slot = lane % 8;
-      const int c = slot ^ ((row / 2) % 8);
-      off[i] = static_cast<uint32_t>(min(row, rows_left - 1)) * static_cast<uint32_t>(ld) + 16 * c;
-    }
-  }
-  __device__ __forceinline__ void load(const uint8_t* base, uint8_t* lds, int wave) const {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_global_load_lds(base + off[i],
-                                       (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + i) * 1024),
-                                       16, 0, 0);
-  }
-  // The last, partial step: chunks past K's end (`left` bytes from base) repeat the last one.
-  __device__ __forceinline__ void load_last(const uint8_t* base, uint8_t* lds, int wave, int lane, int left) const {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = (wave * kLoads + i) * 8 + lane / 8;
-      const uint32_t c = 16 * ((lane % 8) ^ ((row / 2) % 8));
-      const uint32_t last = static_cast<uint32_t>(left - 1) / 16 * 16;
-      __builtin_amdgcn_global_load_lds(base + (off[i] - c + min(c, last)),
-                                       (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + i) * 1024),
-                                       16, 0, 0);
-    }
-  }
-};
-
-__device__ __forceinline__ Frag read_frag(const uint8_t* panel, int row, int g) {
-  const int x = (row / 2) % 8;
-  Frag f;
-  f.lo = *reinterpret_cast<const v4i*>(panel + row * kStep + 16 * (g ^ x));
-  f.hi = *reinterpret_cast<const v4i*>(panel + row * kStep + 16 * ((4 + g) ^ x));
-  return f;
 }
 
 // Zeroes the bytes of a chunk from byte `keep` on.
@@ -160,7 +97,7 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
 // eight neighbours along k are lined up with the largest of them and cut 13
 // bits below it, and only the sums of eight are added as floats.  On normal
 // data that is 1.5e-5 of the result, far below the half step of a 16-bit
-// result (2^-9, 2^-12), and far above a float's: float results use Widened.
+// result (2^-8, 2^-11 of it), and far above a float's: float results use Widened.
 
 // Float scales: a block of 128 is summed from zero and added times its scales'
 // product (the matrix instruction can apply powers of two only).  UNIFORM: all
@@ -259,144 +196,6 @@ struct HalfPair {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(nl, mh, acc, 0, 0, 0);
   }
   static __device__ __forceinline__ v4f value(const Acc& a) { return a; }
-};
-
-// --- the tile -------------------------------------------------------------
-
-template <class P, class T>
-struct Shared {
-  static constexpr int kScales = P::kScaleBytes ? T::BM + T::BN : 0;
-  alignas(16) uint8_t a[2][T::BM * kStep];
-  alignas(16) uint8_t b[2][T::BN * kStep];
-  uint32_t s[2][kScales ? kScales : 1];
-};
-
-// A wavefront's sums.
-template <class P, class T>
-struct Sums {
-  typename P::Acc v[T::NT][T::MT];
-};
-
-// The scale of row `row` (clamped) of a side at step k, as 32 bits.
-template <int BYTES>
-__device__ __forceinline__ uint32_t load_scale(const Side& o, int row, int k) {
-  const int64_t at = int64_t(min(row, o.rows - 1) >> o.shift) * o.s_row + int64_t(k) * o.s_col;
-  if constexpr (BYTES == 4) return static_cast<const uint32_t*>(o.s)[at];
-  return static_cast<const uint8_t*>(o.s)[at];
-}
-
-// Sums the tile at rows m0 of A and n0 of B over steps [k0, k1) of K bytes
-// (the last of which may be partial) into acc.
-template <class P, class T>
-struct TileOp {
-static __device__ __forceinline__ void sum(Shared<P, T>& sh, const Side& A, const Side& B, int m0, int n0, int K,
-                                         int k0, int k1, Sums<P, T>& acc) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-  const int wm = wave % T::WM, wn = wave / T::WM;
-  const int row = lane % 16, g = lane / 16;
-
-#pragma unroll
-  for (int j = 0; j < T::NT; ++j)
-#pragma unroll
-    for (int i = 0; i < T::MT; ++i) P::zero(acc.v[j][i]);
-  if (k0 >= k1) return;
-
-  Panel<T::BM, T::WM * T::WN> pa;
-  Panel<T::BN, T::WM * T::WN> pb;
-  pa.init(wave, lane, A.rows - m0, A.ld);
-  pb.init(wave, lane, B.rows - n0, B.ld);
-  const uint8_t* ga = A.p + int64_t(m0) * A.ld;
-  const uint8_t* gb = B.p + int64_t(n0) * B.ld;
-
-  constexpr int kScales = Shared<P, T>::kScales;
-  constexpr int kPer = (kScales + T::threads - 1) / T::threads;
-  uint32_t sc[kPer ? kPer : 1];
-
-  auto fetch = [&](int k, int buf) {
-    const int left = K - k * kStep;
-    if (left >= kStep) {
-      pa.load(ga + int64_t(k) * kStep, sh.a[buf], wave);
-      pb.load(gb + int64_t(k) * kStep, sh.b[buf], wave);
-    } else {
-      pa.load_last(ga + int64_t(k) * kStep, sh.a[buf], wave, lane, left);
-      pb.load_last(gb + int64_t(k) * kStep, sh.b[buf], wave, lane, left);
-    }
-    if constexpr (kScales > 0) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int r = threadIdx.x + i * T::threads;
-        if (r < T::BM) sc[i] = load_scale<P::kScaleBytes>(A, m0 + r, k);
-        else if (r < kScales) sc[i] = load_scale<P::kScaleBytes>(B, n0 + r - T::BM, k);
-      }
-    }
-  };
-  auto place_scales = [&](int buf) {
-    if constexpr (kScales > 0) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int r = threadIdx.x + i * T::threads;
-        if (r < kScales) sh.s[buf][r] = sc[i];
-      }
-    }
-  };
-  auto step = [&](int buf, bool partial, int left) {
-    typename P::Op mo[T::MT];
-    uint32_t sm[T::MT];
-#pragma unroll
-    for (int i = 0; i < T::MT; ++i) {
-      Frag f = read_frag(sh.a[buf], wm * T::TM + 16 * i + row, g);
-      if (partial) f = mask_frag(f, g, left);
-      mo[i] = P::prepare(f);
-      sm[i] = 0;
-      if constexpr (kScales > 0) sm[i] = sh.s[buf][wm * T::TM + 16 * i + row];
-    }
-#pragma unroll
-    for (int j = 0; j < T::NT; ++j) {
-      Frag f = read_frag(sh.b[buf], wn * T::TN + 16 * j + row, g);
-      if (partial) f = mask_frag(f, g, left);
-      const typename P::Op no = P::prepare(f);
-      if constexpr (P::kRowScales) {
-        v4f sn;
-        const uint32_t* s = &sh.s[buf][T::BM + wn * T::TN + (P::kUniform ? 0 : 16 * j + 4 * g)];
-#pragma unroll
-        for (int i = 0; i < (P::kUniform ? 1 : 4); ++i) sn[i] = scale_value<P::kScaleBytes>(s[i]);
-#pragma unroll
-        for (int i = 0; i < T::MT; ++i) P::mac(acc.v[j][i], no, mo[i], sn, scale_value<P::kScaleBytes>(sm[i]));
-      } else {
-        uint32_t sn = 0;
-        if constexpr (kScales > 0) sn = sh.s[buf][T::BM + wn * T::TN + 16 * j + row];
-#pragma unroll
-        for (int i = 0; i < T::MT; ++i) P::mac(acc.v[j][i], no, mo[i], sn, sm[i]);
-      }
-    }
-  };
-
-  fetch(k0, 0);
-  place_scales(0);
-  for (int k = k0; k < k1; ++k) {
-    const int buf = (k - k0) & 1;
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the barrier alone need not wait for loads to LDS
-    __syncthreads();  // this step's panels have arrived, and the other buffer has been read
-    if (k + 1 < k1) fetch(k + 1, buf ^ 1);
-    const int left = K - k * kStep;
-    if (left >= kStep) step(buf, false, kStep);
-    else step(buf, true, left);
-    if (k + 1 < k1) place_scales(buf ^ 1);
-  }
-}
-
-// Calls epi(m, n, v) for every four neighbours D[m][n .. n+3] that the lane
-// holds, also past D's edges.
-template <class E>
-static __device__ __forceinline__ void out(const Sums<P, T>& acc, int m0, int n0, const E& epi) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-  const int wm = wave % T::WM, wn = wave / T::WM;
-#pragma unroll
-  for (int i = 0; i < T::MT; ++i)
-#pragma unroll
-    for (int j = 0; j < T::NT; ++j)
-      epi(m0 + wm * T::TM + 16 * i + lane % 16, n0 + wn * T::TN + 16 * j + 4 * (lane / 16), P::value(acc.v[j][i]));
-}
 };
 
 }  // namespace nt

@@ -385,24 +385,29 @@ __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_partial(Side A, in
     for (int r = 0; r < 4; ++r) to[f * 256 + r] = acc[f / 4][f % 4 * 4 + r];
 }
 
-// The parts added in their order, half a tile (the 64 rows of one wm) a block.
+// The parts added in their order, a wavefront's share of a tile a block.
 template <class T>
-__global__ __launch_bounds__(T::threads) void k_finish(const float* sums, int tiles, int splits, SymmetricOut out) {
-  static_assert(T::MT == 4 && T::BM == 128, "64 rows a wavefront");
-  __shared__ nt::Sheet<T::BN> sheet;
-  const int tile = blockIdx.x / 2, wm = blockIdx.x % 2, lane = threadIdx.x % 64;
+__global__ __launch_bounds__(256) void k_finish(const float* sums, int tiles, int splits, SymmetricOut out) {
+  static_assert(T::MT == 4 && T::NT == 2, "a sheet of 64 rows, two fragments each of four wavefronts");
+  __shared__ nt::Sheet<16 * T::NT> sheet;
+  const int tile = blockIdx.x / T::waves, share = blockIdx.x % T::waves, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const nt::Place at = triangle(tile);
   out.batch = blockIdx.y;
   out.mirror = at.tm != at.tn;
-  constexpr int kFrags = T::MT * T::NT;
-  for (int q = threadIdx.x / 64; q < T::WN * kFrags; q += T::waves) {
-    const int wn = q / kFrags, f = q % kFrags;  // fragment f = j MT + i of wavefront wn WM + wm
-    const float* from = sums + (int64_t(blockIdx.y) * splits * tiles + tile) * (T::BM * T::BN) + ((wn * T::WM + wm) * kFrags + f) * 256 + lane * 4;
-    v4f v = {0, 0, 0, 0};
-    for (int p = 0; p < splits; ++p) v += *reinterpret_cast<const v4f*>(from + int64_t(p) * tiles * (T::BM * T::BN));
-    sheet.put(f % T::MT * 16 + lane % 16, (wn * T::NT + f / T::MT) * 16 + 4 * (lane / 16), v);
+  const float* from = sums + (int64_t(blockIdx.y) * splits * tiles + tile) * (T::BM * T::BN) + share * (T::MT * T::NT * 256) + wave * 512 + lane * 4;
+  v4f v[2] = {};
+#pragma unroll 4
+  for (int p = 0; p < splits; ++p) {
+    const float* at_p = from + int64_t(p) * tiles * (T::BM * T::BN);
+    v[0] += *reinterpret_cast<const v4f*>(at_p);
+    v[1] += *reinterpret_cast<const v4f*>(at_p + 256);
   }
-  out.sheet<T::threads>(sheet, at.tm * T::BM + 64 * wm, at.tn * T::BN);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int f = 2 * wave + i;  // fragment j MT + i of the wavefront
+    sheet.put(f % T::MT * 16 + lane % 16, f / T::MT * 16 + 4 * (lane / 16), v[i]);
+  }
+  out.sheet<256>(sheet, at.tm * T::BM + share % T::WM * 64, at.tn * T::BN + share / T::WM * 16 * T::NT);
 }
 
 // Which tile takes the products of `batch` matrices, by estimates of the time in
@@ -436,16 +441,17 @@ Choice choose(int batch, int rows, int cols, int K, bool symmetric, bool cut) {
     const int64_t tiles = tiles_of(t), rest = tiles % 256;
     offer(w, 0, base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0)));
   };
-  small(Way::kSmall32, 32, 2.5, 1.5, 0.0105);
-  small(Way::kSmall64, 64, 3.5, 4.0, 0.0225);
-  loop(Way::kLoop128, 128, 6.0, 0.6, 0.69);
-  loop(Way::kLoop192, 192, 8.0, 1.0, 1.4);
+  small(Way::kSmall32, 32, 2.5, 1.4, 0.0085);
+  small(Way::kSmall64, 64, 3.0, 3.4, 0.018);
+  loop(Way::kLoop128, 128, 5.0, 0.45, 0.65);
+  loop(Way::kLoop192, 192, 8.0, 1.0, 1.35);
   loop(Way::kLoop256, 256, 10.0, 1.45, 2.3);
   if (symmetric) {
     const int64_t tiles = tiles_of(128);
     const int64_t most = steps / 2 < kMaxParts ? static_cast<int64_t>(steps / 2) : kMaxParts;
-    const int64_t parts = 256 / tiles < most ? 256 / tiles : most;
-    if (parts > 1) offer(Way::kSplit, static_cast<int>(parts), 11.0 + static_cast<double>(ceil_div(K / 32, parts)) * 0.65 + 0.016 * tiles * parts);
+    // a part's sums are written and read, and there is a second launch
+    for (int64_t parts = 2; parts <= most && parts * tiles <= 256; ++parts)
+      offer(Way::kSplit, static_cast<int>(parts), 8.0 + static_cast<double>(ceil_div(K / 32, parts)) * 0.6 + 0.025 * tiles * parts);
   }
   for (int t = 128; cut && !symmetric && t <= 256; t += 64)  // columns that hardly fill their tiles apart from the rest
     if (cols > t && cols % t) {
@@ -541,7 +547,7 @@ hipError_t launch(int batch, const Source& src, int steps, const float* co, floa
       const int t = static_cast<int>(ceil_div(l.m, Loop128::BM)), tiles = t * (t + 1) / 2;
       float* sums = reinterpret_cast<float*>(ws + l.sums);
       hipLaunchKernelGGL((k_partial<Loop128>), dim3(tiles * c.at, batch), dim3(Loop128::threads), 0, stream, a, K, sums, tiles, c.at);
-      hipLaunchKernelGGL((k_finish<Loop128>), dim3(tiles * 2, batch), dim3(Loop128::threads), 0, stream, sums, tiles, c.at, out);
+      hipLaunchKernelGGL((k_finish<Loop128>), dim3(tiles * Loop128::waves, batch), dim3(256), 0, stream, sums, tiles, c.at, out);
       return;
     }
     with_tile(c.way, [&](auto tile) {
