@@ -140,14 +140,19 @@ def _matrix(name, t):
 
 
 def _same_device(first, *others):
+    device = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != device:
             raise ValueError(f"tensors on {first.device} and {t.device}")
 
 
-def _check(status, what):
-    if status != 0:
-        raise _sgemm.SgemmError(status, what(status))
+def current_stream(index: int) -> int:
+    """The handle of torch's current stream of a device (what
+    torch.cuda.current_stream(index).cuda_stream is, in a twelfth of its 1.1 us
+    where torch has the short way)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 def _call(device, function, what, *args):
@@ -158,7 +163,9 @@ def _call(device, function, what, *args):
     if index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _call(device, function, what, *args)
-    _check(function(*args, torch.cuda.current_stream(index).cuda_stream), what)
+    status = function(*args, current_stream(index))
+    if status != 0:
+        raise _sgemm.SgemmError(status, what(status))
 
 
 def _empty(rows, cols, block_rows, scale, device):

@@ -29,7 +29,7 @@ using nt::v4f;
 
 constexpr float kScaleX = 0x1p12f;  // |X| < 16
 constexpr float kScaleS = 0x1p8f;   // |S|, |P| < 255
-constexpr int kNormBlocks = 256;
+constexpr int kNormBlocks = 1024;
 
 __host__ __device__ inline int64_t pad32(int64_t n) { return (n + 31) / 32 * 32; }
 
@@ -87,17 +87,18 @@ struct Source {
 template <class T>
 __global__ __launch_bounds__(256) void k_norm(Source src, double* part, int parts) {
   const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
-  const int groups = static_cast<int>(ceil_div(src.cols, 4));
+  // sixteen neighbours a thread and turn
+  const int groups = static_cast<int>(ceil_div(src.cols, 16));
   const int64_t items = int64_t(src.rows) * groups;
   double sum = 0;
   for (int64_t it = int64_t(blockIdx.x) * 256 + threadIdx.x; it < items; it += int64_t(parts) * 256) {
     const int64_t row = it / groups;
-    const int col = static_cast<int>(it % groups) * 4;
+    const int col = static_cast<int>(it % groups) * 16;
     const T* p = g + row * src.ld + col;
-    if (col + 4 <= src.cols) {
-      const Pack<4, T> v = load_pack<4>(p);
+    if (col + 16 <= src.cols) {
+      const Pack<16, T> v = load_pack<16>(p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 16; ++i) {
         const double x = to_float(v.v[i]);
         sum = fma(x, x, sum);
       }
@@ -120,7 +121,9 @@ __global__ __launch_bounds__(256) void k_norm(Source src, double* part, int part
 
 // |G|_F + eps from the parts; all threads of a 256-thread block call it.
 __device__ __forceinline__ float divisor(const double* part, int parts, float eps, double* s) {
-  s[threadIdx.x] = static_cast<int>(threadIdx.x) < parts ? part[int64_t(blockIdx.y) * kNormBlocks + threadIdx.x] : 0.0;
+  double sum = 0;
+  for (int p = threadIdx.x; p < parts; p += 256) sum += part[int64_t(blockIdx.y) * kNormBlocks + p];
+  s[threadIdx.x] = sum;
   __syncthreads();
   for (int d = 128; d > 0; d /= 2) {
     if (static_cast<int>(threadIdx.x) < d) s[threadIdx.x] += s[threadIdx.x + d];
@@ -522,8 +525,8 @@ hipError_t launch(int batch, const Source& src, int steps, const float* co, floa
                   int64_t batch_x, uint8_t* ws, hipStream_t stream) {
   const Layout l = layout_of(batch, src.rows, src.cols);
   double* part = reinterpret_cast<double*>(ws + l.part);
-  const int64_t groups = int64_t(src.rows) * ceil_div(src.cols, 4);
-  const int parts = static_cast<int>(ceil_div(groups, 1024) < kNormBlocks ? ceil_div(groups, 1024) : kNormBlocks);
+  const int64_t groups = int64_t(src.rows) * ceil_div(src.cols, 16);
+  const int parts = static_cast<int>(ceil_div(groups, 256) < kNormBlocks ? ceil_div(groups, 256) : kNormBlocks);
   hipLaunchKernelGGL((k_norm<T>), dim3(parts, batch), dim3(256), 0, stream, src, part, parts);
   if (steps == 0) {
     const int64_t blocks = ceil_div(int64_t(src.rows) * src.cols, 256);

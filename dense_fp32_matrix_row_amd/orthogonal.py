@@ -13,6 +13,7 @@ import ctypes
 from typing import Optional, Sequence
 
 from . import sgemm as _sgemm
+from .blockfp8 import current_stream
 
 EXPORTS = ("hip_orthogonalize", "hip_orthogonalize_workspace", "hip_orthogonalize_status_string")
 
@@ -126,5 +127,5 @@ def orthogonalize(g, steps: int = 5, coefficients: Optional[Sequence] = None, ep
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous and on g's device")
     _check(hip_orthogonalize(batch, rows, cols, kind, g, ldg, stride_g, steps, flat, eps, out, ldx, stride_x, workspace,
-                             workspace.numel() * workspace.element_size(), torch.cuda.current_stream().cuda_stream))
+                             workspace.numel() * workspace.element_size(), current_stream(device.index)))
     return out
