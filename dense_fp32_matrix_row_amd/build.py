@@ -37,7 +37,9 @@ def hipcc() -> str:
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+    """csrc/ and, for the low-precision operators, csrc/lowp/ (apart, so that what is
+    recorded of the SGEMM's kernels by a digest of their sources stays theirs)."""
+    return sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + sorted(glob.glob(os.path.join(CSRC, "lowp", "*.hip")))
 
 
 # The assembly K loops of l10_kloop.hip are two asm statements per kernel: a

@@ -1,6 +1,6 @@
 // fp8_gemm.hip -- hip_fp8_gemm: D = alpha A B^T + beta C over e4m3 operands with
 // a scale for each block of 128 along K.
-#include "../../include/blockfp8.h"
+#include "../../../include/blockfp8.h"
 #include "lowp.h"
 #include "nt_direct.h"
 #include "nt_loop.h"

@@ -4,7 +4,7 @@
 //
 // Bound by memory: e bytes read and one written per element and orientation,
 // against some fifteen vector instructions per element and orientation.
-#include "../../include/blockfp8.h"
+#include "../../../include/blockfp8.h"
 #include "lowp.h"
 
 namespace sgemm {

@@ -5,7 +5,7 @@
 #include <hip/hip_bf16.h>
 #include <hip/hip_fp16.h>
 
-#include "sgemm_internal.h"
+#include "../sgemm_internal.h"
 
 namespace sgemm {
 

@@ -15,7 +15,7 @@
 // neighbours in a row of D, stored at once.
 #pragma once
 
-#include "sgemm_internal.h"
+#include "../sgemm_internal.h"
 
 namespace sgemm {
 namespace nt {

@@ -16,7 +16,7 @@
 //   X' = P X                (m x n, K = m; X^T is the other operand), written
 //                           as X' over X, which is not read, and as X'^T into
 //                           the other of two buffers.
-#include "../../include/orthogonal.h"
+#include "../../../include/orthogonal.h"
 #include "lowp.h"
 #include "nt_direct.h"
 #include "nt_loop.h"

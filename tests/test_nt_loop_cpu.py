@@ -1,5 +1,6 @@
 """The large tiles' assembly loops without a GPU: the committed text is what the
-generator writes, and every LDS read of it is waited for before its use."""
+generator writes; replayed, every step's loads go to its stage and have arrived
+at its barrier, and no register that an LDS read is on its way to is touched."""
 
 import os
 import re
@@ -8,7 +9,7 @@ import sys
 import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-CSRC = os.path.join(ROOT, "dense_fp32_matrix_row_amd", "csrc")
+CSRC = os.path.join(ROOT, "dense_fp32_matrix_row_amd", "csrc", "lowp")
 sys.path.insert(0, CSRC)
 import gen_nt_loop  # noqa: E402
 
