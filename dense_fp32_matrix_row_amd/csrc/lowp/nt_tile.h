@@ -121,7 +121,7 @@ struct Fp8F32 {
       for (int i = 0; i < 4; ++i) acc[i] = fmaf(t[i], s, acc[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(t[i], sm * sn[i], acc[i]);
+      for (int i = 0; i < 4; ++i) acc[i] = fmaf(t[i] * sm, sn[i], acc[i]);  // as the large tiles' loops do
     }
   }
   static __device__ __forceinline__ v4f value(const Acc& a) { return a; }

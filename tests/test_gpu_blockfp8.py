@@ -76,6 +76,32 @@ def test_quantize_borders_between_codes(scale):
         same(got.s, s)
 
 
+@pytest.mark.parametrize("kind", ("bf16", "f16"))
+def test_quantize_every_quotient_of_16_bit_mantissas(kind):
+    """With 16-bit elements 448 x / a is exactly a border again and again: every mantissa of bf16 (a
+    sample of f16's) over every largest one, at sizes down to the subnormal codes."""
+    kind = TYPES[kind]
+    bits = 7 if kind == torch.bfloat16 else 10
+    m = torch.arange(2 ** bits) if bits == 7 else torch.arange(0, 2 ** bits, 7)
+    tops = (1 + m / 2.0 ** bits).repeat_interleave(3) * 4.0
+    rows = []
+    for shift in (0, 1, 3, 9, 11, 13, 15, 17):
+        x = torch.zeros(len(tops), 128)
+        x[:, 0] = tops
+        pick = torch.arange(len(m)).view(-1)[:126] if bits == 7 else torch.arange(len(m))
+        for part in range(3):
+            chosen = (1 + m[(pick + part * 53) % len(m)][:127] / 2.0 ** bits) * 2.0 ** (1 - shift)
+            x[part::3, 1:1 + len(chosen)] = chosen * (1 - 2 * (part % 2))
+        rows.append(x)
+    x = torch.cat(rows).to(kind)
+    for block_rows in (1,):
+        q, s = ref.quantize(x, block_rows, False)
+        n, t = blockfp8.quantize(x.cuda(), block_rows), blockfp8.quantize_transposed(x.T.contiguous().cuda(), block_rows)
+        for got in (n, t):
+            same(got.q, q)
+            same(got.s, s)
+
+
 @pytest.mark.parametrize("scale", SCALES)
 @pytest.mark.parametrize("block_rows", (1, 128))
 def test_quantize_infinities_and_nans_stay_visible(block_rows, scale):
@@ -200,6 +226,119 @@ def test_gemm_large_tiles(K, kind, b_block, scale):
     close(blockfp8.gemm(a, b, out_dtype=TYPES[kind]), want, tol)
     want = 0.5 * want - c.double()
     close(blockfp8.gemm(a, b, c=c.cuda(), alpha=0.5, beta=-1.0), want, tolerance(da, db, K, scale, TYPES[kind], want, c.double(), 0.5))
+
+
+def sampled(rows, seed):
+    """Rows at both ends, beside multiples of the tiles' sizes, and some between."""
+    g = torch.Generator().manual_seed(seed)
+    at = {0, 1, 127, 128, 255, 256, rows - 257, rows - 2, rows - 1, *torch.randint(0, rows, (40,), generator=g).tolist()}
+    return torch.tensor(sorted(r for r in at if 0 <= r < rows))
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("b_block", (1, 128))
+@pytest.mark.parametrize("kind", ("bf16", "f32"))
+@pytest.mark.parametrize("M,N,K", [(4090, 4090, 400), (4090, 3900, 513), (4097, 4097, 1290), (4097, 2048, 1000), (2048, 4097, 900),
+                                   (4100, 4200, 1600)])
+def test_gemm_largest_tiles_and_ragged_edges_apart(M, N, K, kind, b_block, scale):
+    """Sizes whose last rows and columns are computed apart, and the largest tiles: rows and columns of D by sample."""
+    a, da = operand(M, K, 1, scale, 16)
+    b, db = operand(N, K, b_block, scale, 17)
+    c = values(M, N, TYPES[kind], 18)
+    got = blockfp8.gemm(a, b, c=c.cuda(), alpha=1.0, beta=0.5).cpu()
+    r, n = sampled(M, 1), sampled(N, 2)
+    for left, right, part, ci in ((da[r], db, got[r], c[r]), (da, db[n], got[:, n], c[:, n])):
+        want = left @ right.T + 0.5 * ci.double()
+        close(part, want, tolerance(left, right, K, scale, TYPES[kind], want, 0.5 * ci.double()))
+    assert torch.equal(got, blockfp8.gemm(a, b, c=c.cuda(), alpha=1.0, beta=0.5).cpu())  # the same again
+
+
+@pytest.mark.parametrize("kind", ("bf16", "f32"))
+@pytest.mark.parametrize("scale", SCALES)
+def test_gemm_large_tiles_scales_of_any_layout_and_kind(scale, kind):
+    """Row-major scales with padding, and the ends of the scales' ranges, against the small tiles'
+    results for the same rows (whole numbers under powers of two: all sums are exact)."""
+    M, N, K = 2300, 2100, 700
+    g = torch.Generator().manual_seed(19)
+    ops = []
+    for rows in (M, N):
+        q = torch.randint(-4, 5, (rows, 704), generator=g).float()
+        q[:, K:] = float("nan")
+        s = torch.exp2(torch.randint(-3, 4, (rows, 9), generator=g).float())
+        if rows == M:
+            s[5], s[7, 2], s[11] = 2.0 ** -127, float("nan"), 2.0 ** 100
+        else:
+            s[6] = 2.0 ** 126
+        raw = s.to(SCALES[scale]).view(torch.uint8).cuda() if scale == "e8m0" else s.cuda()
+        raw = raw.view(SCALES[scale]) if scale == "e8m0" else raw
+        ops.append(blockfp8.BlockFp8(q.to(torch.float8_e4m3fn).cuda()[:, :K], raw[:, :6], 1))
+    got = blockfp8.gemm(*ops, out_dtype=TYPES[kind])
+    part = [blockfp8.BlockFp8(o.q[:40], o.s[:40], 1) for o in ops]
+    few = blockfp8.gemm(*part, out_dtype=TYPES[kind])
+    # Column 6 passes float's range, but for row 5: an infinity or, where two parts of a sum overflow with
+    # opposite signs, a NaN, as the sum's order has it.
+    past = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    past[:, 6] = True
+    past[5, 6] = past[7, 6] = False
+    shown = got.masked_fill(past, 0)
+    assert torch.equal(torch.nan_to_num(shown[:40, :40], nan=-7.0),
+                       torch.nan_to_num(few.masked_fill(past[:40, :40], 0), nan=-7.0))
+    assert torch.isnan(got[7]).all() and not torch.isnan(shown[:7]).any()
+    want = (ops[0].q[:5].cpu().double() * ops[0].s[:5].cpu().double().repeat_interleave(128, 1)[:, :K]) @ (
+        ops[1].q.cpu().double() * ops[1].s.cpu().double().repeat_interleave(128, 1)[:, :K]).T
+    exact = torch.arange(N) != 6
+    assert torch.equal(got[:5].cpu()[:, exact], want[:, exact].to(TYPES[kind]))
+
+
+@pytest.mark.parametrize("M", (3, 600))
+def test_gemm_operands_past_two_gigabytes(M):
+    """A's offsets pass 2^31 bytes; the last rows are checked."""
+    K, rows = 65600, 33000
+    g = torch.Generator(device="cuda").manual_seed(20)
+    q = torch.randint(0, 0x78, (rows, K), generator=g, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+    s = torch.rand(-(-K // 128), rows, generator=g, device="cuda").T + 0.5
+    a = blockfp8.BlockFp8(q, s, 1)
+    b = blockfp8.BlockFp8(q[:M], s[:M], 1)
+    got = blockfp8.gemm(a, b, out_dtype=torch.float32)
+    at = torch.tensor([0, 16384, 32760, rows - 1])
+    da = a.q[at.cuda()].cpu().double() * a.s[at.cuda()].cpu().double().repeat_interleave(128, 1)[:, :K]
+    db = b.q.cpu().double() * b.s.cpu().double().repeat_interleave(128, 1)[:, :K]
+    want = da @ db.T
+    close(got[at.cuda()], want, tolerance(da, db, K, "f32", torch.float32, want))
+
+
+def test_quantize_past_two_gigabytes():
+    rows, cols = 33000, 65600
+    g = torch.Generator(device="cuda").manual_seed(21)
+    x = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16)
+    n, t = blockfp8.quantize_both(x)
+    for r0 in (0, 32768, rows - 232):  # whole blocks of 128 rows, and the last ones
+        part = x[r0 // 128 * 128:][:256, cols - 200:].cpu()
+        q, s = ref.quantize(x[r0 // 128 * 128:][:256, cols // 128 * 128 - 128:].cpu(), 1, False)
+        same(n.q[r0 // 128 * 128:][:256, cols // 128 * 128 - 128:], q)
+        q, s = ref.quantize(part.T, 1, False)
+        same(t.q[cols - 200:, r0 // 128 * 128:][:, :256], q)
+
+
+def test_products_of_every_size_in_a_captured_graph():
+    """One launch, several, and both in turn."""
+    sizes = [(1, 300, 500), (200, 140, 512), (700, 900, 300), (2100, 2100, 300), (4097, 2048, 1000)]
+    for M, N, K in sizes:
+        a = blockfp8.quantize(torch.randn(M, K, device="cuda"))
+        x = torch.randn(N, K, device="cuda")
+        run = lambda: blockfp8.gemm(a, blockfp8.quantize(x, 128), out_dtype=torch.float32)  # noqa: E731
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = run()
+        for i in range(3):
+            x.copy_(torch.randn(N, K, device="cuda") * (i + 1))
+            graph.replay()
+            torch.cuda.synchronize()
+            want = run()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want), (M, N, K)
 
 
 @pytest.mark.parametrize("scale", SCALES)

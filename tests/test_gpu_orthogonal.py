@@ -50,7 +50,7 @@ def test_against_the_definition(shape, kind):
     assert far(got, ref.orthogonalize(g, co, 1e-7)) <= tolerance(co, TYPES[kind])
 
 
-@pytest.mark.parametrize("shape", [(1100, 1300), (1500, 1021), (2, 900, 1500), (2100, 2200), (2800, 2750)])
+@pytest.mark.parametrize("shape", [(1100, 1300), (1500, 1021), (2, 900, 1500), (2100, 2200), (2800, 2750), (640, 4000), (1024, 2049), (3, 50, 1100)])
 def test_large_tiles(shape):
     """Enough for each of the large tiles, ragged on both sides."""
     g = matrix(shape, torch.float32, seed=3)
@@ -133,6 +133,23 @@ def test_refusals_and_empty():
         orthogonal.orthogonalize(g, eps=-1.0)
     assert orthogonal.orthogonalize(torch.empty(0, 6, device="cuda")).shape == (0, 6)
     assert (orthogonal.orthogonalize(torch.zeros(5, 6, device="cuda")) == 0).all()
+
+
+def test_large_sizes_in_a_captured_graph():
+    """The symmetric products in parts, and the last columns apart."""
+    g = torch.randn(1024, 1153, device="cuda")
+    orthogonal.orthogonalize(g, steps=2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = orthogonal.orthogonalize(g, steps=2)
+    for i in range(3):
+        g.copy_(torch.randn(1024, 1153, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = orthogonal.orthogonalize(g, steps=2)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
 
 
 def test_other_streams_and_captured_graphs():
