@@ -91,16 +91,18 @@ class BlockFp8:
 
 _TYPES = None    # of matrices that are not quantised
 _SCALES = None
+_CODES = None    # of quantised ones
 
 
 def _tables():
-    """The type codes by torch's dtypes (torch is imported on first use)."""
-    global _TYPES, _SCALES
+    """The type codes by torch's dtypes, and the dtypes of codes (torch is imported on first use)."""
+    global _TYPES, _SCALES, _CODES
     if _TYPES is None:
         import torch
         _SCALES = {torch.float32: SCALE_F32, torch.float8_e8m0fnu: SCALE_E8M0}
+        _CODES = (torch.float8_e4m3fn, torch.uint8)
         _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
-    return _TYPES, _SCALES
+    return _TYPES, _SCALES, _CODES
 
 
 def _types():
@@ -222,8 +224,8 @@ def _operand(name, o):
     """(rows, K, the C function's arguments) of a quantised matrix."""
     q, s, block_rows = o.q, o.s, o.block_rows
     rows, K, ld = _matrix(name, q)
-    if q.element_size() != 1:
-        raise TypeError(f"{name}'s codes are one byte each, not {q.dtype}")
+    if q.dtype not in _tables()[2]:
+        raise TypeError(f"{name}'s codes are float8_e4m3fn (or its bytes as uint8), not {q.dtype}")
     if rows <= 1 or K == 0:
         ld = max(_ceil(ld, 16) * 16, 16)
     if block_rows not in (1, BLOCK):

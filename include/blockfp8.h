@@ -76,8 +76,8 @@ int hip_fp8_quantize(int rows, int cols, const void *X, int x_type, int ldx,
  * products of eight neighbours along k 13 bits below the largest of them (an
  * error of 1.5e-5 on normal data, 2^-10 of the sum of magnitudes at most); a
  * float D is summed at half that rate with a float's bits throughout.
- * Where a partial sum or a block's s_A s_B passes float's range, D_ij is an infinity or a NaN as the
- * order of the sum, which depends on the sizes, has it.
+ * Where a partial sum or a block's s_A s_B passes float's range, D_ij is an
+ * infinity or a NaN as the order of the sum, which depends on the sizes, has it.
  *   lda, ldb: multiples of 16 bytes, at most HIP_FP8_MAX_LD; A and B 16-byte
  *   aligned; a row is read up to the next multiple of 16 bytes (what lies
  *   past K has no influence).

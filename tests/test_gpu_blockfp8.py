@@ -491,3 +491,14 @@ def test_other_streams_and_captured_graphs():
         want = blockfp8.gemm(blockfp8.quantize(x), blockfp8.quantize(w, 128), out_dtype=torch.float32)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", (torch.float8_e5m2, torch.float8_e4m3fnuz, torch.int8))
+def test_codes_of_another_type_are_refused(dtype):
+    a = blockfp8.quantize(torch.ones(4, 128, device="cuda"))
+    other = blockfp8.BlockFp8(a.q.view(dtype), a.s, 1)
+    for pair in ((a, other), (other, a)):
+        with pytest.raises(TypeError, match="codes"):
+            blockfp8.gemm(*pair)
+    same = blockfp8.BlockFp8(a.q.view(torch.uint8), a.s, 1)
+    assert torch.equal(blockfp8.gemm(same, same), blockfp8.gemm(a, a))
