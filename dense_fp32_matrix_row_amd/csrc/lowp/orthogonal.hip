@@ -5,9 +5,10 @@
 // RN(s x - hi) for a fixed power of two s: 22 significant bits while |s x| is
 // between 2^-3 and 65504, an absolute 2^-25 below (a half's least step is
 // 2^-24).  That is 2^-37 of |X_0|_F = 1, whose elements are 2^-12 in the mean for
-// 4096 x 4096.  The sums are float.  Three half products an element (hi hi', hi lo', lo hi') run at a
-// third of the half rate, five times the float matrix rate, and err no more
-// than float products do.
+// 4096 x 4096.  The sums are float.  Three half products an element (hi hi',
+// hi lo', lo hi') run at a third of the half rate, three times the float matrix
+// rate (4096 x 4096: 443 TFLOP/s of the products asked for, against 150), and
+// err no more than float products do.
 //
 // Per step, with m <= n the sides of the iterate X and X^T kept beside it, all
 // operands have their K side contiguous:
@@ -82,8 +83,17 @@ struct Source {
   int rows, cols;
 };
 
+// The sum of v over a block of 256 threads, in a fixed order; s is not in use.
+__device__ __forceinline__ double block_sum(double v, double (&s)[4]) {
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
+  if (threadIdx.x % 64 == 0) s[threadIdx.x / 64] = v;
+  __syncthreads();
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
 // The sum of squares of a matrix, in doubles: every block a part, in a fixed
-// order (no atomics).
+// order (no atomics).  Bound by memory: 4096 x 4096 floats in 13.8 us, 4.9 TB/s.
 template <class T>
 __global__ __launch_bounds__(256) void k_norm(Source src, double* part, int parts) {
   const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
@@ -109,46 +119,39 @@ __global__ __launch_bounds__(256) void k_norm(Source src, double* part, int part
       }
     }
   }
-  __shared__ double s[256];
-  s[threadIdx.x] = sum;
-  __syncthreads();
-  for (int d = 128; d > 0; d /= 2) {
-    if (static_cast<int>(threadIdx.x) < d) s[threadIdx.x] += s[threadIdx.x + d];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) part[int64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = s[0];
+  __shared__ double s[4];
+  sum = block_sum(sum, s);
+  if (threadIdx.x == 0) part[int64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = sum;
 }
 
 // |G|_F + eps from the parts; all threads of a 256-thread block call it.
-__device__ __forceinline__ float divisor(const double* part, int parts, float eps, double* s) {
+__device__ __forceinline__ float divisor(const double* part, int parts, float eps, double (&s)[4]) {
   double sum = 0;
   for (int p = threadIdx.x; p < parts; p += 256) sum += part[int64_t(blockIdx.y) * kNormBlocks + p];
-  s[threadIdx.x] = sum;
-  __syncthreads();
-  for (int d = 128; d > 0; d /= 2) {
-    if (static_cast<int>(threadIdx.x) < d) s[threadIdx.x] += s[threadIdx.x + d];
-    __syncthreads();
-  }
-  return static_cast<float>(sqrt(s[0])) + eps;
+  return static_cast<float>(sqrt(block_sum(sum, s))) + eps;
 }
 
 // X_0 as pairs, as G lies (`direct`: rows of G) and transposed (`across`), a
-// 64 x 64 tile a block through LDS; both padded with zeros.
+// 64 x 64 tile a block through LDS; both padded with zeros.  Bound by memory:
+// 4096 x 4096 floats, 192 MiB, in 38.5 us (5.2 TB/s; 44.9 with the loads behind
+// the norm), 256 x 256 in 4.8 us (7.0).
 template <class T>
 __global__ __launch_bounds__(256) void k_start(Source src, const double* part, int parts, float eps, Pairs direct,
                                                Pairs across, int tiles_c) {
-  __shared__ double s[256];
+  __shared__ double s[4];
   __shared__ float t[64][65];
-  const float div = divisor(part, parts, eps, s);
   const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
   const int r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
+  T x[16];  // under way while the norm's parts are added
 #pragma unroll
   for (int p = 0; p < 16; ++p) {
     const int r = p * 4 + threadIdx.x / 64, c = threadIdx.x % 64;
-    float v = 0.0f;
-    if (r0 + r < src.rows && c0 + c < src.cols) v = to_float(g[(r0 + r) * src.ld + c0 + c]) / div;
-    t[r][c] = v * kScaleX;
+    x[p] = T{};
+    if (r0 + r < src.rows && c0 + c < src.cols) x[p] = g[(r0 + r) * src.ld + c0 + c];
   }
+  const float div = divisor(part, parts, eps, s);
+#pragma unroll
+  for (int p = 0; p < 16; ++p) t[p * 4 + threadIdx.x / 64][threadIdx.x % 64] = to_float(x[p]) / div * kScaleX;
   __syncthreads();
   uint8_t* dp = direct.p + blockIdx.y * direct.batch;
   uint8_t* ap = across.p + blockIdx.y * across.batch;
@@ -167,7 +170,7 @@ __global__ __launch_bounds__(256) void k_start(Source src, const double* part, i
 template <class T>
 __global__ __launch_bounds__(256) void k_divide(Source src, const double* part, int parts, float eps, T* x,
                                                 int64_t ldx, int64_t batch_x) {
-  __shared__ double s[256];
+  __shared__ double s[4];
   const float div = divisor(part, parts, eps, s);
   const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
   const int64_t items = int64_t(src.rows) * src.cols;
@@ -349,6 +352,10 @@ __device__ __forceinline__ void product(const Side& A, const Side& B, int m0, in
   }
 }
 
+// S = X X^T and P = a + b S + c S S: the lower tiles, mirrored.  Bound by the
+// matrix rate where the tiles fill the CUs: 4096 x 4096 in 165-175 us on 253 tiles
+// of 192 x 192 (136 of 256 x 256 would leave half the CUs idle), MfmaUtil 65 %; by
+// the latency of one trip to memory where they are few: 256 x 256 in 4.4 us.
 template <class T>
 __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_symmetric(Side A, int K, SymmetricOut out) {
   out.batch = blockIdx.y;
@@ -358,6 +365,10 @@ __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_symmetric(Side A, 
   product<T>(A, A, at.tm * T::BM, at.tn * T::BN, K, out);
 }
 
+// X' = P X.  Bound by the matrix rate: 4096 x 4096 in 278 us on 256 tiles of
+// 256 x 256, 1483 TFLOP/s of half products, MfmaUtil 75 %; 1024 x 1024 x 4096 in
+// 29 us on 256 tiles of 128 x 128, whose 32 steps hardly outlast the first loads
+// and the results' way out.
 template <class T, class O>
 __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_iterate(Side A, Side B, int K, IterateOut<O> out,
                                                                       int col0, int tiles_m, int tiles_n) {
@@ -369,7 +380,9 @@ __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_iterate(Side A, Si
 }
 
 // One of `splits` parts of the K of a symmetric product's tiles: the sums as the
-// wavefronts hold them, 16 bytes a lane side by side.
+// wavefronts hold them, 16 bytes a lane side by side.  For where the tiles are
+// far fewer than the CUs: S of 1024 x 4097 in 17.2 us on 36 tiles by 7 parts, with
+// 5.6 us for the parts' sum, against about 80 us on 36 blocks.
 template <class T>
 __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_partial(Side A, int K, float* sums, int tiles, int splits) {
   __shared__ alignas(16) uint8_t smem[T::kLds];
