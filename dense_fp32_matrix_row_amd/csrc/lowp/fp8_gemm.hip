@@ -73,9 +73,10 @@ struct Out {
 // Large tiles.  On one MI355X, kernels alone: 4096^3 with float scales 58-60 us
 // (2300 TFLOP/s; each product's vector instructions of scaling take issue slots
 // beside the matrix instruction), 8192^3 with power-of-two scales, which need none,
-// 377-470 us from box to box (2340-2900 TFLOP/s; MfmaUtil 77 %, the clock is down to about
-// 1.75 GHz: power), 4096^3 with a float result 155-164 us (830 TFLOP/s; 276 vector
-// instructions a wavefront and step widen and scale beside 64 matrix ones).
+// 377-470 us from box to box (2340-2900 TFLOP/s; MfmaUtil 77 %, the clock is down to
+// about 1.75 GHz: power), 4096^3 with a float result 130 us (1056 TFLOP/s; 276 vector
+// instructions a wavefront and step widen and scale beside 64 matrix ones, and more
+// than two a matrix instruction take its time: four make 7.5 ns 11.8).
 template <class L, class O>
 __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, Out<O> out, int tiles_m, int tiles_n) {
   __shared__ alignas(16) uint8_t smem[L::kLds];
@@ -164,15 +165,20 @@ Choice choose(int M, int N, int K, bool wide, bool loops, int cuts) {
   offer(Way::kSmall32, 0, small(32, 2.3, 1.3, wide ? 0.007 : 0.0056));
   offer(Way::kSmall64, 0, wide ? small(64, 2.0, 4.5, 0.024) : small(64, 3.0, 2.2, 0.0135));
   if (!loops) return best;
-  offer(Way::kLoop128, 0, wide ? loop(128, 7.0, 1.45, 2.0) : loop(128, 6.0, 0.65, 0.98));
-  if (!wide) offer(Way::kLoop256, 0, loop(256, 7.0, 1.0, 1.6));
+  if (wide) {  // two blocks a CU: with one each, a step takes little more than half the time
+    const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128), rest = tiles % 512;
+    offer(Way::kLoop128, 0, 5.0 + steps * (tiles / 512 * 1.92 + (rest == 0 ? 0 : rest <= 256 ? 1.09 : 1.92)));
+  } else {
+    offer(Way::kLoop128, 0, loop(128, 6.0, 0.65, 0.98));
+    offer(Way::kLoop256, 0, loop(256, 7.0, 1.0, 1.6));
+  }
   // rows or columns that hardly fill their tiles apart from the rest
   for (int t = 128; cuts > 0 && t <= 256; t *= 2) {
     if (N > t && N % t) {
       const int at = N - N % t;
       offer(Way::kColumns, at, choose(M, at, K, wide, loops, cuts - 1).us + choose(M, N - at, K, wide, loops, 0).us);
     }
-    if (t == 256 && M > t && M % t) {
+    if ((wide || t == 256) && M > t && M % t) {
       const int at = M - M % t;
       offer(Way::kRows, at, choose(at, N, K, wide, loops, cuts - 1).us + choose(M - at, N, K, wide, loops, 0).us);
     }
@@ -189,8 +195,14 @@ Side from_row(Side o, int row, int scale_bytes) {  // row: a multiple of 128
 
 template <class P, nt::Kind KIND, class O>
 void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s, int cuts = 2) {
-  using Loop128 = nt::Loop<KIND, 4, 4, 4, 2, 3>;
   constexpr bool wide = sizeof(O) == 4;
+  // 256 x 128 of eight wavefronts; for float results 128 x 128 of four, two blocks a
+  // CU, so that one widens while the other multiplies and results leave meanwhile:
+  // as fast as 256 x 128 where there are many (4096^3 127 and 130 us, 8000 x 8000 x
+  // 1000 167 and 156), and fewer are needed (2048 x 2048 x 4096 55 and 39, 1500 x
+  // 1500 x 4096 84 and 41).  With 8-bit instructions the loads to LDS, a third more
+  // a product, would bound it.
+  using Loop128 = nt::Loop<KIND, 4, 4, wide ? 2 : 4, 2, wide ? 2 : 3>;
   const Choice c = choose(out.M, out.N, K, wide, K > 0 && Loop128::fits(A) && Loop128::fits(B), cuts);
   switch (c.way) {
     case Way::kSmall16: return launch_direct<nt::Direct<P, 1, 1, 8>>(A, B, K, out, s);

@@ -602,7 +602,7 @@ class Loop:
 LOOPS = [
     ("e8m0", 8, 4, 2, 4, 2), ("f32u", 8, 4, 2, 4, 2), ("f32n", 8, 4, 2, 4, 2),
     ("e8m0", 4, 4, 4, 2, 3), ("f32u", 4, 4, 4, 2, 3), ("f32n", 4, 4, 4, 2, 3),
-    ("w32u", 4, 4, 4, 2, 3), ("w32n", 4, 4, 4, 2, 3), ("w8u", 4, 4, 4, 2, 3), ("w8n", 4, 4, 4, 2, 3),
+    ("w32u", 4, 4, 2, 2, 2), ("w32n", 4, 4, 2, 2, 2), ("w8u", 4, 4, 2, 2, 2), ("w8n", 4, 4, 2, 2, 2),
     ("pair", 8, 4, 2, 4, 2), ("pair", 6, 6, 2, 2, 3), ("pair", 4, 2, 2, 4, 4),
 ]
 

@@ -135,10 +135,10 @@ __device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Sid
     if constexpr (L::KIND == Kind::kE8M0) { NT_LOOP_BOTH(e8m0); }
     else if constexpr (L::KIND == Kind::kF32Uniform) { NT_LOOP_BOTH(f32u); }
     else if constexpr (L::KIND == Kind::kF32Rows) { NT_LOOP_BOTH(f32n); }
-    else if constexpr (L::KIND == Kind::kWideF32Uniform) NT_LOOP_RUN(w32u_256x128, NT_SUMS_4, NT_SCALES_OUT, NT_DIRECT_IN);
-    else if constexpr (L::KIND == Kind::kWideF32Rows) NT_LOOP_RUN(w32n_256x128, NT_SUMS_4, NT_SCALES_OUT, NT_DIRECT_IN);
-    else if constexpr (L::KIND == Kind::kWideE8M0Uniform) NT_LOOP_RUN(w8u_256x128, NT_SUMS_4, NT_BYTES_OUT, NT_BYTES_IN);
-    else NT_LOOP_RUN(w8n_256x128, NT_SUMS_4, NT_BYTES_OUT, NT_BYTES_IN);
+    else if constexpr (L::KIND == Kind::kWideF32Uniform) NT_LOOP_RUN(w32u_128x128, NT_SUMS_4, NT_SCALES_OUT, NT_DIRECT_IN);
+    else if constexpr (L::KIND == Kind::kWideF32Rows) NT_LOOP_RUN(w32n_128x128, NT_SUMS_4, NT_SCALES_OUT, NT_DIRECT_IN);
+    else if constexpr (L::KIND == Kind::kWideE8M0Uniform) NT_LOOP_RUN(w8u_128x128, NT_SUMS_4, NT_BYTES_OUT, NT_BYTES_IN);
+    else NT_LOOP_RUN(w8n_128x128, NT_SUMS_4, NT_BYTES_OUT, NT_BYTES_IN);
   } else if constexpr (L::BM == 256) {
     NT_LOOP_RUN(pair_256x256, NT_SUMS_8, NT_NONE, NT_NONE);
   } else if constexpr (L::BM == 192) {
