@@ -18,36 +18,43 @@ struct Out {
   int64_t ldd, ldc;
   int M, N;
   float alpha, beta;
-  // COUNT neighbours of row m from column n, those inside D; WHOLE: all are.
+  // C's COUNT neighbours of row m from column n, those inside; WHOLE: all are.
+  template <bool WHOLE, int COUNT>
+  __device__ __forceinline__ Pack<COUNT, O> old(int m, int n) const {
+    Pack<COUNT, O> o{};
+    if (!WHOLE && (m >= M || n >= N)) return o;
+    const O* const from = c + m * ldc + n;
+    if (WHOLE || n + COUNT <= N) return load_pack<COUNT>(from);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+      if (n + i < N) o.v[i] = from[i];
+    return o;
+  }
+  // D's, of their sums and of C's where ADD.
   template <bool WHOLE, bool ADD, int COUNT>
-  __device__ __forceinline__ void row(int m, int n, const float (&v)[COUNT]) const {
+  __device__ __forceinline__ void put(int m, int n, const float (&v)[COUNT], const Pack<COUNT, O>& o) const {
     if (!WHOLE && (m >= M || n >= N)) return;
     O* const to = d + m * ldd + n;
-    const O* const from = c + m * ldc + n;
-    const bool whole = WHOLE || n + COUNT <= N;
-    Pack<COUNT, O> r, o{};
-    if (ADD) {
-      if (whole) {
-        o = load_pack<COUNT>(from);
-      } else {
-#pragma unroll
-        for (int i = 0; i < COUNT; ++i)
-          if (n + i < N) o.v[i] = from[i];
-      }
-    }
+    Pack<COUNT, O> r;
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
       float x = alpha * v[i];
       if (ADD) x = fmaf(beta, to_float(o.v[i]), x);
       from_float(x, r.v[i]);
     }
-    if (whole) {
+    if (WHOLE || n + COUNT <= N) {
       store_pack(to, r);
     } else {
 #pragma unroll
       for (int i = 0; i < COUNT; ++i)
         if (n + i < N) to[i] = r.v[i];
     }
+  }
+  template <bool WHOLE, bool ADD, int COUNT>
+  __device__ __forceinline__ void row(int m, int n, const float (&v)[COUNT]) const {
+    Pack<COUNT, O> o{};
+    if (ADD) o = old<WHOLE, COUNT>(m, n);
+    put<WHOLE, ADD>(m, n, v, o);
   }
   __device__ __forceinline__ void operator()(int m, int n, v4f v) const {
     const float x[4] = {v[0], v[1], v[2], v[3]};
@@ -86,9 +93,16 @@ __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, O
   nt::loop_sum<L>(smem, A, B, m0, n0, K, acc);
   if constexpr (sizeof(O) == 4) {  // four neighbours are 16 bytes, four lanes 64
     out.tile(m0, n0, L::BM, L::BN, [&](auto whole, auto add) {
+      // all of C first: it may be D, so a load would wait for the stores before it
+      // (8000 x 8000 x 1000 223 -> 200 us)
+      Pack<4, O> old[L::MT * L::NT];
+      int at = 0;
+      if (add.value)
+        nt::loop_out<L>(acc, m0, n0, [&](int m, int n, v4f) { old[at++] = out.template old<whole.value, 4>(m, n); });
+      at = 0;
       nt::loop_out<L>(acc, m0, n0, [&](int m, int n, v4f v) {
         const float x[4] = {v[0], v[1], v[2], v[3]};
-        out.template row<whole.value, add.value>(m, n, x);
+        out.template put<whole.value, add.value>(m, n, x, old[at++]);
       });
     });
   } else {  // by way of LDS, so that 16-byte stores fill whole lines: 61 -> 60 us at 4096^3
@@ -113,26 +127,42 @@ void launch_loop(const Side& A, const Side& B, int K, const Out<O>& out, hipStre
                      static_cast<int>(tm), static_cast<int>(tn));
 }
 
+// The tiles from column n0, all rows; then those from row m0 left of it.
+struct Part {
+  int tiles_m, n0;
+  int64_t tiles;
+  int low_m, m0;
+};
+
 // Small tiles.  Bound by a launch and one trip to memory, or the weight's read:
 // 1 x 4096 x 4096 in 4.9 us (3.4 TB/s; 16 x 16 tiles, 256 blocks), 256 x 1024 x
 // 1024 in 4.9 us (32 x 32, 256 blocks).
 template <class D, class O>
-__global__ __launch_bounds__(D::threads, 2) void k_direct(Side A, Side B, int K, Out<O> out, int tiles_m, int64_t tiles) {
+__global__ __launch_bounds__(D::threads, 2) void k_direct(Side A, Side B, int K, Out<O> out, Part part, int64_t tiles) {
   __shared__ typename D::Meet meet;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t id = xcd_contiguous(t, tiles);
-    const int m0 = static_cast<int>(id % tiles_m) * D::BM, n0 = static_cast<int>(id / tiles_m) * D::BN;
+    const int64_t id = xcd_contiguous(t, tiles), low = id - part.tiles;
+    const int m0 = low < 0 ? static_cast<int>(id % part.tiles_m) * D::BM : part.m0 + static_cast<int>(low % part.low_m) * D::BM;
+    const int n0 = low < 0 ? part.n0 + static_cast<int>(id / part.tiles_m) * D::BN : static_cast<int>(low / part.low_m) * D::BN;
     D::run(meet, A, B, m0, n0, K, out);
     __syncthreads();  // the next tile writes the same LDS
   }
 }
 
+// Of D, what is neither left of column n0 nor above row m0, one launch for both
+// edges (2050 x 2049 x 4096, float result: 51 -> 47 us); all of it for 0, 0.
 template <class D, class O>
-void launch_direct(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
-  const int64_t tm = ceil_div(out.M, D::BM), tiles = tm * ceil_div(out.N, D::BN);
-  const int64_t cap = kMaxWorkItems / D::threads;
+void launch_direct(const Side& A, const Side& B, int K, const Out<O>& out, int m0, int n0, hipStream_t s) {
+  Part part;
+  const int64_t tm = ceil_div(out.M, D::BM), low = ceil_div(out.M - m0, D::BM);
+  part.tiles_m = static_cast<int>(tm);
+  part.n0 = n0;
+  part.tiles = tm * ceil_div(out.N - n0, D::BN);
+  part.low_m = static_cast<int>(low);
+  part.m0 = m0;
+  const int64_t tiles = part.tiles + low * (n0 / D::BN), cap = kMaxWorkItems / D::threads;
   hipLaunchKernelGGL((k_direct<D, O>), dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)), dim3(D::threads), 0, s,
-                     A, B, K, out, static_cast<int>(tm), tiles);
+                     A, B, K, out, part, tiles);
 }
 
 // Which tile takes a product, by estimates of the time in us: of a small tile
@@ -193,6 +223,14 @@ Side from_row(Side o, int row, int scale_bytes) {  // row: a multiple of 128
   return o;
 }
 
+// The small tiles of a way, over the part of D that launch_direct takes.
+template <class P, class O>
+void launch_small(Way way, const Side& A, const Side& B, int K, const Out<O>& out, int m0, int n0, hipStream_t s) {
+  if (way == Way::kSmall16) launch_direct<nt::Direct<P, 1, 1, 8>>(A, B, K, out, m0, n0, s);
+  else if (way == Way::kSmall32) launch_direct<nt::Direct<P, 2, 2, 8>>(A, B, K, out, m0, n0, s);
+  else launch_direct<nt::Direct<P, 4, 4, 8>>(A, B, K, out, m0, n0, s);
+}
+
 template <class P, nt::Kind KIND, class O>
 void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s, int cuts = 2) {
   constexpr bool wide = sizeof(O) == 4;
@@ -203,11 +241,27 @@ void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t 
   // 1500 x 4096 84 and 41).  With 8-bit instructions the loads to LDS, a third more
   // a product, would bound it.
   using Loop128 = nt::Loop<KIND, 4, 4, wide ? 2 : 4, 2, wide ? 2 : 3>;
-  const Choice c = choose(out.M, out.N, K, wide, K > 0 && Loop128::fits(A) && Loop128::fits(B), cuts);
+  const bool loops = K > 0 && Loop128::fits(A) && Loop128::fits(B);
+  const Choice c = choose(out.M, out.N, K, wide, loops, cuts);
+  if (c.way == Way::kRows || c.way == Way::kColumns) {  // both, with small tiles of one size: these in one launch
+    const bool rows = c.way == Way::kRows;
+    const Choice inner = choose(rows ? c.at : out.M, rows ? out.N : c.at, K, wide, loops, cuts - 1);
+    if (inner.way == (rows ? Way::kColumns : Way::kRows)) {
+      const int m0 = rows ? c.at : inner.at, n0 = rows ? inner.at : c.at;
+      const Way right = choose(out.M, out.N - n0, K, wide, loops, 0).way, low = choose(out.M - m0, n0, K, wide, loops, 0).way;
+      if (right == low && right <= Way::kSmall64) {
+        Out<O> first = out;
+        first.M = m0;
+        first.N = n0;
+        launch<P, KIND>(A, B, K, first, s, 0);
+        return launch_small<P>(right, A, B, K, out, m0, n0, s);
+      }
+    }
+  }
   switch (c.way) {
-    case Way::kSmall16: return launch_direct<nt::Direct<P, 1, 1, 8>>(A, B, K, out, s);
-    case Way::kSmall32: return launch_direct<nt::Direct<P, 2, 2, 8>>(A, B, K, out, s);
-    case Way::kSmall64: return launch_direct<nt::Direct<P, 4, 4, 8>>(A, B, K, out, s);
+    case Way::kSmall16:
+    case Way::kSmall32:
+    case Way::kSmall64: return launch_small<P>(c.way, A, B, K, out, 0, 0, s);
     case Way::kLoop128: return launch_loop<Loop128>(A, B, K, out, s);
     case Way::kLoop256:
       if constexpr (!wide) launch_loop<nt::Loop<KIND, 8, 4, 2, 4, 2>>(A, B, K, out, s);
