@@ -81,7 +81,7 @@ struct Out {
 // (2300 TFLOP/s; each product's vector instructions of scaling take issue slots
 // beside the matrix instruction), 8192^3 with power-of-two scales, which need none,
 // 377-470 us from box to box (2340-2900 TFLOP/s; MfmaUtil 77 %, the clock is down to
-// about 1.75 GHz: power), 4096^3 with a float result 130 us (1056 TFLOP/s; 276 vector
+// about 1.75 GHz: power), 4096^3 with a float result 127 us (1078 TFLOP/s; 276 vector
 // instructions a wavefront and step widen and scale beside 64 matrix ones, and more
 // than two a matrix instruction take its time: four make 7.5 ns 11.8).
 template <class L, class O>
@@ -91,25 +91,38 @@ __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, O
   const int m0 = at.tm * L::BM, n0 = at.tn * L::BN;
   nt::v16f acc[L::kAcc];
   nt::loop_sum<L>(smem, A, B, m0, n0, K, acc);
-  if constexpr (sizeof(O) == 4) {  // four neighbours are 16 bytes, four lanes 64
+  // By way of LDS, so that whole lines are written (16-bit results of 4096^3: 61 ->
+  // 60 us; float ones with C read, 4097^3 159 -> 153, 8000 x 8000 x 1000 205 -> 191).
+  using Sheet = nt::Sheet<L::BN>;
+  static_assert(sizeof(Sheet) <= L::kLds, "a sheet fits");
+  Sheet& sheet = *reinterpret_cast<Sheet*>(smem);
+  __syncthreads();  // all wavefronts have left the loop
+  if constexpr (sizeof(O) == 4) {
+    constexpr int kRow = L::BN / 4, kTurns = 64 * kRow / L::threads;
     out.tile(m0, n0, L::BM, L::BN, [&](auto whole, auto add) {
-      // all of C first: it may be D, so a load would wait for the stores before it
-      // (8000 x 8000 x 1000 223 -> 200 us)
-      Pack<4, O> old[L::MT * L::NT];
-      int at = 0;
-      if (add.value)
-        nt::loop_out<L>(acc, m0, n0, [&](int m, int n, v4f) { old[at++] = out.template old<whole.value, 4>(m, n); });
-      at = 0;
-      nt::loop_out<L>(acc, m0, n0, [&](int m, int n, v4f v) {
-        const float x[4] = {v[0], v[1], v[2], v[3]};
-        out.template put<whole.value, add.value>(m, n, x, old[at++]);
+      nt::loop_sheets<L>(sheet, acc, [&](int top) {
+        // all of C first: it may be D, so a load would wait for the stores before it
+        // (8000 x 8000 x 1000 223 -> 200 us)
+        Pack<4, O> old[kTurns];
+        if (add.value) {
+#pragma unroll
+          for (int i = 0; i < kTurns; ++i) {
+            const int t = threadIdx.x + i * L::threads;
+            old[i] = out.template old<whole.value, 4>(m0 + top + t / kRow, n0 + t % kRow * 4);
+          }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+          const int t = threadIdx.x + i * L::threads;
+          float x[4];
+          __builtin_memcpy(x, &sheet.v[t / kRow * Sheet::kLd + t % kRow * 4], 16);
+          out.template put<whole.value, add.value>(m0 + top + t / kRow, n0 + t % kRow * 4, x, old[i]);
+        }
+        __syncthreads();
       });
     });
-  } else {  // by way of LDS, so that 16-byte stores fill whole lines: 61 -> 60 us at 4096^3
-    using Sheet = nt::Sheet<L::BN>;
-    static_assert(sizeof(Sheet) <= L::kLds, "a sheet fits");
-    Sheet& sheet = *reinterpret_cast<Sheet*>(smem);
-    __syncthreads();  // all wavefronts have left the loop
+  } else {
     out.tile(m0, n0, L::BM, L::BN, [&](auto whole, auto add) {
       nt::loop_sheets<L>(sheet, acc, [&](int top) {
         sheet.template out<L::threads>(

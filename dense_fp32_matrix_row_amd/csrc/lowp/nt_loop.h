@@ -148,24 +148,7 @@ __device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Sid
   }
 }
 
-// Calls epi(m, n, v) for every four neighbours D[m][n .. n+3] that the lane
-// holds, also past D's edges.
-template <class L, class E>
-__device__ __forceinline__ void loop_out(const v16f (&acc)[L::kAcc], int m0, int n0, const E& epi) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
-  const int wm = wave % L::WM, wn = wave / L::WM;
-#pragma unroll
-  for (int i = 0; i < L::MT; ++i)
-#pragma unroll
-    for (int j = 0; j < L::NT; ++j) {
-      const int at = j * L::MT + i;
-      const v16f& a = acc[at / 4];
-      epi(m0 + (wm * L::MT + i) * 16 + lane % 16, n0 + (wn * L::NT + j) * 16 + 4 * (lane / 16),
-          v4f{a[at % 4 * 4], a[at % 4 * 4 + 1], a[at % 4 * 4 + 2], a[at % 4 * 4 + 3]});
-    }
-}
-
-// The other way out, through LDS, for what is stored by rows and by columns: 64
+// The way out, through LDS, for what is stored by rows and by columns: 64
 // rows of sums at a time lie in LDS, COLS + 4 floats apart (four columns of 16
 // rows at once, as fragments come, then fall in different banks).
 template <int COLS>
