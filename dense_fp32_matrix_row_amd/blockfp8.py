@@ -17,13 +17,20 @@ from typing import Optional, Tuple
 
 from . import sgemm as _sgemm
 
-EXPORTS = ("hip_fp8_quantize", "hip_fp8_gemm", "hip_fp8_quantize_status_string",
+EXPORTS = ("hip_fp8_quantize", "hip_fp8_gemm", "hip_fp8_gemm_plan", "hip_fp8_quantize_status_string",
            "hip_fp8_gemm_status_string")
 
 F32, BF16, F16 = 0, 1, 2
 SCALE_F32, SCALE_E8M0 = 0, 1
 BLOCK = 128
 MAX_LD = 1 << 23
+MAX_LAUNCHES = 3  # HIP_FP8_GEMM_MAX_LAUNCHES
+
+class _Launch(ctypes.Structure):
+    """hip_fp8_gemm_launch."""
+    _fields_ = [(name, ctypes.c_int) for name in ("tile_m", "tile_n", "row0", "col0", "rows", "cols", "skip_rows",
+                                                  "skip_cols", "threads")] + [("workgroups", ctypes.c_longlong)]
+
 
 _bound = None
 
@@ -40,6 +47,8 @@ def load():
         lib.hip_fp8_gemm.restype = i32
         lib.hip_fp8_gemm.argtypes = [i32, i32, i32, f32, vp, i32, vp, i64, i64, i32,
                                      vp, i32, vp, i64, i64, i32, i32, f32, vp, i32, vp, i32, i32, vp]
+        lib.hip_fp8_gemm_plan.restype = i32
+        lib.hip_fp8_gemm_plan.argtypes = [i32, i32, i32, i32, ctypes.POINTER(_Launch), ctypes.POINTER(i32)]
         for name in ("hip_fp8_quantize_status_string", "hip_fp8_gemm_status_string"):
             getattr(lib, name).restype = ctypes.c_char_p
             getattr(lib, name).argtypes = [i32]
@@ -64,6 +73,15 @@ def hip_fp8_gemm(M, N, K, alpha, A, lda, SA, sa_row, sa_col, a_block_rows, B, ld
                                    int(sa_col), int(a_block_rows), a(B), int(ldb), a(SB), int(sb_row),
                                    int(sb_col), int(b_block_rows), int(scale_type), float(beta), a(C),
                                    int(ldc), a(D), int(ldd), int(c_type), s(stream)))
+
+
+def hip_fp8_gemm_plan(M, N, K, c_type) -> list:
+    """What hip_fp8_gemm enqueues for a shape, a dict a launch (nothing is launched)."""
+    launches, count = (_Launch * MAX_LAUNCHES)(), ctypes.c_int()
+    rc = load().hip_fp8_gemm_plan(int(M), int(N), int(K), int(c_type), launches, ctypes.byref(count))
+    if rc != 0:
+        raise _sgemm.SgemmError(rc, hip_fp8_gemm_status_string(rc))
+    return [{name: getattr(launch, name) for name, _ in _Launch._fields_} for launch in launches[:count.value]]
 
 
 def hip_fp8_quantize_status_string(status) -> str:

@@ -134,10 +134,10 @@ __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, O
 }
 
 template <class L, class O>
-void launch_loop(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
+void launch_loop(const Side& A, const Side& B, int K, const Out<O>& out, unsigned blocks, hipStream_t s) {
   const int64_t tm = ceil_div(out.M, L::BM), tn = ceil_div(out.N, L::BN);
-  hipLaunchKernelGGL((k_loop<L, O>), dim3(static_cast<unsigned>(tm * tn)), dim3(L::threads), 0, s, A, B, K, out,
-                     static_cast<int>(tm), static_cast<int>(tn));
+  hipLaunchKernelGGL((k_loop<L, O>), dim3(blocks), dim3(L::threads), 0, s, A, B, K, out, static_cast<int>(tm),
+                     static_cast<int>(tn));
 }
 
 // The tiles from column n0, all rows; then those from row m0 left of it.
@@ -165,7 +165,8 @@ __global__ __launch_bounds__(D::threads, 2) void k_direct(Side A, Side B, int K,
 // Of D, what is neither left of column n0 nor above row m0, one launch for both
 // edges (2050 x 2049 x 4096, float result: 51 -> 47 us); all of it for 0, 0.
 template <class D, class O>
-void launch_direct(const Side& A, const Side& B, int K, const Out<O>& out, int m0, int n0, hipStream_t s) {
+void launch_direct(const Side& A, const Side& B, int K, const Out<O>& out, int m0, int n0, unsigned blocks,
+                   hipStream_t s) {
   Part part;
   const int64_t tm = ceil_div(out.M, D::BM), low = ceil_div(out.M - m0, D::BM);
   part.tiles_m = static_cast<int>(tm);
@@ -173,9 +174,8 @@ void launch_direct(const Side& A, const Side& B, int K, const Out<O>& out, int m
   part.tiles = tm * ceil_div(out.N - n0, D::BN);
   part.low_m = static_cast<int>(low);
   part.m0 = m0;
-  const int64_t tiles = part.tiles + low * (n0 / D::BN), cap = kMaxWorkItems / D::threads;
-  hipLaunchKernelGGL((k_direct<D, O>), dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)), dim3(D::threads), 0, s,
-                     A, B, K, out, part, tiles);
+  const int64_t tiles = part.tiles + low * (n0 / D::BN);
+  hipLaunchKernelGGL((k_direct<D, O>), dim3(blocks), dim3(D::threads), 0, s, A, B, K, out, part, tiles);
 }
 
 // Which tile takes a product, by estimates of the time in us: of a small tile
@@ -197,23 +197,25 @@ Choice choose(int M, int N, int K, bool wide, bool loops, int cuts) {
     const double blocks = static_cast<double>(ceil_div(M, t) * ceil_div(N, t));
     return base + each * (alone > among * blocks ? alone : among * blocks);
   };
-  const auto loop = [&](int bn, double base, double alone, double full) {
-    const int64_t tiles = ceil_div(M, 256) * ceil_div(N, bn), rest = tiles % 256;
-    return base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0));
-  };
   Choice best{Way::kSmall16, 0, small(16, 2.8, 0.45, 0.003)};
   const auto offer = [&](Way w, int at, double us) {
     if (us < best.us) best = Choice{w, at, us};
+  };
+  const auto loop = [&](Way w, int bn, double base, double alone, double full) {
+    const int64_t tiles = ceil_div(M, 256) * ceil_div(N, bn), rest = tiles % 256;
+    if (tiles > kMaxWorkItems / 512) return;  // a block a tile: more than a launch takes
+    offer(w, 0, base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0)));
   };
   offer(Way::kSmall32, 0, small(32, 2.3, 1.3, wide ? 0.007 : 0.0056));
   offer(Way::kSmall64, 0, wide ? small(64, 2.0, 4.5, 0.024) : small(64, 3.0, 2.2, 0.0135));
   if (!loops) return best;
   if (wide) {  // two blocks a CU: with one each, a step takes little more than half the time
     const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128), rest = tiles % 512;
-    offer(Way::kLoop128, 0, 5.0 + steps * (tiles / 512 * 1.92 + (rest == 0 ? 0 : rest <= 256 ? 1.09 : 1.92)));
+    if (tiles <= kMaxWorkItems / 256)
+      offer(Way::kLoop128, 0, 5.0 + steps * (tiles / 512 * 1.92 + (rest == 0 ? 0 : rest <= 256 ? 1.09 : 1.92)));
   } else {
-    offer(Way::kLoop128, 0, loop(128, 6.0, 0.65, 0.98));
-    offer(Way::kLoop256, 0, loop(256, 7.0, 1.0, 1.6));
+    loop(Way::kLoop128, 128, 6.0, 0.65, 0.98);
+    loop(Way::kLoop256, 256, 7.0, 1.0, 1.6);
   }
   // rows or columns that hardly fill their tiles apart from the rest
   for (int t = 128; cuts > 0 && t <= 256; t *= 2) {
@@ -229,6 +231,76 @@ Choice choose(int M, int N, int K, bool wide, bool loops, int cuts) {
   return best;
 }
 
+// One launch: tiles of one kind (small or large) over rows m0 .. m0 + M - 1 and
+// columns n0 .. n0 + N - 1 of D but, of small tiles, the first skip_m rows of the
+// first skip_n columns.
+struct Piece {
+  Way way;
+  int m0, n0, M, N, skip_m, skip_n;
+};
+// A product's launches; two cuts make three of them.
+struct Plan {
+  Piece piece[3];
+  int count = 0;
+};
+
+void plan(Plan& p, int m0, int n0, int M, int N, int K, bool wide, bool loops, int cuts) {
+  const Choice c = choose(M, N, K, wide, loops, cuts);
+  if (c.way != Way::kRows && c.way != Way::kColumns) {
+    p.piece[p.count++] = Piece{c.way, m0, n0, M, N, 0, 0};
+    return;
+  }
+  const bool rows = c.way == Way::kRows;
+  const Choice inner = choose(rows ? c.at : M, rows ? N : c.at, K, wide, loops, cuts - 1);
+  if (inner.way == (rows ? Way::kColumns : Way::kRows)) {  // both edges, with small tiles of one size: these in one launch
+    const int m = rows ? c.at : inner.at, n = rows ? inner.at : c.at;
+    const Way right = choose(M, N - n, K, wide, loops, 0).way, low = choose(M - m, n, K, wide, loops, 0).way;
+    if (right == low && right <= Way::kSmall64) {
+      plan(p, m0, n0, m, n, K, wide, loops, 0);
+      p.piece[p.count++] = Piece{right, m0, n0, M, N, m, n};
+      return;
+    }
+  }
+  if (rows) {
+    plan(p, m0, n0, c.at, N, K, wide, loops, cuts - 1);
+    plan(p, m0 + c.at, n0, M - c.at, N, K, wide, loops, 0);
+  } else {
+    plan(p, m0, n0, M, c.at, K, wide, loops, cuts - 1);
+    plan(p, m0, n0 + c.at, M, N - c.at, K, wide, loops, 0);
+  }
+}
+constexpr int kCuts = 2;
+
+// Tile and block of a way.
+struct TileShape {
+  int rows, cols, threads;
+};
+constexpr TileShape shape_of(Way way, bool wide) {
+  switch (way) {
+    case Way::kSmall16: return TileShape{16, 16, 512};
+    case Way::kSmall32: return TileShape{32, 32, 512};
+    case Way::kSmall64: return TileShape{64, 64, 512};
+    case Way::kLoop128: return wide ? TileShape{128, 128, 256} : TileShape{256, 128, 512};
+    default: return TileShape{256, 256, 512};
+  }
+}
+
+template <class T>
+constexpr bool is_shape(Way way, bool wide) {
+  const TileShape t = shape_of(way, wide);
+  return t.rows == T::BM && t.cols == T::BN && t.threads == T::threads;
+}
+
+// Blocks of a launch: one a tile, but small tiles past what a launch takes, which
+// the blocks walk.
+int64_t blocks_of(const Piece& p, bool wide) {
+  const TileShape t = shape_of(p.way, wide);
+  const int64_t tiles = ceil_div(p.M, t.rows) * ceil_div(p.N - p.skip_n, t.cols) +
+                        ceil_div(p.M - p.skip_m, t.rows) * (p.skip_n / t.cols);
+  const int64_t cap = kMaxWorkItems / t.threads;
+  return tiles < cap ? tiles : cap;
+}
+
 Side from_row(Side o, int row, int scale_bytes) {  // row: a multiple of 128
   o.p += row * o.ld;
   o.s = static_cast<const uint8_t*>(o.s) + (row >> o.shift) * o.s_row * scale_bytes;
@@ -238,14 +310,16 @@ Side from_row(Side o, int row, int scale_bytes) {  // row: a multiple of 128
 
 // The small tiles of a way, over the part of D that launch_direct takes.
 template <class P, class O>
-void launch_small(Way way, const Side& A, const Side& B, int K, const Out<O>& out, int m0, int n0, hipStream_t s) {
-  if (way == Way::kSmall16) launch_direct<nt::Direct<P, 1, 1, 8>>(A, B, K, out, m0, n0, s);
-  else if (way == Way::kSmall32) launch_direct<nt::Direct<P, 2, 2, 8>>(A, B, K, out, m0, n0, s);
-  else launch_direct<nt::Direct<P, 4, 4, 8>>(A, B, K, out, m0, n0, s);
+void launch_small(Way way, const Side& A, const Side& B, int K, const Out<O>& out, int m0, int n0, unsigned blocks,
+                  hipStream_t s) {
+  using nt::Direct;
+  if (way == Way::kSmall16) launch_direct<Direct<P, 1, 1, 8>>(A, B, K, out, m0, n0, blocks, s);
+  else if (way == Way::kSmall32) launch_direct<Direct<P, 2, 2, 8>>(A, B, K, out, m0, n0, blocks, s);
+  else launch_direct<Direct<P, 4, 4, 8>>(A, B, K, out, m0, n0, blocks, s);
 }
 
 template <class P, nt::Kind KIND, class O>
-void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s, int cuts = 2) {
+void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
   constexpr bool wide = sizeof(O) == 4;
   // 256 x 128 of eight wavefronts; for float results 128 x 128 of four, two blocks a
   // CU, so that one widens while the other multiplies and results leave meanwhile:
@@ -254,49 +328,24 @@ void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t 
   // 1500 x 4096 84 and 41).  With 8-bit instructions the loads to LDS, a third more
   // a product, would bound it.
   using Loop128 = nt::Loop<KIND, 4, 4, wide ? 2 : 4, 2, wide ? 2 : 3>;
-  const bool loops = K > 0 && Loop128::fits(A) && Loop128::fits(B);
-  const Choice c = choose(out.M, out.N, K, wide, loops, cuts);
-  if (c.way == Way::kRows || c.way == Way::kColumns) {  // both, with small tiles of one size: these in one launch
-    const bool rows = c.way == Way::kRows;
-    const Choice inner = choose(rows ? c.at : out.M, rows ? out.N : c.at, K, wide, loops, cuts - 1);
-    if (inner.way == (rows ? Way::kColumns : Way::kRows)) {
-      const int m0 = rows ? c.at : inner.at, n0 = rows ? inner.at : c.at;
-      const Way right = choose(out.M, out.N - n0, K, wide, loops, 0).way, low = choose(out.M - m0, n0, K, wide, loops, 0).way;
-      if (right == low && right <= Way::kSmall64) {
-        Out<O> first = out;
-        first.M = m0;
-        first.N = n0;
-        launch<P, KIND>(A, B, K, first, s, 0);
-        return launch_small<P>(right, A, B, K, out, m0, n0, s);
-      }
-    }
-  }
-  switch (c.way) {
-    case Way::kSmall16:
-    case Way::kSmall32:
-    case Way::kSmall64: return launch_small<P>(c.way, A, B, K, out, 0, 0, s);
-    case Way::kLoop128: return launch_loop<Loop128>(A, B, K, out, s);
-    case Way::kLoop256:
-      if constexpr (!wide) launch_loop<nt::Loop<KIND, 8, 4, 2, 4, 2>>(A, B, K, out, s);
-      return;
-    case Way::kRows: {
-      Out<O> first = out, rest = out;
-      first.M = c.at;
-      rest.M -= c.at;
-      rest.d += c.at * out.ldd;
-      if (out.beta != 0.0f) rest.c += c.at * out.ldc;
-      launch<P, KIND>(A, B, K, first, s, cuts - 1);
-      return launch<P, KIND>(from_row(A, c.at, P::kScaleBytes), B, K, rest, s, 0);
-    }
-    case Way::kColumns: {
-      Out<O> first = out, rest = out;
-      first.N = c.at;
-      rest.N -= c.at;
-      rest.d += c.at;
-      if (out.beta != 0.0f) rest.c += c.at;
-      launch<P, KIND>(A, B, K, first, s, cuts - 1);
-      return launch<P, KIND>(A, from_row(B, c.at, P::kScaleBytes), K, rest, s, 0);
-    }
+  using Loop256 = nt::Loop<KIND, 8, 4, 2, 4, 2>;
+  static_assert(is_shape<Loop128>(Way::kLoop128, wide) && is_shape<Loop256>(Way::kLoop256, wide) &&
+                is_shape<nt::Direct<P, 1, 1, 8>>(Way::kSmall16, wide) && is_shape<nt::Direct<P, 2, 2, 8>>(Way::kSmall32, wide) &&
+                is_shape<nt::Direct<P, 4, 4, 8>>(Way::kSmall64, wide));
+  Plan p;
+  plan(p, 0, 0, out.M, out.N, K, wide, K > 0 && Loop128::fits(A) && Loop128::fits(B), kCuts);
+  for (int i = 0; i < p.count; ++i) {
+    const Piece& at = p.piece[i];
+    Out<O> part = out;
+    part.M = at.M;
+    part.N = at.N;
+    part.d += at.m0 * out.ldd + at.n0;
+    if (out.beta != 0.0f) part.c += at.m0 * out.ldc + at.n0;
+    const Side a = from_row(A, at.m0, P::kScaleBytes), b = from_row(B, at.n0, P::kScaleBytes);
+    const unsigned blocks = static_cast<unsigned>(blocks_of(at, wide));
+    if (at.way <= Way::kSmall64) launch_small<P>(at.way, a, b, K, part, at.skip_m, at.skip_n, blocks, s);
+    else if (at.way == Way::kLoop128) launch_loop<Loop128>(a, b, K, part, blocks, s);
+    else if constexpr (!wide) launch_loop<Loop256>(a, b, K, part, blocks, s);
   }
 }
 
@@ -371,6 +420,24 @@ int hip_fp8_gemm(int M, int N, int K, float alpha, const void* A, int lda, const
                Out<_Float16>{static_cast<_Float16*>(D), static_cast<const _Float16*>(C), ldd, ldc, M, N, alpha, beta},
                stream);
   return static_cast<int>(hipGetLastError());
+}
+
+int hip_fp8_gemm_plan(int M, int N, int K, int c_type, hip_fp8_gemm_launch* launches, int* count) {
+  if (M < 0) return -1;
+  if (N < 0) return -2;
+  if (K < 0) return -3;
+  if (c_type != HIP_FP8_F32 && c_type != HIP_FP8_BF16 && c_type != HIP_FP8_F16) return -23;
+  Plan p;
+  const bool wide = c_type == HIP_FP8_F32;
+  if (M > 0 && N > 0) plan(p, 0, 0, M, N, K, wide, K > 0, kCuts);
+  for (int i = 0; launches && i < p.count; ++i) {
+    const Piece& at = p.piece[i];
+    const TileShape t = shape_of(at.way, wide);
+    launches[i] = hip_fp8_gemm_launch{t.rows, t.cols, at.m0, at.n0, at.M, at.N, at.skip_m, at.skip_n, t.threads,
+                                      blocks_of(at, wide)};
+  }
+  if (count) *count = p.count;
+  return 0;
 }
 
 const char* hip_fp8_gemm_status_string(int status) {

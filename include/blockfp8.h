@@ -99,6 +99,23 @@ int hip_fp8_gemm(int M, int N, int K, float alpha,
                  float beta, const void *C, int ldc, void *D, int ldd, int c_type,
                  hipStream_t stream);
 
+/*
+ * What hip_fp8_gemm enqueues for a shape (alpha != 0, scales whose s_row is
+ * small, as the quantiser lays them out), decided on the host from M, N, K and
+ * c_type alone without launching anything: *count launches over disjoint parts
+ * of D, at most HIP_FP8_GEMM_MAX_LAUNCHES, described in launches[0 .. *count).
+ * Either pointer may be NULL.  0, or -1, -2, -3, -23 as hip_fp8_gemm.
+ */
+#define HIP_FP8_GEMM_MAX_LAUNCHES 3
+typedef struct {
+  int tile_m, tile_n;         /* of D a block sums at a time */
+  int row0, col0, rows, cols; /* the part of D ... */
+  int skip_rows, skip_cols;   /* ... but its first skip_rows rows of its first skip_cols columns */
+  int threads;                /* of a block */
+  long long workgroups;       /* workgroups * threads <= 2^31 */
+} hip_fp8_gemm_launch;
+int hip_fp8_gemm_plan(int M, int N, int K, int c_type, hip_fp8_gemm_launch *launches, int *count);
+
 const char *hip_fp8_quantize_status_string(int status);
 const char *hip_fp8_gemm_status_string(int status);
 
