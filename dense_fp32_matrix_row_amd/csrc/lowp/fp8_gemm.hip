@@ -19,12 +19,13 @@ struct Out {
   int M, N;
   float alpha, beta;
   // C's COUNT neighbours of row m from column n, those inside; WHOLE: all are.
+  // (Ends are compared as N - COUNT: n + COUNT passes 2^31 for the widest D.)
   template <bool WHOLE, int COUNT>
   __device__ __forceinline__ Pack<COUNT, O> old(int m, int n) const {
     Pack<COUNT, O> o{};
     if (!WHOLE && (m >= M || n >= N)) return o;
     const O* const from = c + m * ldc + n;
-    if (WHOLE || n + COUNT <= N) return load_pack<COUNT>(from);
+    if (WHOLE || n <= N - COUNT) return load_pack<COUNT>(from);
 #pragma unroll
     for (int i = 0; i < COUNT; ++i)
       if (n + i < N) o.v[i] = from[i];
@@ -42,7 +43,7 @@ struct Out {
       if (ADD) x = fmaf(beta, to_float(o.v[i]), x);
       from_float(x, r.v[i]);
     }
-    if (WHOLE || n + COUNT <= N) {
+    if (WHOLE || n <= N - COUNT) {
       store_pack(to, r);
     } else {
 #pragma unroll
@@ -64,7 +65,7 @@ struct Out {
   // f with what of a rows x cols tile at m0, n0 is known beforehand.
   template <class F>
   __device__ __forceinline__ void tile(int m0, int n0, int rows, int cols, const F& f) const {
-    const bool whole = m0 + rows <= M && n0 + cols <= N;
+    const bool whole = m0 <= M - rows && n0 <= N - cols;
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
     if (beta == 0.0f) {

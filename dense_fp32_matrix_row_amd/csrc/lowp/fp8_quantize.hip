@@ -126,10 +126,11 @@ __device__ __forceinline__ void store_scale(void* s, int64_t at, const Scale& q)
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// Eight neighbours of a row from column `col`, zeros past `cols`.
+// Eight neighbours of a row from column `col`, zeros past `cols` (whose end is
+// compared as cols - 8: col + 8 passes 2^31 in the widest row).
 template <class X>
 __device__ __forceinline__ Pack<8, X> load8(const X* row, int col, int cols) {
-  if (col + 8 <= cols) return load_pack<8>(row + col);
+  if (col <= cols - 8) return load_pack<8>(row + col);
   Pack<8, X> p{};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -145,7 +146,7 @@ __device__ __forceinline__ uint2 codes8(const Pack<8, X>& p, Factor q) {
 
 // Eight codes of a row from column `col`, none past `cols`.
 __device__ __forceinline__ void store8(uint8_t* row, int col, int cols, uint2 c) {
-  if (col + 8 <= cols) {
+  if (col <= cols - 8) {
     __builtin_memcpy(row + col, &c, 8);
   } else {
 #pragma unroll
