@@ -124,11 +124,13 @@ __global__ __launch_bounds__(256) void k_norm(Source src, double* part, int part
   if (threadIdx.x == 0) part[int64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = sum;
 }
 
-// |G|_F + eps from the parts; all threads of a 256-thread block call it.
-__device__ __forceinline__ float divisor(const double* part, int parts, float eps, double (&s)[4]) {
+// 1 / (|G|_F + eps) from the parts; all threads of a 256-thread block call it.  In
+// double, and x times it too: the norm of finite floats can pass a float's largest
+// number or lie below its normal ones.
+__device__ __forceinline__ double factor(const double* part, int parts, float eps, double (&s)[4]) {
   double sum = 0;
   for (int p = threadIdx.x; p < parts; p += 256) sum += part[int64_t(blockIdx.y) * kNormBlocks + p];
-  return static_cast<float>(sqrt(block_sum(sum, s))) + eps;
+  return 1.0 / (sqrt(block_sum(sum, s)) + eps);
 }
 
 // X_0 as pairs, as G lies (`direct`: rows of G) and transposed (`across`), a
@@ -149,9 +151,9 @@ __global__ __launch_bounds__(256) void k_start(Source src, const double* part, i
     x[p] = T{};
     if (r0 + r < src.rows && c0 + c < src.cols) x[p] = g[(r0 + r) * src.ld + c0 + c];
   }
-  const float div = divisor(part, parts, eps, s);
+  const double by = factor(part, parts, eps, s) * kScaleX;
 #pragma unroll
-  for (int p = 0; p < 16; ++p) t[p * 4 + threadIdx.x / 64][threadIdx.x % 64] = to_float(x[p]) / div * kScaleX;
+  for (int p = 0; p < 16; ++p) t[p * 4 + threadIdx.x / 64][threadIdx.x % 64] = static_cast<float>(to_float(x[p]) * by);
   __syncthreads();
   uint8_t* dp = direct.p + blockIdx.y * direct.batch;
   uint8_t* ap = across.p + blockIdx.y * across.batch;
@@ -171,12 +173,12 @@ template <class T>
 __global__ __launch_bounds__(256) void k_divide(Source src, const double* part, int parts, float eps, T* x,
                                                 int64_t ldx, int64_t batch_x) {
   __shared__ double s[4];
-  const float div = divisor(part, parts, eps, s);
+  const double by = factor(part, parts, eps, s);
   const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
   const int64_t items = int64_t(src.rows) * src.cols;
   for (int64_t it = int64_t(blockIdx.x) * 256 + threadIdx.x; it < items; it += int64_t(gridDim.x) * 256) {
     const int64_t r = it / src.cols, c = it % src.cols;
-    from_float(to_float(g[r * src.ld + c]) / div, x[blockIdx.y * batch_x + r * ldx + c]);
+    from_float(static_cast<float>(to_float(g[r * src.ld + c]) * by), x[blockIdx.y * batch_x + r * ldx + c]);
   }
 }
 

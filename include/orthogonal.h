@@ -47,9 +47,10 @@ int hip_orthogonalize_workspace(int batch, int rows, int cols, int type, long lo
  *   workspace  device memory of at least the bytes above, 256-byte aligned;
  *         calls that overlap in time need workspaces of their own.
  * steps 0 gives G / (|G|_F + eps).  A zero matrix gives zeros (eps > 0).  A
- * matrix with an infinity or NaN gives NaN.
+ * matrix with an infinity or NaN gives NaN throughout; for steps 0 a NaN makes
+ * all elements NaN, an infinity only the infinite ones (finite ones become 0).
  *
- * The norm is summed in double.  The iterate and the products' operands are
+ * The norm is summed, and divided by, in double.  The iterate and the products' operands are
  * kept as pairs of halfs, 22 significant bits, and multiplied on the
  * matrix cores with float sums; their fixed-point range asks for
  * |X_i| < 16, |S|, |a + b S + c S^2| < 255 element by element, which every
