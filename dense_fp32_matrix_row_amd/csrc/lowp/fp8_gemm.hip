@@ -408,6 +408,7 @@ int hip_fp8_gemm(int M, int N, int K, float alpha, const void* A, int lda, const
   if (c_type != HIP_FP8_F32 && c_type != HIP_FP8_BF16 && c_type != HIP_FP8_F16) return -23;
   if (!some) return 0;
   const int k = product ? K : 0;
+  if (k == 0) alpha = 0.0f;  // an empty sum times an infinity would be NaN
   const Side a{static_cast<const uint8_t*>(A), lda, M, SA, sa_row, sa_col, a_block_rows == 128 ? 7 : 0, 0};
   const Side b{static_cast<const uint8_t*>(B), ldb, N, SB, sb_row, sb_col, b_block_rows == 128 ? 7 : 0, 0};
   if (c_type == HIP_FP8_F32)
