@@ -311,8 +311,11 @@ def linear_backward(dy, xt: BlockFp8, wt: BlockFp8, dw=None, out_dtype=None):
 
     dy: T x O; xt: x^T as linear_forward returned it; wt: w^T quantised (I x O).
     dx has dy's type by default.  dw is float32, a new tensor, or added to the
-    tensor given, in place."""
+    tensor given, in place (float32 too: sums that grow over many calls lose what
+    a 16-bit type cuts off in each)."""
     import torch
+    if dw is not None and dw.dtype != torch.float32:
+        raise TypeError(f"dw is float32, not {dw.dtype}")
     dyq, dyt = quantize_both(dy, 1, wt.s.dtype)
     dx = gemm(dyq, wt, out_dtype=out_dtype or dy.dtype)
     if dw is None:
