@@ -7,6 +7,10 @@ quantize, quantize_transposed, quantize_both, gemm, linear_forward and
 linear_backward take and return torch device tensors, run on torch's current
 stream of the tensors' device and raise on errors.  Every operation runs in the
 library's HIP kernels; there is no fallback.
+
+Results carry no autograd graph, also those of tensors that require gradients:
+a layer's gradients are linear_backward's.  A tensor that is written in place
+(out, dw) counts as modified for autograd.
 """
 
 from __future__ import annotations
@@ -188,6 +192,14 @@ def _call(device, function, what, *args):
         raise _sgemm.SgemmError(status, what(status))
 
 
+def written(t):
+    """Tells autograd that t has been written to, as torch's own in-place operations
+    do, so that a graph that saved it notices."""
+    import torch
+    if not t.is_inference():  # these have no version to advance
+        torch.autograd.graph.increment_version(t)
+
+
 def _empty(rows, cols, block_rows, scale, device):
     """Room for a quantised matrix: rows of a multiple of 16 bytes, the scales
     of one block column side by side.  And the row stride."""
@@ -286,7 +298,8 @@ def gemm(a: BlockFp8, b: BlockFp8, c=None, alpha: float = 1.0, beta: float = 0.0
             raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {(M, N)} {dtype}")
     _same_device(a.q, a.s, b.q, b.s, c, out)
     device = a.q.device
-    if out is None:
+    new = out is None
+    if new:
         out = torch.empty((M, N), dtype=dtype, device=device)
         ldd = max(N, 1)
     else:
@@ -294,6 +307,8 @@ def gemm(a: BlockFp8, b: BlockFp8, c=None, alpha: float = 1.0, beta: float = 0.0
     from_c, ldc = (c.data_ptr(), _matrix("c", c)[2]) if c is not None else (None, 0)
     _call(device, load().hip_fp8_gemm, hip_fp8_gemm_status_string, M, N, K, alpha, *left, *right, kind, beta,
           from_c, ldc, out.data_ptr(), ldd, c_type)
+    if not new:
+        written(out)
     return out
 
 

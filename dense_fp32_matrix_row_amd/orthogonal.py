@@ -4,7 +4,8 @@ include/orthogonal.h).
 hip_orthogonalize and hip_orthogonalize_workspace carry the C ABI's names;
 orthogonalize takes and returns torch device tensors, runs on torch's current
 stream of the tensor's device and raises on errors.  Every operation runs in
-the library's HIP kernels; there is no fallback.
+the library's HIP kernels; there is no fallback.  The result carries no autograd
+graph; an `out` counts as modified for autograd.
 """
 
 from __future__ import annotations
@@ -13,7 +14,7 @@ import ctypes
 from typing import Optional, Sequence
 
 from . import sgemm as _sgemm
-from .blockfp8 import current_stream
+from .blockfp8 import current_stream, written
 
 EXPORTS = ("hip_orthogonalize", "hip_orthogonalize_workspace", "hip_orthogonalize_status_string")
 
@@ -116,7 +117,8 @@ def orthogonalize(g, steps: int = 5, coefficients: Optional[Sequence] = None, ep
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return orthogonalize(g, steps, co, eps, out, workspace)
-    if out is None:
+    new = out is None
+    if new:
         out = torch.empty(g.shape, dtype=g.dtype, device=device)
     if out.shape != g.shape or out.dtype != g.dtype or out.device != device:
         raise ValueError(f"out is {tuple(out.shape)} {out.dtype}, not {tuple(g.shape)} {g.dtype}")
@@ -128,4 +130,6 @@ def orthogonalize(g, steps: int = 5, coefficients: Optional[Sequence] = None, ep
         raise ValueError("the workspace must be contiguous and on g's device")
     _check(hip_orthogonalize(batch, rows, cols, kind, g, ldg, stride_g, steps, flat, eps, out, ldx, stride_x, workspace,
                              workspace.numel() * workspace.element_size(), current_stream(device.index)))
+    if not new:
+        written(out)
     return out
