@@ -99,9 +99,12 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
 // data that is 1.5e-5 of the result, far below the half step of a 16-bit
 // result (2^-8, 2^-11 of it), and far above a float's: float results use Widened.
 
-// Float scales: a block of 128 is summed from zero and added times its scales'
-// product (the matrix instruction can apply powers of two only).  UNIFORM: all
-// B rows of a wavefront share a scale.
+// Float scales: a block of 128 is summed from zero and added times its scales
+// (the matrix instruction can apply powers of two only).  UNIFORM: all B rows of a
+// wavefront share a scale, so the scales' product is formed once a row of A and a
+// step, and a result costs one vector instruction instead of two (beside an 8-bit
+// product five fit: 13.7 ns; eight make 19).  It loses bits below 2^-126, where
+// scaling one after the other would not; the header says so.
 template <bool UNIFORM>
 struct Fp8F32 {
   static constexpr int kScaleBytes = 4;

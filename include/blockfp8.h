@@ -78,6 +78,10 @@ int hip_fp8_quantize(int rows, int cols, const void *X, int x_type, int ldx,
  * float D is summed at half that rate with a float's bits throughout.
  * Where a partial sum or a block's s_A s_B passes float's range, D_ij is an
  * infinity or a NaN as the order of the sum, which depends on the sizes, has it.
+ * Float scales, and scales of either type of a float D, multiply a block's sum as
+ * floats: with b_block_rows 1 by s_A and then by s_B; with 128 by s_A s_B, rounded
+ * to float first, which costs half the multiplications and, where s_A s_B is below
+ * 2^-126, bits: an error of up to 2^-150 times the block's sum of code products.
  *   lda, ldb: multiples of 16 bytes, at most HIP_FP8_MAX_LD; A and B 16-byte
  *   aligned; a row is read up to the next multiple of 16 bytes (what lies
  *   past K has no influence).
