@@ -479,6 +479,40 @@ Choice choose(int batch, int rows, int cols, int K, bool symmetric, bool cut) {
   return best;
 }
 
+// A step's three products: S and P, which are alike at every step, and P X, whose
+// columns from `cut` on (0: none) may have a launch of their own.
+struct Plan {
+  Choice s, p, x;
+  int cut;
+  Way rest;
+};
+
+Plan plan(int batch, int m, int n) {
+  const int km = static_cast<int>(pad32(m)), kn = static_cast<int>(pad32(n));
+  Plan l;
+  l.s = choose(batch, m, m, kn, true, false);
+  l.p = choose(batch, m, m, km, true, false);
+  l.x = choose(batch, m, n, km, false, true);
+  l.cut = 0;
+  l.rest = Way::kSmall32;
+  if (l.x.way == Way::kColumns) {
+    l.cut = l.x.at;
+    l.rest = choose(batch, m, n - l.cut, km, false, false).way;
+    l.x = choose(batch, m, l.cut, km, false, false);
+  }
+  return l;
+}
+
+int tile_of(Way way) {
+  switch (way) {
+    case Way::kSmall32: return 32;
+    case Way::kSmall64: return 64;
+    case Way::kLoop192: return 192;
+    case Way::kLoop256: return 256;
+    default: return 128;
+  }
+}
+
 using Loop128 = Assembled<4, 2, 2, 4, 4>;
 
 // Calls f with the tile.
@@ -559,8 +593,8 @@ hipError_t launch(int batch, const Source& src, int steps, const float* co, floa
                      eps, tall ? XT : X, tall ? X : XT, static_cast<int>(tc));
   const auto side = [](const Pairs& p, int rows) { return Side{p.p, p.ld, rows, nullptr, 0, 0, 0, p.batch}; };
   const int km = static_cast<int>(pad32(l.m)), kn = static_cast<int>(pad32(l.n));
-  const auto symmetric = [&](const Side& a, int K, const SymmetricOut& out) {
-    const Choice c = choose(batch, l.m, l.m, K, true, false);
+  const Plan choice = plan(batch, l.m, l.n);
+  const auto symmetric = [&](const Choice& c, const Side& a, int K, const SymmetricOut& out) {
     if (c.way == Way::kSplit) {
       const int t = static_cast<int>(ceil_div(l.m, Loop128::BM)), tiles = t * (t + 1) / 2;
       float* sums = reinterpret_cast<float*>(ws + l.sums);
@@ -585,18 +619,13 @@ hipError_t launch(int batch, const Source& src, int steps, const float* co, floa
   };
   for (int i = 0; i < steps; ++i) {
     const float a = co[3 * i], b = co[3 * i + 1], c = co[3 * i + 2];
-    symmetric(side(X, l.m), kn,
+    symmetric(choice.s, side(X, l.m), kn,
               SymmetricOut{S, Pairs{nullptr, 0, 0}, l.m, kScaleS / (kScaleX * kScaleX), 0.0f, 0.0f, 0, false});
-    symmetric(side(S, l.m), km, SymmetricOut{P, S, l.m, c / kScaleS, b, a * kScaleS, 0, false});
+    symmetric(choice.p, side(S, l.m), km, SymmetricOut{P, S, l.m, c / kScaleS, b, a * kScaleS, 0, false});
     const bool last = i + 1 == steps;
     const IterateOut<T> out{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, 0, tall};
-    const Choice way = choose(batch, l.m, l.n, km, false, true);
-    if (way.way == Way::kColumns) {
-      iterate(side(P, l.m), side(XT, l.n), 0, way.at, choose(batch, l.m, way.at, km, false, false).way, out);
-      iterate(side(P, l.m), side(XT, l.n), way.at, l.n - way.at, choose(batch, l.m, l.n - way.at, km, false, false).way, out);
-    } else {
-      iterate(side(P, l.m), side(XT, l.n), 0, l.n, way.way, out);
-    }
+    iterate(side(P, l.m), side(XT, l.n), 0, choice.cut ? choice.cut : l.n, choice.x.way, out);
+    if (choice.cut) iterate(side(P, l.m), side(XT, l.n), choice.cut, l.n - choice.cut, choice.rest, out);
     const Pairs t = XT;
     XT = XT2;
     XT2 = t;
@@ -646,6 +675,24 @@ int hip_orthogonalize(int batch, int rows, int cols, int type, const void* G, in
   else
     e = launch(batch, src, steps, coefficients, eps, static_cast<_Float16*>(X), ldx, stride_x, ws, stream);
   return static_cast<int>(e);
+}
+
+int hip_orthogonalize_plan(int batch, int rows, int cols, hip_orthogonalize_product* products) {
+  const int bad = check_sizes(batch, rows, cols, HIP_ORTHOGONAL_F32);
+  if (bad) return bad;
+  if (!products) return 0;
+  for (int i = 0; i < 3; ++i) products[i] = hip_orthogonalize_product{0, 0, 0, 0};
+  if (batch == 0 || rows == 0 || cols == 0) return 0;
+  const Plan p = plan(batch, rows < cols ? rows : cols, rows < cols ? cols : rows);
+  const auto product = [](const Choice& c) {
+    return hip_orthogonalize_product{tile_of(c.way), c.way == Way::kSplit ? c.at : 1, 0, 0};
+  };
+  products[0] = product(p.s);
+  products[1] = product(p.p);
+  products[2] = product(p.x);
+  products[2].cut = p.cut;
+  products[2].cut_tile = p.cut ? tile_of(p.rest) : 0;
+  return 0;
 }
 
 const char* hip_orthogonalize_status_string(int status) {

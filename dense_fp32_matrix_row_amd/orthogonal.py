@@ -16,12 +16,18 @@ from typing import Optional, Sequence
 from . import sgemm as _sgemm
 from .blockfp8 import current_stream, written
 
-EXPORTS = ("hip_orthogonalize", "hip_orthogonalize_workspace", "hip_orthogonalize_status_string")
+EXPORTS = ("hip_orthogonalize", "hip_orthogonalize_workspace", "hip_orthogonalize_plan",
+           "hip_orthogonalize_status_string")
 
 F32, BF16, F16 = 0, 1, 2
 MAX_SIZE = 1 << 20
 MAX_STEPS = 64
 QUINTIC = (3.4445, -4.7750, 2.0315)
+
+class _Product(ctypes.Structure):
+    """hip_orthogonalize_product."""
+    _fields_ = [(name, ctypes.c_int) for name in ("tile", "parts", "cut", "cut_tile")]
+
 
 _bound = None
 
@@ -37,6 +43,8 @@ def load():
                                           vp, i32, i64, vp, i64, vp]
         lib.hip_orthogonalize_workspace.restype = i32
         lib.hip_orthogonalize_workspace.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i64)]
+        lib.hip_orthogonalize_plan.restype = i32
+        lib.hip_orthogonalize_plan.argtypes = [i32, i32, i32, ctypes.POINTER(_Product)]
         lib.hip_orthogonalize_status_string.restype = ctypes.c_char_p
         lib.hip_orthogonalize_status_string.argtypes = [i32]
         _bound = lib
@@ -57,6 +65,13 @@ def hip_orthogonalize_workspace(batch, rows, cols, type) -> int:
     out = ctypes.c_longlong()
     _check(load().hip_orthogonalize_workspace(int(batch), int(rows), int(cols), int(type), ctypes.byref(out)))
     return out.value
+
+
+def hip_orthogonalize_plan(batch, rows, cols) -> list:
+    """The tiles of a step's three products (S, P and P X), a dict each (nothing is launched)."""
+    products = (_Product * 3)()
+    _check(load().hip_orthogonalize_plan(int(batch), int(rows), int(cols), products))
+    return [{name: getattr(p, name) for name, _ in _Product._fields_} for p in products]
 
 
 def hip_orthogonalize(batch, rows, cols, type, G, ldg, stride_g, steps, coefficients, eps, X, ldx, stride_x,

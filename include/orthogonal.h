@@ -69,6 +69,19 @@ int hip_orthogonalize(int batch, int rows, int cols, int type,
                       void *workspace, long long workspace_bytes,
                       hipStream_t stream);
 
+/*
+ * Which tiles the three products of a step take, S = X X^T, P = a + b S + c S^2
+ * and P X, decided on the host from the sizes alone without launching anything.
+ * 0, or -1 .. -3 for a bad batch, rows or cols; all zeros where there is nothing
+ * to do.
+ */
+typedef struct {
+  int tile;          /* rows and columns of a block's tile */
+  int parts;         /* of the sums' long side, joined by a second launch if > 1 */
+  int cut, cut_tile; /* P X: the column from which on a launch of its own computes it, and its tile; 0: none */
+} hip_orthogonalize_product;
+int hip_orthogonalize_plan(int batch, int rows, int cols, hip_orthogonalize_product products[3]);
+
 const char *hip_orthogonalize_status_string(int status);
 
 #ifdef __cplusplus

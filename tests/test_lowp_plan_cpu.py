@@ -1,8 +1,10 @@
-"""Which kernels the 8-bit product takes for a shape, decided on the host."""
+"""Which kernels the 8-bit product and the orthogonalised update take for a shape,
+decided on the host."""
 
 import pytest
 
-from dense_fp32_matrix_row_amd import blockfp8, sgemm
+from dense_fp32_matrix_row_amd import blockfp8, orthogonal, sgemm
+from tests import lowp_shapes as shapes
 
 LIMIT = 1 << 31  # work-items a launch takes
 LARGEST = (1 << 31) - 1
@@ -40,3 +42,41 @@ def test_plan_refusals_and_nothing_to_do():
             blockfp8.hip_fp8_gemm_plan(*args)
         assert e.value.status == status
     assert blockfp8.hip_fp8_gemm_plan(0, 5, 5, 0) == [] == blockfp8.hip_fp8_gemm_plan(5, 0, 5, 0)
+
+
+@pytest.mark.parametrize("table,c_types,tiles", [
+    (shapes.GEMM_FLOAT, (blockfp8.F32,), {(16, 16), (32, 32), (64, 64), (128, 128)}),
+    (shapes.GEMM_16_BIT, (blockfp8.BF16, blockfp8.F16), {(16, 16), (32, 32), (64, 64), (256, 128), (256, 256)}),
+])
+def test_the_gpu_tests_sizes_reach_every_tile_of_the_product(table, c_types, tiles):
+    keys = ("tile_m", "tile_n", "row0", "col0", "skip_rows", "skip_cols")
+    for size, launches in table.items():
+        for c_type in c_types:
+            assert [tuple(p[k] for k in keys) for p in blockfp8.hip_fp8_gemm_plan(*size, c_type)] == launches, size
+    alone = {p[0][:2] for p in table.values() if len(p) == 1}
+    assert alone == tiles
+    edges = {(q[:2], "both" if q[4] else "right" if q[3] else "low") for p in table.values() for q in p[1:]}
+    small = {(16, 16), (32, 32), (64, 64)}
+    assert {t for t, _ in edges} == small and {side for _, side in edges} == {"both", "right", "low"}
+
+
+def test_the_gpu_tests_sizes_reach_every_tile_of_the_update():
+    for size, products in shapes.ORTHOGONALIZE.items():
+        assert [tuple(p.values()) for p in orthogonal.hip_orthogonalize_plan(*size)] == products, size
+        batch, rows, cols = size  # a tall matrix is iterated as its transpose
+        assert [tuple(p.values()) for p in orthogonal.hip_orthogonalize_plan(batch, cols, rows)] == products, size
+    for i in range(3):
+        assert {p[i][0] for p in shapes.ORTHOGONALIZE.values()} == {32, 64, 128, 192, 256}
+    for i in range(2):
+        assert any(p[i][1] > 1 for p in shapes.ORTHOGONALIZE.values())
+    assert {p[2][3] for p in shapes.ORTHOGONALIZE.values()} == {0, 32, 64, 128}
+    assert {p[2][0] for p in shapes.ORTHOGONALIZE.values() if p[2][2]} == {128, 192, 256}
+
+
+def test_update_plan_refusals_and_nothing_to_do():
+    for size, status in (((-1, 4, 4), -1), ((65536, 4, 4), -1), ((1, -1, 4), -2), ((1, 4, orthogonal.MAX_SIZE + 1), -3)):
+        with pytest.raises(sgemm.SgemmError) as e:
+            orthogonal.hip_orthogonalize_plan(*size)
+        assert e.value.status == status
+    for size in ((0, 4, 4), (1, 0, 4), (1, 4, 0)):
+        assert all(v == 0 for p in orthogonal.hip_orthogonalize_plan(*size) for v in p.values())
