@@ -127,7 +127,7 @@ __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, O
     out.tile(m0, n0, L::BM, L::BN, [&](auto whole, auto add) {
       nt::loop_sheets<L>(sheet, acc, [&](int top) {
         sheet.template out<L::threads>(
-            false, [&](int r, int c, float (&v)[8]) { out.template row<whole.value, add.value>(m0 + top + r, n0 + c, v); },
+            false, [&](int r, int c, const float (&v)[8]) { out.template row<whole.value, add.value>(m0 + top + r, n0 + c, v); },
             [](int, int, const float (&)[8]) {});
       });
     });

@@ -124,8 +124,6 @@ __device__ __forceinline__ void store_scale(void* s, int64_t at, const Scale& q)
   else static_cast<uint8_t*>(s)[at] = static_cast<uint8_t>(q.stored);
 }
 
-__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
 // Eight neighbours of a row from column `col`, zeros past `cols` (whose end is
 // compared as cols - 8: col + 8 passes 2^31 in the widest row).
 template <class X>
@@ -178,16 +176,6 @@ struct Args {
   void* st;
   int64_t st_row, st_col;
 };
-
-// Maximum over the 16 lanes of a group: with the neighbour, the next pair, the
-// other half of eight and of sixteen.
-template <int CONTROL>
-__device__ __forceinline__ uint32_t max_with(uint32_t v) {
-  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CONTROL, 0xf, 0xf, true)));
-}
-__device__ __forceinline__ uint32_t max16(uint32_t v) {
-  return max_with<0x140>(max_with<0x141>(max_with<0x4e>(max_with<0xb1>(v))));
-}
 
 // Blocks of 1 x 128 as the matrix lies: sixteen lanes a block, eight neighbours
 // each, nothing shared, so that a few rows still spread over many CUs.  16 x 1024

@@ -42,4 +42,18 @@ __device__ __forceinline__ void store_pack(T* p, const Pack<N, T>& r) {
   __builtin_memcpy(p, &r, sizeof(r));
 }
 
+// The bits of |x|: as unsigned integers magnitudes order like their values, with
+// infinities and then NaNs above.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Maximum over the 16 lanes of a group: with the neighbour, the next pair, the
+// other half of eight and of sixteen.
+template <int CONTROL>
+__device__ __forceinline__ uint32_t max_with(uint32_t v) {
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CONTROL, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  return max_with<0x140>(max_with<0x141>(max_with<0x4e>(max_with<0xb1>(v))));
+}
+
 }  // namespace sgemm

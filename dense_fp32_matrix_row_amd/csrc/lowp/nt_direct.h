@@ -139,10 +139,14 @@ struct Direct {
 
   // Sums the tile at rows m0 of A and n0 of B over K bytes and calls
   // epi(m, n, v) for every four neighbours D[m][n .. n+3], also past D's edges;
-  // the block's wavefronts take a share each.
-  template <class E>
+  // the block's wavefronts take a share each.  started() is called by all threads
+  // with the first loads under way, a barrier before epi.
+  struct Nothing {
+    __device__ __forceinline__ void operator()() const {}
+  };
+  template <class E, class S = Nothing>
   static __device__ __forceinline__ void run(Meet& meet, const Side& A, const Side& B, int m0, int n0, int K,
-                                             const E& epi) {
+                                             const E& epi, const S& started = S{}) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
     const int row = lane % 16, g = lane / 16;
     typename P::Acc acc[NT][MT];
@@ -156,6 +160,7 @@ struct Direct {
       const Reader rd(A, B, m0, n0, K, row, g);
       Raw now, next;
       rd.read(now, wave);
+      started();
       int k = wave;
       for (; k + WAVES < steps; k += WAVES) {
         rd.read(next, k + WAVES);
@@ -166,6 +171,8 @@ struct Direct {
       turn(now, rd);
       if (K - k * kStep < kStep) mask(now, K - k * kStep, g);
       mac(acc, now);
+    } else {
+      started();
     }
 
 #pragma unroll

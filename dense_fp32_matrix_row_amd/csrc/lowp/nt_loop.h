@@ -158,22 +158,22 @@ struct alignas(16) Sheet {
 
   __device__ __forceinline__ void put(int r, int c, v4f x) { *reinterpret_cast<v4f*>(&v[r * kLd + c]) = x; }
 
-  // rows(r, c, x): eight neighbours of row r from column c, which it may change;
-  // when that is done for all, columns(c, r, x): eight of column c from row r,
-  // if `both`.  All threads of the block call it, with the sheet written.
+  // rows(r, c, x): eight neighbours of row r from column c; columns(c, r, x): eight
+  // of column c from row r, if `both`.  All threads of the block call it, with the
+  // sheet written.
   template <int THREADS, class R, class C>
   __device__ __forceinline__ void out(bool both, const R& rows, const C& columns) {
     __syncthreads();
 #pragma unroll 2
     for (int t = threadIdx.x; t < 64 * COLS / 8; t += THREADS) {
-      float* const at = &v[t / (COLS / 8) * kLd + t % (COLS / 8) * 8];
       float x[8];
-      __builtin_memcpy(x, at, 32);
+      __builtin_memcpy(x, &v[t / (COLS / 8) * kLd + t % (COLS / 8) * 8], 32);
       rows(t / (COLS / 8), t % (COLS / 8) * 8, x);
-      if (both) __builtin_memcpy(at, x, 32);
     }
-    __syncthreads();
-    if (!both) return;
+    if (!both) {
+      __syncthreads();
+      return;
+    }
     // four lanes take 32 rows of a column, whose pairs lie side by side
 #pragma unroll 2
     for (int t = threadIdx.x; t < 64 * COLS / 8; t += THREADS) {

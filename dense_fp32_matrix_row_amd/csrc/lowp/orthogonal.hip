@@ -1,26 +1,41 @@
 // orthogonal.hip -- hip_orthogonalize: Newton-Schulz products on the matrix
 // cores with operands as pairs of halfs.
 //
-// A number x of the iterate is kept as hi + lo with halfs hi = RN(s x), lo =
-// RN(s x - hi) for a fixed power of two s: 22 significant bits while |s x| is
-// between 2^-3 and 65504, an absolute 2^-25 below (a half's least step is
-// 2^-24).  That is 2^-37 of |X_0|_F = 1, whose elements are 2^-12 in the mean for
-// 4096 x 4096.  The sums are float.  Three half products an element (hi hi',
-// hi lo', lo hi') run at a third of the half rate, three times the float matrix
-// rate (4096 x 4096: 443 TFLOP/s of the products asked for, against 150), and
-// err no more than float products do.
+// A number x of a matrix is kept as hi + lo with halfs hi = RN(s x), lo =
+// RN(s x - hi) for a power of two s: 22 significant bits while |s x| is between
+// 2^-3 and 65504, an absolute 2^-25 below (a half's least step is 2^-24).  The sums
+// are float.  Three half products an element (hi hi', hi lo', lo hi') run at a
+// third of the half rate, three times the float matrix rate (4096 x 4096: 425
+// TFLOP/s of the products asked for, against 150), and err no more than float
+// products do (4096 x 4096, five steps: 3.3e-6 of the norm against 4.8e-6).
+//
+// So that rows and columns much smaller than the rest keep their bits, X is kept
+// as X^ = D^-1 X and X~ = D^-1 X E^-1 with powers of two D (rows) and E (columns)
+// near the square roots of the rows' and columns' norms.  An element is at most the
+// smaller of its row's and its column's norm, so at most the product of the roots:
+// nothing leaves the range, and a row 2^-40 of the largest is 2^-20 of it here (512 x 1024,
+// five steps, one row in 16 smaller by 1e-4, 1e-6, 1e-9: those rows off by 5e-7,
+// 5e-7, 6e-6 of their norm, with D = E = 1 by 3e-5, 3e-3 and all; float products
+// 8e-7).  It costs 3 % at 4096 x 4096, about half of it power: more bits are set.
+// The roots come from the largest elements, norm <= sqrt(n) max |x|, and grow with
+// the steps as the polynomial lets a norm grow at most; s of each matrix is the
+// largest power of two that its bound allows (schedule()).
 //
 // Per step, with m <= n the sides of the iterate X and X^T kept beside it, all
 // operands have their K side contiguous:
-//   S = X X^T               (m x m, K = n; symmetric: the lower tiles, mirrored)
-//   P = a + b S + c S S     (m x m, K = m; S is its own transpose; symmetric)
-//   X' = P X                (m x n, K = m; X^T is the other operand), written
-//                           as X' over X, which is not read, and as X'^T into
-//                           the other of two buffers.
+//   U = D^-1 S = X^ X^^T D            (m x m, K = n; X^ X^^T is symmetric: the lower
+//                                     tiles, mirrored)
+//   P~ = D^-1 P D = a + (b U + c U U^T D) D  with P = a + b S + c S S
+//                                     (m x m, K = m; U U^T is symmetric)
+//   D^-1 X' E^-1 = P~ X~              (m x n, K = m; X~^T is the other operand),
+//                                     written as X^' over X^, which is not read,
+//                                     and as X~'^T into the other of two buffers.
 #include "../../../include/orthogonal.h"
 #include "lowp.h"
 #include "nt_direct.h"
 #include "nt_loop.h"
+
+#include <cmath>
 
 namespace sgemm {
 namespace {
@@ -28,9 +43,12 @@ namespace {
 using nt::Side;
 using nt::v4f;
 
-constexpr float kScaleX = 0x1p12f;  // |X| < 16
-constexpr float kScaleS = 0x1p8f;   // |S|, |P| < 255
-constexpr int kNormBlocks = 1024;
+// The norms' pass: a block takes kNormRows x 256 elements at a time.  Of each side as
+// many parts as that needs, but columns at most 64, rows at most 256 and such that
+// all are about 1024: what follows reads all parts of 64 rows and columns in every
+// block.
+constexpr int kNormRows = 16, kMaxColParts = 64, kMaxRowParts = 256, kNormBlocks = 1024;
+constexpr int kLeastExponent = -120;  // of a row's or column's norm: its root's inverse stays a float
 
 __host__ __device__ inline int64_t pad32(int64_t n) { return (n + 31) / 32 * 32; }
 
@@ -57,6 +75,18 @@ __device__ __forceinline__ void store_pair(uint8_t* row, int64_t k, float v) {
   *reinterpret_cast<_Float16*>(at + 64) = lo;
 }
 
+// From a matrix that the kernel does not write: such loads need not wait for the
+// stores before them.
+template <class V>
+__device__ __forceinline__ V load_unwritten(const uint8_t* at) {
+  return *reinterpret_cast<const __attribute__((address_space(4))) V*>(reinterpret_cast<uintptr_t>(at));
+}
+
+__device__ __forceinline__ float load_pair(const uint8_t* row, int64_t k) {
+  const uint8_t* at = row + pair_at(k);
+  return static_cast<float>(load_unwritten<_Float16>(at)) + static_cast<float>(load_unwritten<_Float16>(at + 64));
+}
+
 // Four neighbours from k, a multiple of 4.
 __device__ __forceinline__ void store_pairs(uint8_t* row, int64_t k, v4f v) {
   Pack<4, _Float16> hi, lo;
@@ -67,14 +97,29 @@ __device__ __forceinline__ void store_pairs(uint8_t* row, int64_t k, v4f v) {
   *reinterpret_cast<uint2*>(at + 64) = __builtin_bit_cast(uint2, lo);
 }
 
+// Eight neighbours from k, a multiple of 8: two stores of 16 bytes.
+__device__ __forceinline__ void store_pairs8(uint8_t* row, int64_t k, const float (&v)[8]) {
+  Pack<8, _Float16> hi, lo;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split(v[i], hi.v[i], lo.v[i]);
+  uint8_t* at = row + pair_at(k);
+  *reinterpret_cast<uint4*>(at) = __builtin_bit_cast(uint4, hi);
+  *reinterpret_cast<uint4*>(at + 64) = __builtin_bit_cast(uint4, lo);
+}
+
 __device__ __forceinline__ v4f load_pairs(const uint8_t* row, int64_t k) {
   const uint8_t* at = row + pair_at(k);
-  const auto hi = __builtin_bit_cast(Pack<4, _Float16>, *reinterpret_cast<const uint2*>(at));
-  const auto lo = __builtin_bit_cast(Pack<4, _Float16>, *reinterpret_cast<const uint2*>(at + 64));
-  v4f v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = static_cast<float>(hi.v[i]) + static_cast<float>(lo.v[i]);
-  return v;
+  typedef _Float16 v4h __attribute__((ext_vector_type(4)));
+  const v4h hi = load_unwritten<v4h>(at), lo = load_unwritten<v4h>(at + 64);
+  return __builtin_convertvector(hi, v4f) + __builtin_convertvector(lo, v4f);
+}
+
+// Eight, from a multiple of 8.
+typedef float v8f __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ v8f load_pairs8(const uint8_t* row, int64_t k) {
+  const uint8_t* at = row + pair_at(k);
+  const nt::v8h hi = load_unwritten<nt::v8h>(at), lo = load_unwritten<nt::v8h>(at + 64);
+  return __builtin_convertvector(hi, v8f) + __builtin_convertvector(lo, v8f);
 }
 
 struct Source {
@@ -92,68 +137,169 @@ __device__ __forceinline__ double block_sum(double v, double (&s)[4]) {
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// The sum of squares of a matrix, in doubles: every block a part, in a fixed
-// order (no atomics).  Bound by memory: 4096 x 4096 floats in 13.8 us, 4.9 TB/s.
+// The sums of squares of a matrix's parts, in doubles, and of each row within a
+// part's columns, and each column within its rows, the largest magnitude's upper
+// sixteen bits, rounded up (as integers they order like the values, infinities and
+// NaNs above; all of the latter become 0x7f81).
+struct Lines {
+  double* sum;                  // [batch][parts_r][parts_c]
+  uint16_t *row_top, *col_top;  // [batch][parts_c][rows], [batch][parts_r][cols]
+  int parts_r, parts_c, span_r, span_c;
+};
+__device__ __forceinline__ uint16_t top16(uint32_t top) { return static_cast<uint16_t>(min((top + 0xffffu) >> 16, 0x7f81u)); }
+
+// No atomics, so the same sums every time.  Bound by memory: 4096 x 4096 floats in
+// 16.6 us, 4.0 TB/s (13.6 for the sums alone); 256 x 256 in 3.8.
 template <class T>
-__global__ __launch_bounds__(256) void k_norm(Source src, double* part, int parts) {
+__global__ __launch_bounds__(256) void k_norm(Source src, Lines lines) {
+  __shared__ uint32_t col_top[8][256];
   const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
-  // sixteen neighbours a thread and turn
-  const int groups = static_cast<int>(ceil_div(src.cols, 16));
-  const int64_t items = int64_t(src.rows) * groups;
+  const int pr = blockIdx.x / lines.parts_c, pc = blockIdx.x % lines.parts_c;
+  const int row0 = pr * lines.span_r, rows = min(lines.span_r, src.rows - row0);
+  const int col0 = pc * lines.span_c, cols = min(lines.span_c, src.cols - col0);
+  const int lane = threadIdx.x % 32, rg = threadIdx.x / 32;
+  uint16_t* const to_rows = lines.row_top + (int64_t(blockIdx.y) * lines.parts_c + pc) * src.rows + row0;
+  uint16_t* const to_cols = lines.col_top + (int64_t(blockIdx.y) * lines.parts_r + pr) * src.cols + col0;
   double sum = 0;
-  for (int64_t it = int64_t(blockIdx.x) * 256 + threadIdx.x; it < items; it += int64_t(parts) * 256) {
-    const int64_t row = it / groups;
-    const int col = static_cast<int>(it % groups) * 16;
-    const T* p = g + row * src.ld + col;
-    if (col + 16 <= src.cols) {
-      const Pack<16, T> v = load_pack<16>(p);
+  for (int c0 = 0; c0 < cols; c0 += 256) {
+    const int c = c0 + lane * 8, have = cols - c;  // this thread's columns
+    uint32_t ctop[8] = {};
+    for (int r0 = 0; r0 < rows; r0 += kNormRows) {
+      constexpr int kEach = kNormRows / 8;
+      Pack<8, T> v[kEach];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const double x = to_float(v.v[i]);
-        sum = fma(x, x, sum);
+      for (int p = 0; p < kEach; ++p) {
+        const int r = r0 + 8 * p + rg;
+        const T* from = g + (row0 + r) * src.ld + col0 + c;
+        v[p] = Pack<8, T>{};
+        if (r < rows && have >= 8) {
+          v[p] = load_pack<8>(from);
+        } else if (r < rows) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (i < have) v[p].v[i] = from[i];
+        }
       }
-    } else {
-      for (int i = 0; i < src.cols - col; ++i) {
-        const double x = to_float(p[i]);
-        sum = fma(x, x, sum);
+#pragma unroll
+      for (int p = 0; p < kEach; ++p) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = to_float(v[p].v[i]);
+          const uint32_t m = magnitude(f);
+          const double x = f;
+          sum = fma(x, x, sum);
+          top = max(top, m);
+          ctop[i] = max(ctop[i], m);
+        }
+        top = max16(top);
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
+        const int r = r0 + 8 * p + rg;  // always this half wavefront's
+        if (lane == 0 && r < rows) to_rows[r] = c0 ? max(to_rows[r], top16(top)) : top16(top);
       }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) col_top[rg][lane * 8 + i] = ctop[i];
+    __syncthreads();
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, col_top[i][threadIdx.x]);
+    if (c0 + static_cast<int>(threadIdx.x) < cols) to_cols[c0 + threadIdx.x] = top16(top);
+    __syncthreads();
   }
   __shared__ double s[4];
   sum = block_sum(sum, s);
-  if (threadIdx.x == 0) part[int64_t(blockIdx.y) * kNormBlocks + blockIdx.x] = sum;
+  if (threadIdx.x == 0) lines.sum[int64_t(blockIdx.y) * gridDim.x + blockIdx.x] = sum;
 }
 
 // 1 / (|G|_F + eps) from the parts; all threads of a 256-thread block call it.  In
 // double, and x times it too: the norm of finite floats can pass a float's largest
 // number or lie below its normal ones.
-__device__ __forceinline__ double factor(const double* part, int parts, float eps, double (&s)[4]) {
+__device__ __forceinline__ double factor(const Lines& lines, float eps, double (&s)[4]) {
+  const int parts = lines.parts_r * lines.parts_c;
   double sum = 0;
-  for (int p = threadIdx.x; p < parts; p += 256) sum += part[int64_t(blockIdx.y) * kNormBlocks + p];
+#pragma unroll 4
+  for (int p = threadIdx.x; p < parts; p += 256) sum += lines.sum[int64_t(blockIdx.y) * parts + p];
   return 1.0 / (sqrt(block_sum(sum, s)) + eps);
 }
 
+// 2^e of an exponent within a float's normal ones.
+__device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// The exponent of a row's or column's root: half its norm's, p at the start and
+// `grown` more by now, rounded up, at most 0.
+__device__ __forceinline__ int root(int p, int grown) { return min((p + grown + 1) >> 1, 0); }
+
+// The largest of a line's parts, `stride` apart, that this wavefront of four takes.
+__device__ __forceinline__ uint32_t top_of(const uint16_t* from, int64_t stride, int parts, int wave) {
+  uint32_t top = 0;
+  for (int p0 = wave; p0 < parts; p0 += 32) {
+    uint32_t v[8];  // together: one trip to memory
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = min(p0 + 4 * i, parts - 1);
+      v[i] = from[p * stride];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, v[i]);
+  }
+  return top;
+}
+
+// An exponent e with n elements of at most `top` times `by` below 2^e in the 2-norm;
+// root_n: sqrt(n).
+__device__ __forceinline__ int norm_exponent(uint32_t top, double by, double root_n) {
+  const double v = __uint_as_float(top << 16) * by * root_n;
+  if (!(v < 1.0)) return 0;  // NaN among them: all is lost anyway
+  return v > 0.0 ? max(__builtin_amdgcn_frexp_exp(v), kLeastExponent) : kLeastExponent;
+}
+
 // X_0 as pairs, as G lies (`direct`: rows of G) and transposed (`across`), a
-// 64 x 64 tile a block through LDS; both padded with zeros.  Bound by memory:
-// 4096 x 4096 floats, 192 MiB, in 38.5 us (5.2 TB/s; 44.9 with the loads behind
-// the norm), 256 x 256 in 4.8 us (7.0).
+// 64 x 64 tile a block through LDS; both padded with zeros.  The one that is X^
+// (across for a tall G) is divided by its rows' roots, the one that is X~^T by both
+// sides'.  The first tiles of a row or column leave its exponent for what follows.
+// Bound by memory: 4096 x 4096 floats, 192 MiB, in 37 us (5.4 TB/s; 46 with the
+// tops' parts loaded one after the other), 256 x 256 in 6.3.
 template <class T>
-__global__ __launch_bounds__(256) void k_start(Source src, const double* part, int parts, float eps, Pairs direct,
-                                               Pairs across, int tiles_c) {
+__global__ __launch_bounds__(256) void k_start(Source src, Lines lines, float eps, float scale, Pairs direct, Pairs across,
+                                               int* row_exponent, int* col_exponent, int64_t row_batch, int64_t col_batch,
+                                               double root_rows, double root_cols, int tiles_c) {
   __shared__ double s[4];
   __shared__ float t[64][65];
+  __shared__ uint32_t top[2][4][64];
+  __shared__ float line[2][64];  // 1 / root of the rows, of the columns
   const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
   const int r0 = blockIdx.x / tiles_c * 64, c0 = blockIdx.x % tiles_c * 64;
+  const int at = threadIdx.x % 64, wave = threadIdx.x / 64;
   T x[16];  // under way while the norm's parts are added
 #pragma unroll
   for (int p = 0; p < 16; ++p) {
-    const int r = p * 4 + threadIdx.x / 64, c = threadIdx.x % 64;
+    const int r = p * 4 + wave, c = at;
     x[p] = T{};
     if (r0 + r < src.rows && c0 + c < src.cols) x[p] = g[(r0 + r) * src.ld + c0 + c];
   }
-  const double by = factor(part, parts, eps, s) * kScaleX;
+  const int row = min(r0 + at, src.rows - 1), col = min(c0 + at, src.cols - 1);
+  top[0][wave][at] = top_of(lines.row_top + int64_t(blockIdx.y) * lines.parts_c * src.rows + row, src.rows, lines.parts_c, wave);
+  top[1][wave][at] = top_of(lines.col_top + int64_t(blockIdx.y) * lines.parts_r * src.cols + col, src.cols, lines.parts_r, wave);
+  const double by = factor(lines, eps, s);  // which waits for all threads
+  if (wave < 2) {
+    const uint32_t most = max(max(top[wave][0][at], top[wave][1][at]), max(top[wave][2][at], top[wave][3][at]));
+    const int e = norm_exponent(most, by, wave ? root_rows : root_cols);
+    line[wave][at] = power(-root(e, 0));
+    if (wave == 0 && c0 == 0 && r0 + at < src.rows) row_exponent[blockIdx.y * row_batch + r0 + at] = e;
+    if (wave == 1 && r0 == 0 && c0 + at < src.cols) col_exponent[blockIdx.y * col_batch + c0 + at] = e;
+  }
+  __syncthreads();
+  const bool tall = src.rows > src.cols;
+  // x by in floats: a power of two first, which brings x near its place exactly (but
+  // what lies 2^-126 below the norm), then what is left of the factor, rounded
+  const double first = __builtin_amdgcn_ldexp(1.0, min(max(__builtin_amdgcn_frexp_exp(by), -120), 120));
+  const float to_place = static_cast<float>(first), left = static_cast<float>(by / first) * scale;
 #pragma unroll
-  for (int p = 0; p < 16; ++p) t[p * 4 + threadIdx.x / 64][threadIdx.x % 64] = static_cast<float>(to_float(x[p]) * by);
+  for (int p = 0; p < 16; ++p) {
+    const int r = p * 4 + wave;
+    t[r][at] = to_float(x[p]) * to_place * (left * (tall ? line[1][at] : line[0][r]));
+  }
   __syncthreads();
   uint8_t* dp = direct.p + blockIdx.y * direct.batch;
   uint8_t* ap = across.p + blockIdx.y * across.batch;
@@ -161,19 +307,19 @@ __global__ __launch_bounds__(256) void k_start(Source src, const double* part, i
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
     const int r = p * 16 + threadIdx.x / 16, c = threadIdx.x % 16 * 4;
+    const float d = tall ? line[0][r] : 1.0f, a = tall ? 1.0f : line[1][r];
     if (r0 + r < src.rows && c0 + c < dpad)
-      store_pairs(dp + (r0 + r) * direct.ld, c0 + c, v4f{t[r][c], t[r][c + 1], t[r][c + 2], t[r][c + 3]});
+      store_pairs(dp + (r0 + r) * direct.ld, c0 + c, v4f{t[r][c] * d, t[r][c + 1] * d, t[r][c + 2] * d, t[r][c + 3] * d});
     if (c0 + r < src.cols && r0 + c < apad)
-      store_pairs(ap + (c0 + r) * across.ld, r0 + c, v4f{t[c][r], t[c + 1][r], t[c + 2][r], t[c + 3][r]});
+      store_pairs(ap + (c0 + r) * across.ld, r0 + c, v4f{t[c][r] * a, t[c + 1][r] * a, t[c + 2][r] * a, t[c + 3][r] * a});
   }
 }
 
 // steps == 0: G / (|G|_F + eps).
 template <class T>
-__global__ __launch_bounds__(256) void k_divide(Source src, const double* part, int parts, float eps, T* x,
-                                                int64_t ldx, int64_t batch_x) {
+__global__ __launch_bounds__(256) void k_divide(Source src, Lines lines, float eps, T* x, int64_t ldx, int64_t batch_x) {
   __shared__ double s[4];
-  const double by = factor(part, parts, eps, s);
+  const double by = factor(lines, eps, s);
   const T* g = static_cast<const T*>(src.g) + blockIdx.y * src.batch;
   const int64_t items = int64_t(src.rows) * src.cols;
   for (int64_t it = int64_t(blockIdx.x) * 256 + threadIdx.x; it < items; it += int64_t(gridDim.x) * 256) {
@@ -182,103 +328,177 @@ __global__ __launch_bounds__(256) void k_divide(Source src, const double* part, 
   }
 }
 
-// Eight neighbours from k, a multiple of 8: two stores of 16 bytes.
-__device__ __forceinline__ void store_pairs8(uint8_t* row, int64_t k, const float (&v)[8]) {
-  Pack<8, _Float16> hi, lo;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) split(v[i], hi.v[i], lo.v[i]);
-  uint8_t* at = row + pair_at(k);
-  *reinterpret_cast<uint4*>(at) = __builtin_bit_cast(uint4, hi);
-  *reinterpret_cast<uint4*>(at + 64) = __builtin_bit_cast(uint4, lo);
-}
+// The exponents of the norms of X_0's rows (or columns) and by how much they have
+// grown.
+struct Norms {
+  const int* p;
+  int64_t batch;
+  int size, grown;
+  __device__ __forceinline__ int at(int matrix, int line) const { return p[matrix * batch + min(line, size - 1)]; }
+};
 
-// What becomes of the sums of a symmetric m x m matrix: scaled, `b` times `add`
-// added (if there is one) and `diagonal` on the diagonal, written as pairs at
-// its place and, off the diagonal tiles, mirrored.  Both indexes run on past m
-// to the padding, where zeros go.
+// What a tile's sums are multiplied by, of each of its rows and columns, in LDS: in
+// a row-wise result and in a column-wise one.  The exponents are loaded before the
+// sum, a line a thread, and become factors behind it.
+template <int ROWS, int COLS>
+struct alignas(16) Factors {
+  static constexpr int kLines = ROWS + COLS;
+  float row[ROWS], col[COLS], across[COLS];
+};
+template <int THREADS, int ROWS, int COLS>
+struct Held {
+  static constexpr int kEach = (ROWS + COLS + THREADS - 1) / THREADS;
+  int e[kEach];
+  template <class O>
+  __device__ __forceinline__ Held(const O& out, int r0, int c0) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int l = threadIdx.x + i * THREADS;
+      e[i] = l < ROWS ? out.row_norms().at(out.batch, r0 + l) : out.col_norms().at(out.batch, c0 + l - ROWS);
+    }
+  }
+  template <class O>
+  __device__ __forceinline__ void put(const O& out, Factors<ROWS, COLS>& f) const {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int l = threadIdx.x + i * THREADS;
+      int x = e[i];
+      asm volatile("" : "+v"(x));  // here, and not where it is loaded, is it waited for
+      if (l < ROWS) {
+        f.row[l] = out.by_row(x);
+      } else if (l < ROWS + COLS) {
+        f.col[l - ROWS] = out.by_col(x);
+        f.across[l - ROWS] = out.by_col_across(x);
+      }
+    }
+  }
+};
+
+// What becomes of the sums v of a symmetric m x m matrix at row r, column c: with
+// the root d_c of row c of X
+//   U:   scale v d_c
+//   P~:  (scale v d_c + b U_rc) d_c, and `diagonal` on the diagonal
+// written as pairs at its place and, off the diagonal tiles, at the mirrored one
+// (with d_r, U_cr).  Both indexes run on past m to the padding, where zeros go.
 struct SymmetricOut {
-  Pairs out, add;
+  Pairs out, add;  // add: U, for P~
   int m;
   float scale, b, diagonal;
+  Norms rows;
   int batch;
   bool mirror;
-  __device__ __forceinline__ float value(int r, int c, float v, float old) const {
-    return r < m && c < m ? fmaf(v, scale, b * old) + (r == c ? diagonal : 0.0f) : 0.0f;
+  __device__ __forceinline__ const Norms& row_norms() const { return rows; }
+  __device__ __forceinline__ const Norms& col_norms() const { return rows; }
+  __device__ __forceinline__ float by_row(int e) const { return power(root(e, rows.grown)); }
+  __device__ __forceinline__ float by_col(int e) const { return by_row(e); }
+  __device__ __forceinline__ float by_col_across(int) const { return 0.0f; }
+  __device__ __forceinline__ float value(float v, float old, float d) const {
+    const float x = v * scale * d;
+    return add.p ? fmaf(b, old, x) * d : x;
   }
-  // four neighbours of a row
-  __device__ __forceinline__ void operator()(int r, int c, v4f v) const {
+  __device__ __forceinline__ float value(int r, int c, float v, float old, float d) const {
+    return r < m && c < m ? value(v, old, d) + (r == c ? diagonal : 0.0f) : 0.0f;
+  }
+  // four neighbours of a row; dr, dc: the roots of row r and of columns c ..
+  __device__ __forceinline__ void four(int r, int c, v4f v, float dr, v4f dc, v4f) const {
     if (r >= pad32(m) || c >= pad32(m)) return;
     uint8_t* base = out.p + batch * out.batch;
-    v4f x = {0, 0, 0, 0};
-    if (r < m) {
-      const v4f old = add.p ? load_pairs(add.p + batch * add.batch + r * add.ld, c) : x;
+    const uint8_t* from = add.p + batch * add.batch;
+    v4f old = {}, across = {};
+    if (add.p) {
+      old = load_pairs(from + min(r, m - 1) * add.ld, c);
+      across = old;  // U_rc = U_cr where the roots are alike
+      if (mirror && !(dr == dc[0] && dr == dc[1] && dr == dc[2] && dr == dc[3])) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = value(r, c + i, v[i], old[i]);
+        for (int i = 0; i < 4; ++i) across[i] = load_pair(from + min(c + i, m - 1) * add.ld, r);
+      }
+    }
+    if (r < m) {
+      v4f x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = value(r, c + i, v[i], old[i], dc[i]);
       store_pairs(base + r * out.ld, c, x);
     }
     if (mirror) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (c + i < m) store_pair(base + (c + i) * out.ld, r, x[i]);
+        if (c + i < m) store_pair(base + (c + i) * out.ld, r, value(c + i, r, v[i], across[i], dr));
     }
+  }
+  // eight neighbours of row r, wherever their sums lay (past m these are 0: the large
+  // tiles read zeros there); d: their roots
+  __device__ __forceinline__ void eight(int r, int c, const float (&v)[8], const float* d) const {
+    if (r >= m || c >= pad32(m)) return;
+    v8f old = {};
+    if (add.p) old = load_pairs8(add.p + batch * add.batch + r * add.ld, c);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = value(v[i], old[i], d[i]);
+    if (!mirror) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] += r == c + i ? diagonal : 0.0f;
+    }
+    store_pairs8(out.p + batch * out.batch + r * out.ld, c, x);
   }
   // 64 rows of a tile, from row r0 and column c0
   template <int THREADS, int COLS>
-  __device__ __forceinline__ void sheet(nt::Sheet<COLS>& s, int r0, int c0) const {
-    uint8_t* base = out.p + batch * out.batch;
-    s.template out<THREADS>(
-        mirror,
-        [&](int r, int c, float (&v)[8]) {
-          r += r0, c += c0;
-          if (c >= pad32(m)) return;
-          v4f old[2] = {};
-          if (add.p && r < m) {
-            old[0] = load_pairs(add.p + batch * add.batch + r * add.ld, c);
-            old[1] = load_pairs(add.p + batch * add.batch + r * add.ld, c + 4);
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = value(r, c + i, v[i], old[i / 4][i % 4]);
-          if (r < m) store_pairs8(base + r * out.ld, c, v);
-        },
-        [&](int c, int r, const float (&v)[8]) {
-          if (c0 + c < m && r0 + r < pad32(m)) store_pairs8(base + (c0 + c) * out.ld, r0 + r, v);
-        });
+  __device__ __forceinline__ void sheet(nt::Sheet<COLS>& s, int r0, int c0, const float* dr, const float* dc,
+                                        const float*) const {
+    s.template out<THREADS>(mirror, [&](int r, int c, const float (&v)[8]) { eight(r0 + r, c0 + c, v, dc + c); },
+                            [&](int c, int r, const float (&v)[8]) { eight(c0 + c, r0 + r, v, dr + r); });
   }
 };
 
-// P X: as pairs and transposed pairs, or at the last step as the result.
+// P~ X~ = D^-1 X' E^-1: as pairs X^' and X~'^T under the roots of the next step, or
+// at the last step as the result X'.
 template <class T>
 struct IterateOut {
   Pairs x, xt;
   T* out;  // not NULL at the last step
   int64_t ldo, batch_o;
   int m, n;
+  float scale;  // the sums' scale to the next step's, or to 1
+  Norms rows, cols;
+  int next;  // `grown` of the next step
   int batch;
   bool tall;
-  __device__ __forceinline__ void operator()(int r, int c, v4f v) const {
+  __device__ __forceinline__ const Norms& row_norms() const { return rows; }
+  __device__ __forceinline__ const Norms& col_norms() const { return cols; }
+  // D over the next step's (over 1 for the result); E, and for X~' over the next step's
+  __device__ __forceinline__ float by_row(int e) const {
+    return power(root(e, rows.grown) - (out ? 0 : root(e, next))) * scale;
+  }
+  __device__ __forceinline__ float by_col(int e) const { return power(root(e, cols.grown)); }
+  __device__ __forceinline__ float by_col_across(int e) const {
+    return power(root(e, cols.grown) - (out ? 0 : root(e, next)));
+  }
+  // four neighbours of a row; d, e, f: the factors of row r, of columns c .. in X^', in X~'
+  __device__ __forceinline__ void four(int r, int c, v4f v, float d, v4f e, v4f f) const {
     if (r >= pad32(m) || c >= pad32(n)) return;
     v4f y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = r < m && c + i < n ? v[i] * (1.0f / kScaleS) : 0.0f;
+    for (int i = 0; i < 4; ++i) y[i] = r < m && c + i < n ? v[i] * d : 0.0f;
     if (out) {
       if (r >= m) return;
       T* o = out + batch * batch_o;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (c + i < n) from_float(y[i] * (1.0f / kScaleX), tall ? o[(c + i) * ldo + r] : o[r * ldo + c + i]);
+        if (c + i < n) from_float(y[i] * e[i], tall ? o[(c + i) * ldo + r] : o[r * ldo + c + i]);
     } else {
-      if (r < m) store_pairs(x.p + batch * x.batch + r * x.ld, c, y);
       uint8_t* t = xt.p + batch * xt.batch;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (c + i < n) store_pair(t + (c + i) * xt.ld, r, y[i]);
+        if (c + i < n) store_pair(t + (c + i) * xt.ld, r, y[i] * f[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] *= e[i];
+      if (r < m) store_pairs(x.p + batch * x.batch + r * x.ld, c, y);
     }
   }
   // `count` of eight neighbours of the result, from `at`
   __device__ __forceinline__ void result(T* at, int count, const float (&v)[8]) const {
     Pack<8, T> p;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) from_float(v[i] * (1.0f / (kScaleS * kScaleX)), p.v[i]);
+    for (int i = 0; i < 8; ++i) from_float(v[i], p.v[i]);
     if (count >= 8) {
       store_pack(at, p);
     } else {
@@ -288,30 +508,31 @@ struct IterateOut {
     }
   }
   template <int THREADS, int COLS>
-  __device__ __forceinline__ void sheet(nt::Sheet<COLS>& s, int r0, int c0) const {
+  __device__ __forceinline__ void sheet(nt::Sheet<COLS>& s, int r0, int c0, const float* d, const float* e,
+                                        const float* f) const {
     T* o = out + batch * batch_o;
     uint8_t *xp = x.p + batch * x.batch, *tp = xt.p + batch * xt.batch;
     s.template out<THREADS>(
         !out || tall,
-        [&](int r, int c, float (&v)[8]) {
-          r += r0, c += c0;
-          if (out) {
-            if (!tall && r < m && c < n) result(o + r * ldo + c, n - c, v);
-            return;
-          }
-          if (c >= pad32(n)) return;
+        [&](int r, int c, const float (&v)[8]) {
+          const int row = r0 + r, col = c0 + c;
+          if (row >= m || col >= (out ? n : pad32(n)) || (out && tall)) return;
+          const float k = d[r];
+          float y[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = r < m && c + i < n ? v[i] * (1.0f / kScaleS) : 0.0f;
-          if (r < m) store_pairs8(xp + r * x.ld, c, v);
+          for (int i = 0; i < 8; ++i) y[i] = v[i] * k * e[c + i];  // past n: 0, as the sums there
+          if (out) result(o + row * ldo + col, n - col, y);
+          else store_pairs8(xp + row * x.ld, col, y);
         },
         [&](int c, int r, const float (&v)[8]) {
-          r += r0, c += c0;
-          if (c >= n) return;
-          if (!out) {
-            if (r < pad32(m)) store_pairs8(tp + c * xt.ld, r, v);
-          } else if (r < m) {
-            result(o + c * ldo + r, m - r, v);
-          }
+          const int row = r0 + r, col = c0 + c;
+          if (col >= n || row >= (out ? m : pad32(m))) return;
+          const float k = f[c];
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = v[i] * k * d[r + i];
+          if (out) result(o + col * ldo + row, m - row, y);
+          else store_pairs8(tp + col * xt.ld, row, y);
         });
   }
 };
@@ -339,25 +560,37 @@ struct Assembled : nt::Loop<nt::Kind::kPair, MT, NT, WM, WN, STAGES> {
 
 template <class T, class E>
 __device__ __forceinline__ void product(const Side& A, const Side& B, int m0, int n0, int K, const E& epi) {
+  __shared__ Factors<T::BM, T::BN> by;
+  const Held<T::threads, T::BM, T::BN> held(epi, m0, n0);
   if constexpr (T::kDirect) {
     __shared__ typename T::Meet meet;
-    T::run(meet, A, B, m0, n0, K * 4, epi);
+    T::run(meet, A, B, m0, n0, K * 4,
+           [&](int r, int c, v4f v) {
+             float d = by.row[r - m0];
+             v4f e = *reinterpret_cast<const v4f*>(&by.col[c - n0]), f = *reinterpret_cast<const v4f*>(&by.across[c - n0]);
+             asm volatile("" : "+v"(d), "+v"(e), "+v"(f));  // read together, not one by one where they are used
+             epi.four(r, c, v, d, e, f);
+           },
+           [&] { held.put(epi, by); });
   } else {
     __shared__ alignas(16) uint8_t smem[T::kLds];
     nt::v16f acc[T::kAcc];
     nt::loop_sum<T>(smem, A, B, m0, n0, K * 4, acc);
+    held.put(epi, by);
     using Sheet = nt::Sheet<T::BN>;
     static_assert(sizeof(Sheet) <= T::kLds, "a sheet fits");
     Sheet& sheet = *reinterpret_cast<Sheet*>(smem);
     __syncthreads();  // all wavefronts have left the loop
-    nt::loop_sheets<T>(sheet, acc, [&](int top) { epi.template sheet<T::threads>(sheet, m0 + top, n0); });
+    nt::loop_sheets<T>(sheet, acc, [&](int top) {
+      epi.template sheet<T::threads>(sheet, m0 + top, n0, by.row + top, by.col, by.across);
+    });
   }
 }
 
 // S = X X^T and P = a + b S + c S S: the lower tiles, mirrored.  Bound by the
-// matrix rate where the tiles fill the CUs: 4096 x 4096 in 165-175 us on 253 tiles
+// matrix rate where the tiles fill the CUs: 4096 x 4096 in 174-187 us on 253 tiles
 // of 192 x 192 (136 of 256 x 256 would leave half the CUs idle), MfmaUtil 65 %; by
-// the latency of one trip to memory where they are few: 256 x 256 in 4.4 us.
+// the latency of one trip to memory where they are few: 256 x 256 in 4.4-5.0 us.
 template <class T>
 __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_symmetric(Side A, int K, SymmetricOut out) {
   out.batch = blockIdx.y;
@@ -367,8 +600,8 @@ __global__ __launch_bounds__(T::threads, T::kMinWaves) void k_symmetric(Side A, 
   product<T>(A, A, at.tm * T::BM, at.tn * T::BN, K, out);
 }
 
-// X' = P X.  Bound by the matrix rate: 4096 x 4096 in 278 us on 256 tiles of
-// 256 x 256, 1483 TFLOP/s of half products, MfmaUtil 75 %; 1024 x 1024 x 4096 in
+// X' = P X.  Bound by the matrix rate: 4096 x 4096 in 281-292 us on 256 tiles of
+// 256 x 256, 1440 TFLOP/s of half products, MfmaUtil 75 %; 1024 x 1024 x 4096 in
 // 29 us on 256 tiles of 128 x 128, whose 32 steps hardly outlast the first loads
 // and the results' way out.
 template <class T, class O>
@@ -408,10 +641,13 @@ template <class T>
 __global__ __launch_bounds__(256) void k_finish(const float* sums, int tiles, int splits, SymmetricOut out) {
   static_assert(T::MT == 4 && T::NT == 2, "a sheet of 64 rows, two fragments each of four wavefronts");
   __shared__ nt::Sheet<16 * T::NT> sheet;
+  __shared__ Factors<64, 16 * T::NT> by;
   const int tile = blockIdx.x / T::waves, share = blockIdx.x % T::waves, lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const nt::Place at = triangle(tile);
   out.batch = blockIdx.y;
   out.mirror = at.tm != at.tn;
+  const int r0 = at.tm * T::BM + share % T::WM * 64, c0 = at.tn * T::BN + share / T::WM * 16 * T::NT;
+  const Held<256, 64, 16 * T::NT> held(out, r0, c0);
   const float* from = sums + (int64_t(blockIdx.y) * splits * tiles + tile) * (T::BM * T::BN) + share * (T::MT * T::NT * 256) + wave * 512 + lane * 4;
   v4f v[2] = {};
 #pragma unroll 4
@@ -425,7 +661,8 @@ __global__ __launch_bounds__(256) void k_finish(const float* sums, int tiles, in
     const int f = 2 * wave + i;  // fragment j MT + i of the wavefront
     sheet.put(f % T::MT * 16 + lane % 16, f / T::MT * 16 + 4 * (lane / 16), v[i]);
   }
-  out.sheet<256>(sheet, at.tm * T::BM + share % T::WM * 64, at.tn * T::BN + share / T::WM * 16 * T::NT);
+  held.put(out, by);
+  out.sheet<256>(sheet, r0, c0, by.row, by.col, by.across);
 }
 
 // Which tile takes the products of `batch` matrices, by estimates of the time in
@@ -527,12 +764,13 @@ void with_tile(Way way, const F& f) {
   }
 }
 
-// The workspace: per-block parts of the norms, then X, X^T twice, S and P, and the
-// parts of the symmetric products' sums.
+// The workspace: parts of the norms, the rows' and columns' exponents, then X^, X~^T
+// twice, U and P~, and the parts of the symmetric products' sums.
 struct Layout {
-  int m, n;
-  int64_t part, x, xt[2], s, p, sums, bytes;
-  int64_t ldx, ldm;  // bytes of a row of X, and of the others
+  int m, n, parts_r, parts_c, span_r, span_c;
+  int64_t sum, row_top, col_top, p, q, x, xt[2], s, ps, sums, bytes;
+  int64_t ldx, ldm;  // bytes of a row of X^, and of the others
+  int64_t lm, ln;    // exponents of a matrix
 };
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -543,22 +781,89 @@ Layout layout_of(int batch, int rows, int cols) {
   l.n = rows < cols ? cols : rows;
   l.ldx = pad32(l.n) * 4;
   l.ldm = pad32(l.m) * 4;
+  const auto split = [](int size, int unit, int most, int& span) {
+    span = static_cast<int>(ceil_div(ceil_div(size, unit), most)) * unit;
+    return static_cast<int>(ceil_div(size, span > 0 ? span : unit));
+  };
+  const auto rows_of = [&](int size, int parts_c, int& span) {
+    const int most = parts_c > 0 ? kNormBlocks / parts_c : kMaxRowParts;  // 16 to 1024
+    return split(size, kNormRows, most < kMaxRowParts ? most : kMaxRowParts, span);
+  };
+  l.parts_c = split(cols, 256, kMaxColParts, l.span_c);
+  l.parts_r = rows_of(rows, l.parts_c, l.span_r);
+  // as many bytes for G as for its transpose
+  int across_span;
+  const int across_c = split(rows, 256, kMaxColParts, across_span), across_r = rows_of(cols, across_c, across_span);
+  const auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     const int64_t here = at;
     at += up256(bytes);
     return here;
   };
-  l.part = take(int64_t(batch) * kNormBlocks * 8);
+  l.sum = take(batch * most(l.parts_r * l.parts_c, across_r * across_c) * 8);
+  l.row_top = take(batch * most(int64_t(l.parts_c) * rows, int64_t(across_c) * cols) * 2);
+  l.col_top = take(batch * most(int64_t(l.parts_r) * cols, int64_t(across_r) * rows) * 2);
+  l.lm = up256(l.m);
+  l.ln = up256(l.n);
+  l.p = take(batch * l.lm * 4);
+  l.q = take(batch * l.ln * 4);
   l.x = take(batch * (l.m * l.ldx));
   l.xt[0] = take(batch * (l.n * l.ldm));
   l.xt[1] = take(batch * (l.n * l.ldm));
   l.s = take(batch * (l.m * l.ldm));
-  l.p = take(batch * (l.m * l.ldm));
+  l.ps = take(batch * (l.m * l.ldm));
   const int64_t t = ceil_div(l.m, Loop128::BM), tiles = batch * (t * (t + 1) / 2);
   l.sums = take(tiles > 0 && tiles <= 128 ? (256 / tiles < kMaxParts ? 256 / tiles : kMaxParts) * tiles * (Loop128::BM * Loop128::BN * 4) : 0);
   l.bytes = at;
   return l;
+}
+
+// What bounds a step's matrices, from the polynomials a + b x + c x^2 so far: the
+// largest singular value is at most `sigma`, and norms have grown by 2^grown at most.
+struct Step {
+  float x, s, p;  // the scales of X^ and X~, U, P~
+  int grown;
+};
+
+// The largest power of two that keeps numbers up to `bound`, with some room for
+// rounding, within a half.
+float scale_for(double bound) {
+  if (!(bound < 0x1p60)) return 0x1p-60f;
+  return static_cast<float>(std::exp2(std::floor(std::log2(61000.0 / std::fmax(bound, 1.0)))));
+}
+
+// steps + 1 of them; the last one for what a next step would find.
+void schedule(int steps, const float* co, Step* out) {
+  double sigma = 1.0, grown = 0.0;
+  for (int i = 0; i <= steps; ++i) {
+    const double most = std::fmax(sigma, 1.0), square = most * most;
+    // |X^|, |X~| <= most; |U| = |S| over a row's root <= most^2, |U U^T| <= most^4
+    const double a = i < steps ? co[3 * i] : 0, b = i < steps ? co[3 * i + 1] : 0, c = i < steps ? co[3 * i + 2] : 0;
+    out[i].x = scale_for(most);
+    out[i].s = scale_for(square);
+    out[i].p = scale_for(std::fabs(a) + std::fabs(b) * square + std::fabs(c) * square * square);
+    out[i].grown = grown < 1000 ? static_cast<int>(std::ceil(grown)) : 1000;
+    // the largest |p(x)| and sqrt(x) |p(x)| over 0 <= x <= sigma^2: at the ends or where they are flat
+    const auto poly = [&](double x) { return std::fabs(a + b * x + c * x * x); };
+    const double end = sigma * sigma;
+    double grow = std::fmax(poly(0), poly(end)), next = sigma * poly(end);
+    const auto flat = [&](double x, bool root) {
+      if (!(x > 0 && x < end)) return;
+      if (root) next = std::fmax(next, std::sqrt(x) * poly(x));
+      else grow = std::fmax(grow, poly(x));
+    };
+    if (c != 0) flat(-b / (2 * c), false);
+    const double disc = 9 * b * b - 20 * a * c;  // of a + 3 b x + 5 c x^2
+    if (c != 0 && disc >= 0) {
+      flat((-3 * b + std::sqrt(disc)) / (10 * c), true);
+      flat((-3 * b - std::sqrt(disc)) / (10 * c), true);
+    } else if (c == 0 && b != 0) {
+      flat(-a / (3 * b), true);
+    }
+    if (grow > 1) grown += std::log2(grow);
+    sigma = next;
+  }
 }
 
 int check_sizes(int batch, int rows, int cols, int type) {
@@ -573,24 +878,28 @@ template <class T>
 hipError_t launch(int batch, const Source& src, int steps, const float* co, float eps, T* x, int64_t ldx,
                   int64_t batch_x, uint8_t* ws, hipStream_t stream) {
   const Layout l = layout_of(batch, src.rows, src.cols);
-  double* part = reinterpret_cast<double*>(ws + l.part);
-  const int64_t groups = int64_t(src.rows) * ceil_div(src.cols, 16);
-  const int parts = static_cast<int>(ceil_div(groups, 256) < kNormBlocks ? ceil_div(groups, 256) : kNormBlocks);
-  hipLaunchKernelGGL((k_norm<T>), dim3(parts, batch), dim3(256), 0, stream, src, part, parts);
+  const Lines lines{reinterpret_cast<double*>(ws + l.sum), reinterpret_cast<uint16_t*>(ws + l.row_top),
+                    reinterpret_cast<uint16_t*>(ws + l.col_top), l.parts_r, l.parts_c, l.span_r, l.span_c};
+  hipLaunchKernelGGL((k_norm<T>), dim3(l.parts_r * l.parts_c, batch), dim3(256), 0, stream, src, lines);
   if (steps == 0) {
     const int64_t blocks = ceil_div(int64_t(src.rows) * src.cols, 256);
     hipLaunchKernelGGL((k_divide<T>), dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), batch), dim3(256), 0,
-                       stream, src, part, parts, eps, x, ldx, batch_x);
+                       stream, src, lines, eps, x, ldx, batch_x);
     return hipGetLastError();
   }
   const bool tall = src.rows > src.cols;
   const Pairs X{ws + l.x, l.ldx, l.m * l.ldx};
   Pairs XT{ws + l.xt[0], l.ldm, l.n * l.ldm}, XT2{ws + l.xt[1], l.ldm, l.n * l.ldm};
-  const Pairs S{ws + l.s, l.ldm, l.m * l.ldm}, P{ws + l.p, l.ldm, l.m * l.ldm};
+  const Pairs S{ws + l.s, l.ldm, l.m * l.ldm}, P{ws + l.ps, l.ldm, l.m * l.ldm};
+  int *const p = reinterpret_cast<int*>(ws + l.p), *const q = reinterpret_cast<int*>(ws + l.q);
+  Step step[HIP_ORTHOGONAL_MAX_STEPS + 1];
+  schedule(steps, co, step);
   // 64-wide tiles: both paddings (to 32) lie inside them
   const int64_t tr = ceil_div(src.rows, 64), tc = ceil_div(src.cols, 64);
-  hipLaunchKernelGGL((k_start<T>), dim3(static_cast<unsigned>(tr * tc), batch), dim3(256), 0, stream, src, part, parts,
-                     eps, tall ? XT : X, tall ? X : XT, static_cast<int>(tc));
+  hipLaunchKernelGGL((k_start<T>), dim3(static_cast<unsigned>(tr * tc), batch), dim3(256), 0, stream, src, lines, eps,
+                     step[0].x, tall ? XT : X, tall ? X : XT, tall ? q : p, tall ? p : q, tall ? l.ln : l.lm,
+                     tall ? l.lm : l.ln, std::sqrt(static_cast<double>(src.rows)), std::sqrt(static_cast<double>(src.cols)),
+                     static_cast<int>(tc));
   const auto side = [](const Pairs& p, int rows) { return Side{p.p, p.ld, rows, nullptr, 0, 0, 0, p.batch}; };
   const int km = static_cast<int>(pad32(l.m)), kn = static_cast<int>(pad32(l.n));
   const Plan choice = plan(batch, l.m, l.n);
@@ -619,11 +928,15 @@ hipError_t launch(int batch, const Source& src, int steps, const float* co, floa
   };
   for (int i = 0; i < steps; ++i) {
     const float a = co[3 * i], b = co[3 * i + 1], c = co[3 * i + 2];
+    const Step &now = step[i], &next = step[i + 1];
+    const Norms rows{p, l.lm, l.m, now.grown}, cols{q, l.ln, l.n, now.grown};
     symmetric(choice.s, side(X, l.m), kn,
-              SymmetricOut{S, Pairs{nullptr, 0, 0}, l.m, kScaleS / (kScaleX * kScaleX), 0.0f, 0.0f, 0, false});
-    symmetric(choice.p, side(S, l.m), km, SymmetricOut{P, S, l.m, c / kScaleS, b, a * kScaleS, 0, false});
+              SymmetricOut{S, Pairs{nullptr, 0, 0}, l.m, now.s / (now.x * now.x), 0.0f, 0.0f, rows, 0, false});
+    symmetric(choice.p, side(S, l.m), km,
+              SymmetricOut{P, S, l.m, c * (now.p / (now.s * now.s)), b * (now.p / now.s), a * now.p, rows, 0, false});
     const bool last = i + 1 == steps;
-    const IterateOut<T> out{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, 0, tall};
+    const IterateOut<T> out{X, XT2, last ? x : nullptr, ldx, batch_x, l.m, l.n, (last ? 1.0f : next.x) / (now.p * now.x),
+                            rows, cols, next.grown, 0, tall};
     iterate(side(P, l.m), side(XT, l.n), 0, choice.cut ? choice.cut : l.n, choice.x.way, out);
     if (choice.cut) iterate(side(P, l.m), side(XT, l.n), choice.cut, l.n - choice.cut, choice.rest, out);
     const Pairs t = XT;

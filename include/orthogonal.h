@@ -50,12 +50,15 @@ int hip_orthogonalize_workspace(int batch, int rows, int cols, int type, long lo
  * matrix with an infinity or NaN gives NaN throughout; for steps 0 a NaN makes
  * all elements NaN, an infinity only the infinite ones (finite ones become 0).
  *
- * The norm is summed, and divided by, in double.  The iterate and the products' operands are
- * kept as pairs of halfs, 22 significant bits, and multiplied on the
- * matrix cores with float sums; their fixed-point range asks for
- * |X_i| < 16, |S|, |a + b S + c S^2| < 255 element by element, which every
- * convergent polynomial keeps (the singular values of X_0 are at most 1);
- * where a polynomial leaves it the result is infinite or NaN.
+ * The norm is summed, and divided by, in double.  The products' operands are
+ * kept as pairs of halfs and multiplied on the matrix cores with float sums.  A
+ * pair has 22 significant bits of numbers down to 2^-18 of its matrix's range and
+ * an absolute 2^-40 of the range below; each row and each column of X_i is
+ * scaled by the root of its norm first, so that a row or column is computed as
+ * float products would compute it, relative to its own norm, while that is above
+ * 1e-7 of the largest, and loses a bit for each factor of 4 below.  The ranges
+ * follow the polynomials' bounds on the singular values, which in X_0 are at most
+ * 1: a polynomial may let them grow, until a float sum overflows (infinities, NaN).
  *
  * Status codes: 0 enqueued; -i the i-th argument is invalid (numbered from 1:
  * batch, rows, cols, type, G, ldg, stride_g, steps, coefficients, eps, X, ldx,
