@@ -205,6 +205,8 @@ def _empty(rows, cols, block_rows, scale, device):
     of one block column side by side.  And the row stride."""
     import torch
     ld = max(_ceil(cols, 16) * 16, 16)
+    if ld >= 1 << 31:  # more than a stride can be, and than a product takes
+        ld = cols
     q = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)
     if ld != cols:
         q = q[:, :cols]
