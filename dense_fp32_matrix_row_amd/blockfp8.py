@@ -17,7 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
-from typing import Optional, Tuple
+from typing import Tuple
 
 from . import sgemm as _sgemm
 

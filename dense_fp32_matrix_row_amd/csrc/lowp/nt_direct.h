@@ -23,7 +23,6 @@ struct Direct {
   static constexpr int MT = MT_, NT = NT_, WAVES = WAVES_;
   static constexpr int BM = 16 * MT, BN = 16 * NT, threads = 64 * WAVES;
   static constexpr int kFrags = MT * NT;
-  static constexpr int kOwn = (kFrags + WAVES - 1) / WAVES;  // fragments of D a wavefront finishes
   static constexpr int kChunk = kFrags < 8 ? kFrags : 8;     // fragments that meet at a time
   static constexpr bool kScaled = P::kScaleBytes > 0;
   static constexpr int kSn = !kScaled ? 0 : !P::kRowScales || P::kUniform ? 1 : 4;  // scales a lane takes of 16 rows of B

@@ -551,11 +551,12 @@ struct Small : nt::Direct<nt::HalfPair, T, T, 8> {
   static constexpr bool kDirect = true;
   static constexpr int kMinWaves = 2;
 };
-// Large ones, with their loop in assembly; several wavefronts a SIMD where registers allow.
+// Large ones, with their loop in assembly; LDS holds one block a CU, so of four
+// wavefronts one a SIMD, of eight two.
 template <int MT, int NT, int WM, int WN, int STAGES>
 struct Assembled : nt::Loop<nt::Kind::kPair, MT, NT, WM, WN, STAGES> {
   static constexpr bool kDirect = false;
-  static constexpr int kMinWaves = 2;
+  static constexpr int kMinWaves = WM * WN / 4;
 };
 
 template <class T, class E>
