@@ -275,7 +275,9 @@ def _operand(name, o):
 def gemm(a: BlockFp8, b: BlockFp8, c=None, alpha: float = 1.0, beta: float = 0.0, out=None, out_dtype=None):
     """alpha * a @ b^T + beta * c as a new tensor, or in `out` (which may be c).
 
-    The result's type is out's, c's, or out_dtype (default bfloat16)."""
+    The result's type is out's, c's, or out_dtype (default bfloat16).  The sums of
+    a 16-bit result cut products 13 bits below the largest of eight neighbours;
+    who wants a float's sums takes a float32 result and rounds it."""
     import torch
     M, K, left = _operand("a", a)
     N, L, right = _operand("b", b)
