@@ -78,13 +78,14 @@ struct Out {
   }
 };
 
-// Large tiles.  On one MI355X, kernels alone: 4096^3 with float scales 58-60 us
+// Large tiles.  On one MI355X, kernels alone: 4096^3 with float scales 58-61 us
 // (2300 TFLOP/s; each product's vector instructions of scaling take issue slots
-// beside the matrix instruction), 8192^3 with power-of-two scales, which need none,
-// 377-470 us from box to box (2340-2900 TFLOP/s; MfmaUtil 77 %, the clock is down to
-// about 1.75 GHz: power), 4096^3 with a float result 127 us (1078 TFLOP/s; 276 vector
-// instructions a wavefront and step widen and scale beside 64 matrix ones, and more
-// than two a matrix instruction take its time: four make 7.5 ns 11.8).
+// beside the matrix instruction; 68 where B has a scale a row, two instructions a
+// result), 8192^3 with power-of-two scales, which need none, 381-476 us (2310-2890
+// TFLOP/s, the clock down to about 1.75 GHz: power; MfmaUtil 77 %), 4096^3 with a
+// float result 117-134 us (1030-1170 TFLOP/s; 276 vector instructions a wavefront and
+// step widen and scale beside 64 matrix ones, and more than two a matrix instruction
+// take its time: four make 7.5 ns 11.8).
 template <class L, class O>
 __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, Out<O> out, int tiles_m, int tiles_n) {
   __shared__ alignas(16) uint8_t smem[L::kLds];
@@ -149,8 +150,12 @@ struct Part {
 };
 
 // Small tiles.  Bound by a launch and one trip to memory, or the weight's read:
-// 1 x 4096 x 4096 in 4.9 us (3.4 TB/s; 16 x 16 tiles, 256 blocks), 256 x 1024 x
-// 1024 in 4.9 us (32 x 32, 256 blocks).
+// 1 x 4096 x 4096 in 4.4-5.3 us (3.2-3.8 TB/s; 16 x 16 tiles, 256 blocks), 256 x
+// 1024 x 1024 in 4.3-5.1 us (32 x 32, 256 blocks).  The 64 x 64 tile is short of
+// registers: with a scale for each row of B, and for float results with any, some
+// of 13 to 73 registers that do not fit come and go in the loop (1024 x 1024 x 4096
+// bf16 15 us with one scale for B's rows or powers of two, 22 with a float each;
+// float 19-21, 31 and 46).
 template <class D, class O>
 __global__ __launch_bounds__(D::threads, 2) void k_direct(Side A, Side B, int K, Out<O> out, Part part, int64_t tiles) {
   __shared__ typename D::Meet meet;
@@ -182,9 +187,11 @@ void launch_direct(const Side& A, const Side& B, int K, const Out<O>& out, int m
 // Which tile takes a product, by estimates of the time in us: of a small tile
 // (16, 32 or 64 square) what a launch takes, what one of its wavefronts' steps
 // takes alone, and what a step of one block takes among many; of a large one
-// what a step takes alone and in a full round over the 256 CUs.  Measured over
-// 28 sizes from 1 x 4096 x 4096 to 4096^3 of each kind, which they meet within
-// a quarter.  16-bit results; float ones, whose codes are widened.
+// what a step takes alone and in a full round over the 256 CUs.  The constants are
+// fitted.  Of 160 products measured since (20 sizes from 1 x 4096 x 4096 to 8192^3,
+// 16-bit and float results, both scales, B in blocks of 1 and 128) four in five took
+// between 0.8 and 1.25 of the estimate; 1024 x 1024 x 32768 mostly less (from 0.46),
+// 64 x 64 tiles with scales for rows of B more (up to 1.8).
 enum class Way { kSmall16, kSmall32, kSmall64, kLoop128, kLoop256, kRows, kColumns };
 struct Choice {
   Way way;

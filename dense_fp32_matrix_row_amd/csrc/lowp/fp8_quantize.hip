@@ -179,7 +179,7 @@ struct Args {
 
 // Blocks of 1 x 128 as the matrix lies: sixteen lanes a block, eight neighbours
 // each, nothing shared, so that a few rows still spread over many CUs.  16 x 1024
-// in 2.8 us, all of it a launch.
+// in 2.9 us, all of it a launch; 8192 x 8192 bf16 in 41 us (4.9 TB/s), floats in 56.
 template <class X, int KIND>
 __global__ __launch_bounds__(256) void k_rows(const X* __restrict__ x, Args a, int64_t items, int blocks) {
   const int lane = threadIdx.x % 16;
@@ -202,9 +202,12 @@ __global__ __launch_bounds__(256) void k_rows(const X* __restrict__ x, Args a, i
 // maximum through LDS); a thread each works out those 256 scales.  Transposed
 // codes go through LDS too, so that they leave in 128-byte rows: column c's eight
 // bytes of row group rg lie in slot rg ^ (c / 8) of 16, which spreads both sides
-// over the banks.  Bound by memory: 8192 x 8192 bf16 both ways, 260 MiB, in 62 us
-// (4.4 TB/s; a copy reaches 4.9), 4097 x 2049 floats, whose odd rows are loaded four
-// bytes at a time, in 14.7 us (3.4 TB/s).
+// over the banks.  Bound by memory: 8192 x 8192 bf16 both ways, 260 MiB, in 61-62 us
+// (4.4 TB/s; a copy reaches 4.9), one way in 40 (5.0).  Rows of an odd number of
+// floats begin off the 16 bytes that a load takes and lie over one more cache line:
+// 4096 x 2048 in 9.7 us (5.2 TB/s), 4097 x 2048 in 10.3, 4096 x 2049 in 14.2, 4097 x
+// 2049 in 14.7-15.0 (3.4); 8192 x 4096 32.2, 8193 x 4097 41.5.  A tile a block, so
+// few tokens leave CUs idle: 256 x 1024 bf16 both ways on 16 blocks in 6.7-7.4.
 template <class X, int KIND, int BR, bool AS_IS, bool TRANS>
 __global__ __launch_bounds__(256, 2) void k_tile(const X* __restrict__ x, Args a, int tiles_c, int64_t tiles) {
   __shared__ uint32_t part[16][128];
