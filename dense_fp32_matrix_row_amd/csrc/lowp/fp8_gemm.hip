@@ -2,14 +2,16 @@
 // a scale for each block of 128 along K.
 #include "../../../include/blockfp8.h"
 #include "lowp.h"
-#include "nt_direct.h"
 #include "nt_loop.h"
+#include "nt_plan.h"
 
 namespace sgemm {
 namespace {
 
+using nt::Plan;
 using nt::Side;
 using nt::v4f;
+using nt::Way;
 
 template <class O>
 struct Out {
@@ -142,13 +144,6 @@ void launch_loop(const Side& A, const Side& B, int K, const Out<O>& out, unsigne
                      static_cast<int>(tn));
 }
 
-// The tiles from column n0, all rows; then those from row m0 left of it.
-struct Part {
-  int tiles_m, n0;
-  int64_t tiles;
-  int low_m, m0;
-};
-
 // Small tiles.  Bound by a launch and one trip to memory, or the weight's read:
 // 1 x 4096 x 4096 in 4.4-5.3 us (3.2-3.8 TB/s; 16 x 16 tiles, 256 blocks), 256 x
 // 1024 x 1024 in 4.3-5.1 us (32 x 32, 256 blocks).  The 64 x 64 tile is short of
@@ -156,175 +151,51 @@ struct Part {
 // of 13 to 73 registers that do not fit come and go in the loop (1024 x 1024 x 4096
 // bf16 15 us with one scale for B's rows or powers of two, 22 with a float each;
 // float 19-21, 31 and 46).
-template <class D, class O>
-__global__ __launch_bounds__(D::threads, 2) void k_direct(Side A, Side B, int K, Out<O> out, Part part, int64_t tiles) {
-  __shared__ typename D::Meet meet;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int64_t id = xcd_contiguous(t, tiles), low = id - part.tiles;
-    const int m0 = low < 0 ? static_cast<int>(id % part.tiles_m) * D::BM : part.m0 + static_cast<int>(low % part.low_m) * D::BM;
-    const int n0 = low < 0 ? part.n0 + static_cast<int>(id / part.tiles_m) * D::BN : static_cast<int>(low / part.low_m) * D::BN;
-    D::run(meet, A, B, m0, n0, K, out);
-    __syncthreads();  // the next tile writes the same LDS
-  }
-}
-
-// Of D, what is neither left of column n0 nor above row m0, one launch for both
-// edges (2050 x 2049 x 4096, float result: 51 -> 47 us); all of it for 0, 0.
-template <class D, class O>
-void launch_direct(const Side& A, const Side& B, int K, const Out<O>& out, int m0, int n0, unsigned blocks,
-                   hipStream_t s) {
-  Part part;
-  const int64_t tm = ceil_div(out.M, D::BM), low = ceil_div(out.M - m0, D::BM);
-  part.tiles_m = static_cast<int>(tm);
-  part.n0 = n0;
-  part.tiles = tm * ceil_div(out.N - n0, D::BN);
-  part.low_m = static_cast<int>(low);
-  part.m0 = m0;
-  const int64_t tiles = part.tiles + low * (n0 / D::BN);
-  hipLaunchKernelGGL((k_direct<D, O>), dim3(blocks), dim3(D::threads), 0, s, A, B, K, out, part, tiles);
-}
-
+//
 // Which tile takes a product, by estimates of the time in us: of a small tile
-// (16, 32 or 64 square) what a launch takes, what one of its wavefronts' steps
-// takes alone, and what a step of one block takes among many; of a large one
-// what a step takes alone and in a full round over the 256 CUs.  The constants are
-// fitted.  Of 160 products measured since (20 sizes from 1 x 4096 x 4096 to 8192^3,
-// 16-bit and float results, both scales, B in blocks of 1 and 128) four in five took
-// between 0.8 and 1.25 of the estimate; 1024 x 1024 x 32768 mostly less (from 0.46),
-// 64 x 64 tiles with scales for rows of B more (up to 1.8).
-enum class Way { kSmall16, kSmall32, kSmall64, kLoop128, kLoop256, kRows, kColumns };
-struct Choice {
-  Way way;
-  int at;  // kRows, kColumns: where D is cut in two
-  double us;
-};
+// what a launch takes, what one of its wavefronts' steps takes alone, and what a
+// step of one block takes among many; of a large one what a step takes alone and
+// in a full round over the 256 CUs.  The constants are fitted.  Of 160 products
+// measured since (20 sizes from 1 x 4096 x 4096 to 8192^3, 16-bit and float
+// results, both scales, B in blocks of 1 and 128) four in five took between 0.8
+// and 1.25 of the estimate; 1024 x 1024 x 32768 mostly less (from 0.46), 64 x 64
+// tiles with scales for rows of B more (up to 1.8).
+struct Model {
+  bool wide;  // a float result
 
-Choice choose(int M, int N, int K, bool wide, bool loops, int cuts) {
-  const double steps = static_cast<double>(ceil_div(K, nt::kStep)), each = static_cast<double>(ceil_div(K, 8 * nt::kStep));
-  const auto small = [&](int t, double base, double alone, double among) {
-    const double blocks = static_cast<double>(ceil_div(M, t) * ceil_div(N, t));
-    return base + each * (alone > among * blocks ? alone : among * blocks);
-  };
-  Choice best{Way::kSmall16, 0, small(16, 2.8, 0.45, 0.003)};
-  const auto offer = [&](Way w, int at, double us) {
-    if (us < best.us) best = Choice{w, at, us};
-  };
-  const auto loop = [&](Way w, int bn, double base, double alone, double full) {
-    const int64_t tiles = ceil_div(M, 256) * ceil_div(N, bn), rest = tiles % 256;
-    if (tiles > kMaxWorkItems / 512) return;  // a block a tile: more than a launch takes
-    offer(w, 0, base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0)));
-  };
-  offer(Way::kSmall32, 0, small(32, 2.3, 1.3, wide ? 0.007 : 0.0056));
-  offer(Way::kSmall64, 0, wide ? small(64, 2.0, 4.5, 0.024) : small(64, 3.0, 2.2, 0.0135));
-  if (!loops) return best;
-  if (wide) {  // two blocks a CU: with one each, a step takes little more than half the time
-    const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128), rest = tiles % 512;
-    if (tiles <= kMaxWorkItems / 256)
-      offer(Way::kLoop128, 0, 5.0 + steps * (tiles / 512 * 1.92 + (rest == 0 ? 0 : rest <= 256 ? 1.09 : 1.92)));
-  } else {
-    loop(Way::kLoop128, 128, 6.0, 0.65, 0.98);
-    loop(Way::kLoop256, 256, 7.0, 1.0, 1.6);
+  nt::SmallCost small(int i) const {
+    if (i == 0) return {2.8, 0.45, 0.003};
+    if (i == 1) return {2.3, 1.3, wide ? 0.007 : 0.0056};
+    if (wide) return {2.0, 4.5, 0.024};
+    return {3.0, 2.2, 0.0135};
   }
-  // rows or columns that hardly fill their tiles apart from the rest
-  for (int t = 128; cuts > 0 && t <= 256; t *= 2) {
-    if (N > t && N % t) {
-      const int at = N - N % t;
-      offer(Way::kColumns, at, choose(M, at, K, wide, loops, cuts - 1).us + choose(M, N - at, K, wide, loops, 0).us);
-    }
-    if ((wide || t == 256) && M > t && M % t) {
-      const int at = M - M % t;
-      offer(Way::kRows, at, choose(at, N, K, wide, loops, cuts - 1).us + choose(M - at, N, K, wide, loops, 0).us);
+  template <class F>
+  void loops(int M, int N, double steps, const F& offer) const {
+    const auto loop = [&](Way w, int bn, double base, double alone, double full) {
+      const int64_t tiles = ceil_div(M, 256) * ceil_div(N, bn), rest = tiles % 256;
+      if (tiles > kMaxWorkItems / 512) return;  // a block a tile: more than a launch takes
+      offer(w, base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0)));
+    };
+    if (wide) {  // two blocks a CU: with one each, a step takes little more than half the time
+      const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128), rest = tiles % 512;
+      if (tiles <= kMaxWorkItems / 256)
+        offer(Way::kLoop128, 5.0 + steps * (tiles / 512 * 1.92 + (rest == 0 ? 0 : rest <= 256 ? 1.09 : 1.92)));
+    } else {
+      loop(Way::kLoop128, 128, 6.0, 0.65, 0.98);
+      loop(Way::kLoop256, 256, 7.0, 1.0, 1.6);
     }
   }
-  return best;
-}
-
-// One launch: tiles of one kind (small or large) over rows m0 .. m0 + M - 1 and
-// columns n0 .. n0 + N - 1 of D but, of small tiles, the first skip_m rows of the
-// first skip_n columns.
-struct Piece {
-  Way way;
-  int m0, n0, M, N, skip_m, skip_n;
-};
-// A product's launches; two cuts make three of them.
-struct Plan {
-  Piece piece[3];
-  int count = 0;
-};
-
-void plan(Plan& p, int m0, int n0, int M, int N, int K, bool wide, bool loops, int cuts) {
-  const Choice c = choose(M, N, K, wide, loops, cuts);
-  if (c.way != Way::kRows && c.way != Way::kColumns) {
-    p.piece[p.count++] = Piece{c.way, m0, n0, M, N, 0, 0};
-    return;
-  }
-  const bool rows = c.way == Way::kRows;
-  const Choice inner = choose(rows ? c.at : M, rows ? N : c.at, K, wide, loops, cuts - 1);
-  if (inner.way == (rows ? Way::kColumns : Way::kRows)) {  // both edges, with small tiles of one size: these in one launch
-    const int m = rows ? c.at : inner.at, n = rows ? inner.at : c.at;
-    const Way right = choose(M, N - n, K, wide, loops, 0).way, low = choose(M - m, n, K, wide, loops, 0).way;
-    if (right == low && right <= Way::kSmall64) {
-      plan(p, m0, n0, m, n, K, wide, loops, 0);
-      p.piece[p.count++] = Piece{right, m0, n0, M, N, m, n};
-      return;
+  bool cuts_rows(int t) const { return wide || t == 256; }
+  constexpr nt::TileShape shape(Way way) const {
+    switch (way) {
+      case Way::kSmall16: return {16, 16, 512};
+      case Way::kSmall32: return {32, 32, 512};
+      case Way::kSmall64: return {64, 64, 512};
+      case Way::kLoop128: return wide ? nt::TileShape{128, 128, 256} : nt::TileShape{256, 128, 512};
+      default: return {256, 256, 512};
     }
   }
-  if (rows) {
-    plan(p, m0, n0, c.at, N, K, wide, loops, cuts - 1);
-    plan(p, m0 + c.at, n0, M - c.at, N, K, wide, loops, 0);
-  } else {
-    plan(p, m0, n0, M, c.at, K, wide, loops, cuts - 1);
-    plan(p, m0, n0 + c.at, M, N - c.at, K, wide, loops, 0);
-  }
-}
-constexpr int kCuts = 2;
-
-// Tile and block of a way.
-struct TileShape {
-  int rows, cols, threads;
 };
-constexpr TileShape shape_of(Way way, bool wide) {
-  switch (way) {
-    case Way::kSmall16: return TileShape{16, 16, 512};
-    case Way::kSmall32: return TileShape{32, 32, 512};
-    case Way::kSmall64: return TileShape{64, 64, 512};
-    case Way::kLoop128: return wide ? TileShape{128, 128, 256} : TileShape{256, 128, 512};
-    default: return TileShape{256, 256, 512};
-  }
-}
-
-template <class T>
-constexpr bool is_shape(Way way, bool wide) {
-  const TileShape t = shape_of(way, wide);
-  return t.rows == T::BM && t.cols == T::BN && t.threads == T::threads;
-}
-
-// Blocks of a launch: one a tile, but small tiles past what a launch takes, which
-// the blocks walk.
-int64_t blocks_of(const Piece& p, bool wide) {
-  const TileShape t = shape_of(p.way, wide);
-  const int64_t tiles = ceil_div(p.M, t.rows) * ceil_div(p.N - p.skip_n, t.cols) +
-                        ceil_div(p.M - p.skip_m, t.rows) * (p.skip_n / t.cols);
-  const int64_t cap = kMaxWorkItems / t.threads;
-  return tiles < cap ? tiles : cap;
-}
-
-Side from_row(Side o, int row, int scale_bytes) {  // row: a multiple of 128
-  o.p += row * o.ld;
-  o.s = static_cast<const uint8_t*>(o.s) + (row >> o.shift) * o.s_row * scale_bytes;
-  o.rows -= row;
-  return o;
-}
-
-// The small tiles of a way, over the part of D that launch_direct takes.
-template <class P, class O>
-void launch_small(Way way, const Side& A, const Side& B, int K, const Out<O>& out, int m0, int n0, unsigned blocks,
-                  hipStream_t s) {
-  using nt::Direct;
-  if (way == Way::kSmall16) launch_direct<Direct<P, 1, 1, 8>>(A, B, K, out, m0, n0, blocks, s);
-  else if (way == Way::kSmall32) launch_direct<Direct<P, 2, 2, 8>>(A, B, K, out, m0, n0, blocks, s);
-  else launch_direct<Direct<P, 4, 4, 8>>(A, B, K, out, m0, n0, blocks, s);
-}
 
 template <class P, nt::Kind KIND, class O>
 void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
@@ -337,21 +208,24 @@ void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t 
   // a product, would bound it.
   using Loop128 = nt::Loop<KIND, 4, 4, wide ? 2 : 4, 2, wide ? 2 : 3>;
   using Loop256 = nt::Loop<KIND, 8, 4, 2, 4, 2>;
-  static_assert(is_shape<Loop128>(Way::kLoop128, wide) && is_shape<Loop256>(Way::kLoop256, wide) &&
-                is_shape<nt::Direct<P, 1, 1, 8>>(Way::kSmall16, wide) && is_shape<nt::Direct<P, 2, 2, 8>>(Way::kSmall32, wide) &&
-                is_shape<nt::Direct<P, 4, 4, 8>>(Way::kSmall64, wide));
+  constexpr Model model{wide};
+  using nt::is_shape;
+  static_assert(is_shape<Loop128>(model.shape(Way::kLoop128)) && is_shape<Loop256>(model.shape(Way::kLoop256)) &&
+                is_shape<nt::Direct<P, 1, 1, 8>>(model.shape(Way::kSmall16)) &&
+                is_shape<nt::Direct<P, 2, 2, 8>>(model.shape(Way::kSmall32)) &&
+                is_shape<nt::Direct<P, 4, 4, 8>>(model.shape(Way::kSmall64)));
   Plan p;
-  plan(p, 0, 0, out.M, out.N, K, wide, K > 0 && Loop128::fits(A) && Loop128::fits(B), kCuts);
+  plan(model, p, 0, 0, out.M, out.N, K, K > 0 && Loop128::fits(A) && Loop128::fits(B), nt::kCuts);
   for (int i = 0; i < p.count; ++i) {
-    const Piece& at = p.piece[i];
+    const nt::Piece& at = p.piece[i];
     Out<O> part = out;
     part.M = at.M;
     part.N = at.N;
     part.d += at.m0 * out.ldd + at.n0;
     if (out.beta != 0.0f) part.c += at.m0 * out.ldc + at.n0;
     const Side a = from_row(A, at.m0, P::kScaleBytes), b = from_row(B, at.n0, P::kScaleBytes);
-    const unsigned blocks = static_cast<unsigned>(blocks_of(at, wide));
-    if (at.way <= Way::kSmall64) launch_small<P>(at.way, a, b, K, part, at.skip_m, at.skip_n, blocks, s);
+    const unsigned blocks = static_cast<unsigned>(blocks_of(model, at));
+    if (at.way <= Way::kSmall64) nt::launch_small<P>(at.way, a, b, K, part, at.skip_m, at.skip_n, blocks, s);
     else if (at.way == Way::kLoop128) launch_loop<Loop128>(a, b, K, part, blocks, s);
     else if constexpr (!wide) launch_loop<Loop256>(a, b, K, part, blocks, s);
   }
@@ -438,12 +312,13 @@ int hip_fp8_gemm_plan(int M, int N, int K, int c_type, hip_fp8_gemm_launch* laun
   if (c_type != HIP_FP8_F32 && c_type != HIP_FP8_BF16 && c_type != HIP_FP8_F16) return -23;
   Plan p;
   const bool wide = c_type == HIP_FP8_F32;
-  if (M > 0 && N > 0) plan(p, 0, 0, M, N, K, wide, K > 0, kCuts);
+  const Model model{wide};
+  if (M > 0 && N > 0) plan(model, p, 0, 0, M, N, K, K > 0, nt::kCuts);
   for (int i = 0; launches && i < p.count; ++i) {
-    const Piece& at = p.piece[i];
-    const TileShape t = shape_of(at.way, wide);
+    const nt::Piece& at = p.piece[i];
+    const nt::TileShape t = model.shape(at.way);
     launches[i] = hip_fp8_gemm_launch{t.rows, t.cols, at.m0, at.n0, at.M, at.N, at.skip_m, at.skip_n, t.threads,
-                                      blocks_of(at, wide)};
+                                      blocks_of(model, at)};
   }
   if (count) *count = p.count;
   return 0;

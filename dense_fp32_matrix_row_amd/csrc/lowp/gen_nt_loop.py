@@ -1,5 +1,5 @@
-"""Write nt_loop.inc: the K loops of the large tiles of nt_loop.h as GCN assembly
-text for gfx950.
+"""Write nt_loop.inc and int8_loop.inc: the K loops of the large tiles of nt_loop.h
+as GCN assembly text for gfx950.
 
 The C++ part sets up addresses and runs the epilogue; the loop is written
 instruction by instruction, because the compiler neither keeps sums, fragments
@@ -32,6 +32,7 @@ Kinds:
          row's scale and the one scale of the wavefront's B rows
   f32n   the same with a scale for each of B's rows
   pair   numbers as pairs of halfs (64 bytes hi, 64 bytes lo), three products
+  int8   8-bit integers, two products of 64 along K each, sums of 32-bit integers
   w32u, w32n, w8u, w8n
          8-bit codes widened to halfs, four products, scaled afterwards as f32u
          and f32n; the scales floats (w32) or bytes (w8), which a thread each
@@ -44,15 +45,15 @@ widened once a step: a half of A and all of B stay widened, and the codes of one
 half of each side are on their way.  Those of a step have all been read after
 its second quarter, where the barrier is then.
 
-Run as a script to rewrite nt_loop.inc; a test checks that the committed file
-is what this writes.
+Run as a script to rewrite both; tests check that the committed files are what
+this writes.
 """
 
 from __future__ import annotations
 
 import os
 
-OUT = os.path.join(os.path.dirname(os.path.abspath(__file__)), "nt_loop.inc")
+HERE = os.path.dirname(os.path.abspath(__file__))
 
 
 class Loop:
@@ -68,12 +69,14 @@ class Loop:
         self.bm, self.bn = 16 * mt * wm, 16 * nt * wn
         self.la, self.lb = self.bm // 8 // self.waves, self.bn // 8 // self.waves
         self.stride = 128 * (self.bm + self.bn)  # bytes from one stage to the next
-        self.scaled = kind != "pair"
+        self.scaled = kind not in ("pair", "int8")
+        self.terms = {"pair": 3, "int8": 2}.get(kind, 1)  # products of a sum that lie apart
         self.wide = kind[0] == "w"
         self.after = self.wide or kind[0] == "f"
         self.uniform = self.after and kind[-1] == "u"
         self.rows = self.after and kind[-1] == "n"
         self.bytes = kind.startswith("w8")
+        self.tail = self.scaled and not self.wide or kind == "int8"  # the last step has a form that masks
         # loads of 64 scales a wavefront
         self.scale_loads = -(-((self.bm + self.bn) // 64) // self.waves) if self.scaled else 0
         self.scale_stage = 256 * self.waves * self.scale_loads
@@ -262,9 +265,9 @@ class Loop:
         `first` or later, and before the first that wants what `tag` names."""
         side = list(side)
         order = []
-        if self.kind == "pair":  # the terms of a sum lie four apart
+        if self.terms > 1:  # the terms of a sum lie four apart
             for i0 in range(0, self.hm, 2):
-                order += [(i, j, term) for term in range(3) for i in range(i0, min(i0 + 2, self.hm)) for j in range(self.hn)]
+                order += [(i, j, term) for term in range(self.terms) for i in range(i0, min(i0 + 2, self.hm)) for j in range(self.hn)]
         elif self.wide:
             order = [(i, j, q) for i in range(self.hm) for q in range(4) for j in range(self.hn)]
         else:
@@ -299,6 +302,9 @@ class Loop:
                 elif self.kind == "pair":
                     self.emit(f"v_mfma_f32_16x16x32_f16 {self.acc(j, i)}, {self.fb(j, int(part == 2))}, "
                               f"{self.fa(i, int(part == 1))}, {self.acc(j, i)}")
+                elif self.kind == "int8":
+                    self.emit(f"v_mfma_i32_16x16x64_i8 {self.acc(j, i)}, {self.fb(j, part)}, {self.fa(i, part)}, "
+                              f"{self.acc(j, i)}")
                 else:
                     t = self.t0 + 4 * (self.count % 4)
                     self.count += 1
@@ -374,8 +380,8 @@ class Loop:
         before = (position - 1) % self.stages
         split = self.split()
         m = lambda side, h: [(side, h * n + k) for n in [self.hm if side == "a" else self.hn] for k in range(n)] if masked else []  # noqa: E731
-        per = self.hn * (3 if self.kind == "pair" else 1)  # matrix instructions a fragment of A has in a quarter
-        group = 2 if self.kind == "pair" else 1
+        per = self.hn * self.terms  # matrix instructions a fragment of A has in a quarter
+        group = 2 if self.terms > 1 else 1
         done = lambda i: per * min(i // group * group + group, self.hm) - 1  # noqa: E731  the last of them
         late = self.settled if self.after else 0
 
@@ -565,12 +571,12 @@ class Loop:
         self.emit(".Lnt_single_%=:")
         self.prime(1, True)
         self.emit(".Lnt_last_%=:")
-        if self.scaled and not self.wide:
+        if self.tail:
             self.emit("s_cmp_lg_u32 %[partial], 0")
             self.emit("s_cbranch_scc1 .Lnt_masked_%=")
         take(top, "whole", last=True, masked=self.wide)
         self.drain()
-        if self.scaled and not self.wide:
+        if self.tail:
             self.emit("s_branch .Lnt_end_%=")
             take(top, "masked", last=True, masked=True)
             self.drain()
@@ -607,9 +613,14 @@ LOOPS = [
 ]
 
 
-def generate() -> str:
+INT8_LOOPS = [("int8", 8, 4, 2, 4, 2), ("int8", 4, 4, 4, 2, 3)]
+
+FILES = {"nt_loop.inc": LOOPS, "int8_loop.inc": INT8_LOOPS}
+
+
+def generate(loops=LOOPS) -> str:
     out = ["// Generated by gen_nt_loop.py (the K loops of nt_loop.h); do not edit."]
-    for args in LOOPS:
+    for args in loops:
         loop = Loop(*args)
         name = loop.name()
         text = loop.text()
@@ -623,5 +634,6 @@ def generate() -> str:
 
 
 if __name__ == "__main__":
-    with open(OUT, "w") as f:
-        f.write(generate())
+    for name, loops in FILES.items():
+        with open(os.path.join(HERE, name), "w") as f:
+            f.write(generate(loops))

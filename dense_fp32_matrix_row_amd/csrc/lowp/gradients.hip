@@ -1,0 +1,483 @@
+// gradients.hip -- hip_gradient_norm, hip_gradient_clip and hip_gradient_clip_by: the
+// norm over many tensors, and scaling by it.
+//
+// Bound by memory: every element is read for the norm, and again, and written,
+// where it is scaled.  All tensors' elements are cut into chunks of one size, which
+// a grid of blocks walks, whatever the tensors' own sizes; a table says which
+// tensor a chunk lies in.  The norm's launch leaves a sum for each block, and each
+// block of the next launch adds them up for itself in the same order: no atomics,
+// no third launch.
+#include <algorithm>
+#include <limits>
+#include <vector>
+
+#include "../../../include/gradients.h"
+#include "rows.h"
+
+namespace sgemm {
+namespace {
+
+struct Entry {
+  const void* x;
+  void* y;
+  int64_t cols, ldx, ldy;
+  int64_t first;  // chunk of all tensors'
+  int64_t rows;
+  int32_t split;  // > 0: chunks a row; < 0: rows a chunk
+  int32_t type;
+};
+static_assert(sizeof(Entry) == 64);
+
+constexpr int kInline = 56;  // tensors that fit a launch's arguments (4 KiB)
+struct Table {
+  Entry e[kInline];
+};
+constexpr int kThreads = 256;
+constexpr int64_t kBlocks = 2048;  // at most, of a launch: eight for each CU
+constexpr int64_t kPartBytes = kBlocks * 8;
+
+// The tensor that a chunk lies in: the last whose first chunk is not behind it, found
+// 64 at a time.
+__device__ __forceinline__ int find(const Entry* e, int count, int64_t chunk) {
+  int lo = 0, n = count;
+  while (n > 1) {
+    const int lane = threadIdx.x % 64, step = (n + 63) / 64;
+    const bool before = lane * step < n && e[lo + min(lane * step, n - 1)].first <= chunk;
+    const int at = (__popcll(__ballot(before)) - 1) * step;
+    lo += at;
+    n = min(step, n - at);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// 16 bytes of elements.
+template <class T>
+using Wide = Pack<16 / sizeof(T), T>;
+
+// Calls one(i) for every element i < n and wide(i) for those that lie in whole 16
+// bytes from `p` on, four at a time, spread over the block's threads.
+template <class T, class W, class O>
+__device__ __forceinline__ void walk(const T* p, int n, const W& wide, const O& one) {
+  constexpr int kWide = 16 / sizeof(T);
+  const int head = min(n, static_cast<int>((16 - reinterpret_cast<uintptr_t>(p) % 16) % 16 / sizeof(T)));
+  const int count = (n - head) / kWide;
+  int t = threadIdx.x;
+  for (; t + 3 * kThreads < count; t += 4 * kThreads) wide(head + t * kWide, std::integral_constant<int, 4>{});
+  for (; t < count; t += kThreads) wide(head + t * kWide, std::integral_constant<int, 1>{});
+  const int rest = n - head - count * kWide;  // before and behind
+  for (int i = threadIdx.x; i < head + rest; i += kThreads) one(i < head ? i : head + count * kWide + (i - head));
+}
+
+template <class T>
+__device__ __forceinline__ double square(T x) {
+  const double d = static_cast<double>(to_float(x));
+  return d * d;
+}
+
+struct Squares {
+  double sum = 0.0;
+  template <class T>
+  __device__ __forceinline__ void flat(const T* x, T*, int n) {
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    walk(
+        x, n,
+        [&](int i, auto many) {
+          Wide<T> v[many.value];
+#pragma unroll
+          for (int k = 0; k < many.value; ++k) v[k] = load_pack<16 / sizeof(T)>(x + i + k * (kThreads * (16 / sizeof(T))));
+#pragma unroll
+          for (int k = 0; k < many.value; ++k)
+#pragma unroll
+            for (int j = 0; j < 16 / int(sizeof(T)); ++j) {
+              const double d = static_cast<double>(to_float(v[k].v[j]));
+              s[j % 4] = fma(d, d, s[j % 4]);
+            }
+        },
+        [&](int i) { s[0] += square(x[i]); });
+    sum += (s[0] + s[1]) + (s[2] + s[3]);
+  }
+  template <class T>
+  __device__ __forceinline__ void one(const T* x, T*) { sum += square(*x); }
+};
+
+// x c, with c = f 2^-64 where c is too small for a float's bits (a norm past 10^38),
+// f and 1 elsewhere.
+struct Scale {
+  float f, shift;
+  __device__ __forceinline__ explicit Scale(double c)
+      : f(static_cast<float>(c < 0x1p-64 ? c * 0x1p64 : c)), shift(c < 0x1p-64 ? 0x1p-64f : 1.0f) {}
+  __device__ __forceinline__ float operator()(float x) const { return x * f * shift; }
+  template <class T>
+  __device__ __forceinline__ void flat(const T* x, T* y, int n) {
+    walk(
+        x, n,
+        [&](int i, auto many) {
+          constexpr int kWide = 16 / sizeof(T);
+          Wide<T> v[many.value];
+#pragma unroll
+          for (int k = 0; k < many.value; ++k) v[k] = load_pack<kWide>(x + i + k * (kThreads * kWide));
+#pragma unroll
+          for (int k = 0; k < many.value; ++k) {
+#pragma unroll
+            for (int j = 0; j < kWide; ++j) from_float((*this)(to_float(v[k].v[j])), v[k].v[j]);
+            store_pack(y + i + k * (kThreads * kWide), v[k]);
+          }
+        },
+        [&](int i) { one(x + i, y + i); });
+  }
+  template <class T>
+  __device__ __forceinline__ void one(const T* x, T* y) { from_float((*this)(to_float(*x)), *y); }
+};
+
+template <class T, class F>
+__device__ __forceinline__ void do_chunk(const Entry& e, int64_t k, int chunk, F& f) {
+  const T* const x = static_cast<const T*>(e.x);
+  T* const y = static_cast<T*>(e.y);
+  if (e.split > 0) {
+    const int64_t row = e.split == 1 ? k : k / e.split, col = (k - row * e.split) * chunk;
+    f.flat(x + row * e.ldx + col, y + row * e.ldy + col, static_cast<int>(min(int64_t(chunk), e.cols - col)));
+  } else {
+    const int64_t row = k * -e.split;
+    const int rows = static_cast<int>(min(int64_t(-e.split), e.rows - row)), cols = static_cast<int>(e.cols);
+    for (int i = threadIdx.x; i < rows * cols; i += kThreads)
+      f.one(x + (row + i / cols) * e.ldx + i % cols, y + (row + i / cols) * e.ldy + i % cols);
+  }
+}
+
+// The chunks of a block, in order.
+template <class F>
+__device__ __forceinline__ void do_chunks(const Entry* table, int count, int64_t chunks, int chunk, bool skip_in_place, F& f) {
+  for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+    const Entry& e = table[find(table, count, k)];
+    if (skip_in_place && e.x == e.y) continue;
+    if (e.type == HIP_GRADIENT_F32) do_chunk<float>(e, k - e.first, chunk, f);
+    else if (e.type == HIP_GRADIENT_BF16) do_chunk<bf16>(e, k - e.first, chunk, f);
+    else do_chunk<_Float16>(e, k - e.first, chunk, f);
+  }
+}
+
+struct Add {
+  __device__ __forceinline__ double operator()(double a, double b) const { return a + b; }
+};
+
+__device__ __forceinline__ void norm_body(const Entry* table, int count, int64_t chunks, int chunk, double* parts) {
+  using S = RowShape<kThreads, 1>;
+  __shared__ double meet[S::threads / 64][1];
+  Squares f;
+  do_chunks(table, count, chunks, chunk, false, f);
+  double sum[1] = {f.sum};
+  join_row<S>(sum, meet, Add{});
+  if (threadIdx.x == 0) parts[blockIdx.x] = sum[0];
+}
+__global__ __launch_bounds__(kThreads) void k_norm(Table t, int count, int64_t chunks, int chunk, double* parts) {
+  norm_body(t.e, count, chunks, chunk, parts);
+}
+__global__ __launch_bounds__(kThreads) void k_norm_long(const Entry* __restrict__ table, int count, int64_t chunks, int chunk,
+                                                        double* parts) {
+  norm_body(table, count, chunks, chunk, parts);
+}
+
+// The norm from the blocks' sums, the same in every thread of every block.
+__device__ __forceinline__ double join_parts(const double* parts, int count) {
+  using S = RowShape<kThreads, 1>;
+  __shared__ double meet[S::threads / 64][1];
+  double sum[1] = {0.0};
+  for (int i = threadIdx.x; i < count; i += kThreads) sum[0] += parts[i];
+  join_row<S>(sum, meet, Add{});
+  return sqrt(sum[0]);
+}
+__global__ __launch_bounds__(kThreads) void k_finish(const double* parts, int count, float* norm) {
+  const double v = join_parts(parts, count);
+  if (threadIdx.x == 0) *norm = static_cast<float>(v);
+}
+
+struct Limit {
+  const double* parts;  // the blocks' sums, or NULL:
+  int count;
+  const float* given;  // the norm
+  float* norm;         // where it goes, or NULL
+  float max_norm, eps;
+  bool all_in_place;
+};
+__device__ __forceinline__ void clip_body(const Entry* table, int count, int64_t chunks, int chunk, const Limit& l) {
+  const double norm = l.given ? static_cast<double>(*l.given) : join_parts(l.parts, l.count);
+  if (l.norm && blockIdx.x == 0 && threadIdx.x == 0) *l.norm = static_cast<float>(norm);
+  const double all = norm + static_cast<double>(l.eps), most = static_cast<double>(l.max_norm);
+  const bool same = all <= most;  // not for a NaN
+  Scale f(same ? 1.0 : most / all);
+  if (same && l.all_in_place) return;
+  do_chunks(table, count, chunks, chunk, same, f);
+}
+__global__ __launch_bounds__(kThreads) void k_clip(Table t, int count, int64_t chunks, int chunk, Limit l) {
+  clip_body(t.e, count, chunks, chunk, l);
+}
+__global__ __launch_bounds__(kThreads) void k_clip_long(const Entry* __restrict__ table, int count, int64_t chunks, int chunk,
+                                                        Limit l) {
+  clip_body(table, count, chunks, chunk, l);
+}
+
+// Entries that come as arguments into memory.
+__global__ __launch_bounds__(64) void k_table(Table t, int count, Entry* to) {
+  for (int i = threadIdx.x; i < count; i += 64) to[i] = t.e[i];
+}
+
+// What a call works on: the tensors that have elements.
+struct Work {
+  std::vector<Entry> entries;
+  int64_t chunks = 0;
+  int chunk = 0;
+  bool all_in_place = true;
+};
+
+bool valid(const hip_gradient& g, bool clip) {
+  if (g.rows < 0 || g.cols < 0 || g.type < 0 || g.type > HIP_GRADIENT_F16) return false;
+  if (g.rows > (int64_t(1) << 40) || g.cols > (int64_t(1) << 40)) return false;  // more than memory, less than overflows below
+  if (g.rows == 0 || g.cols == 0) return true;
+  const uintptr_t align = g.type == HIP_GRADIENT_F32 ? 4 : 2;
+  if (!g.x || reinterpret_cast<uintptr_t>(g.x) % align) return false;
+  if (g.rows > 1 && (g.ldx < g.cols || g.ldx > (int64_t(1) << 40))) return false;
+  if (!clip) return true;
+  if (!g.y || reinterpret_cast<uintptr_t>(g.y) % align) return false;
+  return !(g.rows > 1 && (g.ldy < g.cols || g.ldy > (int64_t(1) << 40)));
+}
+
+void collect(Work& w, int count, const hip_gradient* tensors, bool clip) {
+  w.entries.reserve(count);
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    const hip_gradient& g = tensors[i];
+    if (g.rows == 0 || g.cols == 0) continue;
+    Entry e{};
+    e.x = g.x;
+    e.y = clip ? g.y : const_cast<void*>(g.x);
+    e.rows = g.rows;
+    e.cols = g.cols;
+    e.ldx = g.rows > 1 ? g.ldx : g.cols;
+    e.ldy = !clip ? e.ldx : g.rows > 1 ? g.ldy : g.cols;
+    e.type = static_cast<int32_t>(g.type);
+    if (e.rows > 1 && e.ldx == e.cols && e.ldy == e.cols) {  // dense
+      e.cols *= e.rows;
+      e.rows = 1;
+    }
+    if (e.rows == 1) e.ldx = e.ldy = 0;
+    w.all_in_place = w.all_in_place && e.x == e.y;
+    total += e.rows * e.cols;
+    w.entries.push_back(e);
+  }
+  // two chunks or more for each block where there is that much, down to four 16-byte
+  // loads a thread, and eight for an even end where there is more
+  w.chunk = 4096;
+  while (w.chunk < 16384 && total / w.chunk > 2 * kBlocks) w.chunk *= 2;
+  for (Entry& e : w.entries) {
+    e.first = w.chunks;
+    if (e.rows == 1 || e.cols >= w.chunk) {
+      const int64_t per = ceil_div(e.cols, w.chunk);
+      e.split = e.rows == 1 ? std::numeric_limits<int32_t>::max() : static_cast<int32_t>(per);
+      w.chunks += e.rows * per;
+    } else {
+      const int64_t per = w.chunk / e.cols;
+      e.split = static_cast<int32_t>(-per);
+      w.chunks += ceil_div(e.rows, per);
+    }
+  }
+}
+
+// Whether what a clipping call writes overlaps anything else that it touches.
+struct Range {
+  uintptr_t from, to;  // bytes
+  uintptr_t row, ld;   // of a strided one
+  bool writes;
+};
+bool meet(const Range& a, const Range& b) {
+  if (!(a.writes || b.writes) || a.to <= b.from || b.to <= a.from) return false;
+  if (a.ld == 0 || a.ld != b.ld) return true;
+  // two sets of columns of one matrix
+  const uintptr_t off = a.from <= b.from ? (b.from - a.from) % a.ld : (a.ld - (a.from - b.from) % a.ld) % a.ld;
+  return off < a.row || off + b.row > a.ld;
+}
+bool overlaps(const Work& w, const float* norm) {
+  std::vector<Range> ranges;
+  ranges.reserve(2 * w.entries.size() + 1);
+  for (const Entry& e : w.entries) {
+    const uintptr_t size = e.type == HIP_GRADIENT_F32 ? 4 : 2, row = e.cols * size;
+    const auto add = [&](const void* p, int64_t ld, bool writes) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      ranges.push_back(Range{at, at + (e.rows - 1) * ld * size + row, row, e.rows > 1 ? ld * size : 0, writes});
+    };
+    const bool in_place = e.x == e.y && e.ldx == e.ldy;
+    add(e.y, e.ldy, true);
+    if (!in_place) add(e.x, e.ldx, false);
+  }
+  if (norm) ranges.push_back(Range{reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, 4, 0, true});
+  std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+  std::vector<const Range*> open;  // those that reach past the present one's begin
+  for (const Range& r : ranges) {
+    size_t kept = 0;
+    for (const Range* o : open) {
+      if (o->to <= r.from) continue;
+      if (meet(*o, r)) return true;
+      open[kept++] = o;
+    }
+    open.resize(kept);
+    open.push_back(&r);
+  }
+  return false;
+}
+
+// Launches f(table or pointer) with the entries where the kernels find them.
+void put_table(const Work& w, Entry* to, hipStream_t stream) {
+  const int n = static_cast<int>(w.entries.size());
+  for (int at = 0; at < n; at += kInline) {
+    Table t{};
+    const int some = std::min(kInline, n - at);
+    std::copy_n(w.entries.begin() + at, some, t.e);
+    hipLaunchKernelGGL(k_table, dim3(1), dim3(64), 0, stream, t, some, to + at);
+  }
+}
+Table inline_table(const Work& w) {
+  Table t{};
+  std::copy(w.entries.begin(), w.entries.end(), t.e);
+  return t;
+}
+
+struct Memory {
+  double* parts;
+  Entry* table;
+};
+Memory memory(void* workspace) {
+  uint8_t* const p = static_cast<uint8_t*>(workspace);
+  return Memory{reinterpret_cast<double*>(p), reinterpret_cast<Entry*>(p + kPartBytes)};
+}
+int64_t bytes_for(int count) { return kPartBytes + (count > kInline ? int64_t(count) * int64_t(sizeof(Entry)) : 0); }
+
+unsigned blocks_for(const Work& w) { return static_cast<unsigned>(std::min(w.chunks, kBlocks)); }
+
+void launch_norm(const Work& w, const Memory& m, hipStream_t stream) {
+  const int n = static_cast<int>(w.entries.size());
+  if (n == 0) return;
+  if (n <= kInline)
+    hipLaunchKernelGGL(k_norm, dim3(blocks_for(w)), dim3(kThreads), 0, stream, inline_table(w), n, w.chunks, w.chunk, m.parts);
+  else
+    hipLaunchKernelGGL(k_norm_long, dim3(blocks_for(w)), dim3(kThreads), 0, stream, m.table, n, w.chunks, w.chunk, m.parts);
+}
+void launch_clip(const Work& w, const Memory& m, const Limit& l, hipStream_t stream) {
+  const int n = static_cast<int>(w.entries.size());
+  const dim3 grid(std::max(1u, blocks_for(w)));
+  if (n <= kInline) hipLaunchKernelGGL(k_clip, grid, dim3(kThreads), 0, stream, inline_table(w), n, w.chunks, w.chunk, l);
+  else hipLaunchKernelGGL(k_clip_long, grid, dim3(kThreads), 0, stream, m.table, n, w.chunks, w.chunk, l);
+}
+
+bool bad_count(int count) { return count < 0 || count > HIP_GRADIENT_MAX_COUNT; }
+bool off256(const void* p) { return reinterpret_cast<uintptr_t>(p) % 256 != 0; }
+
+// What the three calls share, their arguments' numbers being the same but the
+// norm's: 0, or a status.
+int begin(Work& w, int count, const hip_gradient* tensors, bool clip, const float* norm, void* workspace,
+          long long workspace_bytes, int workspace_at, hipStream_t stream) {
+  if (bad_count(count)) return -1;
+  if (count > 0 && tensors == nullptr) return -2;
+  for (int i = 0; i < count; ++i)
+    if (!valid(tensors[i], clip)) return -2;
+  if (workspace == nullptr || off256(workspace)) return -workspace_at;
+  if (workspace_bytes < bytes_for(count)) return -(workspace_at + 1);
+  collect(w, count, tensors, clip);
+  if (clip && overlaps(w, norm)) return -2;
+  if (static_cast<int>(w.entries.size()) > kInline) put_table(w, memory(workspace).table, stream);
+  return 0;
+}
+
+int clip(int count, const hip_gradient* tensors, float max_norm, float eps, float* norm, const float* given,
+         void* workspace, long long workspace_bytes, hipStream_t stream) {
+  if (!(max_norm >= 0.0f)) return -3;
+  if (!(eps >= 0.0f) || eps == std::numeric_limits<float>::infinity()) return -4;
+  Work w;
+  const int status = begin(w, count, tensors, true, given ? given : norm, workspace, workspace_bytes, 6, stream);
+  if (status != 0) return status;
+  const Memory m = memory(workspace);
+  if (!given) launch_norm(w, m, stream);
+  if (w.chunks > 0 || norm)
+    launch_clip(w, m, Limit{m.parts, static_cast<int>(blocks_for(w)), given, norm, max_norm, eps, w.all_in_place}, stream);
+  return static_cast<int>(hipGetLastError());
+}
+
+// No exception leaves a C function.
+template <class F>
+int guarded(const F& f) {
+  try {
+    return f();
+  } catch (...) {
+    return static_cast<int>(hipErrorOutOfMemory);
+  }
+}
+
+}  // namespace
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" {
+
+int hip_gradient_workspace(int count, long long* bytes) {
+  if (bad_count(count)) return -1;
+  if (bytes) *bytes = bytes_for(count);
+  return 0;
+}
+
+int hip_gradient_norm(int count, const hip_gradient* tensors, float* norm, void* workspace, long long workspace_bytes,
+                      hipStream_t stream) {
+  return guarded([&] {
+    if (norm == nullptr) return -3;
+    Work w;
+    const int status = begin(w, count, tensors, false, nullptr, workspace, workspace_bytes, 4, stream);
+    if (status != 0) return status;
+    const Memory m = memory(workspace);
+    launch_norm(w, m, stream);
+    hipLaunchKernelGGL(k_finish, dim3(1), dim3(kThreads), 0, stream, m.parts, static_cast<int>(blocks_for(w)), norm);
+    return static_cast<int>(hipGetLastError());
+  });
+}
+
+int hip_gradient_clip(int count, const hip_gradient* tensors, float max_norm, float eps, float* norm, void* workspace,
+                      long long workspace_bytes, hipStream_t stream) {
+  return guarded([&] { return clip(count, tensors, max_norm, eps, norm, nullptr, workspace, workspace_bytes, stream); });
+}
+
+int hip_gradient_clip_by(int count, const hip_gradient* tensors, float max_norm, float eps, const float* norm,
+                         void* workspace, long long workspace_bytes, hipStream_t stream) {
+  return guarded([&] {
+    if (norm == nullptr) return -5;
+    return clip(count, tensors, max_norm, eps, nullptr, norm, workspace, workspace_bytes, stream);
+  });
+}
+
+const char* hip_gradient_norm_status_string(int status) {
+  switch (status) {
+    case 0: return "success";
+    case -1: return "argument 1 (count) is negative or above HIP_GRADIENT_MAX_COUNT";
+    case -2: return "argument 2 (tensors) is NULL, or has a bad size, stride, type or pointer";
+    case -3: return "argument 3 (norm) is NULL";
+    case -4: return "argument 4 (workspace) is NULL or not 256-byte aligned";
+    case -5: return "argument 5 (workspace_bytes) is less than hip_gradient_workspace says";
+    default: break;
+  }
+  if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));
+  return "unknown status";
+}
+
+const char* hip_gradient_clip_status_string(int status) {
+  switch (status) {
+    case 0: return "success";
+    case -1: return "argument 1 (count) is negative or above HIP_GRADIENT_MAX_COUNT";
+    case -2: return "argument 2 (tensors) is NULL, has a bad size, stride, type or pointer, or what is written overlaps";
+    case -3: return "argument 3 (max_norm) is negative or NaN";
+    case -4: return "argument 4 (eps) is negative, infinite or NaN";
+    case -5: return "argument 5 (norm) is NULL";
+    case -6: return "argument 6 (workspace) is NULL or not 256-byte aligned";
+    case -7: return "argument 7 (workspace_bytes) is less than hip_gradient_workspace says";
+    default: break;
+  }
+  if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));
+  return "unknown status";
+}
+
+}  // extern "C"

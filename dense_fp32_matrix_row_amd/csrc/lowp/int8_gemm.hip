@@ -1,0 +1,369 @@
+// int8_gemm.hip -- hip_int8_gemm: D = A B^T, scaled by a float for each row of A
+// and of B, plus a bias, over 8-bit integers; hip_int8_linear: the quantiser and
+// that product.
+#include "../../../include/int8.h"
+#include "int8_internal.h"
+#include "lowp.h"
+#include "nt_loop.h"
+#include "nt_plan.h"
+
+namespace sgemm {
+namespace {
+
+using nt::Plan;
+using nt::Side;
+using nt::v4f;
+using nt::v4i;
+using nt::Way;
+
+// The bias of COUNT neighbours from column n; those inside.
+struct Bias {
+  const void* p;
+  int type;
+  template <class T, int COUNT>
+  __device__ __forceinline__ void load(float (&b)[COUNT], int n, int N) const {
+    const T* const from = static_cast<const T*>(p) + n;
+    if (n <= N - COUNT) {
+      const Pack<COUNT, T> v = load_pack<COUNT>(from);
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) b[i] = to_float(v.v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) b[i] = n + i < N ? to_float(from[i]) : 0.0f;
+    }
+  }
+  template <int COUNT>
+  __device__ __forceinline__ void get(float (&b)[COUNT], int n, int N) const {
+    if (type == HIP_INT8_F32) load<float>(b, n, N);
+    else if (type == HIP_INT8_BF16) load<bf16>(b, n, N);
+    else load<_Float16>(b, n, N);
+  }
+  Bias from(int n) const {
+    if (!p) return *this;
+    return Bias{static_cast<const uint8_t*>(p) + int64_t(n) * (type == HIP_INT8_F32 ? 4 : 2), type};
+  }
+};
+
+template <class O>
+struct Out {
+  O* d;
+  int64_t ldd;
+  int M, N;
+  const float* sa;
+  int64_t sa_inc;
+  const float* sb;
+  int64_t sb_inc;
+  Bias bias;
+
+  // D's COUNT neighbours of row m from column n, those inside, of their sums.
+  // (Ends are compared as N - COUNT: n + COUNT passes 2^31 for the widest D.)
+  template <int COUNT>
+  __device__ __forceinline__ void row(int m, int n, const float (&v)[COUNT]) const {
+    if (m >= M || n >= N) return;
+    const float s = sa[m * sa_inc];
+    float t[COUNT];
+    if (sb_inc == 1 && n <= N - COUNT) {
+      const Pack<COUNT, float> p = load_pack<COUNT>(sb + n);
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) t[i] = p.v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) t[i] = n + i < N ? sb[(n + i) * sb_inc] : 0.0f;
+    }
+    Pack<COUNT, O> r;
+    if (bias.p) {
+      float b[COUNT];
+      bias.get(b, n, N);
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) from_float(fmaf(v[i] * s, t[i], b[i]), r.v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) from_float(v[i] * s * t[i], r.v[i]);
+    }
+    O* const to = d + m * ldd + n;
+    if (n <= N - COUNT) {
+      store_pack(to, r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i)
+        if (n + i < N) to[i] = r.v[i];
+    }
+  }
+  __device__ __forceinline__ void operator()(int m, int n, v4i v) const {
+    const float x[4] = {static_cast<float>(v[0]), static_cast<float>(v[1]), static_cast<float>(v[2]),
+                        static_cast<float>(v[3])};
+    row(m, n, x);
+  }
+  Out from(int m0, int n0, int rows, int cols) const {
+    Out o = *this;
+    o.d += m0 * ldd + n0;
+    o.M = rows;
+    o.N = cols;
+    o.sa += m0 * sa_inc;
+    o.sb += n0 * sb_inc;
+    o.bias = bias.from(n0);
+    return o;
+  }
+};
+
+// Large tiles: the K loop in assembly, results by way of LDS as floats, so that
+// whole lines are written.
+template <class L, class O>
+__global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, Out<O> out, int tiles_m, int tiles_n) {
+  __shared__ alignas(16) uint8_t smem[L::kLds];
+  const nt::Place at = nt::place_of(xcd_contiguous(blockIdx.x, gridDim.x), tiles_m, tiles_n, 8);
+  const int m0 = at.tm * L::BM, n0 = at.tn * L::BN;
+  nt::v16f acc[L::kAcc];
+  nt::loop_sum<L>(smem, A, B, m0, n0, K, acc);
+#pragma unroll
+  for (int i = 0; i < L::kAcc; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][r] = static_cast<float>(__float_as_int(acc[i][r]));
+  using Sheet = nt::Sheet<L::BN>;
+  static_assert(sizeof(Sheet) <= L::kLds, "a sheet fits");
+  Sheet& sheet = *reinterpret_cast<Sheet*>(smem);
+  __syncthreads();  // all wavefronts have left the loop
+  nt::loop_sheets<L>(sheet, acc, [&](int top) {
+    sheet.template out<L::threads>(
+        false, [&](int r, int c, const float (&v)[8]) { out.row(m0 + top + r, n0 + c, v); },
+        [](int, int, const float (&)[8]) {});
+  });
+}
+
+template <class L, class O>
+void launch_loop(const Side& A, const Side& B, int K, const Out<O>& out, unsigned blocks, hipStream_t s) {
+  const int64_t tm = ceil_div(out.M, L::BM), tn = ceil_div(out.N, L::BN);
+  hipLaunchKernelGGL((k_loop<L, O>), dim3(blocks), dim3(L::threads), 0, s, A, B, K, out, static_cast<int>(tm),
+                     static_cast<int>(tn));
+}
+
+struct Model {
+  nt::SmallCost small(int i) const {
+    if (i == 0) return {2.8, 0.45, 0.003};
+    if (i == 1) return {2.3, 1.3, 0.0056};
+    return {3.0, 2.2, 0.0135};
+  }
+  template <class F>
+  void loops(int M, int N, double steps, const F& offer) const {
+    const auto loop = [&](Way w, int bn, double base, double alone, double full) {
+      const int64_t tiles = ceil_div(M, 256) * ceil_div(N, bn), rest = tiles % 256;
+      if (tiles > kMaxWorkItems / 512) return;  // a block a tile: more than a launch takes
+      offer(w, base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0)));
+    };
+    loop(Way::kLoop128, 128, 6.0, 0.65, 0.98);
+    loop(Way::kLoop256, 256, 7.0, 1.0, 1.6);
+  }
+  bool cuts_rows(int t) const { return t == 256; }
+  constexpr nt::TileShape shape(Way way) const {
+    switch (way) {
+      case Way::kSmall16: return {16, 16, 512};
+      case Way::kSmall32: return {32, 32, 512};
+      case Way::kSmall64: return {64, 64, 512};
+      case Way::kLoop128: return {256, 128, 512};
+      default: return {256, 256, 512};
+    }
+  }
+};
+
+template <class O>
+void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
+  using Loop128 = nt::Loop<nt::Kind::kInt8, 4, 4, 4, 2, 3>;
+  using Loop256 = nt::Loop<nt::Kind::kInt8, 8, 4, 2, 4, 2>;
+  using P = nt::Int8;
+  constexpr Model model{};
+  using nt::is_shape;
+  static_assert(is_shape<Loop128>(model.shape(Way::kLoop128)) && is_shape<Loop256>(model.shape(Way::kLoop256)) &&
+                is_shape<nt::Direct<P, 1, 1, 8>>(model.shape(Way::kSmall16)) &&
+                is_shape<nt::Direct<P, 2, 2, 8>>(model.shape(Way::kSmall32)) &&
+                is_shape<nt::Direct<P, 4, 4, 8>>(model.shape(Way::kSmall64)));
+  Plan p;
+  plan(model, p, 0, 0, out.M, out.N, K, K > 0, nt::kCuts);
+  for (int i = 0; i < p.count; ++i) {
+    const nt::Piece& at = p.piece[i];
+    const Out<O> part = out.from(at.m0, at.n0, at.M, at.N);
+    const Side a = from_row(A, at.m0, 0), b = from_row(B, at.n0, 0);
+    const unsigned blocks = static_cast<unsigned>(blocks_of(model, at));
+    if (at.way <= Way::kSmall64) nt::launch_small<P>(at.way, a, b, K, part, at.skip_m, at.skip_n, blocks, s);
+    else if (at.way == Way::kLoop128) launch_loop<Loop128>(a, b, K, part, blocks, s);
+    else launch_loop<Loop256>(a, b, K, part, blocks, s);
+  }
+}
+
+// The sum is empty: D is the bias.
+template <class O>
+__global__ __launch_bounds__(256) void k_bias(Out<O> out, int64_t items, int per_row) {
+  for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < items; t += int64_t(gridDim.x) * 256) {
+    const int64_t m = t / per_row;
+    const int n = static_cast<int>(t % per_row) * 4;
+    float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (out.bias.p) out.bias.get(b, n, out.N);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n < out.N - i) from_float(b[i], out.d[m * out.ldd + n + i]);
+  }
+}
+
+template <class O>
+void launch_out(const Int8Product& p, hipStream_t stream) {
+  const Out<O> out{static_cast<O*>(p.d), p.ldd, p.M, p.N, p.sa, p.sa_inc, p.sb, p.sb_inc, Bias{p.bias, p.bias_type}};
+  if (p.K == 0) {
+    const int64_t per = ceil_div(p.N, 4), items = per * p.M, blocks = ceil_div(items, 256), cap = kMaxWorkItems / 256;
+    hipLaunchKernelGGL((k_bias<O>), dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(256), 0, stream, out,
+                       items, static_cast<int>(per));
+    return;
+  }
+  const Side a{static_cast<const uint8_t*>(p.a), p.lda, p.M, nullptr, 0, 0, 0, 0};
+  const Side b{static_cast<const uint8_t*>(p.b), p.ldb, p.N, nullptr, 0, 0, 0, 0};
+  launch<O>(a, b, p.K, out, stream);
+}
+
+bool bad_type(int t) { return t != HIP_INT8_F32 && t != HIP_INT8_BF16 && t != HIP_INT8_F16; }
+bool bad_ld(int ld, int K) { return ld < (K > 1 ? K : 1) || ld % 16 != 0 || ld > HIP_INT8_MAX_LD; }
+bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
+// of the codes of a linear layer's tokens
+int64_t code_stride(int inputs) { return inputs > 0 ? ceil_div(inputs, 16) * 16 : 16; }
+
+}  // namespace
+
+void launch_int8_gemm(const Int8Product& p, hipStream_t stream) {
+  if (p.d_type == HIP_INT8_F32) launch_out<float>(p, stream);
+  else if (p.d_type == HIP_INT8_BF16) launch_out<bf16>(p, stream);
+  else launch_out<_Float16>(p, stream);
+}
+
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" {
+
+int hip_int8_gemm(int M, int N, int K, const void* A, int lda, const float* SA, long long sa_inc, const void* B, int ldb,
+                  const float* SB, long long sb_inc, const void* bias, int bias_type, void* D, int ldd, int d_type,
+                  hipStream_t stream) {
+  if (M < 0) return -1;
+  if (N < 0) return -2;
+  if (K < 0 || K > HIP_INT8_MAX_K) return -3;
+  const bool some = M > 0 && N > 0, product = some && K > 0;
+  if (product && (A == nullptr || off16(A))) return -4;
+  if (bad_ld(lda, K)) return -5;
+  if (product && SA == nullptr) return -6;
+  if (sa_inc < 0) return -7;
+  if (product && (B == nullptr || off16(B))) return -8;
+  if (bad_ld(ldb, K)) return -9;
+  if (product && SB == nullptr) return -10;
+  if (sb_inc < 0) return -11;
+  if (bias != nullptr && bad_type(bias_type)) return -13;
+  if (some && D == nullptr) return -14;
+  if (ldd < (N > 1 ? N : 1)) return -15;
+  if (bad_type(d_type)) return -16;
+  if (!some) return 0;
+  launch_int8_gemm(Int8Product{M, N, K, A, lda, SA, sa_inc, B, ldb, SB, sb_inc, bias, bias_type, D, ldd, d_type}, stream);
+  return static_cast<int>(hipGetLastError());
+}
+
+int hip_int8_gemm_plan(int M, int N, int K, hip_int8_gemm_launch* launches, int* count) {
+  if (M < 0) return -1;
+  if (N < 0) return -2;
+  if (K < 0 || K > HIP_INT8_MAX_K) return -3;
+  Plan p;
+  const Model model{};
+  if (M > 0 && N > 0 && K > 0) plan(model, p, 0, 0, M, N, K, true, nt::kCuts);
+  for (int i = 0; launches && i < p.count; ++i) {
+    const nt::Piece& at = p.piece[i];
+    const nt::TileShape t = model.shape(at.way);
+    launches[i] = hip_int8_gemm_launch{t.rows, t.cols, at.m0, at.n0, at.M, at.N, at.skip_m, at.skip_n, t.threads,
+                                       blocks_of(model, at)};
+  }
+  if (count) *count = p.count;
+  return 0;
+}
+
+int hip_int8_linear_workspace(int tokens, int inputs, long long* bytes) {
+  if (tokens < 0) return -1;
+  if (inputs < 0 || inputs > HIP_INT8_MAX_K) return -2;
+  if (bytes) *bytes = tokens * (code_stride(inputs) + 4);
+  return 0;
+}
+
+int hip_int8_linear(int tokens, int inputs, int outputs, const void* X, int x_type, int ldx, const void* W, int ldw,
+                    const float* SW, long long sw_inc, const void* bias, int bias_type, void* Y, int ldy, int y_type,
+                    void* workspace, long long workspace_bytes, hipStream_t stream) {
+  if (tokens < 0) return -1;
+  if (inputs < 0 || inputs > HIP_INT8_MAX_K) return -2;
+  if (outputs < 0) return -3;
+  const bool some = tokens > 0 && outputs > 0, product = some && inputs > 0;
+  if (product && X == nullptr) return -4;
+  if (bad_type(x_type)) return -5;
+  if (ldx < (inputs > 1 ? inputs : 1)) return -6;
+  if (product && (W == nullptr || off16(W))) return -7;
+  if (bad_ld(ldw, inputs)) return -8;
+  if (product && SW == nullptr) return -9;
+  if (sw_inc < 0) return -10;
+  if (bias != nullptr && bad_type(bias_type)) return -12;
+  if (some && Y == nullptr) return -13;
+  if (ldy < (outputs > 1 ? outputs : 1)) return -14;
+  if (bad_type(y_type)) return -15;
+  if (product && (workspace == nullptr || off16(workspace))) return -16;
+  if (product && workspace_bytes < tokens * (code_stride(inputs) + 4)) return -17;
+  if (!some) return 0;
+  const int64_t ldq = code_stride(inputs);
+  int8_t* const q = static_cast<int8_t*>(workspace);
+  float* const s = product ? reinterpret_cast<float*>(q + tokens * ldq) : nullptr;
+  if (product) launch_int8_quantize(tokens, inputs, X, x_type, ldx, q, ldq, s, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return static_cast<int>(e);
+  launch_int8_gemm(Int8Product{tokens, outputs, inputs, q, ldq, s, 1, W, ldw, SW, sw_inc, bias, bias_type, Y, ldy, y_type},
+                   stream);
+  return static_cast<int>(hipGetLastError());
+}
+
+const char* hip_int8_gemm_status_string(int status) {
+  switch (status) {
+    case 0: return "success";
+    case -1: return "argument 1 (M) is negative";
+    case -2: return "argument 2 (N) is negative";
+    case -3: return "argument 3 (K) is negative or above HIP_INT8_MAX_K";
+    case -4: return "argument 4 (A) is NULL or not 16-byte aligned";
+    case -5: return "argument 5 (lda) is smaller than max(1, K), no multiple of 16, or above HIP_INT8_MAX_LD";
+    case -6: return "argument 6 (SA) is NULL";
+    case -7: return "argument 7 (sa_inc) is negative";
+    case -8: return "argument 8 (B) is NULL or not 16-byte aligned";
+    case -9: return "argument 9 (ldb) is smaller than max(1, K), no multiple of 16, or above HIP_INT8_MAX_LD";
+    case -10: return "argument 10 (SB) is NULL";
+    case -11: return "argument 11 (sb_inc) is negative";
+    case -13: return "argument 13 (bias_type) is not a known type";
+    case -14: return "argument 14 (D) is NULL";
+    case -15: return "argument 15 (ldd) is smaller than max(1, N)";
+    case -16: return "argument 16 (d_type) is not a known type";
+    default: break;
+  }
+  if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));
+  return "unknown status";
+}
+
+const char* hip_int8_linear_status_string(int status) {
+  switch (status) {
+    case 0: return "success";
+    case -1: return "argument 1 (tokens) is negative";
+    case -2: return "argument 2 (inputs) is negative or above HIP_INT8_MAX_K";
+    case -3: return "argument 3 (outputs) is negative";
+    case -4: return "argument 4 (X) is NULL";
+    case -5: return "argument 5 (x_type) is not a known type";
+    case -6: return "argument 6 (ldx) is smaller than max(1, inputs)";
+    case -7: return "argument 7 (W) is NULL or not 16-byte aligned";
+    case -8: return "argument 8 (ldw) is smaller than max(1, inputs), no multiple of 16, or above HIP_INT8_MAX_LD";
+    case -9: return "argument 9 (SW) is NULL";
+    case -10: return "argument 10 (sw_inc) is negative";
+    case -12: return "argument 12 (bias_type) is not a known type";
+    case -13: return "argument 13 (Y) is NULL";
+    case -14: return "argument 14 (ldy) is smaller than max(1, outputs)";
+    case -15: return "argument 15 (y_type) is not a known type";
+    case -16: return "argument 16 (workspace) is NULL or not 16-byte aligned";
+    case -17: return "argument 17 (workspace_bytes) is less than hip_int8_linear_workspace says";
+    default: break;
+  }
+  if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));
+  return "unknown status";
+}
+
+}  // extern "C"

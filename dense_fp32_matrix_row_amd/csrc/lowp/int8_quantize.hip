@@ -1,0 +1,169 @@
+// int8_quantize.hip -- hip_int8_quantize: the rows of a matrix into 8-bit integers
+// with a scale each.
+//
+// Bound by memory: e bytes read and one written per element, against some twelve
+// vector instructions.
+#include "../../../include/int8.h"
+#include "int8_internal.h"
+#include "rows.h"
+
+namespace sgemm {
+namespace {
+
+constexpr uint32_t kAmaxFloor = (127u - 100u) << 23;  // 2^-100
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// s, and its float reciprocal; r is 0 where a row holds an infinity or a NaN.
+struct Scale {
+  float s, r;
+};
+
+__device__ __forceinline__ Scale make_scale(uint32_t top) {
+  if (top >= kInfBits) return Scale{__uint_as_float(0x7fc00000u), 0.0f};
+  const float a = __uint_as_float(top < kAmaxFloor ? kAmaxFloor : top), s = a / 127.0f;
+  return Scale{s, 1.0f / s};
+}
+
+// x / s rounded once, ties to even.  t = |x| r is within 127 * 2^-22 of the
+// quotient, so the quotient lies within half a step and that of floor(t) + 1/2,
+// the one border between integers that can decide: on which side of it |x| / s
+// lies is the sign of |x| - border * s, which fma gives as it is (border has 8
+// bits and s 24, so the difference, where it is small, is a float).  A tie goes to the even
+// of the two.
+__device__ __forceinline__ int code(float x, Scale q) {
+  if (q.r == 0.0f) return 0;
+  const float a = fabsf(x), f = floorf(a * q.r), rest = fmaf(-(f + 0.5f), q.s, a);
+  int k = static_cast<int>(f);
+  k += rest > 0.0f || (rest == 0.0f && (k & 1)) ? 1 : 0;
+  return x < 0.0f ? -k : k;
+}
+
+template <class X>
+__device__ __forceinline__ Pack<8, int8_t> codes8(const Pack<8, X>& x, Scale q) {
+  Pack<8, int8_t> c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c.v[i] = static_cast<int8_t>(code(to_float(x.v[i]), q));
+  return c;
+}
+
+struct Max {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
+};
+
+template <class X>
+__device__ __forceinline__ uint32_t top8(uint32_t top, const Pack<8, X>& x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, magnitude(to_float(x.v[i])));
+  return top;
+}
+
+// A row in the registers of its lanes: read once.
+template <class S, class X>
+__global__ __launch_bounds__(S::threads) void k_rows(const X* __restrict__ x, int64_t ldx, int8_t* __restrict__ q,
+                                                     int64_t ldq, float* __restrict__ s, int rows, int cols) {
+  __shared__ uint32_t meet[S::threads / 64][1];
+  const int lane = threadIdx.x % S::LANES;
+  const int64_t steps = ceil_div(rows, S::rows);
+  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
+    const int64_t row = step * S::rows + threadIdx.x / S::LANES;
+    if (S::waves == 1 && row >= rows) return;
+    Pack<8, X> v[S::COUNT];
+    uint32_t top[1] = {0};
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(x + row * ldx, (c * S::LANES + lane) * 8, cols);
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) top[0] = top8(top[0], v[c]);
+    join_row<S>(top, meet, Max{});
+    const Scale by = make_scale(top[0]);
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) store_row8(q + row * ldq, (c * S::LANES + lane) * 8, cols, codes8(v[c], by));
+    if (lane == 0) s[row] = by.s;
+    if constexpr (S::waves > 1) __syncthreads();  // the next row writes the same LDS
+  }
+}
+
+// Rows longer than registers hold: read twice.
+template <class X>
+__global__ __launch_bounds__(1024) void k_long(const X* __restrict__ x, int64_t ldx, int8_t* __restrict__ q,
+                                               int64_t ldq, float* __restrict__ s, int rows, int cols) {
+  using S = RowShape<1024, 1>;
+  __shared__ uint32_t meet[S::threads / 64][1];
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    uint32_t top[1] = {0};
+    for (int64_t c = threadIdx.x * 8; c < cols; c += S::width)
+      top[0] = top8(top[0], load_row8(x + row * ldx, static_cast<int>(c), cols));
+    join_row<S>(top, meet, Max{});
+    const Scale by = make_scale(top[0]);
+    for (int64_t c = threadIdx.x * 8; c < cols; c += S::width)
+      store_row8(q + row * ldq, static_cast<int>(c), cols, codes8(load_row8(x + row * ldx, static_cast<int>(c), cols), by));
+    if (threadIdx.x == 0) s[row] = by.s;
+    __syncthreads();
+  }
+}
+
+template <class X>
+void launch_type(int rows, int cols, const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* s, hipStream_t stream) {
+  const X* p = static_cast<const X*>(x);
+  if (cols > kRowWidth) {
+    const int64_t cap = kMaxWorkItems / 1024;
+    const dim3 grid(static_cast<unsigned>(rows < cap ? rows : cap));
+    hipLaunchKernelGGL((k_long<X>), grid, dim3(1024), 0, stream, p, ldx, q, ldq, s, rows, cols);
+    return;
+  }
+  with_row_shape(cols, [&](auto shape) {
+    using S = decltype(shape);
+    const int64_t steps = ceil_div(rows, S::rows), cap = kMaxWorkItems / S::threads;
+    const dim3 grid(static_cast<unsigned>(steps < cap ? steps : cap));
+    hipLaunchKernelGGL((k_rows<S, X>), grid, dim3(S::threads), 0, stream, p, ldx, q, ldq, s, rows, cols);
+  });
+}
+
+}  // namespace
+
+void launch_int8_quantize(int rows, int cols, const void* x, int x_type, int64_t ldx, int8_t* q, int64_t ldq, float* s,
+                          hipStream_t stream) {
+  if (x_type == HIP_INT8_F32) launch_type<float>(rows, cols, x, ldx, q, ldq, s, stream);
+  else if (x_type == HIP_INT8_BF16) launch_type<bf16>(rows, cols, x, ldx, q, ldq, s, stream);
+  else launch_type<_Float16>(rows, cols, x, ldx, q, ldq, s, stream);
+}
+
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" {
+
+int hip_int8_quantize(int rows, int cols, const void* X, int x_type, int ldx, void* Q, int ldq, float* S,
+                      hipStream_t stream) {
+  if (rows < 0) return -1;
+  if (cols < 0) return -2;
+  const bool some = rows > 0 && cols > 0;
+  if (some && X == nullptr) return -3;
+  if (x_type != HIP_INT8_F32 && x_type != HIP_INT8_BF16 && x_type != HIP_INT8_F16) return -4;
+  if (ldx < (cols > 1 ? cols : 1)) return -5;
+  if (some && Q == nullptr) return -6;
+  if (ldq < (cols > 1 ? cols : 1)) return -7;
+  if (some && S == nullptr) return -8;
+  if (!some) return 0;
+  launch_int8_quantize(rows, cols, X, x_type, ldx, static_cast<int8_t*>(Q), ldq, S, stream);
+  return static_cast<int>(hipGetLastError());
+}
+
+const char* hip_int8_quantize_status_string(int status) {
+  switch (status) {
+    case 0: return "success";
+    case -1: return "argument 1 (rows) is negative";
+    case -2: return "argument 2 (cols) is negative";
+    case -3: return "argument 3 (X) is NULL";
+    case -4: return "argument 4 (x_type) is not a known type";
+    case -5: return "argument 5 (ldx) is smaller than max(1, cols)";
+    case -6: return "argument 6 (Q) is NULL";
+    case -7: return "argument 7 (ldq) is smaller than max(1, cols)";
+    case -8: return "argument 8 (S) is NULL";
+    default: break;
+  }
+  if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));
+  return "unknown status";
+}
+
+}  // extern "C"

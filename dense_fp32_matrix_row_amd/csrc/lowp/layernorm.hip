@@ -1,0 +1,508 @@
+// layernorm.hip -- hip_layernorm_forward and hip_layernorm_backward.
+//
+// Bound by memory: the forward pass reads x and writes y, the backward pass reads
+// x and dy and writes dx, each once, against some ten vector instructions an
+// element; rows lie in registers (rows.h) from the sums to the results.
+#include "../../../include/layernorm.h"
+#include "rows.h"
+
+namespace sgemm {
+namespace {
+
+static_assert(HIP_LAYERNORM_ROW == kRowWidth);
+
+struct Sum {
+  template <class T>
+  __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+
+// w or b: numbers of a type side by side, or one number for all.
+struct Param {
+  const void* p;
+  int type;
+  float fill;
+  template <class T>
+  __device__ __forceinline__ void load(float (&v)[8], int col, int cols) const {
+    const Pack<8, T> r = load_row8(static_cast<const T*>(p), col, cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_float(r.v[i]);
+  }
+  __device__ __forceinline__ void get(float (&v)[8], int col, int cols) const {
+    if (!p) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fill;
+    } else if (type == HIP_LAYERNORM_F32) {
+      load<float>(v, col, cols);
+    } else if (type == HIP_LAYERNORM_BF16) {
+      load<bf16>(v, col, cols);
+    } else {
+      load<_Float16>(v, col, cols);
+    }
+  }
+};
+
+// A row's mean, what its rounding to float left over, and rstd.
+struct Stats {
+  float mean, rest, rstd;
+};
+__device__ __forceinline__ Stats load_stats(const float* stats, int64_t row, int64_t rows) {
+  return Stats{stats[row], stats[rows + row], stats[2 * rows + row]};
+}
+__device__ __forceinline__ void store_stats(float* stats, int64_t row, int64_t rows, const Stats& s) {
+  stats[row] = s.mean;
+  stats[rows + row] = s.rest;
+  stats[2 * rows + row] = s.rstd;
+}
+// (x - mean) rstd: x - mean is exact where x is near the mean, and the rest small.
+__device__ __forceinline__ float normalised(float x, const Stats& s) { return ((x - s.mean) - s.rest) * s.rstd; }
+
+// The mean rounded to float is off by up to 2^-24 of itself, which for a row far
+// off zero is much of its differences, so their own mean is taken beside their
+// squares': with d = x - mean, the mean is mean + avg d and the variance
+// avg d^2 - (avg d)^2.
+template <class S, class X>
+__global__ __launch_bounds__(S::threads) void k_forward(const X* x, int64_t ldx, Param w, Param b, float eps, X* y,
+                                                        int64_t ldy, float* __restrict__ stats, int rows, int cols) {
+  __shared__ float first[S::threads / 64][1], second[S::threads / 64][2];
+  const int lane = threadIdx.x % S::LANES;
+  const int64_t steps = ceil_div(rows, S::rows);
+  const float n = static_cast<float>(cols);
+  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
+    const int64_t row = step * S::rows + threadIdx.x / S::LANES;
+    if (S::waves == 1 && row >= rows) return;
+    Pack<8, X> v[S::COUNT];
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(x + row * ldx, (c * S::LANES + lane) * 8, cols);
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] += to_float(v[c].v[i]);
+    join_row<S>(sum, first, Sum{});
+    Stats s{sum[0] / n, 0.0f, 0.0f};
+    float d[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = (c * S::LANES + lane) * 8 < cols - i ? to_float(v[c].v[i]) - s.mean : 0.0f;
+        d[0] += t;
+        d[1] = fmaf(t, t, d[1]);
+      }
+    join_row<S>(d, second, Sum{});
+    s.rest = d[0] / n;
+    s.rstd = 1.0f / sqrtf(fmaxf(d[1] / n - s.rest * s.rest, 0.0f) + eps);
+    if (!(fabsf(d[1]) < INFINITY)) s.rstd = __uint_as_float(0x7fc00000u);  // fmaxf takes no NaN over
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) {
+      const int col = (c * S::LANES + lane) * 8;
+      float wv[8], bv[8];
+      w.get(wv, col, cols);
+      b.get(bv, col, cols);
+      Pack<8, X> r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) from_float(fmaf(normalised(to_float(v[c].v[i]), s), wv[i], bv[i]), r.v[i]);
+      store_row8(y + row * ldy, col, cols, r);
+    }
+    if (stats && lane == 0) store_stats(stats, row, rows, s);
+  }
+}
+
+// Rows longer than registers hold: read three times, sums in double.
+template <class X>
+__global__ __launch_bounds__(1024) void k_forward_long(const X* x, int64_t ldx, Param w, Param b, float eps, X* y,
+                                                       int64_t ldy, float* __restrict__ stats, int rows, int cols) {
+  using S = RowShape<1024, 1>;
+  __shared__ double first[S::threads / 64][1], second[S::threads / 64][2];
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const X* const from = x + row * ldx;
+    double sum[1] = {0.0};
+    for (int64_t c = threadIdx.x * 8; c < cols; c += S::width) {
+      const Pack<8, X> v = load_row8(from, static_cast<int>(c), cols);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[0] += static_cast<double>(to_float(v.v[i]));
+    }
+    join_row<S>(sum, first, Sum{});
+    const double mean = sum[0] / cols;
+    double d[2] = {0.0, 0.0};
+    for (int64_t c = threadIdx.x * 8; c < cols; c += S::width) {
+      const Pack<8, X> v = load_row8(from, static_cast<int>(c), cols);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const double t = c + i < cols ? static_cast<double>(to_float(v.v[i])) - mean : 0.0;
+        d[0] += t;
+        d[1] = fma(t, t, d[1]);
+      }
+    }
+    join_row<S>(d, second, Sum{});
+    Stats s;
+    s.mean = static_cast<float>(mean);
+    s.rest = static_cast<float>(mean - static_cast<double>(s.mean));
+    s.rstd = static_cast<float>(1.0 / sqrt(d[1] / cols + static_cast<double>(eps)));
+    for (int64_t c = threadIdx.x * 8; c < cols; c += S::width) {
+      const Pack<8, X> v = load_row8(from, static_cast<int>(c), cols);
+      float wv[8], bv[8];
+      w.get(wv, static_cast<int>(c), cols);
+      b.get(bv, static_cast<int>(c), cols);
+      Pack<8, X> r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) from_float(fmaf(normalised(to_float(v.v[i]), s), wv[i], bv[i]), r.v[i]);
+      store_row8(y + row * ldy, static_cast<int>(c), cols, r);
+    }
+    if (stats && threadIdx.x == 0) store_stats(stats, row, rows, s);
+  }
+}
+
+// dw and db of a block's rows lie in its threads' registers, a thread's columns
+// being the same in every row, and leave once, into the block's part of the
+// workspace; k_join adds the parts in their order.
+template <class S, class X>
+__global__ __launch_bounds__(S::threads) void k_backward(const X* dy, int64_t lddy, const X* x, int64_t ldx,
+                                                         const float* __restrict__ stats, Param w, X* dx, int64_t lddx,
+                                                         float* __restrict__ parts, int rows, int cols) {
+  __shared__ float meet[2][S::threads / 64][2];
+  const int lane = threadIdx.x % S::LANES;
+  const int64_t steps = ceil_div(rows, S::rows);
+  const float n = static_cast<float>(cols);
+  float wv[S::COUNT][8], pw[S::COUNT][8], pb[S::COUNT][8];
+#pragma unroll
+  for (int c = 0; c < S::COUNT; ++c) {
+    w.get(wv[c], (c * S::LANES + lane) * 8, cols);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pw[c][i] = pb[c][i] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x, turn ^= 1) {
+    const int64_t row = step * S::rows + threadIdx.x / S::LANES;
+    if (S::waves == 1 && row >= rows) break;
+    Pack<8, X> xv[S::COUNT], gv[S::COUNT];
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) {
+      xv[c] = load_row8(x + row * ldx, (c * S::LANES + lane) * 8, cols);
+      gv[c] = load_row8(dy + row * lddy, (c * S::LANES + lane) * 8, cols);
+    }
+    const Stats s = load_stats(stats, row, rows);
+    float h[S::COUNT][8], sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float t = to_float(gv[c].v[i]), g = t * wv[c][i];
+        h[c][i] = normalised(to_float(xv[c].v[i]), s);  // past the row's end times dy's zeros
+        pw[c][i] = fmaf(t, h[c][i], pw[c][i]);
+        pb[c][i] += t;
+        sum[0] += g;
+        sum[1] = fmaf(g, h[c][i], sum[1]);
+      }
+    if (!dx) continue;
+    join_row<S>(sum, meet[turn], Sum{});
+    const float c1 = sum[0] / n, c2 = sum[1] / n;
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) {
+      Pack<8, X> r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        from_float((fmaf(to_float(gv[c].v[i]), wv[c][i], -c1) - h[c][i] * c2) * s.rstd, r.v[i]);
+      store_row8(dx + row * lddx, (c * S::LANES + lane) * 8, cols, r);
+    }
+  }
+  if (!parts) return;
+  float* const to = parts + int64_t(blockIdx.x) * 2 * cols;
+  if constexpr (S::rows > 1) {  // the block's wavefronts first
+    __shared__ float all[S::rows][S::width];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k) __syncthreads();
+#pragma unroll
+      for (int c = 0; c < S::COUNT; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all[threadIdx.x / S::LANES][(c * S::LANES + lane) * 8 + i] = k ? pb[c][i] : pw[c][i];
+      __syncthreads();
+      for (int n = threadIdx.x; n < cols; n += S::threads) {
+        float v = all[0][n];
+#pragma unroll
+        for (int r = 1; r < S::rows; ++r) v += all[r][n];
+        to[k * cols + n] = v;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int c = 0; c < S::COUNT; ++c) {
+        Pack<8, float> v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.v[i] = k ? pb[c][i] : pw[c][i];
+        store_row8(to + k * cols, (c * S::LANES + lane) * 8, cols, v);
+      }
+  }
+}
+
+// Rows longer than registers hold: first dw and db (dx may be written over dy), a
+// block for 2048 columns of a share of the rows; then dx, a block a row, read twice.
+template <class X>
+__global__ __launch_bounds__(256) void k_params_long(const X* __restrict__ dy, int64_t lddy, const X* __restrict__ x,
+                                                     int64_t ldx, const float* __restrict__ stats,
+                                                     float* __restrict__ parts, int rows, int cols, int strips) {
+  const int64_t strip = blockIdx.x % strips, part = blockIdx.x / strips, count = gridDim.x / strips;
+  const int64_t at = strip * 2048 + threadIdx.x * 8;
+  if (at >= cols) return;
+  const int col = static_cast<int>(at);
+  Pack<8, float> pw{}, pb{};
+  for (int64_t row = part; row < rows; row += count) {
+    const Pack<8, X> xv = load_row8(x + row * ldx, col, cols), gv = load_row8(dy + row * lddy, col, cols);
+    const Stats s = load_stats(stats, row, rows);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = to_float(gv.v[i]);
+      pw.v[i] = fmaf(t, normalised(to_float(xv.v[i]), s), pw.v[i]);
+      pb.v[i] += t;
+    }
+  }
+  store_row8(parts + part * 2 * cols, col, cols, pw);
+  store_row8(parts + part * 2 * cols + cols, col, cols, pb);
+}
+
+template <class X>
+__global__ __launch_bounds__(1024) void k_backward_long(const X* dy, int64_t lddy, const X* x, int64_t ldx,
+                                                        const float* __restrict__ stats, Param w, X* dx, int64_t lddx,
+                                                        int rows, int cols) {
+  using S = RowShape<1024, 1>;
+  __shared__ double meet[2][S::threads / 64][2];
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+    const Stats s = load_stats(stats, row, rows);
+    double sum[2] = {0.0, 0.0};
+    for (int64_t c = threadIdx.x * 8; c < cols; c += S::width) {
+      const int col = static_cast<int>(c);
+      const Pack<8, X> xv = load_row8(x + row * ldx, col, cols), gv = load_row8(dy + row * lddy, col, cols);
+      float wv[8];
+      w.get(wv, col, cols);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float g = to_float(gv.v[i]) * wv[i];
+        sum[0] += static_cast<double>(g);
+        sum[1] = fma(static_cast<double>(g), static_cast<double>(normalised(to_float(xv.v[i]), s)), sum[1]);
+      }
+    }
+    join_row<S>(sum, meet[turn], Sum{});
+    const float c1 = static_cast<float>(sum[0] / cols), c2 = static_cast<float>(sum[1] / cols);
+    for (int64_t c = threadIdx.x * 8; c < cols; c += S::width) {
+      const int col = static_cast<int>(c);
+      const Pack<8, X> xv = load_row8(x + row * ldx, col, cols), gv = load_row8(dy + row * lddy, col, cols);
+      float wv[8];
+      w.get(wv, col, cols);
+      Pack<8, X> r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        from_float((fmaf(to_float(gv.v[i]), wv[i], -c1) - normalised(to_float(xv.v[i]), s) * c2) * s.rstd, r.v[i]);
+      store_row8(dx + row * lddx, col, cols, r);
+    }
+  }
+}
+
+// dw (blockIdx.y 0) and db (1): the sums of the parts' columns, 32 columns a block,
+// eight shares of the parts, each in its order, then the shares.
+__global__ __launch_bounds__(256) void k_join(const float* __restrict__ parts, int count, float* dw, float* db, int cols,
+                                              int accumulate) {
+  __shared__ float meet[8][32];
+  float* const out = blockIdx.y ? db : dw;
+  if (!out) return;
+  const int share = threadIdx.x / 32;
+  for (int64_t tile = blockIdx.x; tile < ceil_div(cols, 32); tile += gridDim.x) {
+    const int64_t col = tile * 32 + threadIdx.x % 32;
+    float v = 0.0f;
+    if (col < cols)
+      for (int p = share; p < count; p += 8) v += parts[(int64_t(p) * 2 + blockIdx.y) * cols + col];
+    meet[share][threadIdx.x % 32] = v;
+    __syncthreads();
+    if (share == 0 && col < cols) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i) v += meet[i][threadIdx.x];
+      out[col] = accumulate ? out[col] + v : v;
+    }
+    __syncthreads();  // the next columns write the same LDS
+  }
+}
+constexpr int64_t kJoinBlocks = int64_t(1) << 20;
+
+// Blocks of the backward pass, each with a part of dw and db in the workspace.
+int64_t parts_of(int rows, int cols) {
+  if (cols > kRowWidth) {
+    const int64_t share = 2048 / ceil_div(cols, 2048), most = share < 1 ? 1 : share < 64 ? share : 64;
+    return rows < most ? rows : most;
+  }
+  int64_t parts = 0;
+  with_row_shape(cols, [&](auto shape) {
+    using S = decltype(shape);
+    const int64_t steps = ceil_div(rows, S::rows), cap = 512 * 256 / S::threads;
+    parts = steps < cap ? steps : cap;
+  });
+  return parts;
+}
+
+struct Backward {
+  int rows, cols;
+  const void* dy;
+  int64_t lddy;
+  const void* x;
+  int64_t ldx;
+  const float* stats;
+  Param w;
+  void* dx;
+  int64_t lddx;
+  float* parts;
+  int count;
+};
+
+template <class X>
+void forward_type(int rows, int cols, const void* x, int64_t ldx, Param w, Param b, float eps, void* y, int64_t ldy,
+                  float* stats, hipStream_t stream) {
+  if (cols > kRowWidth) {
+    const int64_t cap = kMaxWorkItems / 1024;
+    hipLaunchKernelGGL((k_forward_long<X>), dim3(static_cast<unsigned>(rows < cap ? rows : cap)), dim3(1024), 0, stream,
+                       static_cast<const X*>(x), ldx, w, b, eps, static_cast<X*>(y), ldy, stats, rows, cols);
+    return;
+  }
+  with_row_shape(cols, [&](auto shape) {
+    using S = decltype(shape);
+    const int64_t steps = ceil_div(rows, S::rows), cap = kMaxWorkItems / S::threads;
+    hipLaunchKernelGGL((k_forward<S, X>), dim3(static_cast<unsigned>(steps < cap ? steps : cap)), dim3(S::threads), 0,
+                       stream, static_cast<const X*>(x), ldx, w, b, eps, static_cast<X*>(y), ldy, stats, rows, cols);
+  });
+}
+
+template <class X>
+void backward_type(const Backward& a, hipStream_t stream) {
+  const X* const dy = static_cast<const X*>(a.dy);
+  const X* const x = static_cast<const X*>(a.x);
+  X* const dx = static_cast<X*>(a.dx);
+  if (a.cols > kRowWidth) {
+    const int strips = static_cast<int>(ceil_div(a.cols, 2048));
+    if (a.parts)
+      hipLaunchKernelGGL((k_params_long<X>), dim3(static_cast<unsigned>(strips * a.count)), dim3(256), 0, stream, dy,
+                         a.lddy, x, a.ldx, a.stats, a.parts, a.rows, a.cols, strips);
+    const int64_t cap = kMaxWorkItems / 1024;
+    if (dx)
+      hipLaunchKernelGGL((k_backward_long<X>), dim3(static_cast<unsigned>(a.rows < cap ? a.rows : cap)), dim3(1024), 0,
+                         stream, dy, a.lddy, x, a.ldx, a.stats, a.w, dx, a.lddx, a.rows, a.cols);
+    return;
+  }
+  with_row_shape(a.cols, [&](auto shape) {
+    using S = decltype(shape);
+    hipLaunchKernelGGL((k_backward<S, X>), dim3(static_cast<unsigned>(a.count)), dim3(S::threads), 0, stream, dy, a.lddy,
+                       x, a.ldx, a.stats, a.w, dx, a.lddx, a.parts, a.rows, a.cols);
+  });
+}
+
+bool bad_type(int t) { return t != HIP_LAYERNORM_F32 && t != HIP_LAYERNORM_BF16 && t != HIP_LAYERNORM_F16; }
+
+}  // namespace
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" {
+
+int hip_layernorm_forward(int rows, int cols, int type, const void* X, int ldx, const void* w, const void* b, int w_type,
+                          float eps, void* Y, int ldy, float* stats, hipStream_t stream) {
+  if (rows < 0) return -1;
+  if (cols < 0) return -2;
+  const bool some = rows > 0 && cols > 0;
+  if (bad_type(type)) return -3;
+  if (some && X == nullptr) return -4;
+  if (ldx < (cols > 1 ? cols : 1)) return -5;
+  if ((w != nullptr || b != nullptr) && bad_type(w_type)) return -8;
+  if (!(eps >= 0.0f)) return -9;
+  if (some && Y == nullptr) return -10;
+  if (ldy < (cols > 1 ? cols : 1)) return -11;
+  if (!some) return 0;
+  const Param pw{w, w_type, 1.0f}, pb{b, w_type, 0.0f};
+  if (type == HIP_LAYERNORM_F32) forward_type<float>(rows, cols, X, ldx, pw, pb, eps, Y, ldy, stats, stream);
+  else if (type == HIP_LAYERNORM_BF16) forward_type<bf16>(rows, cols, X, ldx, pw, pb, eps, Y, ldy, stats, stream);
+  else forward_type<_Float16>(rows, cols, X, ldx, pw, pb, eps, Y, ldy, stats, stream);
+  return static_cast<int>(hipGetLastError());
+}
+
+int hip_layernorm_backward_workspace(int rows, int cols, long long* bytes) {
+  if (rows < 0) return -1;
+  if (cols < 0) return -2;
+  if (bytes) *bytes = rows > 0 && cols > 0 ? parts_of(rows, cols) * 2 * cols * 4 : 0;
+  return 0;
+}
+
+int hip_layernorm_backward(int rows, int cols, int type, const void* DY, int lddy, const void* X, int ldx,
+                           const float* stats, const void* w, int w_type, void* DX, int lddx, float* dw, float* db,
+                           int accumulate, void* workspace, long long workspace_bytes, hipStream_t stream) {
+  if (rows < 0) return -1;
+  if (cols < 0) return -2;
+  const bool some = rows > 0 && cols > 0, params = dw != nullptr || db != nullptr;
+  if (bad_type(type)) return -3;
+  if (some && DY == nullptr) return -4;
+  if (lddy < (cols > 1 ? cols : 1)) return -5;
+  if (some && X == nullptr) return -6;
+  if (ldx < (cols > 1 ? cols : 1)) return -7;
+  if (some && stats == nullptr) return -8;
+  if (w != nullptr && bad_type(w_type)) return -10;
+  if (DX != nullptr && lddx < (cols > 1 ? cols : 1)) return -12;
+  if (accumulate != 0 && accumulate != 1) return -15;
+  const int64_t count = some ? parts_of(rows, cols) : 0;
+  if (some && params && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)) return -16;
+  if (some && params && workspace_bytes < count * 2 * cols * 4) return -17;
+  if (cols == 0 || (!params && (rows == 0 || DX == nullptr))) return 0;
+  if (rows > 0) {
+    const Backward a{rows, cols, DY, lddy, X, ldx, stats, Param{w, w_type, 1.0f}, DX, lddx,
+                     params ? static_cast<float*>(workspace) : nullptr, static_cast<int>(count)};
+    if (type == HIP_LAYERNORM_F32) backward_type<float>(a, stream);
+    else if (type == HIP_LAYERNORM_BF16) backward_type<bf16>(a, stream);
+    else backward_type<_Float16>(a, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return static_cast<int>(e);
+  }
+  if (params)
+    hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>(min(ceil_div(cols, 32), kJoinBlocks)), 2), dim3(256), 0, stream,
+                       static_cast<const float*>(workspace), static_cast<int>(count), dw, db, cols, accumulate);
+  return static_cast<int>(hipGetLastError());
+}
+
+const char* hip_layernorm_forward_status_string(int status) {
+  switch (status) {
+    case 0: return "success";
+    case -1: return "argument 1 (rows) is negative";
+    case -2: return "argument 2 (cols) is negative";
+    case -3: return "argument 3 (type) is not a known type";
+    case -4: return "argument 4 (X) is NULL";
+    case -5: return "argument 5 (ldx) is smaller than max(1, cols)";
+    case -8: return "argument 8 (w_type) is not a known type";
+    case -9: return "argument 9 (eps) is negative or NaN";
+    case -10: return "argument 10 (Y) is NULL";
+    case -11: return "argument 11 (ldy) is smaller than max(1, cols)";
+    default: break;
+  }
+  if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));
+  return "unknown status";
+}
+
+const char* hip_layernorm_backward_status_string(int status) {
+  switch (status) {
+    case 0: return "success";
+    case -1: return "argument 1 (rows) is negative";
+    case -2: return "argument 2 (cols) is negative";
+    case -3: return "argument 3 (type) is not a known type";
+    case -4: return "argument 4 (DY) is NULL";
+    case -5: return "argument 5 (lddy) is smaller than max(1, cols)";
+    case -6: return "argument 6 (X) is NULL";
+    case -7: return "argument 7 (ldx) is smaller than max(1, cols)";
+    case -8: return "argument 8 (stats) is NULL";
+    case -10: return "argument 10 (w_type) is not a known type";
+    case -12: return "argument 12 (lddx) is smaller than max(1, cols)";
+    case -15: return "argument 15 (accumulate) is not 0 or 1";
+    case -16: return "argument 16 (workspace) is NULL or not 16-byte aligned";
+    case -17: return "argument 17 (workspace_bytes) is less than hip_layernorm_backward_workspace says";
+    default: break;
+  }
+  if (status > 0) return hipGetErrorString(static_cast<hipError_t>(status));
+  return "unknown status";
+}
+
+}  // extern "C"

@@ -27,7 +27,8 @@ struct Direct {
   static constexpr bool kScaled = P::kScaleBytes > 0;
   static constexpr int kSn = !kScaled ? 0 : !P::kRowScales || P::kUniform ? 1 : 4;  // scales a lane takes of 16 rows of B
 
-  using Meet = v4f[WAVES][kChunk][64];
+  using Sum = typename P::Acc;
+  using Meet = Sum[WAVES][kChunk][64];
 
   struct Raw {
     Frag a[MT], b[NT];
@@ -184,7 +185,7 @@ struct Direct {
       for (int o = 0; o < kChunk; o += WAVES) {
         const int f = o + wave;  // in the order of the wavefronts, whoever adds
         if (f < kChunk && c + f < kFrags) {
-          v4f v = meet[0][f][lane];
+          Sum v = meet[0][f][lane];
 #pragma unroll
           for (int w = 1; w < WAVES; ++w) v += meet[w][f][lane];
           epi(m0 + 16 * ((c + f) % MT) + row, n0 + 16 * ((c + f) / MT) + 4 * g, v);

@@ -1,9 +1,10 @@
-// nt_loop.h -- the large tiles of the block-scaled 8-bit product and the
-// orthogonalised update: D = A * B^T over operands whose rows are contiguous
-// along K (nt_tile.h has the operands' form), with the K loop in assembly
-// (nt_loop.inc, written by gen_nt_loop.py).
+// nt_loop.h -- the large tiles of the 8-bit products and the orthogonalised
+// update: D = A * B^T over operands whose rows are contiguous along K (nt_tile.h
+// has the operands' form), with the K loop in assembly (nt_loop.inc and
+// int8_loop.inc, written by gen_nt_loop.py).
 #pragma once
 
+#include "int8_loop.inc"
 #include "nt_loop.inc"
 #include "nt_tile.h"
 
@@ -13,7 +14,7 @@ namespace nt {
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 // What a loop multiplies and how it scales (gen_nt_loop.py).
-enum class Kind { kE8M0, kF32Uniform, kF32Rows, kWideF32Uniform, kWideF32Rows, kWideE8M0Uniform, kWideE8M0Rows, kPair };
+enum class Kind { kE8M0, kF32Uniform, kF32Rows, kWideF32Uniform, kWideF32Rows, kWideE8M0Uniform, kWideE8M0Rows, kPair, kInt8 };
 
 // Block tile of WM x WN wavefronts of 16 MT x 16 NT, at most 256 registers each.
 template <Kind KIND_, int MT_, int NT_, int WM_, int WN_, int STAGES_>
@@ -22,7 +23,7 @@ struct Loop {
   static constexpr int MT = MT_, NT = NT_, WM = WM_, WN = WN_, STAGES = STAGES_;
   static constexpr int kPositions = STAGES % 2 ? 2 * STAGES : STAGES;  // steps that the loop is unrolled over
   static constexpr int BM = 16 * MT * WM, BN = 16 * NT * WN, waves = WM * WN, threads = 64 * waves;
-  static constexpr bool kScaled = KIND != Kind::kPair;
+  static constexpr bool kScaled = KIND != Kind::kPair && KIND != Kind::kInt8;
   static constexpr bool kBytes = KIND == Kind::kWideE8M0Uniform || KIND == Kind::kWideE8M0Rows;
   static constexpr bool kUniform =
       KIND == Kind::kF32Uniform || KIND == Kind::kWideF32Uniform || KIND == Kind::kWideE8M0Uniform;
@@ -53,14 +54,15 @@ struct Loop {
   NT_SUMS_4, "=&{v[64:79]}"(acc[4]), "=&{v[80:95]}"(acc[5]), "=&{v[96:111]}"(acc[6]), "=&{v[112:127]}"(acc[7])
 #define NT_SUMS_9 NT_SUMS_8, "=&{v[128:143]}"(acc[8])
 #define NT_SCALES_OUT , "+{s[68:71]}"(rs), [aS] "+v"(aS), [bS] "+v"(bS)
-#define NT_SCALES_IN                                                                                               \
-  , "{s[86:87]}"(ss), [gS] "v"(gs), [maskLo0] "v"(mask[0]), [maskLo1] "v"(mask[1]), [maskLo2] "v"(mask[2]),       \
-      [maskLo3] "v"(mask[3]), [maskHi0] "v"(mask[4]), [maskHi1] "v"(mask[5]), [maskHi2] "v"(mask[6]),              \
-      [maskHi3] "v"(mask[7])
+#define NT_MASKS_IN                                                                                                \
+  , [maskLo0] "v"(mask[0]), [maskLo1] "v"(mask[1]), [maskLo2] "v"(mask[2]), [maskLo3] "v"(mask[3]),                \
+      [maskHi0] "v"(mask[4]), [maskHi1] "v"(mask[5]), [maskHi2] "v"(mask[6]), [maskHi3] "v"(mask[7])
+#define NT_SCALES_IN , "{s[86:87]}"(ss), [gS] "v"(gs) NT_MASKS_IN
 #define NT_DIRECT_IN NT_SCALES_IN, [ldsS] "s"(lds_s)
 #define NT_PARTIAL_IN NT_DIRECT_IN, [partial] "s"(partial)
 #define NT_BYTES_OUT NT_SCALES_OUT, [tmp] "=&v"(tmp)
 #define NT_BYTES_IN NT_SCALES_IN, [wS] "v"(wS), [half] "v"(0x400000)
+#define NT_INT8_IN NT_MASKS_IN, [partial] "s"(partial)
 #define NT_NONE
 
 // A value that all lanes of a wavefront share, in a scalar register.
@@ -105,6 +107,13 @@ __device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Sid
   uint32_t aLo = lds + wm * L::MT * 16 * kStep + at, aHi = lds + wm * L::MT * 16 * kStep + (at ^ 64);
   uint32_t bLo = lds + (L::BM + wn * L::NT * 16) * kStep + at, bHi = lds + (L::BM + wn * L::NT * 16) * kStep + (at ^ 64);
 
+  // what of a fragment's words lies before K's end in the last step
+  const int last = K - (static_cast<int>(steps) - 1) * kStep;  // bytes of it
+  const auto last_mask = [&](int w) {
+    const int keep = last - 16 * (w < 4 ? g : 4 + g) - 4 * (w % 4);
+    return keep >= 4 ? -1 : keep <= 0 ? 0 : (1 << (8 * keep)) - 1;
+  };
+
   if constexpr (L::kScaled) {
     // A wavefront loads 64 rows' scales, all of one side; the wavefronts past the last row's repeat it.
     const bool on_a = wave * 64 < L::BM;
@@ -119,14 +128,10 @@ __device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Sid
     const uint32_t s = lds + L::STAGES * L::kStage;
     uint32_t aS = s + stage * L::kScaleStage + 4 * (wm * L::MT * 16 + row);
     uint32_t bS = s + stage * L::kScaleStage + 4 * (L::BM + wn * L::NT * 16 + (L::KIND == Kind::kE8M0 ? row : L::kUniform ? 0 : 4 * g));
-    const int last = K - (static_cast<int>(steps) - 1) * kStep;  // bytes of the last step
     const uint32_t partial = uniform(static_cast<uint32_t>(last < kStep));
     int mask[8];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const int keep = last - 16 * (w < 4 ? g : 4 + g) - 4 * (w % 4);
-      mask[w] = keep >= 4 ? -1 : keep <= 0 ? 0 : (1 << (8 * keep)) - 1;
-    }
+    for (int w = 0; w < 8; ++w) mask[w] = last_mask(w);
     [[maybe_unused]] uint32_t tmp;
     [[maybe_unused]] const uint32_t wS = s + 4 * threadIdx.x;
 #define NT_LOOP_BOTH(KIND)                                                                             \
@@ -139,6 +144,13 @@ __device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Sid
     else if constexpr (L::KIND == Kind::kWideF32Rows) NT_LOOP_RUN(w32n_128x128, NT_SUMS_4, NT_SCALES_OUT, NT_DIRECT_IN);
     else if constexpr (L::KIND == Kind::kWideE8M0Uniform) NT_LOOP_RUN(w8u_128x128, NT_SUMS_4, NT_BYTES_OUT, NT_BYTES_IN);
     else NT_LOOP_RUN(w8n_128x128, NT_SUMS_4, NT_BYTES_OUT, NT_BYTES_IN);
+  } else if constexpr (L::KIND == Kind::kInt8) {
+    const uint32_t partial = uniform(static_cast<uint32_t>(last < kStep));
+    int mask[8];
+#pragma unroll
+    for (int w = 0; w < 8; ++w) mask[w] = last_mask(w);
+    if constexpr (L::BN == 256) NT_LOOP_RUN(int8_256x256, NT_SUMS_8, NT_NONE, NT_INT8_IN);
+    else NT_LOOP_RUN(int8_256x128, NT_SUMS_4, NT_NONE, NT_INT8_IN);
   } else if constexpr (L::BM == 256) {
     NT_LOOP_RUN(pair_256x256, NT_SUMS_8, NT_NONE, NT_NONE);
   } else if constexpr (L::BM == 192) {

@@ -1,10 +1,10 @@
-// nt_tile.h -- what the tiles of the block-scaled 8-bit product (fp8_gemm.hip)
-// and of the orthogonalised update (orthogonal.hip) share: D = A * B^T over
-// operands whose rows are contiguous along K.  nt_direct.h has the small tiles,
-// nt_loop.h the large ones.
+// nt_tile.h -- what the tiles of the block-scaled 8-bit product (fp8_gemm.hip),
+// of the integer product (int8_gemm.hip) and of the orthogonalised update
+// (orthogonal.hip) share: D = A * B^T over operands whose rows are contiguous
+// along K.  nt_direct.h has the small tiles, nt_loop.h the large ones.
 //
-// Both operands are rows of bytes, taken 128 bytes a step: 128 e4m3 codes, or
-// 32 numbers as halfs hi and lo (64 bytes each).  A step is eight 16-byte
+// Both operands are rows of bytes, taken 128 bytes a step: 128 e4m3 codes or 8-bit
+// integers, or 32 numbers as halfs hi and lo (64 bytes each).  A step is eight 16-byte
 // chunks of a row; lane group g = lane / 16 of a wavefront takes chunks g and
 // 4 + g of row lane % 16.  For the 8-bit matrix instruction that is some
 // permutation of the block's 128 k, the same one on both sides, which leaves
@@ -199,6 +199,21 @@ struct HalfPair {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(nl, mh, acc, 0, 0, 0);
   }
   static __device__ __forceinline__ v4f value(const Acc& a) { return a; }
+};
+
+// 8-bit integers, summed in 32 bits: exact while K <= 131071 (128 x 128 a term).
+struct Int8 {
+  static constexpr int kScaleBytes = 0;
+  static constexpr bool kUniform = false, kRowScales = false;
+  using Acc = v4i;
+  using Op = Frag;
+  static __device__ __forceinline__ Op prepare(const Frag& f) { return f; }
+  static __device__ __forceinline__ void zero(Acc& a) { a = v4i{0, 0, 0, 0}; }
+  static __device__ __forceinline__ void mac(Acc& acc, const Op& n, const Op& m, uint32_t, uint32_t) {
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(n.lo, m.lo, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(n.hi, m.hi, acc, 0, 0, 0);
+  }
+  static __device__ __forceinline__ v4i value(const Acc& a) { return a; }
 };
 
 }  // namespace nt

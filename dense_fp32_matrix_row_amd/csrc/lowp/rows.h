@@ -1,0 +1,102 @@
+// rows.h -- rows held in registers, as the integer quantiser (int8_quantize.hip)
+// and the layer norm (layernorm.hip) take them: LANES threads a row, COUNT chunks
+// of eight neighbours each, chunk c of thread t at column (c LANES + t) 8.
+#pragma once
+
+#include <type_traits>
+
+#include "lowp.h"
+
+namespace sgemm {
+
+template <int LANES_, int COUNT_>
+struct RowShape {
+  static constexpr int LANES = LANES_, COUNT = COUNT_;
+  static constexpr int threads = LANES < 256 ? 256 : LANES;  // of a block
+  static constexpr int rows = threads / LANES;               // a block's at a time
+  static constexpr int width = LANES * COUNT * 8;            // longest row
+  static constexpr int waves = LANES / 64;                   // that share a row
+  static_assert(LANES % 64 == 0 && (LANES == 64 || LANES >= 256), "whole wavefronts; one row a block where they share it");
+};
+constexpr int kRowWidth = 16384;  // the widest shape's
+
+// Calls f with the shape that takes rows of `cols` (at most kRowWidth).  Lanes that
+// share a row in a wavefront need no barrier, and more rows in a block keep more
+// loads under way; longer rows take more lanes rather than more registers.
+template <class F>
+void with_row_shape(int cols, const F& f) {
+  if (cols <= 512) f(RowShape<64, 1>{});
+  else if (cols <= 1024) f(RowShape<64, 2>{});
+  else if (cols <= 2048) f(RowShape<256, 1>{});
+  else if (cols <= 4096) f(RowShape<256, 2>{});
+  else if (cols <= 8192) f(RowShape<512, 2>{});
+  else f(RowShape<1024, 2>{});
+}
+
+// Eight neighbours of a row from column `col`, zeros past `cols` (whose end is
+// compared as cols - 8: col + 8 passes 2^31 in the widest row).
+template <class X>
+__device__ __forceinline__ Pack<8, X> load_row8(const X* row, int col, int cols) {
+  if (col <= cols - 8) return load_pack<8>(row + col);
+  Pack<8, X> p{};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (col + i < cols) p.v[i] = row[col + i];
+  return p;
+}
+// Those inside of eight neighbours of a row.
+template <class X>
+__device__ __forceinline__ void store_row8(X* row, int col, int cols, const Pack<8, X>& p) {
+  if (col <= cols - 8) {
+    store_pack(row + col, p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (col + i < cols) row[col + i] = p.v[i];
+  }
+}
+
+// Another lane's value: the neighbour's, the next pair's, the other half of eight's
+// and of sixteen's.
+template <int CONTROL, class T>
+__device__ __forceinline__ T from_lane(T v) {
+  constexpr int words = sizeof(T) / 4;
+  int w[words];
+  __builtin_memcpy(w, &v, sizeof(T));
+#pragma unroll
+  for (int i = 0; i < words; ++i) w[i] = __builtin_amdgcn_update_dpp(0, w[i], CONTROL, 0xf, 0xf, true);
+  __builtin_memcpy(&v, w, sizeof(T));
+  return v;
+}
+
+// v joined over the lanes of a row, the same in each: within the wavefront, then
+// by LDS in the wavefronts' order.  Where wavefronts share a row all threads of the
+// block call it; a `meet` may be used again once all have met in another call.
+template <class S, int N, class T, class F>
+__device__ __forceinline__ void join_row(T (&v)[N], T (&meet)[S::threads / 64][N], const F& f) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = f(v[i], from_lane<0xb1>(v[i]));
+    v[i] = f(v[i], from_lane<0x4e>(v[i]));
+    v[i] = f(v[i], from_lane<0x141>(v[i]));
+    v[i] = f(v[i], from_lane<0x140>(v[i]));
+    v[i] = f(v[i], __shfl_xor(v[i], 16));
+    v[i] = f(v[i], __shfl_xor(v[i], 32));
+  }
+  if constexpr (S::waves > 1) {
+    static_assert(S::rows == 1, "the block's wavefronts share one row");
+    if (threadIdx.x % 64 == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) meet[threadIdx.x / 64][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      T all = meet[0][i];
+#pragma unroll
+      for (int w = 1; w < S::waves; ++w) all = f(all, meet[w][i]);
+      v[i] = all;
+    }
+  }
+}
+
+}  // namespace sgemm

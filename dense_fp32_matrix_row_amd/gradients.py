@@ -1,0 +1,263 @@
+"""The global norm of many gradients, and clipping by it (ctypes binding of
+include/gradients.h).
+
+hip_gradient_norm, hip_gradient_clip and hip_gradient_clip_by carry the C ABI's names
+and argument order and return its status codes; their tensors are a ctypes array of
+hip_gradient.  grad_norm, clip_grad_norm and clip_by_norm take and return torch
+device tensors, run on torch's current stream of the tensors' device and raise on
+errors.  Every operation runs in the library's HIP kernels; there is no fallback.
+Results carry no autograd graph; tensors that are written in place count as modified
+for autograd.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+from . import sgemm as _sgemm
+from .blockfp8 import _call, _types
+
+EXPORTS = ("hip_gradient_norm", "hip_gradient_clip", "hip_gradient_clip_by", "hip_gradient_workspace",
+           "hip_gradient_norm_status_string", "hip_gradient_clip_status_string")
+
+F32, BF16, F16 = 0, 1, 2
+MAX_COUNT = 1 << 20  # HIP_GRADIENT_MAX_COUNT
+
+
+class Gradient(ctypes.Structure):
+    """hip_gradient."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [(name, ctypes.c_longlong) for name in (
+        "rows", "cols", "ldx", "ldy", "type")]
+
+
+_bound = None
+
+
+def load():
+    """The library with this header's functions declared."""
+    global _bound
+    lib = _sgemm.load()
+    if lib is not _bound:
+        i32, i64, f32, vp = ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_void_p
+        lib.hip_gradient_norm.restype = i32
+        lib.hip_gradient_norm.argtypes = [i32, vp, vp, vp, i64, vp]
+        for name in ("hip_gradient_clip", "hip_gradient_clip_by"):
+            getattr(lib, name).restype = i32
+            getattr(lib, name).argtypes = [i32, vp, f32, f32, vp, vp, i64, vp]
+        lib.hip_gradient_workspace.restype = i32
+        lib.hip_gradient_workspace.argtypes = [i32, ctypes.POINTER(i64)]
+        for name in EXPORTS[-2:]:
+            getattr(lib, name).restype = ctypes.c_char_p
+            getattr(lib, name).argtypes = [i32]
+        _bound = lib
+    return lib
+
+
+def hip_gradient_norm(count, tensors, norm, workspace, workspace_bytes, stream=None) -> int:
+    """norm <- the tensors' norm; returns the status code (0 = enqueued)."""
+    a, s = _sgemm._addr, _sgemm._stream
+    return int(load().hip_gradient_norm(int(count), tensors, a(norm), a(workspace), int(workspace_bytes), s(stream)))
+
+
+def hip_gradient_clip(count, tensors, max_norm, eps, norm, workspace, workspace_bytes, stream=None) -> int:
+    """norm <- the tensors' norm, y <- c x; returns the status code."""
+    a, s = _sgemm._addr, _sgemm._stream
+    return int(load().hip_gradient_clip(int(count), tensors, float(max_norm), float(eps), a(norm), a(workspace),
+                                        int(workspace_bytes), s(stream)))
+
+
+def hip_gradient_clip_by(count, tensors, max_norm, eps, norm, workspace, workspace_bytes, stream=None) -> int:
+    """y <- c x by the norm given; returns the status code."""
+    a, s = _sgemm._addr, _sgemm._stream
+    return int(load().hip_gradient_clip_by(int(count), tensors, float(max_norm), float(eps), a(norm), a(workspace),
+                                           int(workspace_bytes), s(stream)))
+
+
+def hip_gradient_workspace(count) -> int:
+    """Bytes of workspace of a call (nothing is launched)."""
+    out = ctypes.c_longlong()
+    rc = load().hip_gradient_workspace(int(count), ctypes.byref(out))
+    if rc != 0:
+        raise _sgemm.SgemmError(rc, hip_gradient_norm_status_string(rc))
+    return out.value
+
+
+def hip_gradient_norm_status_string(status) -> str:
+    return load().hip_gradient_norm_status_string(int(status)).decode()
+
+
+def hip_gradient_clip_status_string(status) -> str:
+    return load().hip_gradient_clip_status_string(int(status)).decode()
+
+
+def _layout(t, what):
+    """(rows, cols, row stride) of a tensor that is rows of neighbours at one stride."""
+    sizes = [(n, s) for n, s in zip(t.shape, t.stride()) if n != 1]
+    sizes.sort(key=lambda e: -e[1])  # any order of the dimensions: every element once is all that counts
+    cols = 1
+    while sizes and sizes[-1][1] == cols:
+        cols *= sizes.pop()[0]
+    if not sizes:
+        return 1, cols, cols
+    rows, ld = sizes.pop()
+    while sizes and sizes[-1][1] == ld * rows:
+        rows *= sizes.pop()[0]
+    if sizes or ld < cols:
+        raise ValueError(f"{what} of sizes {tuple(t.shape)} and strides {t.stride()} is not dense, nor rows of neighbours at one stride")
+    return rows, cols, ld
+
+
+def _describe(tensors, outs):
+    """(device, count, a flat list with seven numbers a tensor, as hip_gradient has them)."""
+    types = _types()
+    flat = []
+    add = flat.extend
+    index = -2
+    for i, t in enumerate(tensors):
+        at = t.get_device()
+        if at != index:
+            if index != -2:
+                raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
+            if at < 0:
+                raise TypeError("gradients must live on the GPU")
+            index = at
+        kind = types.get(t.dtype)
+        if kind is None:
+            raise TypeError(f"gradients are float32, bfloat16 or float16, not {t.dtype}")
+        x = t.data_ptr()
+        o = t if outs is None else outs[i]
+        if o is t:
+            if t.is_contiguous():
+                n = t.numel()
+                add((x, x, 1, n, n, n, kind))
+            else:
+                rows, cols, ld = _layout(t, "a gradient") if t.numel() else (0, 0, 0)
+                add((x, x, rows, cols, ld, ld, kind))
+            continue
+        if o.shape != t.shape or o.dtype != t.dtype:
+            raise ValueError(f"out is {tuple(o.shape)} {o.dtype}, not {tuple(t.shape)} {t.dtype}")
+        if o.get_device() != at:
+            raise ValueError(f"tensors on {t.device} and {o.device}")
+        if t.is_contiguous() and o.is_contiguous():
+            n = t.numel()
+            add((x, o.data_ptr(), 1, n, n, n, kind))
+        elif t.numel() == 0:
+            add((x, o.data_ptr(), 0, 0, 0, 0, kind))
+        else:
+            add((x, o.data_ptr(), *_pair(t, o), kind))
+    return (tensors[0].device if tensors else None), len(tensors), flat
+
+
+def _pair(t, o):
+    """(rows, cols, strides of both) of a gradient and another tensor for its result."""
+    if t.stride() == o.stride():
+        rows, cols, ld = _layout(t, "a gradient")
+        return rows, cols, ld, ld
+    # elements correspond by their places in both: the dimensions in the gradient's order
+    order = sorted((d for d in range(t.dim()) if t.shape[d] != 1), key=lambda d: -t.stride(d))
+    shape = [t.shape[d] for d in order]
+    if t.stride(order[-1]) != 1 or o.stride(order[-1]) != 1:
+        shape.append(1)  # rows of one element
+    cols, strides = shape[-1], []
+    for v in (t, o):
+        outer = [(v.shape[d], v.stride(d)) for d in order][:len(shape) - 1]
+        ld = outer[-1][1] if outer else cols
+        if any(s != n * r for (_, s), (n, r) in zip(outer, outer[1:])) or ld < cols:
+            raise ValueError(f"a gradient and its out, of strides {t.stride()} and {o.stride()}, are not rows of neighbours "
+                             "in one order, each at one stride")
+        strides.append(ld)
+    return t.numel() // cols, cols, *strides
+
+
+def _run(function, what, device, count, flat, *args):
+    """A call with the tensors, a workspace and torch's current stream."""
+    import torch
+    array = (ctypes.c_longlong * max(len(flat), 1))(*flat)
+    bytes = hip_gradient_workspace(count)
+    workspace = torch.empty(bytes, dtype=torch.uint8, device=device)
+    _call(device, function, what, count, ctypes.addressof(array), *args, workspace.data_ptr(), bytes)
+
+
+def _outs(tensors, out):
+    """(where the results go, those of them that count as modified)."""
+    import torch
+    if out is None:
+        new = [torch.empty_like(t) for t in tensors]
+        return new, ()
+    out = tensors if out is tensors else list(out)
+    if len(out) != len(tensors):
+        raise ValueError(f"{len(out)} tensors in out, {len(tensors)} gradients")
+    return out, out
+
+
+def _written(tensors):
+    import torch
+    live = [t for t in tensors if not t.is_inference()]
+    if live:
+        torch.autograd.graph.increment_version(live)
+
+
+def _list(tensors):
+    tensors = tensors if isinstance(tensors, list) else list(tensors)
+    if len(tensors) > MAX_COUNT:
+        raise ValueError(f"{len(tensors)} tensors, at most {MAX_COUNT}")
+    return tensors
+
+
+def _limits(max_norm, eps):
+    if not max_norm >= 0:
+        raise ValueError(f"max_norm is {max_norm}, not 0 or more")
+    if not 0 <= eps < float("inf"):
+        raise ValueError(f"eps is {eps}, not 0 or more")
+
+
+def grad_norm(tensors):
+    """The 2-norm of all elements of the tensors (any shapes, dense or rows of
+    neighbours at one stride, float32, bfloat16 and float16 mixed, one device), as a
+    0-dimensional float32 tensor.  A tensor that is given twice counts twice."""
+    import torch
+    tensors = _list(tensors)
+    if not tensors:
+        raise ValueError("no tensors")
+    device, count, flat = _describe(tensors, None)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    _run(load().hip_gradient_norm, hip_gradient_norm_status_string, device, count, flat, norm.data_ptr())
+    return norm
+
+
+def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, out=None):
+    """(the norm, as grad_norm gives it, and the tensors times min(1, max_norm / (norm +
+    eps))).  The results are new tensors, or `out`'s: as many tensors of the same shapes
+    and types, which may be the gradients themselves (`out=tensors` clips in place, and
+    writes nothing while the norm is within the limit).  No two of the results may share
+    memory, nor one with another's gradient: such a call is refused."""
+    import torch
+    tensors = _list(tensors)
+    _limits(max_norm, eps)
+    if not tensors:
+        raise ValueError("no tensors")
+    outs, modified = _outs(tensors, out)
+    device, count, flat = _describe(tensors, None if outs is tensors else outs)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    _run(load().hip_gradient_clip, hip_gradient_clip_status_string, device, count, flat, max_norm, eps, norm.data_ptr())
+    _written(modified)
+    return norm, outs
+
+
+def clip_by_norm(tensors, norm, max_norm: float, eps: float = 1e-6, out=None):
+    """clip_grad_norm's tensors by a norm that is there (one float32 number on the
+    tensors' device): grad_norm's, or the root of several ranks' summed squares."""
+    import torch
+    tensors = _list(tensors)
+    _limits(max_norm, eps)
+    if not tensors:
+        raise ValueError("no tensors")
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError(f"norm is {tuple(norm.shape)} {norm.dtype}, not one torch.float32")
+    outs, modified = _outs(tensors, out)
+    device, count, flat = _describe(tensors, None if outs is tensors else outs)
+    if norm.device != device:
+        raise ValueError(f"tensors on {device} and {norm.device}")
+    _run(load().hip_gradient_clip_by, hip_gradient_clip_status_string, device, count, flat, max_norm, eps, norm.data_ptr())
+    _written(modified)
+    return outs
