@@ -57,6 +57,21 @@ __device__ __forceinline__ uint32_t top8(uint32_t top, const Pack<8, X>& x) {
   return top;
 }
 
+// Calls f with the shape that takes rows of `cols` (at most kRowWidth).  Lanes that
+// share a row in a wavefront need no barrier, and more rows in a block keep more
+// loads under way; longer rows take more lanes rather than more registers.
+template <class F>
+void with_row_shape(int cols, const F& f) {
+  if (cols <= 128) f(RowShape<16, 1>{});
+  else if (cols <= 256) f(RowShape<32, 1>{});
+  else if (cols <= 512) f(RowShape<64, 1>{});
+  else if (cols <= 1024) f(RowShape<64, 2>{});
+  else if (cols <= 2048) f(RowShape<256, 1>{});
+  else if (cols <= 4096) f(RowShape<256, 2>{});
+  else if (cols <= 8192) f(RowShape<512, 2>{});
+  else f(RowShape<1024, 2>{});
+}
+
 // A row in the registers of its lanes: read once.
 template <class S, class X>
 __global__ __launch_bounds__(S::threads) void k_rows(const X* __restrict__ x, int64_t ldx, int8_t* __restrict__ q,

@@ -16,30 +16,18 @@ struct Sum {
   __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
 };
 
-// w or b: numbers of a type side by side, or one number for all.
-struct Param {
-  const void* p;
-  int type;
-  float fill;
-  template <class T>
-  __device__ __forceinline__ void load(float (&v)[8], int col, int cols) const {
-    const Pack<8, T> r = load_row8(static_cast<const T*>(p), col, cols);
+// w or b: numbers side by side, of X's type or floats, or (NULL) one number for all.
+template <class W>
+__device__ __forceinline__ void load_param(float (&v)[8], const W* p, float fill, int col, int cols) {
+  if (!p) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float(r.v[i]);
+    for (int i = 0; i < 8; ++i) v[i] = fill;
+    return;
   }
-  __device__ __forceinline__ void get(float (&v)[8], int col, int cols) const {
-    if (!p) {
+  const Pack<8, W> r = load_row8(p, col, cols);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fill;
-    } else if (type == HIP_LAYERNORM_F32) {
-      load<float>(v, col, cols);
-    } else if (type == HIP_LAYERNORM_BF16) {
-      load<bf16>(v, col, cols);
-    } else {
-      load<_Float16>(v, col, cols);
-    }
-  }
-};
+  for (int i = 0; i < 8; ++i) v[i] = to_float(r.v[i]);
+}
 
 // A row's mean, what its rounding to float left over, and rstd.
 struct Stats {
@@ -56,28 +44,59 @@ __device__ __forceinline__ void store_stats(float* stats, int64_t row, int64_t r
 // (x - mean) rstd: x - mean is exact where x is near the mean, and the rest small.
 __device__ __forceinline__ float normalised(float x, const Stats& s) { return ((x - s.mean) - s.rest) * s.rstd; }
 
+// A lane's share of a row.
+template <class S, class X>
+struct Share {
+  Pack<8, X> v[S::COUNT];
+  __device__ __forceinline__ void load(const X* row, int lane, int cols) {
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(row, (c * S::LANES + lane) * 8, cols);
+  }
+  // Makes the compiler forget what it made of the elements so far, lest it keep them
+  // as floats beside the halves that they come as.
+  __device__ __forceinline__ void forget() {
+    if constexpr (sizeof(X) == 2) {
+#pragma unroll
+      for (int c = 0; c < S::COUNT; ++c) {
+        uint4 r = __builtin_bit_cast(uint4, v[c]);
+        asm volatile("" : "+v"(r.x), "+v"(r.y), "+v"(r.z), "+v"(r.w));
+        v[c] = __builtin_bit_cast(Pack<8, X>, r);
+      }
+    }
+  }
+};
+
+// Blocks walk the rows, with w and b in registers (read for each row, floats of them
+// would be twice the bytes of 16-bit x and y: 8192 x 4096 39 us).
+//
 // The mean rounded to float is off by up to 2^-24 of itself, which for a row far
 // off zero is much of its differences, so their own mean is taken beside their
 // squares': with d = x - mean, the mean is mean + avg d and the variance
 // avg d^2 - (avg d)^2.
-template <class S, class X>
-__global__ __launch_bounds__(S::threads) void k_forward(const X* x, int64_t ldx, Param w, Param b, float eps, X* y,
-                                                        int64_t ldy, float* __restrict__ stats, int rows, int cols) {
+template <class S, class X, class W>
+__global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward(const X* x, int64_t ldx, const W* __restrict__ w,
+                                                        const W* __restrict__ b, float eps, X* y, int64_t ldy,
+                                                        float* __restrict__ stats, int rows, int cols) {
   __shared__ float first[S::threads / 64][1], second[S::threads / 64][2];
   const int lane = threadIdx.x % S::LANES;
   const int64_t steps = ceil_div(rows, S::rows);
   const float n = static_cast<float>(cols);
+  float wv[S::COUNT][8], bv[S::COUNT][8];
+#pragma unroll
+  for (int c = 0; c < S::COUNT; ++c) {
+    load_param(wv[c], w, 1.0f, (c * S::LANES + lane) * 8, cols);
+    load_param(bv[c], b, 0.0f, (c * S::LANES + lane) * 8, cols);
+  }
   for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
     const int64_t row = step * S::rows + threadIdx.x / S::LANES;
-    if (S::waves == 1 && row >= rows) return;
-    Pack<8, X> v[S::COUNT];
-#pragma unroll
-    for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(x + row * ldx, (c * S::LANES + lane) * 8, cols);
+    const bool live = S::rows == 1 || row < rows;
+    Share<S, X> now{};
+    if (live) now.load(x + row * ldx, lane, cols);
     float sum[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < S::COUNT; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[0] += to_float(v[c].v[i]);
+      for (int i = 0; i < 8; ++i) sum[0] += to_float(now.v[c].v[i]);
     join_row<S>(sum, first, Sum{});
     Stats s{sum[0] / n, 0.0f, 0.0f};
     float d[2] = {0.0f, 0.0f};
@@ -85,33 +104,33 @@ __global__ __launch_bounds__(S::threads) void k_forward(const X* x, int64_t ldx,
     for (int c = 0; c < S::COUNT; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float t = (c * S::LANES + lane) * 8 < cols - i ? to_float(v[c].v[i]) - s.mean : 0.0f;
+        const float t = (c * S::LANES + lane) * 8 < cols - i ? to_float(now.v[c].v[i]) - s.mean : 0.0f;
         d[0] += t;
         d[1] = fmaf(t, t, d[1]);
       }
     join_row<S>(d, second, Sum{});
+    now.forget();
     s.rest = d[0] / n;
     s.rstd = 1.0f / sqrtf(fmaxf(d[1] / n - s.rest * s.rest, 0.0f) + eps);
     if (!(fabsf(d[1]) < INFINITY)) s.rstd = __uint_as_float(0x7fc00000u);  // fmaxf takes no NaN over
+    if (live) {
 #pragma unroll
-    for (int c = 0; c < S::COUNT; ++c) {
-      const int col = (c * S::LANES + lane) * 8;
-      float wv[8], bv[8];
-      w.get(wv, col, cols);
-      b.get(bv, col, cols);
-      Pack<8, X> r;
+      for (int c = 0; c < S::COUNT; ++c) {
+        Pack<8, X> r;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) from_float(fmaf(normalised(to_float(v[c].v[i]), s), wv[i], bv[i]), r.v[i]);
-      store_row8(y + row * ldy, col, cols, r);
+        for (int i = 0; i < 8; ++i) from_float(fmaf(normalised(to_float(now.v[c].v[i]), s), wv[c][i], bv[c][i]), r.v[i]);
+        store_row8(y + row * ldy, (c * S::LANES + lane) * 8, cols, r);
+      }
+      if (stats && lane == 0) store_stats(stats, row, rows, s);
     }
-    if (stats && lane == 0) store_stats(stats, row, rows, s);
   }
 }
 
 // Rows longer than registers hold: read three times, sums in double.
-template <class X>
-__global__ __launch_bounds__(1024) void k_forward_long(const X* x, int64_t ldx, Param w, Param b, float eps, X* y,
-                                                       int64_t ldy, float* __restrict__ stats, int rows, int cols) {
+template <class X, class W>
+__global__ __launch_bounds__(1024) void k_forward_long(const X* x, int64_t ldx, const W* __restrict__ w,
+                                                       const W* __restrict__ b, float eps, X* y, int64_t ldy,
+                                                       float* __restrict__ stats, int rows, int cols) {
   using S = RowShape<1024, 1>;
   __shared__ double first[S::threads / 64][1], second[S::threads / 64][2];
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -142,8 +161,8 @@ __global__ __launch_bounds__(1024) void k_forward_long(const X* x, int64_t ldx, 
     for (int64_t c = threadIdx.x * 8; c < cols; c += S::width) {
       const Pack<8, X> v = load_row8(from, static_cast<int>(c), cols);
       float wv[8], bv[8];
-      w.get(wv, static_cast<int>(c), cols);
-      b.get(bv, static_cast<int>(c), cols);
+      load_param(wv, w, 1.0f, static_cast<int>(c), cols);
+      load_param(bv, b, 0.0f, static_cast<int>(c), cols);
       Pack<8, X> r;
 #pragma unroll
       for (int i = 0; i < 8; ++i) from_float(fmaf(normalised(to_float(v.v[i]), s), wv[i], bv[i]), r.v[i]);
@@ -156,73 +175,91 @@ __global__ __launch_bounds__(1024) void k_forward_long(const X* x, int64_t ldx, 
 // dw and db of a block's rows lie in its threads' registers, a thread's columns
 // being the same in every row, and leave once, into the block's part of the
 // workspace; k_join adds the parts in their order.
-template <class S, class X>
-__global__ __launch_bounds__(S::threads) void k_backward(const X* dy, int64_t lddy, const X* x, int64_t ldx,
-                                                         const float* __restrict__ stats, Param w, X* dx, int64_t lddx,
-                                                         float* __restrict__ parts, int rows, int cols) {
+template <class S, class X, class W>
+__global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 4) void k_backward(const X* dy, int64_t lddy, const X* x, int64_t ldx,
+                                                         const float* __restrict__ stats, const W* __restrict__ w, X* dx,
+                                                         int64_t lddx, float* __restrict__ parts, int rows, int cols) {
   __shared__ float meet[2][S::threads / 64][2];
   const int lane = threadIdx.x % S::LANES;
   const int64_t steps = ceil_div(rows, S::rows);
   const float n = static_cast<float>(cols);
+  // w too, but in the widest rows, whose threads have 128 registers (4096 x 16384 bf16:
+  // with some of them spilled 159 us, with w read in each row 125)
+  constexpr bool kHold = S::LANES < 1024;
   float wv[S::COUNT][8], pw[S::COUNT][8], pb[S::COUNT][8];
+  const auto load_w = [&](int c) { load_param(wv[c], w, 1.0f, (c * S::LANES + lane) * 8, cols); };
 #pragma unroll
   for (int c = 0; c < S::COUNT; ++c) {
-    w.get(wv[c], (c * S::LANES + lane) * 8, cols);
+    if (kHold) load_w(c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) pw[c][i] = pb[c][i] = 0.0f;
   }
+  Share<S, X> xv, gv;
+  Stats s;
+  const auto load = [&](int64_t step) {  // rows past the last repeat it
+    const int64_t row = min(step * S::rows + threadIdx.x / S::LANES, int64_t(rows) - 1);
+    xv.load(x + row * ldx, lane, cols);
+    gv.load(dy + row * lddy, lane, cols);
+    s = load_stats(stats, row, rows);
+  };
+  load(blockIdx.x);
   int turn = 0;
   for (int64_t step = blockIdx.x; step < steps; step += gridDim.x, turn ^= 1) {
     const int64_t row = step * S::rows + threadIdx.x / S::LANES;
-    if (S::waves == 1 && row >= rows) break;
-    Pack<8, X> xv[S::COUNT], gv[S::COUNT];
+    const bool live = S::rows == 1 || row < rows;
+    float sum[2] = {0.0f, 0.0f};
+    if (live) {
 #pragma unroll
-    for (int c = 0; c < S::COUNT; ++c) {
-      xv[c] = load_row8(x + row * ldx, (c * S::LANES + lane) * 8, cols);
-      gv[c] = load_row8(dy + row * lddy, (c * S::LANES + lane) * 8, cols);
-    }
-    const Stats s = load_stats(stats, row, rows);
-    float h[S::COUNT][8], sum[2] = {0.0f, 0.0f};
+      for (int c = 0; c < S::COUNT; ++c) {
+        if (!kHold) load_w(c);
 #pragma unroll
-    for (int c = 0; c < S::COUNT; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float t = to_float(gv[c].v[i]), g = t * wv[c][i];
-        h[c][i] = normalised(to_float(xv[c].v[i]), s);  // past the row's end times dy's zeros
-        pw[c][i] = fmaf(t, h[c][i], pw[c][i]);
-        pb[c][i] += t;
-        sum[0] += g;
-        sum[1] = fmaf(g, h[c][i], sum[1]);
+        for (int i = 0; i < 8; ++i) {  // past the row's end dy is zero
+          const float t = to_float(gv.v[c].v[i]), g = t * wv[c][i], h = normalised(to_float(xv.v[c].v[i]), s);
+          pw[c][i] = fmaf(t, h, pw[c][i]);
+          pb[c][i] += t;
+          sum[0] += g;
+          sum[1] = fmaf(g, h, sum[1]);
+        }
       }
-    if (!dx) continue;
-    join_row<S>(sum, meet[turn], Sum{});
-    const float c1 = sum[0] / n, c2 = sum[1] / n;
-#pragma unroll
-    for (int c = 0; c < S::COUNT; ++c) {
-      Pack<8, X> r;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        from_float((fmaf(to_float(gv[c].v[i]), wv[c][i], -c1) - h[c][i] * c2) * s.rstd, r.v[i]);
-      store_row8(dx + row * lddx, (c * S::LANES + lane) * 8, cols, r);
     }
+    if (dx) {
+      join_row<S>(sum, meet[turn], Sum{});
+      xv.forget();
+      gv.forget();
+      const float c1 = sum[0] / n, c2 = sum[1] / n;
+      if (live) {
+#pragma unroll
+        for (int c = 0; c < S::COUNT; ++c) {
+          if (!kHold) load_w(c);
+          Pack<8, X> r;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float g = fmaf(to_float(gv.v[c].v[i]), wv[c][i], -c1), h = normalised(to_float(xv.v[c].v[i]), s);
+            from_float((g - h * c2) * s.rstd, r.v[i]);
+          }
+          store_row8(dx + row * lddx, (c * S::LANES + lane) * 8, cols, r);
+        }
+      }
+    }
+    if (step + gridDim.x < steps) load(step + gridDim.x);
   }
   if (!parts) return;
   float* const to = parts + int64_t(blockIdx.x) * 2 * cols;
-  if constexpr (S::rows > 1) {  // the block's wavefronts first
+  if constexpr (S::rows > 1) {  // the block's rows first
     __shared__ float all[S::rows][S::width];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (k) __syncthreads();
+      __syncthreads();
 #pragma unroll
       for (int c = 0; c < S::COUNT; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) all[threadIdx.x / S::LANES][(c * S::LANES + lane) * 8 + i] = k ? pb[c][i] : pw[c][i];
       __syncthreads();
-      for (int n = threadIdx.x; n < cols; n += S::threads) {
-        float v = all[0][n];
+      for (int at = threadIdx.x; at < cols; at += S::threads) {
+        float v = all[0][at];
 #pragma unroll
-        for (int r = 1; r < S::rows; ++r) v += all[r][n];
-        to[k * cols + n] = v;
+        for (int r = 1; r < S::rows; ++r) v += all[r][at];
+        to[k * cols + at] = v;
       }
     }
   } else {
@@ -263,10 +300,10 @@ __global__ __launch_bounds__(256) void k_params_long(const X* __restrict__ dy, i
   store_row8(parts + part * 2 * cols + cols, col, cols, pb);
 }
 
-template <class X>
+template <class X, class W>
 __global__ __launch_bounds__(1024) void k_backward_long(const X* dy, int64_t lddy, const X* x, int64_t ldx,
-                                                        const float* __restrict__ stats, Param w, X* dx, int64_t lddx,
-                                                        int rows, int cols) {
+                                                        const float* __restrict__ stats, const W* __restrict__ w, X* dx,
+                                                        int64_t lddx, int rows, int cols) {
   using S = RowShape<1024, 1>;
   __shared__ double meet[2][S::threads / 64][2];
   int turn = 0;
@@ -277,7 +314,7 @@ __global__ __launch_bounds__(1024) void k_backward_long(const X* dy, int64_t ldd
       const int col = static_cast<int>(c);
       const Pack<8, X> xv = load_row8(x + row * ldx, col, cols), gv = load_row8(dy + row * lddy, col, cols);
       float wv[8];
-      w.get(wv, col, cols);
+      load_param(wv, w, 1.0f, col, cols);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float g = to_float(gv.v[i]) * wv[i];
@@ -291,7 +328,7 @@ __global__ __launch_bounds__(1024) void k_backward_long(const X* dy, int64_t ldd
       const int col = static_cast<int>(c);
       const Pack<8, X> xv = load_row8(x + row * ldx, col, cols), gv = load_row8(dy + row * lddy, col, cols);
       float wv[8];
-      w.get(wv, col, cols);
+      load_param(wv, w, 1.0f, col, cols);
       Pack<8, X> r;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -301,30 +338,64 @@ __global__ __launch_bounds__(1024) void k_backward_long(const X* dy, int64_t ldd
   }
 }
 
-// dw (blockIdx.y 0) and db (1): the sums of the parts' columns, 32 columns a block,
-// eight shares of the parts, each in its order, then the shares.
-__global__ __launch_bounds__(256) void k_join(const float* __restrict__ parts, int count, float* dw, float* db, int cols,
-                                              int accumulate) {
-  __shared__ float meet[8][32];
+// dw (blockIdx.y 0) and db (1): the sums of the parts' columns, 32 columns a block (a
+// cache line of each part; 16 read the lines twice, 8192 x 4096 51 -> 60 us), 32
+// shares of the parts, each in its order with twelve loads under way, then the shares.
+// (Eight shares and one load after another took 25 of 8192 x 1024's 34 us.)
+__global__ __launch_bounds__(1024) void k_join(const float* __restrict__ parts, int count, float* dw, float* db, int cols,
+                                               int accumulate) {
+  constexpr int kShares = 32, kLoads = 12;
+  __shared__ float meet[kShares][33];
   float* const out = blockIdx.y ? db : dw;
   if (!out) return;
-  const int share = threadIdx.x / 32;
+  const int share = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int64_t tile = blockIdx.x; tile < ceil_div(cols, 32); tile += gridDim.x) {
-    const int64_t col = tile * 32 + threadIdx.x % 32;
+    const int64_t col = tile * 32 + lane;
+    const float* const from = parts + int64_t(blockIdx.y) * cols + min(col, int64_t(cols) - 1);
     float v = 0.0f;
-    if (col < cols)
-      for (int p = share; p < count; p += 8) v += parts[(int64_t(p) * 2 + blockIdx.y) * cols + col];
-    meet[share][threadIdx.x % 32] = v;
+    for (int p = share; p < count; p += kShares * kLoads) {
+      float t[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) t[i] = p + i * kShares < count ? from[int64_t(p + i * kShares) * 2 * cols] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) v += t[i];
+    }
+    meet[share][lane] = v;
     __syncthreads();
     if (share == 0 && col < cols) {
 #pragma unroll
-      for (int i = 1; i < 8; ++i) v += meet[i][threadIdx.x];
+      for (int i = 1; i < kShares; ++i) v += meet[i][lane];
       out[col] = accumulate ? out[col] + v : v;
     }
     __syncthreads();  // the next columns write the same LDS
   }
 }
 constexpr int64_t kJoinBlocks = int64_t(1) << 20;
+
+// Calls f with the shape of rows of `cols` (at most kRowWidth).
+template <class F>
+void with_forward_shape(int cols, const F& f) {
+  if (cols <= 128) f(RowShape<16, 1>{});
+  else if (cols <= 256) f(RowShape<32, 1>{});
+  else if (cols <= 512) f(RowShape<64, 1>{});
+  else if (cols <= 1024) f(RowShape<64, 2>{});
+  else if (cols <= 2048) f(RowShape<128, 2>{});
+  else if (cols <= 4096) f(RowShape<256, 2>{});
+  else if (cols <= 8192) f(RowShape<512, 2>{});
+  else f(RowShape<1024, 2>{});
+}
+// Several rows a block, which share its part of dw and db.
+template <class F>
+void with_backward_shape(int cols, const F& f) {
+  if (cols <= 128) f(RowShape<16, 1, 512>{});
+  else if (cols <= 256) f(RowShape<32, 1, 512>{});
+  else if (cols <= 512) f(RowShape<64, 1, 512>{});
+  else if (cols <= 1024) f(RowShape<128, 1, 512>{});
+  else if (cols <= 2048) f(RowShape<256, 1, 512>{});
+  else if (cols <= 4096) f(RowShape<512, 1, 512>{});
+  else if (cols <= 8192) f(RowShape<512, 2, 512>{});
+  else f(RowShape<1024, 2>{});
+}
 
 // Blocks of the backward pass, each with a part of dw and db in the workspace.
 int64_t parts_of(int rows, int cols) {
@@ -333,14 +404,23 @@ int64_t parts_of(int rows, int cols) {
     return rows < most ? rows : most;
   }
   int64_t parts = 0;
-  with_row_shape(cols, [&](auto shape) {
+  with_backward_shape(cols, [&](auto shape) {
     using S = decltype(shape);
-    const int64_t steps = ceil_div(rows, S::rows), cap = 512 * 256 / S::threads;
+    const int64_t steps = ceil_div(rows, S::rows), cap = 256 * (S::COUNT == 1 ? 1536 : 1024) / S::threads;
     parts = steps < cap ? steps : cap;
   });
   return parts;
 }
-
+struct Forward {
+  int rows, cols;
+  const void* x;
+  int64_t ldx;
+  const void *w, *b;
+  float eps;
+  void* y;
+  int64_t ldy;
+  float* stats;
+};
 struct Backward {
   int rows, cols;
   const void* dy;
@@ -348,34 +428,36 @@ struct Backward {
   const void* x;
   int64_t ldx;
   const float* stats;
-  Param w;
+  const void* w;
   void* dx;
   int64_t lddx;
   float* parts;
   int count;
 };
 
-template <class X>
-void forward_type(int rows, int cols, const void* x, int64_t ldx, Param w, Param b, float eps, void* y, int64_t ldy,
-                  float* stats, hipStream_t stream) {
-  if (cols > kRowWidth) {
+template <class X, class W>
+void launch(const Forward& a, hipStream_t stream) {
+  const X* const x = static_cast<const X*>(a.x);
+  const W *const w = static_cast<const W*>(a.w), *const b = static_cast<const W*>(a.b);
+  X* const y = static_cast<X*>(a.y);
+  if (a.cols > kRowWidth) {
     const int64_t cap = kMaxWorkItems / 1024;
-    hipLaunchKernelGGL((k_forward_long<X>), dim3(static_cast<unsigned>(rows < cap ? rows : cap)), dim3(1024), 0, stream,
-                       static_cast<const X*>(x), ldx, w, b, eps, static_cast<X*>(y), ldy, stats, rows, cols);
+    hipLaunchKernelGGL((k_forward_long<X, W>), dim3(static_cast<unsigned>(a.rows < cap ? a.rows : cap)), dim3(1024), 0,
+                       stream, x, a.ldx, w, b, a.eps, y, a.ldy, a.stats, a.rows, a.cols);
     return;
   }
-  with_row_shape(cols, [&](auto shape) {
+  with_forward_shape(a.cols, [&](auto shape) {
     using S = decltype(shape);
-    const int64_t steps = ceil_div(rows, S::rows), cap = kMaxWorkItems / S::threads;
-    hipLaunchKernelGGL((k_forward<S, X>), dim3(static_cast<unsigned>(steps < cap ? steps : cap)), dim3(S::threads), 0,
-                       stream, static_cast<const X*>(x), ldx, w, b, eps, static_cast<X*>(y), ldy, stats, rows, cols);
+    const int64_t steps = ceil_div(a.rows, S::rows), cap = 256 * (S::COUNT == 2 && S::LANES <= 256 ? 1280 : 2048) / S::threads;
+    hipLaunchKernelGGL((k_forward<S, X, W>), dim3(static_cast<unsigned>(steps < cap ? steps : cap)), dim3(S::threads), 0,
+                       stream, x, a.ldx, w, b, a.eps, y, a.ldy, a.stats, a.rows, a.cols);
   });
 }
 
-template <class X>
-void backward_type(const Backward& a, hipStream_t stream) {
-  const X* const dy = static_cast<const X*>(a.dy);
-  const X* const x = static_cast<const X*>(a.x);
+template <class X, class W>
+void launch(const Backward& a, hipStream_t stream) {
+  const X *const dy = static_cast<const X*>(a.dy), *const x = static_cast<const X*>(a.x);
+  const W* const w = static_cast<const W*>(a.w);
   X* const dx = static_cast<X*>(a.dx);
   if (a.cols > kRowWidth) {
     const int strips = static_cast<int>(ceil_div(a.cols, 2048));
@@ -384,17 +466,29 @@ void backward_type(const Backward& a, hipStream_t stream) {
                          a.lddy, x, a.ldx, a.stats, a.parts, a.rows, a.cols, strips);
     const int64_t cap = kMaxWorkItems / 1024;
     if (dx)
-      hipLaunchKernelGGL((k_backward_long<X>), dim3(static_cast<unsigned>(a.rows < cap ? a.rows : cap)), dim3(1024), 0,
-                         stream, dy, a.lddy, x, a.ldx, a.stats, a.w, dx, a.lddx, a.rows, a.cols);
+      hipLaunchKernelGGL((k_backward_long<X, W>), dim3(static_cast<unsigned>(a.rows < cap ? a.rows : cap)), dim3(1024), 0,
+                         stream, dy, a.lddy, x, a.ldx, a.stats, w, dx, a.lddx, a.rows, a.cols);
     return;
   }
-  with_row_shape(a.cols, [&](auto shape) {
+  with_backward_shape(a.cols, [&](auto shape) {
     using S = decltype(shape);
-    hipLaunchKernelGGL((k_backward<S, X>), dim3(static_cast<unsigned>(a.count)), dim3(S::threads), 0, stream, dy, a.lddy,
-                       x, a.ldx, a.stats, a.w, dx, a.lddx, a.parts, a.rows, a.cols);
+    hipLaunchKernelGGL((k_backward<S, X, W>), dim3(static_cast<unsigned>(a.count)), dim3(S::threads), 0, stream, dy,
+                       a.lddy, x, a.ldx, a.stats, w, dx, a.lddx, a.parts, a.rows, a.cols);
   });
 }
 
+// w and b of X's type, or floats.
+template <class A>
+void launch_type(int type, int w_type, const A& a, hipStream_t stream) {
+  const bool wide = w_type == HIP_LAYERNORM_F32;
+  if (type == HIP_LAYERNORM_F32) launch<float, float>(a, stream);
+  else if (type == HIP_LAYERNORM_BF16 && wide) launch<bf16, float>(a, stream);
+  else if (type == HIP_LAYERNORM_BF16) launch<bf16, bf16>(a, stream);
+  else if (wide) launch<_Float16, float>(a, stream);
+  else launch<_Float16, _Float16>(a, stream);
+}
+
+bool bad_param(int t, int type) { return t != HIP_LAYERNORM_F32 && t != type; }
 bool bad_type(int t) { return t != HIP_LAYERNORM_F32 && t != HIP_LAYERNORM_BF16 && t != HIP_LAYERNORM_F16; }
 
 }  // namespace
@@ -412,15 +506,13 @@ int hip_layernorm_forward(int rows, int cols, int type, const void* X, int ldx, 
   if (bad_type(type)) return -3;
   if (some && X == nullptr) return -4;
   if (ldx < (cols > 1 ? cols : 1)) return -5;
-  if ((w != nullptr || b != nullptr) && bad_type(w_type)) return -8;
+  const bool params = w != nullptr || b != nullptr;
+  if (params && bad_param(w_type, type)) return -8;
   if (!(eps >= 0.0f)) return -9;
   if (some && Y == nullptr) return -10;
   if (ldy < (cols > 1 ? cols : 1)) return -11;
   if (!some) return 0;
-  const Param pw{w, w_type, 1.0f}, pb{b, w_type, 0.0f};
-  if (type == HIP_LAYERNORM_F32) forward_type<float>(rows, cols, X, ldx, pw, pb, eps, Y, ldy, stats, stream);
-  else if (type == HIP_LAYERNORM_BF16) forward_type<bf16>(rows, cols, X, ldx, pw, pb, eps, Y, ldy, stats, stream);
-  else forward_type<_Float16>(rows, cols, X, ldx, pw, pb, eps, Y, ldy, stats, stream);
+  launch_type(type, params ? w_type : HIP_LAYERNORM_F32, Forward{rows, cols, X, ldx, w, b, eps, Y, ldy, stats}, stream);
   return static_cast<int>(hipGetLastError());
 }
 
@@ -443,7 +535,7 @@ int hip_layernorm_backward(int rows, int cols, int type, const void* DY, int ldd
   if (some && X == nullptr) return -6;
   if (ldx < (cols > 1 ? cols : 1)) return -7;
   if (some && stats == nullptr) return -8;
-  if (w != nullptr && bad_type(w_type)) return -10;
+  if (w != nullptr && bad_param(w_type, type)) return -10;
   if (DX != nullptr && lddx < (cols > 1 ? cols : 1)) return -12;
   if (accumulate != 0 && accumulate != 1) return -15;
   const int64_t count = some ? parts_of(rows, cols) : 0;
@@ -451,16 +543,15 @@ int hip_layernorm_backward(int rows, int cols, int type, const void* DY, int ldd
   if (some && params && workspace_bytes < count * 2 * cols * 4) return -17;
   if (cols == 0 || (!params && (rows == 0 || DX == nullptr))) return 0;
   if (rows > 0) {
-    const Backward a{rows, cols, DY, lddy, X, ldx, stats, Param{w, w_type, 1.0f}, DX, lddx,
-                     params ? static_cast<float*>(workspace) : nullptr, static_cast<int>(count)};
-    if (type == HIP_LAYERNORM_F32) backward_type<float>(a, stream);
-    else if (type == HIP_LAYERNORM_BF16) backward_type<bf16>(a, stream);
-    else backward_type<_Float16>(a, stream);
+    launch_type(type, w != nullptr ? w_type : HIP_LAYERNORM_F32,
+                Backward{rows, cols, DY, lddy, X, ldx, stats, w, DX, lddx, params ? static_cast<float*>(workspace) : nullptr,
+                         static_cast<int>(count)},
+                stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return static_cast<int>(e);
   }
   if (params)
-    hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>(min(ceil_div(cols, 32), kJoinBlocks)), 2), dim3(256), 0, stream,
+    hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>(min(ceil_div(cols, 32), kJoinBlocks)), 2), dim3(1024), 0, stream,
                        static_cast<const float*>(workspace), static_cast<int>(count), dw, db, cols, accumulate);
   return static_cast<int>(hipGetLastError());
 }
@@ -473,7 +564,7 @@ const char* hip_layernorm_forward_status_string(int status) {
     case -3: return "argument 3 (type) is not a known type";
     case -4: return "argument 4 (X) is NULL";
     case -5: return "argument 5 (ldx) is smaller than max(1, cols)";
-    case -8: return "argument 8 (w_type) is not a known type";
+    case -8: return "argument 8 (w_type) is neither HIP_LAYERNORM_F32 nor the type of X";
     case -9: return "argument 9 (eps) is negative or NaN";
     case -10: return "argument 10 (Y) is NULL";
     case -11: return "argument 11 (ldy) is smaller than max(1, cols)";
@@ -494,7 +585,7 @@ const char* hip_layernorm_backward_status_string(int status) {
     case -6: return "argument 6 (X) is NULL";
     case -7: return "argument 7 (ldx) is smaller than max(1, cols)";
     case -8: return "argument 8 (stats) is NULL";
-    case -10: return "argument 10 (w_type) is not a known type";
+    case -10: return "argument 10 (w_type) is neither HIP_LAYERNORM_F32 nor the type of X";
     case -12: return "argument 12 (lddx) is smaller than max(1, cols)";
     case -15: return "argument 15 (accumulate) is not 0 or 1";
     case -16: return "argument 16 (workspace) is NULL or not 16-byte aligned";

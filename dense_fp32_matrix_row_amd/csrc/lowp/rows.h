@@ -9,29 +9,16 @@
 
 namespace sgemm {
 
-template <int LANES_, int COUNT_>
+template <int LANES_, int COUNT_, int THREADS_ = (LANES_ < 256 ? 256 : LANES_)>
 struct RowShape {
   static constexpr int LANES = LANES_, COUNT = COUNT_;
-  static constexpr int threads = LANES < 256 ? 256 : LANES;  // of a block
-  static constexpr int rows = threads / LANES;               // a block's at a time
-  static constexpr int width = LANES * COUNT * 8;            // longest row
-  static constexpr int waves = LANES / 64;                   // that share a row
-  static_assert(LANES % 64 == 0 && (LANES == 64 || LANES >= 256), "whole wavefronts; one row a block where they share it");
+  static constexpr int threads = THREADS_;          // of a block
+  static constexpr int rows = threads / LANES;      // a block's at a time
+  static constexpr int width = LANES * COUNT * 8;   // longest row
+  static constexpr int waves = (LANES + 63) / 64;   // that share a row
+  static_assert(threads % LANES == 0 && (LANES == 16 || LANES == 32 || LANES % 64 == 0));
 };
 constexpr int kRowWidth = 16384;  // the widest shape's
-
-// Calls f with the shape that takes rows of `cols` (at most kRowWidth).  Lanes that
-// share a row in a wavefront need no barrier, and more rows in a block keep more
-// loads under way; longer rows take more lanes rather than more registers.
-template <class F>
-void with_row_shape(int cols, const F& f) {
-  if (cols <= 512) f(RowShape<64, 1>{});
-  else if (cols <= 1024) f(RowShape<64, 2>{});
-  else if (cols <= 2048) f(RowShape<256, 1>{});
-  else if (cols <= 4096) f(RowShape<256, 2>{});
-  else if (cols <= 8192) f(RowShape<512, 2>{});
-  else f(RowShape<1024, 2>{});
-}
 
 // Eight neighbours of a row from column `col`, zeros past `cols` (whose end is
 // compared as cols - 8: col + 8 passes 2^31 in the widest row).
@@ -80,20 +67,20 @@ __device__ __forceinline__ void join_row(T (&v)[N], T (&meet)[S::threads / 64][N
     v[i] = f(v[i], from_lane<0x4e>(v[i]));
     v[i] = f(v[i], from_lane<0x141>(v[i]));
     v[i] = f(v[i], from_lane<0x140>(v[i]));
-    v[i] = f(v[i], __shfl_xor(v[i], 16));
-    v[i] = f(v[i], __shfl_xor(v[i], 32));
+    if constexpr (S::LANES > 16) v[i] = f(v[i], __shfl_xor(v[i], 16));
+    if constexpr (S::LANES > 32) v[i] = f(v[i], __shfl_xor(v[i], 32));
   }
   if constexpr (S::waves > 1) {
-    static_assert(S::rows == 1, "the block's wavefronts share one row");
     if (threadIdx.x % 64 == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) meet[threadIdx.x / 64][i] = v[i];
     __syncthreads();
+    const int first = S::rows > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / S::LANES) * S::waves : 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      T all = meet[0][i];
+      T all = meet[first][i];
 #pragma unroll
-      for (int w = 1; w < S::waves; ++w) all = f(all, meet[w][i]);
+      for (int w = 1; w < S::waves; ++w) all = f(all, meet[first + w][i]);
       v[i] = all;
     }
   }

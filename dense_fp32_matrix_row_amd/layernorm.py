@@ -103,25 +103,26 @@ def _vector(name, v, cols, dtype=None):
         raise TypeError(f"{name} is {dtype}, not {v.dtype}")
 
 
-def _params(weight, bias, cols):
+def _params(weight, bias, cols, x):
     """(addresses of both, their type)."""
-    kind = None
+    first = weight if weight is not None else bias
+    if first is None:
+        return None, None, F32
     for name, v in (("weight", weight), ("bias", bias)):
         if v is not None:
             _vector(name, v, cols)
-            this = _types().get(v.dtype)
-            if this is None:
-                raise TypeError(f"{name} is float32, bfloat16 or float16, not {v.dtype}")
-            if kind is not None and this != kind:
+            if v.dtype != first.dtype:
                 raise TypeError(f"weight and bias of two types: {weight.dtype} and {bias.dtype}")
-            kind = this
-    return weight.data_ptr() if weight is not None else None, bias.data_ptr() if bias is not None else None, kind or 0
+    kind = _types().get(first.dtype)
+    if kind is None or kind != F32 and first.dtype != x.dtype:
+        raise TypeError(f"weight and bias are float32 or of x's type, not {first.dtype}")
+    return weight.data_ptr() if weight is not None else None, bias.data_ptr() if bias is not None else None, kind
 
 
 def _forward(x, weight, bias, eps, out, keep):
     import torch
     rows, cols, ldx, kind = _tokens("x", x)
-    w, b, w_type = _params(weight, bias, cols)
+    w, b, w_type = _params(weight, bias, cols, x)
     if not eps >= 0:
         raise ValueError(f"eps is {eps}, not 0 or more")
     _same_device(x, weight, bias, out)
@@ -141,7 +142,7 @@ def _forward(x, weight, bias, eps, out, keep):
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None):
     """The layer norm of tokens x (T x I, rows may be strided) over their last
     dimension, as a new tensor of x's type or in `out` (which may be x).  weight and
-    bias: I numbers of one type, or None."""
+    bias: I numbers, float32 or of x's type, or None."""
     return _forward(x, weight, bias, eps, out, False)[0]
 
 
@@ -160,7 +161,7 @@ def layer_norm_backward(dy, x, stats, weight=None, dw=None, db=None, out=None):
     import torch
     rows, cols, ldx, kind = _tokens("x", x)
     lddy = _like("dy", dy, x)
-    w, _, w_type = _params(weight, None, cols)
+    w, _, w_type = _params(weight, None, cols, x)
     if tuple(stats.shape) != (3, rows) or stats.dtype != torch.float32 or not stats.is_contiguous():
         raise ValueError(f"stats are {tuple(stats.shape)} {stats.dtype}, not {(3, rows)} torch.float32, contiguous")
     given = dw is not None, db is not None

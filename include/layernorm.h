@@ -39,7 +39,8 @@ extern "C" {
  * Y <- the layer norm of X's rows.
  *   X, Y: rows x cols of `type`, row strides ldx, ldy; element alignment suffices.  Y
  *   may be X itself (same stride) and must not overlap it otherwise.
- *   w, b: cols numbers of w_type side by side; either may be NULL (1 and 0).
+ *   w, b: cols numbers of w_type (`type`, or HIP_LAYERNORM_F32) side by side; either
+ *   may be NULL (1 and 0).
  *   eps: at least 0.  stats: NULL, or 3 * rows floats that the backward pass takes:
  *   the means, what their rounding left over, and rstd.
  *   rows == 0 or cols == 0: nothing is done.

@@ -87,7 +87,7 @@ FORWARD = dict(rows=4, cols=8, type=0, X=FAKE, ldx=8, w=FAKE, b=FAKE, w_type=0, 
 
 @pytest.mark.parametrize("change,status", [
     (dict(rows=-1), -1), (dict(cols=-1), -2), (dict(type=3), -3), (dict(X=None), -4), (dict(ldx=7), -5), (dict(w_type=3), -8),
-    (dict(w=None, w_type=-1), -8), (dict(eps=-1e-9), -9), (dict(eps=float("nan")), -9), (dict(Y=None), -10), (dict(ldy=7), -11),
+    (dict(w_type=1), -8), (dict(type=1, w_type=2), -8), (dict(w=None, w_type=-1), -8), (dict(eps=-1e-9), -9), (dict(eps=float("nan")), -9), (dict(Y=None), -10), (dict(ldy=7), -11),
     (dict(rows=0), 0), (dict(cols=0, X=None, w=None, b=None, w_type=7), 0),
 ])
 def test_layernorm_forward_refusals(change, status):
@@ -100,7 +100,7 @@ BACKWARD = dict(rows=4, cols=8, type=0, DY=FAKE, lddy=8, X=FAKE, ldx=8, stats=FA
 
 @pytest.mark.parametrize("change,status", [
     (dict(rows=-1), -1), (dict(cols=-1), -2), (dict(type=-1), -3), (dict(DY=None), -4), (dict(lddy=7), -5), (dict(X=None), -6),
-    (dict(ldx=7), -7), (dict(stats=None), -8), (dict(w_type=3), -10), (dict(lddx=7), -12), (dict(accumulate=2), -15),
+    (dict(ldx=7), -7), (dict(stats=None), -8), (dict(w_type=3), -10), (dict(w_type=1), -10), (dict(lddx=7), -12), (dict(accumulate=2), -15),
     (dict(workspace=None), -16), (dict(workspace=FAKE + 8), -16), (dict(workspace_bytes=8), -17),
     (dict(cols=0), 0), (dict(rows=0, dw=None, db=None, workspace=None), 0), (dict(DX=None, dw=None, db=None, workspace=None), 0),
 ])
