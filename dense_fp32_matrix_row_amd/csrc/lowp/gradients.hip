@@ -17,28 +17,27 @@
 namespace sgemm {
 namespace {
 
-struct Entry {
-  const void* x;
-  void* y;
-  int64_t cols, ldx, ldy;
-  int64_t first;  // chunk of all tensors'
-  int64_t rows;
-  int32_t split;  // > 0: chunks a row; < 0: rows a chunk
-  int32_t type;
+// A tensor in the table: where it lies, its first chunk of all tensors', and its type;
+// one of several rows has a second slot behind it, of the same first chunk.
+struct Slot {
+  int64_t x, y, cols;  // addresses; or rows, ldx, ldy
+  uint32_t first;
+  int32_t kind;  // the type, with kRows where a slot follows; kSecond
 };
-static_assert(sizeof(Entry) == 64);
+constexpr int32_t kRows = 4, kSecond = 8;
+static_assert(sizeof(Slot) == 32);
 
-constexpr int kInline = 56;  // tensors that fit a launch's arguments (4 KiB)
+constexpr int kInline = 120;  // slots that fit a launch's arguments (4 KiB)
 struct Table {
-  Entry e[kInline];
+  Slot e[kInline];
 };
 constexpr int kThreads = 256;
 constexpr int64_t kBlocks = 2048;  // at most, of a launch: eight for each CU
 constexpr int64_t kPartBytes = kBlocks * 8;
 
-// The tensor that a chunk lies in: the last whose first chunk is not behind it, found
-// 64 at a time.
-__device__ __forceinline__ int find(const Entry* e, int count, int64_t chunk) {
+// The slot of the tensor that a chunk lies in: the last whose first chunk is not behind
+// it (or the one before), found 64 at a time.
+__device__ __forceinline__ int find(const Slot* e, int count, uint32_t chunk) {
   int lo = 0, n = count;
   while (n > 1) {
     const int lane = threadIdx.x % 64, step = (n + 63) / 64;
@@ -47,7 +46,8 @@ __device__ __forceinline__ int find(const Entry* e, int count, int64_t chunk) {
     lo += at;
     n = min(step, n - at);
   }
-  return __builtin_amdgcn_readfirstlane(lo);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  return e[lo].kind == kSecond ? lo - 1 : lo;
 }
 
 // 16 bytes of elements.
@@ -129,30 +129,41 @@ struct Scale {
   __device__ __forceinline__ void one(const T* x, T* y) { from_float((*this)(to_float(*x)), *y); }
 };
 
+// Chunk k of a tensor: a piece of a row, or several rows shorter than a chunk.
 template <class T, class F>
-__device__ __forceinline__ void do_chunk(const Entry& e, int64_t k, int chunk, F& f) {
-  const T* const x = static_cast<const T*>(e.x);
-  T* const y = static_cast<T*>(e.y);
-  if (e.split > 0) {
-    const int64_t row = e.split == 1 ? k : k / e.split, col = (k - row * e.split) * chunk;
-    f.flat(x + row * e.ldx + col, y + row * e.ldy + col, static_cast<int>(min(int64_t(chunk), e.cols - col)));
+__device__ __forceinline__ void do_chunk(const Slot* e, uint32_t k, int chunk, F& f) {
+  const T* const x = reinterpret_cast<const T*>(e->x);
+  T* const y = reinterpret_cast<T*>(e->y);
+  const int64_t cols = e->cols;
+  if (!(e->kind & kRows)) {
+    const int64_t at = int64_t(k) * chunk;
+    f.flat(x + at, y + at, static_cast<int>(min(int64_t(chunk), cols - at)));
+    return;
+  }
+  const int64_t rows = e[1].x, ldx = e[1].y, ldy = e[1].cols;
+  if (cols >= chunk) {
+    const int64_t per = ceil_div(cols, chunk), row = k / per, at = (k - row * per) * chunk;
+    f.flat(x + row * ldx + at, y + row * ldy + at, static_cast<int>(min(int64_t(chunk), cols - at)));
   } else {
-    const int64_t row = k * -e.split;
-    const int rows = static_cast<int>(min(int64_t(-e.split), e.rows - row)), cols = static_cast<int>(e.cols);
-    for (int i = threadIdx.x; i < rows * cols; i += kThreads)
-      f.one(x + (row + i / cols) * e.ldx + i % cols, y + (row + i / cols) * e.ldy + i % cols);
+    const int few = static_cast<int>(cols), per = chunk / few;
+    const int64_t row = int64_t(k) * per;
+    const int count = static_cast<int>(min(int64_t(per), rows - row)) * few;
+    for (int i = threadIdx.x; i < count; i += kThreads)
+      f.one(x + (row + i / few) * ldx + i % few, y + (row + i / few) * ldy + i % few);
   }
 }
 
 // The chunks of a block, in order.
 template <class F>
-__device__ __forceinline__ void do_chunks(const Entry* table, int count, int64_t chunks, int chunk, bool skip_in_place, F& f) {
-  for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
-    const Entry& e = table[find(table, count, k)];
-    if (skip_in_place && e.x == e.y) continue;
-    if (e.type == HIP_GRADIENT_F32) do_chunk<float>(e, k - e.first, chunk, f);
-    else if (e.type == HIP_GRADIENT_BF16) do_chunk<bf16>(e, k - e.first, chunk, f);
-    else do_chunk<_Float16>(e, k - e.first, chunk, f);
+__device__ __forceinline__ void do_chunks(const Slot* table, int count, uint32_t chunks, int chunk, bool skip_in_place, F& f) {
+  for (int64_t at = blockIdx.x; at < chunks; at += gridDim.x) {
+    const uint32_t k = static_cast<uint32_t>(at);
+    const Slot* const e = table + find(table, count, k);
+    if (skip_in_place && e->x == e->y) continue;
+    const int type = e->kind & 3;
+    if (type == HIP_GRADIENT_F32) do_chunk<float>(e, k - e->first, chunk, f);
+    else if (type == HIP_GRADIENT_BF16) do_chunk<bf16>(e, k - e->first, chunk, f);
+    else do_chunk<_Float16>(e, k - e->first, chunk, f);
   }
 }
 
@@ -160,7 +171,7 @@ struct Add {
   __device__ __forceinline__ double operator()(double a, double b) const { return a + b; }
 };
 
-__device__ __forceinline__ void norm_body(const Entry* table, int count, int64_t chunks, int chunk, double* parts) {
+__device__ __forceinline__ void norm_body(const Slot* table, int count, uint32_t chunks, int chunk, double* parts) {
   using S = RowShape<kThreads, 1>;
   __shared__ double meet[S::threads / 64][1];
   Squares f;
@@ -169,10 +180,10 @@ __device__ __forceinline__ void norm_body(const Entry* table, int count, int64_t
   join_row<S>(sum, meet, Add{});
   if (threadIdx.x == 0) parts[blockIdx.x] = sum[0];
 }
-__global__ __launch_bounds__(kThreads) void k_norm(Table t, int count, int64_t chunks, int chunk, double* parts) {
+__global__ __launch_bounds__(kThreads) void k_norm(Table t, int count, uint32_t chunks, int chunk, double* parts) {
   norm_body(t.e, count, chunks, chunk, parts);
 }
-__global__ __launch_bounds__(kThreads) void k_norm_long(const Entry* __restrict__ table, int count, int64_t chunks, int chunk,
+__global__ __launch_bounds__(kThreads) void k_norm_long(const Slot* __restrict__ table, int count, uint32_t chunks, int chunk,
                                                         double* parts) {
   norm_body(table, count, chunks, chunk, parts);
 }
@@ -199,7 +210,7 @@ struct Limit {
   float max_norm, eps;
   bool all_in_place;
 };
-__device__ __forceinline__ void clip_body(const Entry* table, int count, int64_t chunks, int chunk, const Limit& l) {
+__device__ __forceinline__ void clip_body(const Slot* table, int count, uint32_t chunks, int chunk, const Limit& l) {
   const double norm = l.given ? static_cast<double>(*l.given) : join_parts(l.parts, l.count);
   if (l.norm && blockIdx.x == 0 && threadIdx.x == 0) *l.norm = static_cast<float>(norm);
   const double all = norm + static_cast<double>(l.eps), most = static_cast<double>(l.max_norm);
@@ -208,78 +219,82 @@ __device__ __forceinline__ void clip_body(const Entry* table, int count, int64_t
   if (same && l.all_in_place) return;
   do_chunks(table, count, chunks, chunk, same, f);
 }
-__global__ __launch_bounds__(kThreads) void k_clip(Table t, int count, int64_t chunks, int chunk, Limit l) {
+__global__ __launch_bounds__(kThreads) void k_clip(Table t, int count, uint32_t chunks, int chunk, Limit l) {
   clip_body(t.e, count, chunks, chunk, l);
 }
-__global__ __launch_bounds__(kThreads) void k_clip_long(const Entry* __restrict__ table, int count, int64_t chunks, int chunk,
+__global__ __launch_bounds__(kThreads) void k_clip_long(const Slot* __restrict__ table, int count, uint32_t chunks, int chunk,
                                                         Limit l) {
   clip_body(table, count, chunks, chunk, l);
 }
 
-// Entries that come as arguments into memory.
-__global__ __launch_bounds__(64) void k_table(Table t, int count, Entry* to) {
+// Slots that come as arguments into memory.
+__global__ __launch_bounds__(64) void k_table(Table t, int count, Slot* to) {
   for (int i = threadIdx.x; i < count; i += 64) to[i] = t.e[i];
 }
 
 // What a call works on: the tensors that have elements.
+struct Tensor {
+  uintptr_t x, y;
+  int64_t rows, cols, ldx, ldy;
+  int type;
+};
 struct Work {
-  std::vector<Entry> entries;
-  int64_t chunks = 0;
+  std::vector<Tensor> tensors;
+  std::vector<Slot> slots;
+  uint32_t chunks = 0;
   int chunk = 0;
   bool all_in_place = true;
 };
 
+// Sizes and strides below 2^40 and no tensor that reaches over 2^44 elements: more than
+// memory, less than what overflows below.
 bool valid(const hip_gradient& g, bool clip) {
-  if (g.rows < 0 || g.cols < 0 || g.type < 0 || g.type > HIP_GRADIENT_F16) return false;
-  if (g.rows > (int64_t(1) << 40) || g.cols > (int64_t(1) << 40)) return false;  // more than memory, less than overflows below
+  constexpr int64_t kSide = int64_t(1) << 40;
+  if (g.rows < 0 || g.cols < 0 || g.rows > kSide || g.cols > kSide || g.type < 0 || g.type > HIP_GRADIENT_F16) return false;
   if (g.rows == 0 || g.cols == 0) return true;
   const uintptr_t align = g.type == HIP_GRADIENT_F32 ? 4 : 2;
-  if (!g.x || reinterpret_cast<uintptr_t>(g.x) % align) return false;
-  if (g.rows > 1 && (g.ldx < g.cols || g.ldx > (int64_t(1) << 40))) return false;
-  if (!clip) return true;
-  if (!g.y || reinterpret_cast<uintptr_t>(g.y) % align) return false;
-  return !(g.rows > 1 && (g.ldy < g.cols || g.ldy > (int64_t(1) << 40)));
+  const auto bad = [&](const void* p, int64_t ld) {
+    if (!p || reinterpret_cast<uintptr_t>(p) % align) return true;
+    return g.rows > 1 && (ld < g.cols || ld > kSide || static_cast<double>(g.rows) * static_cast<double>(ld) > 0x1p44);
+  };
+  return !bad(g.x, g.ldx) && !(clip && bad(g.y, g.ldy));
 }
 
-void collect(Work& w, int count, const hip_gradient* tensors, bool clip) {
-  w.entries.reserve(count);
-  int64_t total = 0;
+// False where there are more chunks than a number of 32 bits counts.
+bool collect(Work& w, int count, const hip_gradient* tensors, bool clip) {
+  w.tensors.reserve(count);
+  w.slots.reserve(count);
+  double total = 0.0;
   for (int i = 0; i < count; ++i) {
     const hip_gradient& g = tensors[i];
     if (g.rows == 0 || g.cols == 0) continue;
-    Entry e{};
-    e.x = g.x;
-    e.y = clip ? g.y : const_cast<void*>(g.x);
-    e.rows = g.rows;
-    e.cols = g.cols;
-    e.ldx = g.rows > 1 ? g.ldx : g.cols;
-    e.ldy = !clip ? e.ldx : g.rows > 1 ? g.ldy : g.cols;
-    e.type = static_cast<int32_t>(g.type);
-    if (e.rows > 1 && e.ldx == e.cols && e.ldy == e.cols) {  // dense
-      e.cols *= e.rows;
-      e.rows = 1;
+    Tensor t{reinterpret_cast<uintptr_t>(g.x), reinterpret_cast<uintptr_t>(clip ? g.y : g.x), g.rows, g.cols, g.ldx,
+             clip ? g.ldy : g.ldx, static_cast<int>(g.type)};
+    total += static_cast<double>(t.rows) * static_cast<double>(t.cols);
+    if (t.rows > 1 && t.ldx == t.cols && t.ldy == t.cols && t.rows < (int64_t(1) << 40) / t.cols) {  // dense
+      t.cols *= t.rows;
+      t.rows = 1;
     }
-    if (e.rows == 1) e.ldx = e.ldy = 0;
-    w.all_in_place = w.all_in_place && e.x == e.y;
-    total += e.rows * e.cols;
-    w.entries.push_back(e);
+    w.all_in_place = w.all_in_place && t.x == t.y;
+    w.tensors.push_back(t);
   }
   // two chunks or more for each block where there is that much, down to four 16-byte
   // loads a thread, and eight for an even end where there is more
   w.chunk = 4096;
   while (w.chunk < 16384 && total / w.chunk > 2 * kBlocks) w.chunk *= 2;
-  for (Entry& e : w.entries) {
-    e.first = w.chunks;
-    if (e.rows == 1 || e.cols >= w.chunk) {
-      const int64_t per = ceil_div(e.cols, w.chunk);
-      e.split = e.rows == 1 ? std::numeric_limits<int32_t>::max() : static_cast<int32_t>(per);
-      w.chunks += e.rows * per;
-    } else {
-      const int64_t per = w.chunk / e.cols;
-      e.split = static_cast<int32_t>(-per);
-      w.chunks += ceil_div(e.rows, per);
-    }
+  uint64_t chunks = 0;
+  for (const Tensor& t : w.tensors) {
+    const uint32_t first = static_cast<uint32_t>(chunks);
+    w.slots.push_back(Slot{static_cast<int64_t>(t.x), static_cast<int64_t>(t.y), t.cols, first, t.type | (t.rows > 1 ? kRows : 0)});
+    if (t.rows > 1) w.slots.push_back(Slot{t.rows, t.ldx, t.ldy, first, kSecond});
+    const double many = static_cast<double>(t.rows) * static_cast<double>(ceil_div(t.cols, w.chunk));
+    if (t.rows > 1 && t.cols < w.chunk) chunks += ceil_div(t.rows, w.chunk / t.cols);
+    else if (many < 1e10) chunks += t.rows * ceil_div(t.cols, w.chunk);
+    else return false;
+    if (chunks > std::numeric_limits<uint32_t>::max()) return false;
   }
+  w.chunks = static_cast<uint32_t>(chunks);
+  return true;
 }
 
 // Whether what a clipping call writes overlaps anything else that it touches.
@@ -297,16 +312,14 @@ bool meet(const Range& a, const Range& b) {
 }
 bool overlaps(const Work& w, const float* norm) {
   std::vector<Range> ranges;
-  ranges.reserve(2 * w.entries.size() + 1);
-  for (const Entry& e : w.entries) {
-    const uintptr_t size = e.type == HIP_GRADIENT_F32 ? 4 : 2, row = e.cols * size;
-    const auto add = [&](const void* p, int64_t ld, bool writes) {
-      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-      ranges.push_back(Range{at, at + (e.rows - 1) * ld * size + row, row, e.rows > 1 ? ld * size : 0, writes});
+  ranges.reserve(2 * w.tensors.size() + 1);
+  for (const Tensor& t : w.tensors) {
+    const uintptr_t size = t.type == HIP_GRADIENT_F32 ? 4 : 2, row = t.cols * size;
+    const auto add = [&](uintptr_t at, int64_t ld, bool writes) {
+      ranges.push_back(Range{at, at + (t.rows - 1) * ld * size + row, row, t.rows > 1 ? ld * size : 0, writes});
     };
-    const bool in_place = e.x == e.y && e.ldx == e.ldy;
-    add(e.y, e.ldy, true);
-    if (!in_place) add(e.x, e.ldx, false);
+    add(t.y, t.ldy, true);
+    if (t.x != t.y || (t.rows > 1 && t.ldx != t.ldy)) add(t.x, t.ldx, false);
   }
   if (norm) ranges.push_back(Range{reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, 4, 0, true});
   std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
@@ -324,36 +337,36 @@ bool overlaps(const Work& w, const float* norm) {
   return false;
 }
 
-// Launches f(table or pointer) with the entries where the kernels find them.
-void put_table(const Work& w, Entry* to, hipStream_t stream) {
-  const int n = static_cast<int>(w.entries.size());
+// The slots into memory.
+void put_table(const Work& w, Slot* to, hipStream_t stream) {
+  const int n = static_cast<int>(w.slots.size());
   for (int at = 0; at < n; at += kInline) {
-    Table t{};
+    Table t;
     const int some = std::min(kInline, n - at);
-    std::copy_n(w.entries.begin() + at, some, t.e);
+    std::copy_n(w.slots.begin() + at, some, t.e);
     hipLaunchKernelGGL(k_table, dim3(1), dim3(64), 0, stream, t, some, to + at);
   }
 }
 Table inline_table(const Work& w) {
-  Table t{};
-  std::copy(w.entries.begin(), w.entries.end(), t.e);
+  Table t;
+  std::copy(w.slots.begin(), w.slots.end(), t.e);
   return t;
 }
 
 struct Memory {
   double* parts;
-  Entry* table;
+  Slot* table;
 };
 Memory memory(void* workspace) {
   uint8_t* const p = static_cast<uint8_t*>(workspace);
-  return Memory{reinterpret_cast<double*>(p), reinterpret_cast<Entry*>(p + kPartBytes)};
+  return Memory{reinterpret_cast<double*>(p), reinterpret_cast<Slot*>(p + kPartBytes)};
 }
-int64_t bytes_for(int count) { return kPartBytes + (count > kInline ? int64_t(count) * int64_t(sizeof(Entry)) : 0); }
+int64_t bytes_for(int count) { return kPartBytes + (2 * count > kInline ? 2 * int64_t(count) * int64_t(sizeof(Slot)) : 0); }
 
-unsigned blocks_for(const Work& w) { return static_cast<unsigned>(std::min(w.chunks, kBlocks)); }
+unsigned blocks_for(const Work& w) { return static_cast<unsigned>(std::min(int64_t(w.chunks), kBlocks)); }
 
 void launch_norm(const Work& w, const Memory& m, hipStream_t stream) {
-  const int n = static_cast<int>(w.entries.size());
+  const int n = static_cast<int>(w.slots.size());
   if (n == 0) return;
   if (n <= kInline)
     hipLaunchKernelGGL(k_norm, dim3(blocks_for(w)), dim3(kThreads), 0, stream, inline_table(w), n, w.chunks, w.chunk, m.parts);
@@ -361,7 +374,7 @@ void launch_norm(const Work& w, const Memory& m, hipStream_t stream) {
     hipLaunchKernelGGL(k_norm_long, dim3(blocks_for(w)), dim3(kThreads), 0, stream, m.table, n, w.chunks, w.chunk, m.parts);
 }
 void launch_clip(const Work& w, const Memory& m, const Limit& l, hipStream_t stream) {
-  const int n = static_cast<int>(w.entries.size());
+  const int n = static_cast<int>(w.slots.size());
   const dim3 grid(std::max(1u, blocks_for(w)));
   if (n <= kInline) hipLaunchKernelGGL(k_clip, grid, dim3(kThreads), 0, stream, inline_table(w), n, w.chunks, w.chunk, l);
   else hipLaunchKernelGGL(k_clip_long, grid, dim3(kThreads), 0, stream, m.table, n, w.chunks, w.chunk, l);
@@ -380,9 +393,9 @@ int begin(Work& w, int count, const hip_gradient* tensors, bool clip, const floa
     if (!valid(tensors[i], clip)) return -2;
   if (workspace == nullptr || off256(workspace)) return -workspace_at;
   if (workspace_bytes < bytes_for(count)) return -(workspace_at + 1);
-  collect(w, count, tensors, clip);
+  if (!collect(w, count, tensors, clip)) return -2;
   if (clip && overlaps(w, norm)) return -2;
-  if (static_cast<int>(w.entries.size()) > kInline) put_table(w, memory(workspace).table, stream);
+  if (static_cast<int>(w.slots.size()) > kInline) put_table(w, memory(workspace).table, stream);
   return 0;
 }
 

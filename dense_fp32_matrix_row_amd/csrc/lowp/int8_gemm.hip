@@ -2,10 +2,12 @@
 // and of B, plus a bias, over 8-bit integers; hip_int8_linear: the quantiser and
 // that product.
 #include "../../../include/int8.h"
+#include "int8_codes.h"
 #include "int8_internal.h"
 #include "lowp.h"
 #include "nt_loop.h"
 #include "nt_plan.h"
+#include "rows.h"
 
 namespace sgemm {
 namespace {
@@ -217,11 +219,188 @@ void launch_out(const Int8Product& p, hipStream_t stream) {
   launch<O>(a, b, p.K, out, stream);
 }
 
+// A linear layer of few tokens in one launch: each block quantises all of them for
+// itself, with its first loads of the weight under way, into LDS, and sums 16 x 16
+// results from there, its wavefronts taking every eighth step along K as Direct's do.
+// Bound by a launch, a trip to memory for x and the weight's read: 1 x 1024 x 1024 4.6 us
+// (quantiser and product in two launches 5.9), 1 x 4096 x 4096 6.2 (8.7), 16 x 1024 x
+// 4096 5.6 (6.4), 4 x 4096 x 16384 14.6 (16.9); where many blocks quantise many tokens
+// the second launch would be worth it on the device, 16 x 1024 x 16384 10.6 (9.4), but
+// costs the host 4 us.
+// At most 32 elements a thread, held in registers from the maximum to the codes.
+constexpr int kTokenThreads = 512, kTokenElements = 32 * kTokenThreads, kMostTokens = 16;
+constexpr int64_t kTokenBlocks = 512;  // at most: two a CU, as many as run at a time (4 x 4096 x 16384 with 1024 19 us, 14.6)
+// tokens rounded up to a power of two, so that each takes as many lanes
+__host__ __device__ constexpr int token_rows(int tokens) {
+  int r = 1;
+  while (r < tokens) r *= 2;
+  return r;
+}
+bool few_tokens(int tokens, int inputs) {
+  return tokens <= kMostTokens && int64_t(token_rows(tokens)) * ceil_div(inputs, 8) * 8 <= kTokenElements;
+}
+
+// Eight neighbours of a row, of at least eight or none: the words of the last eight
+// inside where fewer are left, moved to the front when they are looked at.  The load
+// has no branch around it, behind which the compiler would wait for it by itself
+// (1 x 4096 x 4096 8.0 -> 6.2 us).
+template <class X>
+struct Raw8 {
+  static constexpr int kWords = 2 * sizeof(X);
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const X* row, int col, int cols) {
+    if (cols >= 8) {
+      __builtin_memcpy(w, row + min(col, cols - 8), sizeof(w));
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 7; ++i)  // uniform: a row shorter than that
+      if (col + i < cols) {
+        if constexpr (sizeof(X) == 4) w[i] = reinterpret_cast<const uint32_t*>(row)[col + i];
+        else w[i / 2] |= uint32_t(reinterpret_cast<const uint16_t*>(row)[col + i]) << (16 * (i % 2));
+      }
+  }
+  __device__ __forceinline__ Pack<8, X> settled(int col, int cols) const {
+    Raw8 r = *this;
+    if (cols >= 8 && col > cols - 8) {
+      const int off = min(col - (cols - 8), 8);
+      const auto down = [&](bool on, int by) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) r.w[i] = !on ? r.w[i] : i + by < kWords ? r.w[i + by] : 0;
+      };
+      down(off & 8, kWords);
+      down(off & 4, kWords / 2);
+      down(off & 2, kWords / 4);
+      if constexpr (sizeof(X) == 4) {
+        down(off & 1, 1);
+      } else if (off & 1) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) r.w[i] = r.w[i] >> 16 | (i + 1 < kWords ? r.w[i + 1] << 16 : 0);
+      }
+    }
+    return __builtin_bit_cast(Pack<8, X>, r);
+  }
+};
+
+template <int ROWS, class X, class O>
+__global__ __launch_bounds__(kTokenThreads) void k_tokens(const X* __restrict__ x, int64_t ldx, int tokens, Side B, int K,
+                                                          Out<O> out) {
+  constexpr int kLanes = kTokenThreads / ROWS, kChunks = 4, kWaves = kTokenThreads / 64, kAhead = 4;
+  using S = RowShape<kLanes, kChunks, kTokenThreads>;
+  // rows of codes 16 bytes more than a multiple of 128 apart, the last step's filled up with zeros
+  constexpr int kLdMost = kTokenElements / ROWS + 16;
+  __shared__ alignas(16) int8_t codes[ROWS * kLdMost];
+  __shared__ uint32_t meet[kWaves][1];
+  __shared__ float scales[ROWS];
+  __shared__ v4i sums[2][kWaves][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  const int row = lane % 16, g = lane / 16;
+  const int64_t tiles = ceil_div(out.N, 16);
+  const int steps = static_cast<int>(ceil_div(K, nt::kStep)), ld = steps * nt::kStep + 16;
+  const int last = (K - 1) / 16 * 16;  // the last 16 bytes of a row; what they hold past K meets zeros
+  const auto read = [&](nt::Frag& f, int64_t tile, int k) {
+    const uint8_t* const b = B.p + min(tile * 16 + row, int64_t(B.rows) - 1) * B.ld;
+    f.lo = *reinterpret_cast<const v4i*>(b + min(k * nt::kStep + 16 * g, last));
+    f.hi = *reinterpret_cast<const v4i*>(b + min(k * nt::kStep + 16 * (4 + g), last));
+  };
+  // x before the weight: loads arrive in order
+  const int token = threadIdx.x / kLanes, place = threadIdx.x % kLanes;
+  Raw8<X> raw[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) raw[c].load(x + int64_t(min(token, tokens - 1)) * ldx, (c * kLanes + place) * 8, K);
+  // the wavefront's steps wave + 8 u of every 32 pass through fragment u (those past
+  // the end read a row's last bytes: with a branch around them all loads would have to
+  // arrive before x is looked at)
+  nt::Frag f[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) read(f[u], blockIdx.x, wave + u * kWaves);
+  {
+    Pack<8, X> v[kChunks];
+    uint32_t top[1] = {0};
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      v[c] = raw[c].settled((c * kLanes + place) * 8, K);
+      top[0] = int8::top8(top[0], v[c]);
+    }
+    join_row<S>(top, meet, int8::Max{});
+    const int8::Scale by = int8::make_scale(top[0]);
+    if (place == 0) scales[token] = by.s;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int col = (c * kLanes + place) * 8;
+      if (col < ld - 16) {  // past K codes of zeros are zeros
+        const Pack<8, int8_t> q = int8::codes8(v[c], by);
+        __builtin_memcpy(&codes[token * ld + col], &q, 8);
+      }
+    }
+  }
+  __syncthreads();
+  Out<O> o = out;
+  o.sa = scales;
+  o.sa_inc = 1;
+  const int8_t* const a = &codes[min(row, tokens - 1) * ld + 16 * g];
+  int turn = 0;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    v4i acc = {0, 0, 0, 0};
+    for (int k0 = wave; k0 < steps; k0 += kAhead * kWaves) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int k = k0 + u * kWaves;
+        if (k >= steps) break;
+        nt::Frag m;
+        m.lo = *reinterpret_cast<const v4i*>(a + k * nt::kStep);
+        m.hi = *reinterpret_cast<const v4i*>(a + k * nt::kStep + 64);
+        nt::Int8::mac(acc, f[u], m, 0, 0);
+        if (k + kAhead * kWaves < steps) read(f[u], tile, k + kAhead * kWaves);
+        else if (tile + gridDim.x < tiles) read(f[u], tile + gridDim.x, wave + u * kWaves);
+      }
+    }
+    sums[turn][wave][lane] = acc;
+    __syncthreads();  // sums[turn] is free again when all have met in the next tile
+    if (wave == 0) {
+      v4i v = sums[turn][0][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += sums[turn][w][lane];
+      o(row, static_cast<int>(tile * 16) + 4 * g, v);
+    }
+  }
+}
+
+template <class X, class O>
+void launch_tokens(const void* x, int64_t ldx, const Int8Product& p, hipStream_t stream) {
+  const Out<O> out{static_cast<O*>(p.d), p.ldd, p.M, p.N, nullptr, 1, p.sb, p.sb_inc, Bias{p.bias, p.bias_type}};
+  const Side b{static_cast<const uint8_t*>(p.b), p.ldb, p.N, nullptr, 0, 0, 0, 0};
+  const int64_t tiles = ceil_div(p.N, 16);
+  const dim3 grid(static_cast<unsigned>(tiles < kTokenBlocks ? tiles : kTokenBlocks));
+  const auto go = [&](auto rows) {
+    hipLaunchKernelGGL((k_tokens<rows.value, X, O>), grid, dim3(kTokenThreads), 0, stream, static_cast<const X*>(x), ldx,
+                       p.M, b, p.K, out);
+  };
+  switch (token_rows(p.M)) {
+    case 1: return go(std::integral_constant<int, 1>{});
+    case 2: return go(std::integral_constant<int, 2>{});
+    case 4: return go(std::integral_constant<int, 4>{});
+    case 8: return go(std::integral_constant<int, 8>{});
+    default: return go(std::integral_constant<int, 16>{});
+  }
+}
+template <class X>
+void launch_tokens(const void* x, int64_t ldx, const Int8Product& p, hipStream_t stream) {
+  if (p.d_type == HIP_INT8_F32) launch_tokens<X, float>(x, ldx, p, stream);
+  else if (p.d_type == HIP_INT8_BF16) launch_tokens<X, bf16>(x, ldx, p, stream);
+  else launch_tokens<X, _Float16>(x, ldx, p, stream);
+}
+
 bool bad_type(int t) { return t != HIP_INT8_F32 && t != HIP_INT8_BF16 && t != HIP_INT8_F16; }
 bool bad_ld(int ld, int K) { return ld < (K > 1 ? K : 1) || ld % 16 != 0 || ld > HIP_INT8_MAX_LD; }
 bool off16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 != 0; }
-// of the codes of a linear layer's tokens
+// of the codes of a linear layer's tokens in the workspace, and what they take there
 int64_t code_stride(int inputs) { return inputs > 0 ? ceil_div(inputs, 16) * 16 : 16; }
+int64_t linear_bytes(int tokens, int inputs) {
+  return tokens == 0 || inputs == 0 || few_tokens(tokens, inputs) ? 0 : tokens * (code_stride(inputs) + 4);
+}
 
 }  // namespace
 
@@ -281,7 +460,7 @@ int hip_int8_gemm_plan(int M, int N, int K, hip_int8_gemm_launch* launches, int*
 int hip_int8_linear_workspace(int tokens, int inputs, long long* bytes) {
   if (tokens < 0) return -1;
   if (inputs < 0 || inputs > HIP_INT8_MAX_K) return -2;
-  if (bytes) *bytes = tokens * (code_stride(inputs) + 4);
+  if (bytes) *bytes = linear_bytes(tokens, inputs);
   return 0;
 }
 
@@ -303,17 +482,27 @@ int hip_int8_linear(int tokens, int inputs, int outputs, const void* X, int x_ty
   if (some && Y == nullptr) return -13;
   if (ldy < (outputs > 1 ? outputs : 1)) return -14;
   if (bad_type(y_type)) return -15;
-  if (product && (workspace == nullptr || off16(workspace))) return -16;
-  if (product && workspace_bytes < tokens * (code_stride(inputs) + 4)) return -17;
+  const int64_t bytes = product ? linear_bytes(tokens, inputs) : 0;
+  if (bytes > 0 && (workspace == nullptr || off16(workspace))) return -16;
+  if (workspace_bytes < bytes) return -17;
   if (!some) return 0;
-  const int64_t ldq = code_stride(inputs);
-  int8_t* const q = static_cast<int8_t*>(workspace);
-  float* const s = product ? reinterpret_cast<float*>(q + tokens * ldq) : nullptr;
-  if (product) launch_int8_quantize(tokens, inputs, X, x_type, ldx, q, ldq, s, stream);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return static_cast<int>(e);
-  launch_int8_gemm(Int8Product{tokens, outputs, inputs, q, ldq, s, 1, W, ldw, SW, sw_inc, bias, bias_type, Y, ldy, y_type},
-                   stream);
+  Int8Product p{tokens, outputs, inputs, workspace, code_stride(inputs), nullptr, 1, W, ldw, SW, sw_inc, bias, bias_type, Y,
+                ldy, y_type};
+  if (product && bytes == 0) {
+    if (x_type == HIP_INT8_F32) launch_tokens<float>(X, ldx, p, stream);
+    else if (x_type == HIP_INT8_BF16) launch_tokens<bf16>(X, ldx, p, stream);
+    else launch_tokens<_Float16>(X, ldx, p, stream);
+    return static_cast<int>(hipGetLastError());
+  }
+  if (product) {
+    int8_t* const q = static_cast<int8_t*>(workspace);
+    float* const s = reinterpret_cast<float*>(q + tokens * p.lda);
+    launch_int8_quantize(tokens, inputs, X, x_type, ldx, q, p.lda, s, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return static_cast<int>(e);
+    p.sa = s;
+  }
+  launch_int8_gemm(p, stream);
   return static_cast<int>(hipGetLastError());
 }
 

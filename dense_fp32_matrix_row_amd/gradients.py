@@ -12,10 +12,11 @@ for autograd.
 
 from __future__ import annotations
 
+import array
 import ctypes
 
 from . import sgemm as _sgemm
-from .blockfp8 import _call, _types
+from .blockfp8 import _call, _types, written
 
 EXPORTS = ("hip_gradient_norm", "hip_gradient_clip", "hip_gradient_clip_by", "hip_gradient_workspace",
            "hip_gradient_norm_status_string", "hip_gradient_clip_status_string")
@@ -108,44 +109,41 @@ def _layout(t, what):
 
 
 def _describe(tensors, outs):
-    """(device, count, a flat list with seven numbers a tensor, as hip_gradient has them)."""
+    """(device, an array with seven numbers a tensor, as hip_gradient has them)."""
+    device = tensors[0].device
+    index = tensors[0].get_device()
+    if index < 0:
+        raise TypeError("gradients must live on the GPU")
     types = _types()
     flat = []
     add = flat.extend
-    index = -2
-    for i, t in enumerate(tensors):
-        at = t.get_device()
-        if at != index:
-            if index != -2:
-                raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
-            if at < 0:
-                raise TypeError("gradients must live on the GPU")
-            index = at
+    for t, o in zip(tensors, tensors if outs is None else outs):
         kind = types.get(t.dtype)
         if kind is None:
             raise TypeError(f"gradients are float32, bfloat16 or float16, not {t.dtype}")
-        x = t.data_ptr()
-        o = t if outs is None else outs[i]
+        if t.get_device() != index:
+            raise ValueError(f"tensors on {device} and {t.device}")
         if o is t:
+            x = t.data_ptr()
             if t.is_contiguous():
-                n = t.numel()
-                add((x, x, 1, n, n, n, kind))
-            else:
-                rows, cols, ld = _layout(t, "a gradient") if t.numel() else (0, 0, 0)
+                add((x, x, 1, t.numel(), 0, 0, kind))
+            elif t.numel():
+                rows, cols, ld = _layout(t, "a gradient")
                 add((x, x, rows, cols, ld, ld, kind))
+            else:
+                add((x, x, 0, 0, 0, 0, kind))
             continue
         if o.shape != t.shape or o.dtype != t.dtype:
             raise ValueError(f"out is {tuple(o.shape)} {o.dtype}, not {tuple(t.shape)} {t.dtype}")
-        if o.get_device() != at:
-            raise ValueError(f"tensors on {t.device} and {o.device}")
+        if o.get_device() != index:
+            raise ValueError(f"tensors on {device} and {o.device}")
         if t.is_contiguous() and o.is_contiguous():
-            n = t.numel()
-            add((x, o.data_ptr(), 1, n, n, n, kind))
-        elif t.numel() == 0:
-            add((x, o.data_ptr(), 0, 0, 0, 0, kind))
+            add((t.data_ptr(), o.data_ptr(), 1, t.numel(), 0, 0, kind))
+        elif t.numel():
+            add((t.data_ptr(), o.data_ptr(), *_pair(t, o), kind))
         else:
-            add((x, o.data_ptr(), *_pair(t, o), kind))
-    return (tensors[0].device if tensors else None), len(tensors), flat
+            add((0, 0, 0, 0, 0, 0, kind))
+    return device, array.array("q", flat)
 
 
 def _pair(t, o):
@@ -169,13 +167,13 @@ def _pair(t, o):
     return t.numel() // cols, cols, *strides
 
 
-def _run(function, what, device, count, flat, *args):
+def _run(function, what, device, described, *args):
     """A call with the tensors, a workspace and torch's current stream."""
     import torch
-    array = (ctypes.c_longlong * max(len(flat), 1))(*flat)
+    count = len(described) // 7
     bytes = hip_gradient_workspace(count)
     workspace = torch.empty(bytes, dtype=torch.uint8, device=device)
-    _call(device, function, what, count, ctypes.addressof(array), *args, workspace.data_ptr(), bytes)
+    _call(device, function, what, count, described.buffer_info()[0], *args, workspace.data_ptr(), bytes)
 
 
 def _outs(tensors, out):
@@ -192,9 +190,13 @@ def _outs(tensors, out):
 
 def _written(tensors):
     import torch
-    live = [t for t in tensors if not t.is_inference()]
-    if live:
-        torch.autograd.graph.increment_version(live)
+    if not tensors:
+        return
+    try:
+        torch.autograd.graph.increment_version(tensors)
+    except RuntimeError:  # inference tensors have no version to advance
+        for t in tensors:
+            written(t)
 
 
 def _list(tensors):
@@ -219,9 +221,9 @@ def grad_norm(tensors):
     tensors = _list(tensors)
     if not tensors:
         raise ValueError("no tensors")
-    device, count, flat = _describe(tensors, None)
+    device, described = _describe(tensors, None)
     norm = torch.empty((), dtype=torch.float32, device=device)
-    _run(load().hip_gradient_norm, hip_gradient_norm_status_string, device, count, flat, norm.data_ptr())
+    _run(load().hip_gradient_norm, hip_gradient_norm_status_string, device, described, norm.data_ptr())
     return norm
 
 
@@ -237,9 +239,9 @@ def clip_grad_norm(tensors, max_norm: float, eps: float = 1e-6, out=None):
     if not tensors:
         raise ValueError("no tensors")
     outs, modified = _outs(tensors, out)
-    device, count, flat = _describe(tensors, None if outs is tensors else outs)
+    device, described = _describe(tensors, None if outs is tensors else outs)
     norm = torch.empty((), dtype=torch.float32, device=device)
-    _run(load().hip_gradient_clip, hip_gradient_clip_status_string, device, count, flat, max_norm, eps, norm.data_ptr())
+    _run(load().hip_gradient_clip, hip_gradient_clip_status_string, device, described, max_norm, eps, norm.data_ptr())
     _written(modified)
     return norm, outs
 
@@ -255,9 +257,9 @@ def clip_by_norm(tensors, norm, max_norm: float, eps: float = 1e-6, out=None):
     if norm.dtype != torch.float32 or norm.numel() != 1:
         raise ValueError(f"norm is {tuple(norm.shape)} {norm.dtype}, not one torch.float32")
     outs, modified = _outs(tensors, out)
-    device, count, flat = _describe(tensors, None if outs is tensors else outs)
+    device, described = _describe(tensors, None if outs is tensors else outs)
     if norm.device != device:
         raise ValueError(f"tensors on {device} and {norm.device}")
-    _run(load().hip_gradient_clip_by, hip_gradient_clip_status_string, device, count, flat, max_norm, eps, norm.data_ptr())
+    _run(load().hip_gradient_clip_by, hip_gradient_clip_status_string, device, described, max_norm, eps, norm.data_ptr())
     _written(modified)
     return outs

@@ -227,6 +227,13 @@ def gemm(a: Int8, b: Int8, bias=None, out=None, out_dtype=None):
     return d
 
 
+def _linear_bytes(T, I) -> int:
+    """hip_int8_linear_workspace without a call: few tokens need none."""
+    if T <= 16 and (1 << (T - 1).bit_length() if T > 1 else T) * (-(-I // 8) * 8) <= 16384 or I == 0:
+        return 0
+    return T * (_stride(I) + 4)
+
+
 def linear(x, w: Int8, bias=None, out=None, out_dtype=None):
     """x w^T (+ bias) of tokens x (T x I, rows may be strided) and a quantised weight w
     (O x I): gemm(quantize(x), w, bias), bit for bit, in one call.  The result has
@@ -241,10 +248,10 @@ def linear(x, w: Int8, bias=None, out=None, out_dtype=None):
     _same_device(x, w.q, w.s, bias, out)
     device = x.device
     y, y_type, ldy = _result(out, out_dtype, x.dtype, T, O, device)
-    bytes = T * (_stride(I) + 4)  # hip_int8_linear_workspace
-    workspace = torch.empty(bytes, dtype=torch.uint8, device=device)
+    bytes = _linear_bytes(T, I)
+    workspace = torch.empty(bytes, dtype=torch.uint8, device=device) if bytes else None
     _call(device, load().hip_int8_linear, hip_int8_linear_status_string, T, I, O, x.data_ptr(), x_type, ldx, *right,
-          bias_at, bias_type, y.data_ptr(), ldy, y_type, workspace.data_ptr(), bytes)
+          bias_at, bias_type, y.data_ptr(), ldy, y_type, workspace.data_ptr() if bytes else None, bytes)
     if out is not None:
         written(out)
     return y

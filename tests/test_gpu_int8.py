@@ -227,7 +227,10 @@ def test_gemm_degenerate_sizes():
 
 
 @pytest.mark.parametrize("kind", TYPES)
-@pytest.mark.parametrize("T,I,O", [(1, 130, 70), (5, 512, 300), (200, 300, 257), (33, 4097, 65), (1, 17000, 20), (2100, 400, 2100)])
+@pytest.mark.parametrize("T,I,O", [(1, 130, 70), (5, 512, 300), (200, 300, 257), (33, 4097, 65), (1, 17000, 20), (2100, 400, 2100),
+                                   # few tokens in one launch, and just more than that
+                                   (1, 1, 1), (1, 16384, 33), (1, 16377, 16), (2, 8192, 50), (3, 4091, 17), (4, 4096, 100), (7, 1999, 31),
+                                   (8, 2048, 16), (9, 1000, 40), (16, 1024, 300), (16, 1025, 300), (15, 127, 5), (17, 128, 40), (2, 129, 4100)])
 def test_linear_layer(T, I, O, kind):
     x = ref.values(T, I + 5, TYPES[kind], 20)[:, 2:-3]  # rows apart, odd
     w = ref.values(O, I, torch.float32, 21)
@@ -244,12 +247,32 @@ def test_linear_layer(T, I, O, kind):
         assert torch.equal(place, int8.linear(x.cuda(), wq, out_dtype=out_type))
 
 
-def test_linear_nan_stays_in_its_token():
-    x = ref.values(40, 300, torch.bfloat16, 23)
-    x[17, 150], x[20, 3] = float("nan"), float("inf")
+@pytest.mark.parametrize("T", (40, 16, 5))
+@pytest.mark.parametrize("kind", TYPES)
+def test_linear_nan_stays_in_its_token(kind, T):
+    x = ref.values(T, 300, TYPES[kind], 23)
+    x[T - 3, 150], x[1, 3] = float("nan"), float("inf")
     y = int8.linear(x.cuda(), int8.quantize(torch.randn(70, 300, device="cuda")))
     bad = torch.isnan(y).cpu()
-    assert bad[17].all() and bad[20].all() and bad.sum() == 2 * 70
+    assert bad[T - 3].all() and bad[1].all() and bad.sum() == 2 * 70
+
+
+def test_linear_few_tokens_and_more_outputs_than_a_launch_has_tiles():
+    """Blocks that take several tiles; and rows of a weight past 2^31 bytes."""
+    w = torch.randint(-128, 128, (70001, 1024), device="cuda", dtype=torch.int8)
+    s = torch.rand(70001, device="cuda") + 0.5
+    for T in (1, 16):
+        x = ref.values(T, 1000, torch.bfloat16, 27)
+        y = int8.linear(x.cuda(), int8.Int8(w[:, :1000], s), out_dtype=torch.float32)
+        want, size = ref.product(*ref.quantize(x), w[:, :1000].cpu(), s.cpu())
+        ref.close(y, want, ref.product_tolerance(torch.float32, want, size))
+    wide = torch.randint(-128, 128, (140000, 16384), device="cuda", dtype=torch.int8)
+    s = torch.rand(140000, device="cuda") + 0.5
+    x = ref.values(1, 16384, torch.bfloat16, 28)
+    y = int8.linear(x.cuda(), int8.Int8(wide, s), out_dtype=torch.float32)
+    at = torch.tensor([0, 131071, 131072, 139999], device="cuda")
+    want, size = ref.product(*ref.quantize(x), wide[at].cpu(), s[at].cpu())
+    ref.close(y[:, at], want, ref.product_tolerance(torch.float32, want, size))
 
 
 @pytest.mark.parametrize("M", (3, 600))

@@ -59,8 +59,8 @@ def test_gemm_refusals(change, status):
     refused(int8.hip_int8_gemm, int8.hip_int8_gemm_status_string, GEMM, change, status)
 
 
-LINEAR = dict(tokens=4, inputs=200, outputs=8, X=FAKE, x_type=1, ldx=200, W=FAKE, ldw=208, SW=FAKE, sw_inc=1, bias=FAKE,
-              bias_type=0, Y=FAKE, ldy=8, y_type=1, workspace=FAKE, workspace_bytes=4 * (208 + 4))
+LINEAR = dict(tokens=40, inputs=200, outputs=8, X=FAKE, x_type=1, ldx=200, W=FAKE, ldw=208, SW=FAKE, sw_inc=1, bias=FAKE,
+              bias_type=0, Y=FAKE, ldy=8, y_type=1, workspace=FAKE, workspace_bytes=40 * (208 + 4))
 
 
 @pytest.mark.parametrize("change,status", [
@@ -68,15 +68,22 @@ LINEAR = dict(tokens=4, inputs=200, outputs=8, X=FAKE, x_type=1, ldx=200, W=FAKE
     (dict(X=None), -4), (dict(x_type=9), -5), (dict(ldx=199), -6), (dict(W=None), -7), (dict(W=FAKE + 4), -7),
     (dict(ldw=204), -8), (dict(SW=None), -9), (dict(sw_inc=-1), -10), (dict(bias_type=5), -12), (dict(Y=None), -13),
     (dict(ldy=7), -14), (dict(y_type=3), -15), (dict(workspace=None), -16), (dict(workspace=FAKE + 8), -16),
-    (dict(workspace_bytes=4 * (208 + 4) - 1), -17), (dict(tokens=0), 0), (dict(outputs=0), 0),
+    (dict(workspace_bytes=40 * (208 + 4) - 1), -17), (dict(workspace_bytes=-1, tokens=3), -17), (dict(tokens=0), 0), (dict(outputs=0), 0),
 ])
 def test_linear_refusals(change, status):
     refused(int8.hip_int8_linear, int8.hip_int8_linear_status_string, LINEAR, change, status)
 
 
-def test_linear_workspace_holds_codes_and_scales():
-    assert int8.hip_int8_linear_workspace(4, 200) == 4 * (208 + 4) and int8.hip_int8_linear_workspace(0, 5) == 0
+def test_linear_workspace_holds_codes_and_scales_of_all_but_few_tokens():
+    assert int8.hip_int8_linear_workspace(40, 200) == 40 * (208 + 4) and int8.hip_int8_linear_workspace(0, 5) == 0
     assert int8.hip_int8_linear_workspace(2 ** 31 - 1, int8.MAX_K) == (2 ** 31 - 1) * (131072 + 4)
+    for tokens, inputs in ((1, 1), (1, 16384), (16, 1024), (9, 1017), (5, 2048), (3, 4090)):
+        assert int8.hip_int8_linear_workspace(tokens, inputs) == 0
+    for tokens, inputs in ((1, 16385), (17, 8), (16, 1025), (9, 1025), (5, 2049), (3, 4097)):
+        assert int8.hip_int8_linear_workspace(tokens, inputs) > tokens * inputs
+    for tokens in (*range(20), 33):
+        for inputs in (0, 1, 8, 1000, 1017, 1024, 1025, 2048, 4097, 8192, 16377, 16384, 16385):
+            assert int8.hip_int8_linear_workspace(tokens, inputs) == int8._linear_bytes(tokens, inputs)
     for bad in ((-1, 5), (5, -1), (5, int8.MAX_K + 1)):
         with pytest.raises(sgemm.SgemmError):
             int8.hip_int8_linear_workspace(*bad)
@@ -141,6 +148,7 @@ def clip_call(each, function=gradients.hip_gradient_clip, **change):
     ([dict(x=None)], -2), ([dict(x=0x10002)], -2), ([dict(y=None)], -2), ([dict(y=0x20002)], -2), ([dict(rows=-1)], -2),
     ([dict(cols=-1)], -2), ([dict(type=3)], -2), ([dict(type=-1)], -2), ([dict(rows=2, ldx=99)], -2), ([dict(rows=2, ldy=99)], -2),
     ([dict(rows=2, ldx=1 << 41)], -2), ([dict(rows=1 << 41)], -2),
+    ([dict(rows=1 << 30, cols=1 << 30, ldx=1 << 30, ldy=1 << 30)], -2), ([dict(cols=1 << 40)] * 100, -2),
     # what is written overlaps
     ([{}, {}], -2), ([{}, dict(x=0x10000 + 396, y=0x10000 + 396)], -2), ([dict(y=0x10004)], -2),
     ([dict(y=0x20000), dict(x=0x30000, y=0x20000 + 200)], -2), ([dict(y=0x20000), dict(x=0x20000, y=0x40000)], -2),
