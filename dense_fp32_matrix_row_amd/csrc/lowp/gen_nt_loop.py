@@ -613,7 +613,7 @@ LOOPS = [
 ]
 
 
-INT8_LOOPS = [("int8", 8, 4, 2, 4, 2), ("int8", 4, 4, 4, 2, 3)]
+INT8_LOOPS = [("int8", 8, 4, 2, 4, 2), ("int8", 4, 4, 4, 2, 3), ("int8", 4, 4, 2, 2, 4)]
 
 FILES = {"nt_loop.inc": LOOPS, "int8_loop.inc": INT8_LOOPS}
 

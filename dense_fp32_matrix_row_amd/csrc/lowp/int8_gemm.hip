@@ -31,7 +31,7 @@ struct Bias {
       for (int i = 0; i < COUNT; ++i) b[i] = to_float(v.v[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < COUNT; ++i) b[i] = n + i < N ? to_float(from[i]) : 0.0f;
+      for (int i = 0; i < COUNT; ++i) b[i] = n < N - i ? to_float(from[i]) : 0.0f;
     }
   }
   template <int COUNT>
@@ -57,30 +57,40 @@ struct Out {
   int64_t sb_inc;
   Bias bias;
 
-  // D's COUNT neighbours of row m from column n, those inside, of their sums.
-  // (Ends are compared as N - COUNT: n + COUNT passes 2^31 for the widest D.)
+  // What COUNT neighbours of a row from column n take: their scales and biases, those
+  // inside.  (Ends are compared as N - COUNT: n + COUNT passes 2^31 for the widest D.)
   template <int COUNT>
-  __device__ __forceinline__ void row(int m, int n, const float (&v)[COUNT]) const {
-    if (m >= M || n >= N) return;
-    const float s = sa[m * sa_inc];
-    float t[COUNT];
+  struct Columns {
+    float scale[COUNT], bias[COUNT];
+  };
+  template <int COUNT>
+  __device__ __forceinline__ Columns<COUNT> columns(int n) const {
+    Columns<COUNT> c;
     if (sb_inc == 1 && n <= N - COUNT) {
-      const Pack<COUNT, float> p = load_pack<COUNT>(sb + n);
-#pragma unroll
-      for (int i = 0; i < COUNT; ++i) t[i] = p.v[i];
+      __builtin_memcpy(c.scale, sb + n, sizeof(c.scale));
     } else {
 #pragma unroll
-      for (int i = 0; i < COUNT; ++i) t[i] = n + i < N ? sb[(n + i) * sb_inc] : 0.0f;
+      for (int i = 0; i < COUNT; ++i) c.scale[i] = n < N - i ? sb[(n + i) * sb_inc] : 0.0f;
     }
+    if (bias.p && n < N) {
+      bias.get(c.bias, n, N);
+    } else {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) c.bias[i] = 0.0f;
+    }
+    return c;
+  }
+  // D's COUNT neighbours of row m, whose scale is s, from column n, those inside, of their sums.
+  template <int COUNT>
+  __device__ __forceinline__ void row(int m, int n, const float (&v)[COUNT], float s, const Columns<COUNT>& c) const {
+    if (m >= M || n >= N) return;
     Pack<COUNT, O> r;
     if (bias.p) {
-      float b[COUNT];
-      bias.get(b, n, N);
 #pragma unroll
-      for (int i = 0; i < COUNT; ++i) from_float(fmaf(v[i] * s, t[i], b[i]), r.v[i]);
+      for (int i = 0; i < COUNT; ++i) from_float(fmaf(v[i] * s, c.scale[i], c.bias[i]), r.v[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < COUNT; ++i) from_float(v[i] * s * t[i], r.v[i]);
+      for (int i = 0; i < COUNT; ++i) from_float(v[i] * s * c.scale[i], r.v[i]);
     }
     O* const to = d + m * ldd + n;
     if (n <= N - COUNT) {
@@ -88,13 +98,15 @@ struct Out {
     } else {
 #pragma unroll
       for (int i = 0; i < COUNT; ++i)
-        if (n + i < N) to[i] = r.v[i];
+        if (n < N - i) to[i] = r.v[i];
     }
   }
+  __device__ __forceinline__ float row_scale(int m) const { return m < M ? sa[m * sa_inc] : 0.0f; }
   __device__ __forceinline__ void operator()(int m, int n, v4i v) const {
+    if (m >= M || n >= N) return;
     const float x[4] = {static_cast<float>(v[0]), static_cast<float>(v[1]), static_cast<float>(v[2]),
                         static_cast<float>(v[3])};
-    row(m, n, x);
+    row(m, n, x, row_scale(m), columns<4>(n));
   }
   Out from(int m0, int n0, int rows, int cols) const {
     Out o = *this;
@@ -108,8 +120,18 @@ struct Out {
   }
 };
 
-// Large tiles: the K loop in assembly, results by way of LDS as floats, so that
-// whole lines are written.
+// Large tiles.  On one MI355X, kernels alone: 4096^3 61.5 us (2230 TOP/s), 8192^3 434-444
+// (2480-2530; the library's int8 product 63.5 and 441), 2048^3 15 (128 x 128 tiles, 256 of
+// them; 256 x 128 19), 512 x 4096 x 4096 18.7 (27).  A step of 256 x 256 takes 1.53 us,
+// 1.05 without its loads to LDS, 1.39 without its matrix instructions: 64 KB a step and
+// CU, with two stages to be under way in, bound it, and power (the clock at 1.7 GHz,
+// matrix pipes 67 % busy at 8192^3).  32 x 32 x 32 instructions give less at the same
+// power (from registers alone 3500 TOP/s against 4120).
+//
+// The K loop in assembly, results by way of LDS as floats, so that whole
+// lines are written.  A thread stores the same columns of every row, so their scales
+// and biases, and its rows' scales, are read once, all together, behind the loop (read
+// for each eight results they cost a trip to memory each: 4096 x 4096 x 1024 31 -> 27 us).
 template <class L, class O>
 __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, Out<O> out, int tiles_m, int tiles_n) {
   __shared__ alignas(16) uint8_t smem[L::kLds];
@@ -117,6 +139,15 @@ __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, O
   const int m0 = at.tm * L::BM, n0 = at.tn * L::BN;
   nt::v16f acc[L::kAcc];
   nt::loop_sum<L>(smem, A, B, m0, n0, K, acc);
+  constexpr int kRow = L::BN / 8, kStep = L::threads / kRow, kTurns = 64 / kStep;
+  static_assert(L::threads % kRow == 0 && 64 % kStep == 0);
+  const int col = threadIdx.x % kRow * 8, first = threadIdx.x / kRow;
+  float scale[L::BM / 64][kTurns];
+#pragma unroll
+  for (int s = 0; s < L::BM / 64; ++s)
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) scale[s][t] = out.row_scale(m0 + 64 * s + first + t * kStep);
+  const typename Out<O>::template Columns<8> columns = out.template columns<8>(n0 + col);
 #pragma unroll
   for (int i = 0; i < L::kAcc; ++i)
 #pragma unroll
@@ -126,9 +157,15 @@ __global__ __launch_bounds__(L::threads, 2) void k_loop(Side A, Side B, int K, O
   Sheet& sheet = *reinterpret_cast<Sheet*>(smem);
   __syncthreads();  // all wavefronts have left the loop
   nt::loop_sheets<L>(sheet, acc, [&](int top) {
-    sheet.template out<L::threads>(
-        false, [&](int r, int c, const float (&v)[8]) { out.row(m0 + top + r, n0 + c, v); },
-        [](int, int, const float (&)[8]) {});
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      const int r = first + t * kStep;
+      float x[8];
+      __builtin_memcpy(x, &sheet.v[r * Sheet::kLd + col], 32);
+      out.row(m0 + top + r, n0 + col, x, scale[top / 64][t], columns);
+    }
+    __syncthreads();
   });
 }
 
@@ -139,28 +176,45 @@ void launch_loop(const Side& A, const Side& B, int K, const Out<O>& out, unsigne
                      static_cast<int>(tn));
 }
 
+// Which tile takes a product, by estimates of the time in us, whose constants are
+// fitted to 64 sizes from 16 x 4096 x 4096 to 8192^3: of a small tile as SmallCost
+// has it, of a large one a launch, and of each round over the 256 CUs what its tiles'
+// start and end take, which nothing hides, and its steps, a round of few tiles
+// sharing the loads' way with fewer.
 struct Model {
   nt::SmallCost small(int i) const {
     if (i == 0) return {2.8, 0.45, 0.003};
-    if (i == 1) return {2.3, 1.3, 0.0056};
-    return {3.0, 2.2, 0.0135};
+    if (i == 1) return {3.0, 1.25, 0.0046};
+    return {4.0, 2.7, 0.011};
   }
   template <class F>
   void loops(int M, int N, double steps, const F& offer) const {
-    const auto loop = [&](Way w, int bn, double base, double alone, double full) {
-      const int64_t tiles = ceil_div(M, 256) * ceil_div(N, bn), rest = tiles % 256;
-      if (tiles > kMaxWorkItems / 512) return;  // a block a tile: more than a launch takes
-      offer(w, base + steps * (tiles / 256 * full + (rest ? alone + (full - alone) * rest / 256 : 0)));
+    struct Cost {
+      double ends, step;  // of a full round
+      double few_ends, few_step, share;  // of one of less than `share` of the CUs
     };
-    loop(Way::kLoop128, 128, 6.0, 0.65, 0.98);
-    loop(Way::kLoop256, 256, 7.0, 1.0, 1.6);
+    const auto loop = [&](Way w, const Cost& c) {
+      const nt::TileShape t = shape(w);
+      const int64_t tiles = ceil_div(M, t.rows) * ceil_div(N, t.cols), rest = tiles % 256;
+      if (tiles > kMaxWorkItems / t.threads) return;  // a block a tile: more than a launch takes
+      double us = 2.5 + tiles / 256 * (c.ends + c.step * steps);
+      if (rest) {
+        const double more = rest > c.share * 256 ? (rest / 256.0 - c.share) / (1 - c.share) : 0.0;
+        us += c.few_ends + (c.ends - c.few_ends) * more + (c.few_step + (c.step - c.few_step) * more) * steps;
+      }
+      offer(w, us);
+    };
+    loop(Way::kLoopSquare, {6.0, 0.44, 5.5, 0.33, 0.25});
+    loop(Way::kLoop128, {9.2, 0.77, 7.0, 0.56, 0.5});
+    loop(Way::kLoop256, {13.2, 1.43, 11.0, 1.02, 0.0});
   }
-  bool cuts_rows(int t) const { return t == 256; }
+  bool cuts_rows(int) const { return true; }
   constexpr nt::TileShape shape(Way way) const {
     switch (way) {
       case Way::kSmall16: return {16, 16, 512};
       case Way::kSmall32: return {32, 32, 512};
       case Way::kSmall64: return {64, 64, 512};
+      case Way::kLoopSquare: return {128, 128, 256};
       case Way::kLoop128: return {256, 128, 512};
       default: return {256, 256, 512};
     }
@@ -169,12 +223,13 @@ struct Model {
 
 template <class O>
 void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t s) {
+  using LoopSquare = nt::Loop<nt::Kind::kInt8, 4, 4, 2, 2, 4>;
   using Loop128 = nt::Loop<nt::Kind::kInt8, 4, 4, 4, 2, 3>;
   using Loop256 = nt::Loop<nt::Kind::kInt8, 8, 4, 2, 4, 2>;
   using P = nt::Int8;
   constexpr Model model{};
   using nt::is_shape;
-  static_assert(is_shape<Loop128>(model.shape(Way::kLoop128)) && is_shape<Loop256>(model.shape(Way::kLoop256)) &&
+  static_assert(is_shape<LoopSquare>(model.shape(Way::kLoopSquare)) && is_shape<Loop128>(model.shape(Way::kLoop128)) && is_shape<Loop256>(model.shape(Way::kLoop256)) &&
                 is_shape<nt::Direct<P, 1, 1, 8>>(model.shape(Way::kSmall16)) &&
                 is_shape<nt::Direct<P, 2, 2, 8>>(model.shape(Way::kSmall32)) &&
                 is_shape<nt::Direct<P, 4, 4, 8>>(model.shape(Way::kSmall64)));
@@ -186,6 +241,7 @@ void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t 
     const Side a = from_row(A, at.m0, 0), b = from_row(B, at.n0, 0);
     const unsigned blocks = static_cast<unsigned>(blocks_of(model, at));
     if (at.way <= Way::kSmall64) nt::launch_small<P>(at.way, a, b, K, part, at.skip_m, at.skip_n, blocks, s);
+    else if (at.way == Way::kLoopSquare) launch_loop<LoopSquare>(a, b, K, part, blocks, s);
     else if (at.way == Way::kLoop128) launch_loop<Loop128>(a, b, K, part, blocks, s);
     else launch_loop<Loop256>(a, b, K, part, blocks, s);
   }

@@ -150,7 +150,8 @@ __device__ __forceinline__ void loop_sum(uint8_t* smem, const Side& A, const Sid
 #pragma unroll
     for (int w = 0; w < 8; ++w) mask[w] = last_mask(w);
     if constexpr (L::BN == 256) NT_LOOP_RUN(int8_256x256, NT_SUMS_8, NT_NONE, NT_INT8_IN);
-    else NT_LOOP_RUN(int8_256x128, NT_SUMS_4, NT_NONE, NT_INT8_IN);
+    else if constexpr (L::BM == 256) NT_LOOP_RUN(int8_256x128, NT_SUMS_4, NT_NONE, NT_INT8_IN);
+    else NT_LOOP_RUN(int8_128x128, NT_SUMS_4, NT_NONE, NT_INT8_IN);
   } else if constexpr (L::BM == 256) {
     NT_LOOP_RUN(pair_256x256, NT_SUMS_8, NT_NONE, NT_NONE);
   } else if constexpr (L::BM == 192) {

@@ -8,7 +8,7 @@
 namespace sgemm {
 namespace nt {
 
-enum class Way { kSmall16, kSmall32, kSmall64, kLoop128, kLoop256, kRows, kColumns };
+enum class Way { kSmall16, kSmall32, kSmall64, kLoopSquare, kLoop128, kLoop256, kRows, kColumns };
 struct Choice {
   Way way;
   int at;  // kRows, kColumns: where D is cut in two
