@@ -170,24 +170,35 @@ def _same_device(first, *others):
             raise ValueError(f"tensors on {first.device} and {t.device}")
 
 
+_of_torch = None  # torch's current device, and its current stream of a device
+
+
+def _bind_torch():
+    global _of_torch
+    import torch
+    device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _of_torch = device, stream or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _of_torch
+
+
 def current_stream(index: int) -> int:
     """The handle of torch's current stream of a device (what
     torch.cuda.current_stream(index).cuda_stream is, in a twelfth of its 1.1 us
     where torch has the short way)."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    return (_of_torch or _bind_torch())[1](index)
 
 
 def _call(device, function, what, *args):
     """The C function with torch's current stream of the device as its last
     argument, the device current; raises on errors."""
-    import torch
+    present, stream = _of_torch or _bind_torch()
     index = device.index
-    if index != torch.cuda.current_device():
+    if index != present():
+        import torch
         with torch.cuda.device(device):
             return _call(device, function, what, *args)
-    status = function(*args, current_stream(index))
+    status = function(*args, stream(index))
     if status != 0:
         raise _sgemm.SgemmError(status, what(status))
 

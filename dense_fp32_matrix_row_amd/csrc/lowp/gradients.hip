@@ -207,13 +207,13 @@ struct Limit {
   int count;
   const float* given;  // the norm
   float* norm;         // where it goes, or NULL
-  float max_norm, eps;
+  double max_norm, eps;
   bool all_in_place;
 };
 __device__ __forceinline__ void clip_body(const Slot* table, int count, uint32_t chunks, int chunk, const Limit& l) {
   const double norm = l.given ? static_cast<double>(*l.given) : join_parts(l.parts, l.count);
   if (l.norm && blockIdx.x == 0 && threadIdx.x == 0) *l.norm = static_cast<float>(norm);
-  const double all = norm + static_cast<double>(l.eps), most = static_cast<double>(l.max_norm);
+  const double all = norm + l.eps, most = l.max_norm;
   const bool same = all <= most;  // not for a NaN
   Scale f(same ? 1.0 : most / all);
   if (same && l.all_in_place) return;
@@ -399,10 +399,10 @@ int begin(Work& w, int count, const hip_gradient* tensors, bool clip, const floa
   return 0;
 }
 
-int clip(int count, const hip_gradient* tensors, float max_norm, float eps, float* norm, const float* given,
+int clip(int count, const hip_gradient* tensors, double max_norm, double eps, float* norm, const float* given,
          void* workspace, long long workspace_bytes, hipStream_t stream) {
-  if (!(max_norm >= 0.0f)) return -3;
-  if (!(eps >= 0.0f) || eps == std::numeric_limits<float>::infinity()) return -4;
+  if (!(max_norm >= 0.0)) return -3;
+  if (!(eps >= 0.0) || eps == std::numeric_limits<double>::infinity()) return -4;
   Work w;
   const int status = begin(w, count, tensors, true, given ? given : norm, workspace, workspace_bytes, 6, stream);
   if (status != 0) return status;
@@ -450,12 +450,12 @@ int hip_gradient_norm(int count, const hip_gradient* tensors, float* norm, void*
   });
 }
 
-int hip_gradient_clip(int count, const hip_gradient* tensors, float max_norm, float eps, float* norm, void* workspace,
+int hip_gradient_clip(int count, const hip_gradient* tensors, double max_norm, double eps, float* norm, void* workspace,
                       long long workspace_bytes, hipStream_t stream) {
   return guarded([&] { return clip(count, tensors, max_norm, eps, norm, nullptr, workspace, workspace_bytes, stream); });
 }
 
-int hip_gradient_clip_by(int count, const hip_gradient* tensors, float max_norm, float eps, const float* norm,
+int hip_gradient_clip_by(int count, const hip_gradient* tensors, double max_norm, double eps, const float* norm,
                          void* workspace, long long workspace_bytes, hipStream_t stream) {
   return guarded([&] {
     if (norm == nullptr) return -5;

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 
 from . import sgemm as _sgemm
 from .blockfp8 import _call, _types, written
@@ -39,12 +40,12 @@ def load():
     global _bound
     lib = _sgemm.load()
     if lib is not _bound:
-        i32, i64, f32, vp = ctypes.c_int, ctypes.c_longlong, ctypes.c_float, ctypes.c_void_p
+        i32, i64, f64, vp = ctypes.c_int, ctypes.c_longlong, ctypes.c_double, ctypes.c_void_p
         lib.hip_gradient_norm.restype = i32
         lib.hip_gradient_norm.argtypes = [i32, vp, vp, vp, i64, vp]
         for name in ("hip_gradient_clip", "hip_gradient_clip_by"):
             getattr(lib, name).restype = i32
-            getattr(lib, name).argtypes = [i32, vp, f32, f32, vp, vp, i64, vp]
+            getattr(lib, name).argtypes = [i32, vp, f64, f64, vp, vp, i64, vp]
         lib.hip_gradient_workspace.restype = i32
         lib.hip_gradient_workspace.argtypes = [i32, ctypes.POINTER(i64)]
         for name in EXPORTS[-2:]:
@@ -110,40 +111,42 @@ def _layout(t, what):
 
 def _describe(tensors, outs):
     """(device, an array with seven numbers a tensor, as hip_gradient has them)."""
+    from torch import Tensor
     device = tensors[0].device
     index = tensors[0].get_device()
     if index < 0:
         raise TypeError("gradients must live on the GPU")
     types = _types()
-    flat = []
-    add = flat.extend
-    for t, o in zip(tensors, tensors if outs is None else outs):
-        kind = types.get(t.dtype)
-        if kind is None:
-            raise TypeError(f"gradients are float32, bfloat16 or float16, not {t.dtype}")
-        if t.get_device() != index:
-            raise ValueError(f"tensors on {device} and {t.device}")
-        if o is t:
-            x = t.data_ptr()
-            if t.is_contiguous():
-                add((x, x, 1, t.numel(), 0, 0, kind))
-            elif t.numel():
-                rows, cols, ld = _layout(t, "a gradient")
-                add((x, x, rows, cols, ld, ld, kind))
-            else:
-                add((x, x, 0, 0, 0, 0, kind))
-            continue
-        if o.shape != t.shape or o.dtype != t.dtype:
-            raise ValueError(f"out is {tuple(o.shape)} {o.dtype}, not {tuple(t.shape)} {t.dtype}")
-        if o.get_device() != index:
-            raise ValueError(f"tensors on {device} and {o.device}")
-        if t.is_contiguous() and o.is_contiguous():
-            add((t.data_ptr(), o.data_ptr(), 1, t.numel(), 0, 0, kind))
-        elif t.numel():
-            add((t.data_ptr(), o.data_ptr(), *_pair(t, o), kind))
-        else:
-            add((0, 0, 0, 0, 0, 0, kind))
-    return device, array.array("q", flat)
+    kinds = [types.get(t.dtype) for t in tensors]
+    if None in kinds:
+        raise TypeError(f"gradients are float32, bfloat16 or float16, not {tensors[kinds.index(None)].dtype}")
+    places = list(map(Tensor.get_device, tensors))
+    if places.count(index) != len(places):
+        raise ValueError(f"tensors on {device} and {next(t for t, at in zip(tensors, places) if at != index).device}")
+    if outs is not None:
+        for t, o in zip(tensors, outs):
+            if o.shape != t.shape or o.dtype != t.dtype:
+                raise ValueError(f"out is {tuple(o.shape)} {o.dtype}, not {tuple(t.shape)} {t.dtype}")
+            if o.get_device() != index:
+                raise ValueError(f"tensors on {device} and {o.device}")
+    n = len(tensors)
+    x = array.array("q", map(Tensor.data_ptr, tensors))
+    out = array.array("q", bytes(56 * n))
+    out[0::7] = x
+    out[1::7] = x if outs is None else array.array("q", map(Tensor.data_ptr, outs))
+    out[2::7] = array.array("q", [1]) * n
+    out[3::7] = array.array("q", map(Tensor.numel, tensors))
+    out[6::7] = array.array("q", kinds)
+    dense = list(map(Tensor.is_contiguous, tensors))
+    if outs is not None:
+        dense = list(map(operator.and_, dense, map(Tensor.is_contiguous, outs)))
+    if False in dense:  # rows, columns and strides of the others
+        for i in (i for i, flat in enumerate(dense) if not flat):
+            t, o = tensors[i], None if outs is None else outs[i]
+            if t.numel():
+                rows, cols, ldx, ldy = _pair(t, t if o is None else o)
+                out[7 * i + 2:7 * i + 6] = array.array("q", (rows, cols, ldx, ldy))
+    return device, out
 
 
 def _pair(t, o):
@@ -167,11 +170,16 @@ def _pair(t, o):
     return t.numel() // cols, cols, *strides
 
 
+def _workspace_bytes(count) -> int:
+    """hip_gradient_workspace without a call."""
+    return 16384 + (64 * count if count > 60 else 0)
+
+
 def _run(function, what, device, described, *args):
     """A call with the tensors, a workspace and torch's current stream."""
     import torch
     count = len(described) // 7
-    bytes = hip_gradient_workspace(count)
+    bytes = _workspace_bytes(count)
     workspace = torch.empty(bytes, dtype=torch.uint8, device=device)
     _call(device, function, what, count, described.buffer_info()[0], *args, workspace.data_ptr(), bytes)
 

@@ -158,14 +158,20 @@ def quantize(x) -> Int8:
     return Int8(q, s)
 
 
+_kinds = None  # int8, float32 (torch is imported on first use)
+
+
 def _operand(name, o):
     """(rows, K, the C function's arguments) of a quantised matrix."""
-    import torch
+    global _kinds
+    if _kinds is None:
+        import torch
+        _kinds = torch.int8, torch.float32
     q, s = o.q, o.s
     rows, K, ld = _matrix(name, q)
-    if q.dtype != torch.int8:
+    if q.dtype != _kinds[0]:
         raise TypeError(f"{name}'s codes are int8, not {q.dtype}")
-    if s.dtype != torch.float32:
+    if s.dtype != _kinds[1]:
         raise TypeError(f"{name}'s scales are float32, not {s.dtype}")
     if not s.is_cuda:
         raise TypeError(f"{name}'s scales must live on the GPU")

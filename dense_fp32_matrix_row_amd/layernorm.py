@@ -152,6 +152,13 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None):
     return _forward(x, weight, bias, eps, out, True)
 
 
+def _workspace_bytes(rows, cols) -> int:
+    """At least hip_layernorm_backward_workspace, without a call: a part a row, 768 at most."""
+    if cols > 16384:
+        return hip_layernorm_backward_workspace(rows, cols)
+    return min(rows, 768) * 8 * cols
+
+
 def layer_norm_backward(dy, x, stats, weight=None, dw=None, db=None, out=None):
     """The gradients of layer_norm_forward: dx (of x's type, a new tensor or in `out`,
     which may be dy or x), dw and db.
@@ -174,14 +181,14 @@ def layer_norm_backward(dy, x, stats, weight=None, dw=None, db=None, out=None):
     device = x.device
     add = any(given)
     if weight is not None and not add:
-        dw, db = torch.empty((2, cols), dtype=torch.float32, device=device).unbind(0)
+        dw, db = (torch.empty(cols, dtype=torch.float32, device=device) for _ in range(2))
         if not cols:
             return torch.empty_like(x), dw, db
     if out is None:
         dx, lddx = torch.empty((rows, cols), dtype=x.dtype, device=device), max(cols, 1)
     else:
         dx, lddx = out, _like("out", out, x)
-    bytes = hip_layernorm_backward_workspace(rows, cols) if dw is not None or db is not None else 0
+    bytes = _workspace_bytes(rows, cols) if dw is not None or db is not None else 0
     workspace = torch.empty(bytes, dtype=torch.uint8, device=device) if bytes else None
     _call(device, load().hip_layernorm_backward, hip_layernorm_backward_status_string, rows, cols, kind, dy.data_ptr(), lddy,
           x.data_ptr(), ldx, stats.data_ptr(), w, w_type, dx.data_ptr(), lddx,

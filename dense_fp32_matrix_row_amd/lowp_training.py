@@ -1,9 +1,11 @@
 """A small training loop over the low-precision operators, as they are used
 together: linear layers whose products run on block-scaled 8-bit operands,
 fp32 master weights and gradients, and a momentum that is orthogonalised before
-it is applied.
+it is applied; on request layer norms before the layers, gradients clipped by
+their global norm, and the trained weights served as 8-bit integers.
 
     python -m dense_fp32_matrix_row_amd.lowp_training --steps 60
+    python -m dense_fp32_matrix_row_amd.lowp_training --steps 60 --norm --clip 0.1 --serve int8
 
 fits a two-layer network to a fixed random one and prints the loss as it falls,
 then runs the trained network on single tokens.
@@ -14,7 +16,7 @@ from __future__ import annotations
 import argparse
 import math
 
-from . import blockfp8, orthogonal
+from . import blockfp8, gradients, int8, layernorm, orthogonal
 
 
 class Layer:
@@ -42,41 +44,99 @@ class Layer:
         self.quantize()
 
 
-class Network:
-    """y = W2 relu(W1 x) for rows of tokens."""
+class Norm:
+    """A layer norm's weight and bias, and their gradients."""
 
-    def __init__(self, inputs, hidden, outputs, seed=0, scale=None, device="cuda"):
+    def __init__(self, width, device):
+        import torch
+        self.weight, self.bias = torch.ones(width, device=device), torch.zeros(width, device=device)
+        self.weight_gradient, self.bias_gradient = torch.zeros_like(self.weight), torch.zeros_like(self.bias)
+
+    def update(self, rate):
+        for value, gradient in ((self.weight, self.weight_gradient), (self.bias, self.bias_gradient)):
+            value.sub_(gradient, alpha=rate)
+            gradient.zero_()
+
+
+class Network:
+    """y = W2 relu(W1 x) for rows of tokens; with `norm` y = W2 n2(relu(W1 n1(x))), n1
+    and n2 layer norms."""
+
+    def __init__(self, inputs, hidden, outputs, seed=0, scale=None, device="cuda", norm=False):
         import torch
         g = torch.Generator(device=device).manual_seed(seed)
         make = lambda o, i: torch.randn(o, i, generator=g, device=device) / math.sqrt(i)  # noqa: E731
         scale = scale or torch.float32
         self.layers = Layer(make(hidden, inputs), scale), Layer(make(outputs, hidden), scale)
+        self.norms = (Norm(inputs, device), Norm(hidden, device)) if norm else ()
 
     def forward(self, x):
         """The outputs, and what backward needs."""
         one, two = self.layers
-        h, xt = blockfp8.linear_forward(x, one.w)
-        y, ht = blockfp8.linear_forward(h.relu_(), two.w)
-        return y, (xt, h, ht)
+        if not self.norms:
+            h, xt = blockfp8.linear_forward(x, one.w)
+            y, ht = blockfp8.linear_forward(h.relu_(), two.w)
+            return y, (xt, h, ht)
+        n1, n2 = self.norms
+        v, xs = layernorm.layer_norm_forward(x, n1.weight, n1.bias)
+        h, vt = blockfp8.linear_forward(v, one.w)
+        u, hs = layernorm.layer_norm_forward(h.relu_(), n2.weight, n2.bias)
+        y, ut = blockfp8.linear_forward(u, two.w)
+        return y, (vt, h, ut, x, xs, hs)
 
     def backward(self, dy, saved):
-        """Adds the weights' gradients to Layer.gradient."""
-        xt, h, ht = saved
+        """Adds the weights' gradients to Layer.gradient, and the norms' to theirs."""
+        xt, h, ht, *rest = saved
         one, two = self.layers
         dh, _ = blockfp8.linear_backward(dy, ht, two.wt, dw=two.gradient)
-        blockfp8.linear_backward(dh * (h > 0), xt, one.wt, dw=one.gradient)
+        if not rest:
+            blockfp8.linear_backward(dh * (h > 0), xt, one.wt, dw=one.gradient)
+            return
+        x, xs, hs = rest
+        n1, n2 = self.norms
+        dh, _, _ = layernorm.layer_norm_backward(dh, h, hs, n2.weight, dw=n2.weight_gradient, db=n2.bias_gradient)
+        dv, _ = blockfp8.linear_backward(dh * (h > 0), xt, one.wt, dw=one.gradient)
+        layernorm.layer_norm_backward(dv, x, xs, n1.weight, dw=n1.weight_gradient, db=n1.bias_gradient)
+
+    def gradients(self):
+        """All of them, in one list."""
+        return [layer.gradient for layer in self.layers] + [g for n in self.norms for g in (n.weight_gradient, n.bias_gradient)]
 
     def infer(self, x):
         """The outputs alone, for any number of tokens."""
-        one, two = self.layers
-        h = blockfp8.gemm(blockfp8.quantize(x, 1, one.scale), one.w, out_dtype=x.dtype)
-        return blockfp8.gemm(blockfp8.quantize(h.relu_(), 1, two.scale), two.w, out_dtype=x.dtype)
+        for k, layer in enumerate(self.layers):
+            x = x.relu_() if k else x
+            if self.norms:
+                x = layernorm.layer_norm(x, self.norms[k].weight, self.norms[k].bias)
+            x = blockfp8.gemm(blockfp8.quantize(x, 1, layer.scale), layer.w, out_dtype=x.dtype)
+        return x
+
+    def serve(self):
+        """The network with its weights as 8-bit integers, a scale for each output."""
+        return Served([int8.quantize(layer.master) for layer in self.layers], [(n.weight, n.bias) for n in self.norms])
 
 
-def train(steps=60, tokens=512, inputs=256, hidden=384, outputs=130, rate=0.05, seed=0, scale=None):
-    """Trains a Network on a fixed random one's outputs; returns it and the losses."""
+class Served:
+    """A trained network's weights as they are served, and its norms' parameters."""
+
+    def __init__(self, weights, norms):
+        self.weights, self.norms = weights, norms
+
+    def infer(self, x):
+        """The outputs for any number of tokens, each quantised by itself."""
+        for k, w in enumerate(self.weights):
+            x = x.relu_() if k else x
+            if self.norms:
+                x = layernorm.layer_norm(x, *self.norms[k])
+            x = int8.linear(x, w)
+        return x
+
+
+def train(steps=60, tokens=512, inputs=256, hidden=384, outputs=130, rate=0.05, seed=0, scale=None, norm=False, clip=None):
+    """Trains a Network on a fixed random one's outputs; returns it and the losses.
+    `clip`: the most that the gradients' global norm is let to be."""
     import torch
-    network = Network(inputs, hidden, outputs, seed, scale)
+    network = Network(inputs, hidden, outputs, seed, scale, norm=norm)
     g = torch.Generator(device="cuda").manual_seed(seed + 1)
     randn = lambda *shape: torch.randn(*shape, generator=g, device="cuda")  # noqa: E731
     target = randn(outputs, inputs) / math.sqrt(inputs)
@@ -88,8 +148,11 @@ def train(steps=60, tokens=512, inputs=256, hidden=384, outputs=130, rate=0.05, 
         error = y.float() - want
         losses.append(error.square().mean())
         network.backward((error * (2 / error.numel())).bfloat16(), saved)
-        for layer in network.layers:
-            layer.update(rate * (1 - step / steps))
+        if clip is not None:
+            grads = network.gradients()
+            gradients.clip_grad_norm(grads, clip, out=grads)
+        for part in (*network.layers, *network.norms):
+            part.update(rate * (1 - step / steps))
     return network, [float(loss) for loss in losses]
 
 
@@ -98,14 +161,19 @@ def main(argv=None):
     parser = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     parser.add_argument("--steps", type=int, default=60)
     parser.add_argument("--scale", choices=("f32", "e8m0"), default="f32", help="the type of the blocks' scales")
+    parser.add_argument("--norm", action="store_true", help="a layer norm before each layer")
+    parser.add_argument("--clip", type=float, help="clip the gradients by their global norm")
+    parser.add_argument("--serve", choices=("fp8", "int8"), default="fp8", help="what the trained network's products run on")
     args = parser.parse_args(argv)
-    network, losses = train(args.steps, scale=torch.float32 if args.scale == "f32" else torch.float8_e8m0fnu)
+    network, losses = train(args.steps, scale=torch.float32 if args.scale == "f32" else torch.float8_e8m0fnu, norm=args.norm,
+                            clip=args.clip)
     for step in range(0, len(losses), max(len(losses) // 10, 1)):
         print(f"step {step:4d}  loss {losses[step]:.5f}")
     print(f"step {len(losses) - 1:4d}  loss {losses[-1]:.5f}")
     x = torch.randn(8, 256, device="cuda").bfloat16()
-    together = network.infer(x)
-    apart = torch.cat([network.infer(x[i:i + 1]) for i in range(8)])
+    served = network.serve() if args.serve == "int8" else network
+    together = served.infer(x)
+    apart = torch.cat([served.infer(x[i:i + 1]) for i in range(8)])
     print(f"eight tokens at once and one by one differ by {float((together.float() - apart.float()).abs().max()):.2e}")
 
 

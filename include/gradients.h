@@ -74,7 +74,7 @@ int hip_gradient_norm(int count, const hip_gradient *tensors, float *norm, void 
  * Arguments are numbered from 1: count, tensors, max_norm, eps, norm, workspace,
  * workspace_bytes, stream.
  */
-int hip_gradient_clip(int count, const hip_gradient *tensors, float max_norm, float eps, float *norm, void *workspace,
+int hip_gradient_clip(int count, const hip_gradient *tensors, double max_norm, double eps, float *norm, void *workspace,
                       long long workspace_bytes, hipStream_t stream);
 
 /*
@@ -84,7 +84,7 @@ int hip_gradient_clip(int count, const hip_gradient *tensors, float max_norm, fl
  * Arguments are numbered from 1: count, tensors, max_norm, eps, norm, workspace,
  * workspace_bytes, stream.
  */
-int hip_gradient_clip_by(int count, const hip_gradient *tensors, float max_norm, float eps, const float *norm,
+int hip_gradient_clip_by(int count, const hip_gradient *tensors, double max_norm, double eps, const float *norm,
                          void *workspace, long long workspace_bytes, hipStream_t stream);
 
 const char *hip_gradient_norm_status_string(int status);

@@ -121,6 +121,10 @@ def test_layernorm_workspace():
         one = layernorm.hip_layernorm_backward_workspace(1, cols)
         many = layernorm.hip_layernorm_backward_workspace(2 ** 31 - 1, cols)
         assert one == row and many % row == 0 and row <= many <= 2048 * row
+    for rows in (0, 1, 2, 31, 32, 33, 500, 767, 768, 769, 5000, 100_000, 2 ** 31 - 1):
+        for cols in (1, 100, 128, 129, 256, 257, 512, 1000, 2000, 4096, 4097, 8192, 16384, 16385, 100_000):
+            need, has = layernorm.hip_layernorm_backward_workspace(rows, cols), layernorm._workspace_bytes(rows, cols)
+            assert need <= has <= max(768 * 8 * cols, need)
     assert layernorm.hip_layernorm_backward_workspace(0, 5) == 0 == layernorm.hip_layernorm_backward_workspace(5, 0)
     for bad in ((-1, 5), (5, -1)):
         with pytest.raises(sgemm.SgemmError):
@@ -179,6 +183,14 @@ def test_norm_refusals(change, status):
     usual = dict(count=1, tensors=tensors({}), norm=0x4000, workspace=FAKE, workspace_bytes=1 << 20)
     assert gradients.hip_gradient_norm(*{**usual, **change}.values(), stream=0) == status
     assert "unknown" not in gradients.hip_gradient_norm_status_string(status)
+
+
+def test_gradient_workspace():
+    for count in (0, 1, 59, 60, 61, 200, gradients.MAX_COUNT):
+        assert gradients.hip_gradient_workspace(count) == gradients._workspace_bytes(count)
+    for count in (-1, gradients.MAX_COUNT + 1):
+        with pytest.raises(sgemm.SgemmError):
+            gradients.hip_gradient_workspace(count)
 
 
 def test_gradient_struct_is_the_headers():
