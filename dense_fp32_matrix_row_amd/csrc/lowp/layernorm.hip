@@ -277,6 +277,85 @@ __global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 
   }
 }
 
+// Few rows: dx a row of threads each, as above, and beside them in the same launch dw
+// and db, a block for 64 columns, whose wavefronts take every so many-th row with four
+// loads under way: no parts, no second launch to join them (16 x 1000 bf16 6.9 -> 3.2 us,
+// 128 x 4000 9.6 -> 5.0, 256 x 1000 7.7 -> 6.5; 512 x 1000 would take 14.0 against 8.1).  x
+// and dy are read twice, so where dx is written over one of them there are two
+// launches, the columns' first: the same sums.
+template <class S, class X, class W>
+__global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 4) void k_few(
+    const X* dy, int64_t lddy, const X* x, int64_t ldx, const float* __restrict__ stats, const W* __restrict__ w, X* dx,
+    int64_t lddx, float* dw, float* db, int accumulate, int rows, int cols, int row_blocks) {
+  constexpr int kWaves = S::threads / 64;
+  __shared__ float meet[kWaves][2], all[2][kWaves][64];
+  const float n = static_cast<float>(cols);
+  if (static_cast<int>(blockIdx.x) < row_blocks) {
+    const int lane = threadIdx.x % S::LANES, row = blockIdx.x * S::rows + threadIdx.x / S::LANES, from = min(row, rows - 1);
+    Share<S, X> xv, gv;
+    xv.load(x + from * ldx, lane, cols);
+    gv.load(dy + from * lddy, lane, cols);
+    const Stats s = load_stats(stats, from, rows);
+    float wv[S::COUNT][8], sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) {
+      load_param(wv[c], w, 1.0f, (c * S::LANES + lane) * 8, cols);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float g = to_float(gv.v[c].v[i]) * wv[c][i];
+        sum[0] += g;
+        sum[1] = fmaf(g, normalised(to_float(xv.v[c].v[i]), s), sum[1]);
+      }
+    }
+    join_row<S>(sum, meet, Sum{});
+    const float c1 = sum[0] / n, c2 = sum[1] / n;
+    if (row >= rows) return;
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) {
+      Pack<8, X> r;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float g = fmaf(to_float(gv.v[c].v[i]), wv[c][i], -c1), h = normalised(to_float(xv.v[c].v[i]), s);
+        from_float((g - h * c2) * s.rstd, r.v[i]);
+      }
+      store_row8(dx + row * lddx, (c * S::LANES + lane) * 8, cols, r);
+    }
+    return;
+  }
+  constexpr int kLoads = 4;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, col = (blockIdx.x - row_blocks) * 64 + lane;
+  const int at = min(col, cols - 1);
+  float pw = 0.0f, pb = 0.0f;
+  for (int r0 = wave; r0 < rows; r0 += kLoads * kWaves) {
+    X xv[kLoads], gv[kLoads];
+    Stats s[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int row = min(r0 + u * kWaves, rows - 1);
+      xv[u] = x[row * ldx + at];
+      gv[u] = dy[row * lddy + at];
+      s[u] = load_stats(stats, row, rows);
+    }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u)
+      if (r0 + u * kWaves < rows) {
+        const float t = to_float(gv[u]);
+        pw = fmaf(t, normalised(to_float(xv[u]), s[u]), pw);
+        pb += t;
+      }
+  }
+  all[0][wave][lane] = pw;
+  all[1][wave][lane] = pb;
+  __syncthreads();
+  if (wave > 1 || col >= cols) return;
+  float* const out = wave ? db : dw;
+  if (!out) return;
+  float v = all[wave][0][lane];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) v += all[wave][i][lane];
+  out[col] = accumulate ? out[col] + v : v;
+}
+
 // Rows longer than registers hold: first dw and db (dx may be written over dy), a
 // block for 2048 columns of a share of the rows; then dx, a block a row, read twice.
 template <class X>
@@ -399,8 +478,13 @@ void with_backward_shape(int cols, const F& f) {
   else f(RowShape<1024, 2>{});
 }
 
-// Blocks of the backward pass, each with a part of dw and db in the workspace.
+constexpr int kFewRows = HIP_LAYERNORM_FEW;
+bool few_rows(int rows, int cols) { return rows <= kFewRows && cols <= kRowWidth; }
+
+// Blocks of the backward pass, each with a part of dw and db in the workspace; few rows
+// have none.
 int64_t parts_of(int rows, int cols) {
+  if (few_rows(rows, cols)) return 0;
   if (cols > kRowWidth) {
     const int64_t share = 2048 / ceil_div(cols, 2048), most = share < 1 ? 1 : share < 64 ? share : 64;
     return rows < most ? rows : most;
@@ -436,6 +520,8 @@ struct Backward {
   const void* w;
   void* dx;
   int64_t lddx;
+  float *dw, *db;
+  int accumulate;
   float* parts;
   int count;
 };
@@ -477,6 +563,22 @@ void launch(const Backward& a, hipStream_t stream) {
   }
   with_backward_shape(a.cols, [&](auto shape) {
     using S = decltype(shape);
+    if (few_rows(a.rows, a.cols)) {
+      const int rows = dx ? static_cast<int>(ceil_div(a.rows, S::rows)) : 0;
+      const int columns = a.dw || a.db ? static_cast<int>(ceil_div(a.cols, 64)) : 0;
+      const auto go = [&](int row_blocks, int blocks) {
+        if (blocks > 0)
+          hipLaunchKernelGGL((k_few<S, X, W>), dim3(blocks), dim3(S::threads), 0, stream, dy, a.lddy, x, a.ldx, a.stats, w,
+                             dx, a.lddx, a.dw, a.db, a.accumulate, a.rows, a.cols, row_blocks);
+      };
+      if (dx != dy && dx != x) {
+        go(rows, rows + columns);
+      } else {
+        go(0, columns);
+        go(rows, rows);
+      }
+      return;
+    }
     hipLaunchKernelGGL((k_backward<S, X, W>), dim3(static_cast<unsigned>(a.count)), dim3(S::threads), 0, stream, dy,
                        a.lddy, x, a.ldx, a.stats, w, dx, a.lddx, a.parts, a.rows, a.cols);
   });
@@ -544,18 +646,18 @@ int hip_layernorm_backward(int rows, int cols, int type, const void* DY, int ldd
   if (DX != nullptr && lddx < (cols > 1 ? cols : 1)) return -12;
   if (accumulate != 0 && accumulate != 1) return -15;
   const int64_t count = some ? parts_of(rows, cols) : 0;
-  if (some && params && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)) return -16;
+  if (some && params && count > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)) return -16;
   if (some && params && workspace_bytes < count * 2 * cols * 4) return -17;
   if (cols == 0 || (!params && (rows == 0 || DX == nullptr))) return 0;
   if (rows > 0) {
     launch_type(type, w != nullptr ? w_type : HIP_LAYERNORM_F32,
-                Backward{rows, cols, DY, lddy, X, ldx, stats, w, DX, lddx, params ? static_cast<float*>(workspace) : nullptr,
-                         static_cast<int>(count)},
+                Backward{rows, cols, DY, lddy, X, ldx, stats, w, DX, lddx, dw, db, accumulate,
+                         params ? static_cast<float*>(workspace) : nullptr, static_cast<int>(count)},
                 stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return static_cast<int>(e);
   }
-  if (params)
+  if (params && (rows == 0 || count > 0))
     hipLaunchKernelGGL(k_join, dim3(static_cast<unsigned>(min(ceil_div(cols, 32), kJoinBlocks)), 2), dim3(1024), 0, stream,
                        static_cast<const float*>(workspace), static_cast<int>(count), dw, db, cols, accumulate);
   return static_cast<int>(hipGetLastError());

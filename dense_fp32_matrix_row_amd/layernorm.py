@@ -20,6 +20,7 @@ EXPORTS = ("hip_layernorm_forward", "hip_layernorm_backward", "hip_layernorm_bac
            "hip_layernorm_forward_status_string", "hip_layernorm_backward_status_string")
 
 F32, BF16, F16 = 0, 1, 2
+FEW = 256  # HIP_LAYERNORM_FEW
 
 _bound = None
 
@@ -153,7 +154,10 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None):
 
 
 def _workspace_bytes(rows, cols) -> int:
-    """At least hip_layernorm_backward_workspace, without a call: a part a row, 768 at most."""
+    """At least hip_layernorm_backward_workspace, without a call: a part a row, 768 at most,
+    none of few rows."""
+    if rows <= FEW and cols <= 16384:
+        return 0
     if cols > 16384:
         return hip_layernorm_backward_workspace(rows, cols)
     return min(rows, 768) * 8 * cols

@@ -34,6 +34,8 @@ extern "C" {
 #define HIP_LAYERNORM_F16 2
 
 #define HIP_LAYERNORM_ROW 16384
+/* the backward pass of at most so many rows of at most HIP_LAYERNORM_ROW needs no workspace */
+#define HIP_LAYERNORM_FEW 256
 
 /*
  * Y <- the layer norm of X's rows.

@@ -48,7 +48,7 @@ def test_against_the_formulas(cols, kind):
         check(x, dy, w, b, TYPES[kind])
 
 
-@pytest.mark.parametrize("rows", (500, 2300, 5001))
+@pytest.mark.parametrize("rows", (256, 257, 500, 2300, 5001))
 @pytest.mark.parametrize("cols", (64, 777, 1500, 3001, 5000, 9000, 17000))
 def test_many_rows_share_the_blocks(rows, cols):
     if rows * cols > 3e7:
@@ -118,11 +118,12 @@ def test_infinities_and_nans_stay_in_their_row(cols):
     assert torch.isfinite(dx[others]).all() and torch.isfinite(db[2:]).all() and db[1] == float("inf")
 
 
+@pytest.mark.parametrize("rows", (30, 300))
 @pytest.mark.parametrize("cols", (297, 1501, 3001, 17001))
 @pytest.mark.parametrize("kind", TYPES)
-def test_strided_rows_in_place_and_nothing_outside_is_written(kind, cols):
+def test_strided_rows_in_place_and_nothing_outside_is_written(kind, cols, rows):
     kind = TYPES[kind]
-    big = lambda seed: ref.values(30, cols + 37, kind, seed)  # noqa: E731
+    big = lambda seed: ref.values(rows, cols + 37, kind, seed)  # noqa: E731
     x, dy = big(15), big(16)
     inside = slice(3, 3 + cols)  # odd base and row stride
     w, b = params(cols, kind, 17)

@@ -101,7 +101,7 @@ def test_layernorm_forward_refusals(change, status):
     refused(layernorm.hip_layernorm_forward, layernorm.hip_layernorm_forward_status_string, FORWARD, change, status)
 
 
-BACKWARD = dict(rows=4, cols=8, type=0, DY=FAKE, lddy=8, X=FAKE, ldx=8, stats=FAKE, w=FAKE, w_type=0, DX=FAKE, lddx=8, dw=FAKE,
+BACKWARD = dict(rows=400, cols=8, type=0, DY=FAKE, lddy=8, X=FAKE, ldx=8, stats=FAKE, w=FAKE, w_type=0, DX=FAKE, lddx=8, dw=FAKE,
                 db=FAKE, accumulate=0, workspace=FAKE, workspace_bytes=1 << 20)
 
 
@@ -118,10 +118,11 @@ def test_layernorm_backward_refusals(change, status):
 def test_layernorm_workspace():
     for cols in (1, 512, 513, 4096, 16384, 16385, 2 ** 31 - 1):
         row = 2 * 4 * cols
-        one = layernorm.hip_layernorm_backward_workspace(1, cols)
+        few = [layernorm.hip_layernorm_backward_workspace(n, cols) for n in (1, layernorm.FEW)]
+        assert few[0] == 0 == few[1] if cols <= 16384 else few[0] == row
         many = layernorm.hip_layernorm_backward_workspace(2 ** 31 - 1, cols)
-        assert one == row and many % row == 0 and row <= many <= 2048 * row
-    for rows in (0, 1, 2, 31, 32, 33, 500, 767, 768, 769, 5000, 100_000, 2 ** 31 - 1):
+        assert many % row == 0 and row <= many <= 2048 * row
+    for rows in (0, 1, 2, 31, 32, 33, 255, 256, 257, 500, 767, 768, 769, 5000, 100_000, 2 ** 31 - 1):
         for cols in (1, 100, 128, 129, 256, 257, 512, 1000, 2000, 4096, 4097, 8192, 16384, 16385, 100_000):
             need, has = layernorm.hip_layernorm_backward_workspace(rows, cols), layernorm._workspace_bytes(rows, cols)
             assert need <= has <= max(768 * 8 * cols, need)
