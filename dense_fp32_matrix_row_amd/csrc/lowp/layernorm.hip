@@ -644,6 +644,10 @@ int hip_layernorm_backward(int rows, int cols, int type, const void* DY, int ldd
   if (some && stats == nullptr) return -8;
   if (w != nullptr && bad_param(w_type, type)) return -10;
   if (DX != nullptr && lddx < (cols > 1 ? cols : 1)) return -12;
+  if (dw != nullptr && db != nullptr) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(dw), b = reinterpret_cast<uintptr_t>(db);
+    if ((a < b ? b - a : a - b) < static_cast<uintptr_t>(cols) * 4) return -14;
+  }
   if (accumulate != 0 && accumulate != 1) return -15;
   const int64_t count = some ? parts_of(rows, cols) : 0;
   if (some && params && count > 0 && (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)) return -16;
@@ -694,6 +698,7 @@ const char* hip_layernorm_backward_status_string(int status) {
     case -8: return "argument 8 (stats) is NULL";
     case -10: return "argument 10 (w_type) is neither HIP_LAYERNORM_F32 nor the type of X";
     case -12: return "argument 12 (lddx) is smaller than max(1, cols)";
+    case -14: return "argument 14 (db) overlaps argument 13 (dw)";
     case -15: return "argument 15 (accumulate) is not 0 or 1";
     case -16: return "argument 16 (workspace) is NULL or not 16-byte aligned";
     case -17: return "argument 17 (workspace_bytes) is less than hip_layernorm_backward_workspace says";

@@ -112,6 +112,8 @@ def _layout(t, what):
 def _describe(tensors, outs):
     """(device, an array with seven numbers a tensor, as hip_gradient has them)."""
     from torch import Tensor
+    if any(t is None for t in tensors):  # of a parameter that has none
+        raise TypeError("a gradient is None")
     device = tensors[0].device
     index = tensors[0].get_device()
     if index < 0:

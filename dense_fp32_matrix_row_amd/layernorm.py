@@ -167,8 +167,9 @@ def layer_norm_backward(dy, x, stats, weight=None, dw=None, db=None, out=None):
     """The gradients of layer_norm_forward: dx (of x's type, a new tensor or in `out`,
     which may be dy or x), dw and db.
 
-    dw and db are float32, new tensors, or added to the tensors given, in place.
-    Without a weight, and without dw and db to add to, both are None."""
+    dw and db are float32, new tensors, or added to the tensors given, in place (which
+    must not overlap each other, nor the weight).  Without a weight, and without dw and
+    db to add to, both are None."""
     import torch
     rows, cols, ldx, kind = _tokens("x", x)
     lddy = _like("dy", dy, x)

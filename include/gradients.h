@@ -11,7 +11,9 @@
  * Squares are summed in double, in an order that depends on the sizes alone, and c
  * is worked out in double; it is rounded to float, and the product to y's type.
  * A NaN anywhere makes the norm and every y NaN (also for an infinite max_norm); an
- * infinity makes the norm infinite and c 0: what is finite becomes 0, what is not NaN.
+ * infinity makes the norm infinite and, unless max_norm is infinite too, c 0: what is
+ * finite becomes 0, what is not NaN.  The norm that is written is rounded to float (an
+ * infinity past its range, which c does not see).
  *
  * Status codes: 0 enqueued; -i the i-th argument is invalid; > 0 the
  * hipError_t of a failed launch.  hip_gradient_*_status_string name them.

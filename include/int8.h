@@ -40,7 +40,7 @@ extern "C" {
  *   quotient is rounded, not its float approximation): -127 .. 127.
  * A row that holds an infinity or a NaN gets a NaN scale and codes of 0.  Bytes of
  * a row of Q past cols are not written.  Pointers need the alignment of their
- * element type.
+ * element type; Q and S must not overlap X.  rows == 0 or cols == 0: nothing is done.
  *
  * Arguments are numbered from 1: rows, cols, X, x_type, ldx, Q, ldq, S, stream.
  */
@@ -96,8 +96,9 @@ int hip_int8_linear_workspace(int tokens, int inputs, long long *bytes);
  * Y <- X * W^T + bias of tokens X (tokens x inputs), quantised on the way as
  * hip_int8_quantize does, and a quantised weight W (outputs x inputs): what
  * hip_int8_quantize and hip_int8_gemm give, bit for bit.
- *   workspace: device memory of at least the bytes above, 16-byte aligned; calls
- *   that overlap in time need workspaces of their own.
+ *   workspace: device memory of at least the bytes above (none for few tokens: then it
+ *   may be NULL), 16-byte aligned; calls that overlap in time need workspaces of their
+ *   own.
  * The rest as in hip_int8_quantize and hip_int8_gemm.
  *
  * Arguments are numbered from 1: tokens, inputs, outputs, X, x_type, ldx, W, ldw,

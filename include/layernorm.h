@@ -14,7 +14,9 @@
  *
  * Sums are float, or double for rows of more than HIP_LAYERNORM_ROW; the mean is kept
  * with what its rounding to float left over, so that a row far off zero keeps its
- * differences.  An infinity or NaN in a row of x makes that row of y and dx NaN, and dw.
+ * differences.  An infinity or NaN in a row of x, or a sum of squared differences past a
+ * float's range, makes that row of y and dx NaN, and dw.  A row without differences has
+ * h 0 if eps > 0.
  *
  * Status codes: 0 enqueued; -i the i-th argument is invalid; > 0 the
  * hipError_t of a failed launch.  hip_layernorm_*_status_string name them.
@@ -65,7 +67,8 @@ int hip_layernorm_backward_workspace(int rows, int cols, long long *bytes);
  *   DY, X, DX: rows x cols of `type`, row strides lddy, ldx, lddx.  DX may be DY or X
  *   itself (same stride), and must not overlap them otherwise; NULL: not wanted.
  *   stats: hip_layernorm_forward's.  w: as there (NULL: 1).
- *   dw, db: cols floats; either may be NULL (not wanted).
+ *   dw, db: cols floats; either may be NULL (not wanted).  They must not overlap each
+ *   other, nor anything else that is read or written.
  *   workspace: device memory of at least the bytes above, 16-byte aligned; calls
  *   that overlap in time need workspaces of their own.
  *   rows == 0: dw and db <- 0 without accumulate.  cols == 0: nothing is done.

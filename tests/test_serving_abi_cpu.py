@@ -102,12 +102,13 @@ def test_layernorm_forward_refusals(change, status):
 
 
 BACKWARD = dict(rows=400, cols=8, type=0, DY=FAKE, lddy=8, X=FAKE, ldx=8, stats=FAKE, w=FAKE, w_type=0, DX=FAKE, lddx=8, dw=FAKE,
-                db=FAKE, accumulate=0, workspace=FAKE, workspace_bytes=1 << 20)
+                db=2 * FAKE, accumulate=0, workspace=FAKE, workspace_bytes=1 << 20)
 
 
 @pytest.mark.parametrize("change,status", [
     (dict(rows=-1), -1), (dict(cols=-1), -2), (dict(type=-1), -3), (dict(DY=None), -4), (dict(lddy=7), -5), (dict(X=None), -6),
     (dict(ldx=7), -7), (dict(stats=None), -8), (dict(w_type=3), -10), (dict(w_type=1), -10), (dict(lddx=7), -12), (dict(accumulate=2), -15),
+    (dict(db=FAKE), -14), (dict(db=FAKE + 28), -14), (dict(dw=FAKE + 28, db=FAKE), -14),
     (dict(workspace=None), -16), (dict(workspace=FAKE + 8), -16), (dict(workspace_bytes=8), -17),
     (dict(cols=0), 0), (dict(rows=0, dw=None, db=None, workspace=None), 0), (dict(DX=None, dw=None, db=None, workspace=None), 0),
 ])
@@ -240,7 +241,7 @@ def test_bindings_refuse_host_tensors():
     q = int8.Int8(torch.zeros(4, 16, dtype=torch.int8), torch.ones(4))
     for call in (lambda: int8.quantize(x), lambda: int8.gemm(q, q), lambda: int8.linear(x, q), lambda: layernorm.layer_norm(x),
                  lambda: layernorm.layer_norm_backward(x, x, torch.zeros(3, 4)), lambda: gradients.grad_norm([x]),
-                 lambda: gradients.clip_grad_norm([x], 1.0), lambda: gradients.clip_by_norm([x], torch.ones(()), 1.0)):
+                 lambda: gradients.grad_norm([None]), lambda: gradients.clip_grad_norm([x], 1.0), lambda: gradients.clip_by_norm([x], torch.ones(()), 1.0)):
         with pytest.raises(TypeError):
             call()
 
