@@ -15,7 +15,9 @@ using namespace int8;
 
 // Calls f with the shape that takes rows of `cols` (at most kRowWidth).  Lanes that
 // share a row in a wavefront need no barrier, and more rows in a block keep more
-// loads under way; longer rows take more lanes rather than more registers.
+// loads under way; longer rows take more lanes before more registers, up to 512 (8192 x
+// 8192 bf16 with 256 lanes and four chunks 45 us, with 512 and two 42; 4096 x 16384 with
+// 1024 and two 49, with 512 and four 42).
 template <class F>
 void with_row_shape(int cols, const F& f) {
   if (cols <= 128) f(RowShape<16, 1>{});
@@ -25,11 +27,15 @@ void with_row_shape(int cols, const F& f) {
   else if (cols <= 2048) f(RowShape<256, 1>{});
   else if (cols <= 4096) f(RowShape<256, 2>{});
   else if (cols <= 8192) f(RowShape<512, 2>{});
-  else f(RowShape<1024, 2>{});
+  else f(RowShape<512, 4>{});
 }
 
-// A row in the registers of its lanes: read once.
-template <class S, class X>
+// A row in the registers of its lanes: read once.  One MI355X, kernels alone: 16 x 1024
+// bf16 3.0 us, 8192 x 8192 41-43 us (4.7-4.9 TB/s, what a large copy reaches; with a
+// branch around the loads 46), float32 63 (5.3 TB/s), 65536 x 256 12.8, 4097 x 2049
+// float32 13; rows that no eight divides, 8192 x 8191, 55.  Blocks that walk the rows
+// with the next one's loads under way take no less (42-45, float32 65-69).
+template <bool EVEN, class S, class X>
 __global__ __launch_bounds__(S::threads) void k_rows(const X* __restrict__ x, int64_t ldx, int8_t* __restrict__ q,
                                                      int64_t ldq, float* __restrict__ s, int rows, int cols) {
   __shared__ uint32_t meet[S::threads / 64][1];
@@ -41,7 +47,10 @@ __global__ __launch_bounds__(S::threads) void k_rows(const X* __restrict__ x, in
     Pack<8, X> v[S::COUNT];
     uint32_t top[1] = {0};
 #pragma unroll
-    for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(x + row * ldx, (c * S::LANES + lane) * 8, cols);
+    for (int c = 0; c < S::COUNT; ++c) {
+      const int col = (c * S::LANES + lane) * 8;
+      v[c] = EVEN ? load_even8(x + row * ldx, col, cols) : load_row8(x + row * ldx, col, cols);
+    }
 #pragma unroll
     for (int c = 0; c < S::COUNT; ++c) top[0] = top8(top[0], v[c]);
     join_row<S>(top, meet, Max{});
@@ -85,7 +94,8 @@ void launch_type(int rows, int cols, const void* x, int64_t ldx, int8_t* q, int6
     using S = decltype(shape);
     const int64_t steps = ceil_div(rows, S::rows), cap = kMaxWorkItems / S::threads;
     const dim3 grid(static_cast<unsigned>(steps < cap ? steps : cap));
-    hipLaunchKernelGGL((k_rows<S, X>), grid, dim3(S::threads), 0, stream, p, ldx, q, ldq, s, rows, cols);
+    const auto kernel = cols % 8 == 0 ? k_rows<true, S, X> : k_rows<false, S, X>;
+    hipLaunchKernelGGL(kernel, grid, dim3(S::threads), 0, stream, p, ldx, q, ldq, s, rows, cols);
   });
 }
 

@@ -46,13 +46,22 @@ __device__ __forceinline__ void store_stats(float* stats, int64_t row, int64_t r
 // (x - mean) rstd: x - mean is exact where x is near the mean, and the rest small.
 __device__ __forceinline__ float normalised(float x, const Stats& s) { return ((x - s.mean) - s.rest) * s.rstd; }
 
-// A lane's share of a row.
+// A lane's share of a row, zeros past its end.
 template <class S, class X>
 struct Share {
   Pack<8, X> v[S::COUNT];
+  template <bool EVEN = false>
   __device__ __forceinline__ void load(const X* row, int lane, int cols) {
+    if constexpr (EVEN) {
 #pragma unroll
-    for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(row, (c * S::LANES + lane) * 8, cols);
+      for (int c = 0; c < S::COUNT; ++c) v[c] = load_even8(row, (c * S::LANES + lane) * 8, cols);
+#pragma unroll
+      for (int c = 0; c < S::COUNT; ++c)
+        if ((c * S::LANES + lane) * 8 >= cols) v[c] = Pack<8, X>{};
+    } else {
+#pragma unroll
+      for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(row, (c * S::LANES + lane) * 8, cols);
+    }
   }
   // Makes the compiler forget what it made of the elements so far, lest it keep them
   // as floats beside the halves that they come as.
@@ -75,7 +84,7 @@ struct Share {
 // off zero is much of its differences, so their own mean is taken beside their
 // squares': with d = x - mean, the mean is mean + avg d and the variance
 // avg d^2 - (avg d)^2.
-template <class S, class X, class W>
+template <bool EVEN, class S, class X, class W>
 __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward(const X* x, int64_t ldx, const W* __restrict__ w,
                                                         const W* __restrict__ b, float eps, X* y, int64_t ldy,
                                                         float* __restrict__ stats, int rows, int cols) {
@@ -93,7 +102,7 @@ __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward
     const int64_t row = step * S::rows + threadIdx.x / S::LANES;
     const bool live = S::rows == 1 || row < rows;
     Share<S, X> now{};
-    if (live) now.load(x + row * ldx, lane, cols);
+    if (live) now.template load<EVEN>(x + row * ldx, lane, cols);
     float sum[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < S::COUNT; ++c)
@@ -177,17 +186,18 @@ __global__ __launch_bounds__(1024) void k_forward_long(const X* x, int64_t ldx, 
 // dw and db of a block's rows lie in its threads' registers, a thread's columns
 // being the same in every row, and leave once, into the block's part of the
 // workspace; k_join adds the parts in their order.
-template <class S, class X, class W>
-__global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 4) void k_backward(const X* dy, int64_t lddy, const X* x, int64_t ldx,
-                                                         const float* __restrict__ stats, const W* __restrict__ w, X* dx,
-                                                         int64_t lddx, float* __restrict__ parts, int rows, int cols) {
+template <bool EVEN, class S, class X, class W>
+__global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 4) void k_backward(
+    const X* dy, int64_t lddy, const X* x, int64_t ldx, const float* __restrict__ stats, const W* __restrict__ w, X* dx,
+    int64_t lddx, float* __restrict__ parts, int rows, int cols) {
   __shared__ float meet[2][S::threads / 64][2];
   const int lane = threadIdx.x % S::LANES;
   const int64_t steps = ceil_div(rows, S::rows);
   const float n = static_cast<float>(cols);
   // w too, but in the widest rows, whose threads have 128 registers (4096 x 16384 bf16:
-  // with some of them spilled 159 us, with w read in each row 125)
-  constexpr bool kHold = S::LANES < 1024;
+  // with some of them spilled 159 us, with w read in each row 120), and where it is
+  // fp16 and two chunks a lane, which the compiler spills as well (8192 x 8192 248, 107)
+  constexpr bool kHold = S::LANES < 1024 && !(S::COUNT == 2 && std::is_same_v<W, _Float16>);
   float wv[S::COUNT][8], pw[S::COUNT][8], pb[S::COUNT][8];
   const auto load_w = [&](int c) { load_param(wv[c], w, 1.0f, (c * S::LANES + lane) * 8, cols); };
 #pragma unroll
@@ -200,8 +210,8 @@ __global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 
   Stats s;
   const auto load = [&](int64_t step) {  // rows past the last repeat it
     const int64_t row = min(step * S::rows + threadIdx.x / S::LANES, int64_t(rows) - 1);
-    xv.load(x + row * ldx, lane, cols);
-    gv.load(dy + row * lddy, lane, cols);
+    xv.template load<EVEN>(x + row * ldx, lane, cols);
+    gv.template load<EVEN>(dy + row * lddy, lane, cols);
     s = load_stats(stats, row, rows);
   };
   load(blockIdx.x);
@@ -526,6 +536,12 @@ struct Backward {
   int count;
 };
 
+// Whether rows are loaded without branches: those of two chunks a lane (8192 x 8192 bf16
+// forward 61 -> 57 us, backward 103 -> 96; 4096 x 16384 72 -> 65, 125 -> 120), not those of
+// one (8192 x 4096 backward 51 -> 53, 65536 x 512 forward 29 -> 30).
+template <class S>
+bool even(int cols) { return S::COUNT == 2 && cols % 8 == 0; }
+
 template <class X, class W>
 void launch(const Forward& a, hipStream_t stream) {
   const X* const x = static_cast<const X*>(a.x);
@@ -540,7 +556,8 @@ void launch(const Forward& a, hipStream_t stream) {
   with_forward_shape(a.cols, [&](auto shape) {
     using S = decltype(shape);
     const int64_t steps = ceil_div(a.rows, S::rows), cap = 256 * (S::COUNT == 2 && S::LANES <= 256 ? 1280 : 2048) / S::threads;
-    hipLaunchKernelGGL((k_forward<S, X, W>), dim3(static_cast<unsigned>(steps < cap ? steps : cap)), dim3(S::threads), 0,
+    const auto kernel = even<S>(a.cols) ? k_forward<S::COUNT == 2, S, X, W> : k_forward<false, S, X, W>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(steps < cap ? steps : cap)), dim3(S::threads), 0,
                        stream, x, a.ldx, w, b, a.eps, y, a.ldy, a.stats, a.rows, a.cols);
   });
 }
@@ -579,7 +596,8 @@ void launch(const Backward& a, hipStream_t stream) {
       }
       return;
     }
-    hipLaunchKernelGGL((k_backward<S, X, W>), dim3(static_cast<unsigned>(a.count)), dim3(S::threads), 0, stream, dy,
+    const auto kernel = even<S>(a.cols) ? k_backward<S::COUNT == 2, S, X, W> : k_backward<false, S, X, W>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(a.count)), dim3(S::threads), 0, stream, dy,
                        a.lddy, x, a.ldx, a.stats, w, dx, a.lddx, a.parts, a.rows, a.cols);
   });
 }

@@ -31,6 +31,12 @@ __device__ __forceinline__ Pack<8, X> load_row8(const X* row, int col, int cols)
     if (col + i < cols) p.v[i] = row[col + i];
   return p;
 }
+// The same of a row of whole eights, without a branch around the load, behind which
+// the compiler would wait for it: past `cols` the row's last eight once more.
+template <class X>
+__device__ __forceinline__ Pack<8, X> load_even8(const X* row, int col, int cols) {
+  return load_pack<8>(row + min(col, cols - 8));
+}
 // Those inside of eight neighbours of a row.
 template <class X>
 __device__ __forceinline__ void store_row8(X* row, int col, int cols, const Pack<8, X>& p) {

@@ -112,14 +112,15 @@ def _layout(t, what):
 def _describe(tensors, outs):
     """(device, an array with seven numbers a tensor, as hip_gradient has them)."""
     from torch import Tensor
-    if any(t is None for t in tensors):  # of a parameter that has none
-        raise TypeError("a gradient is None")
+    types = _types()
+    try:
+        kinds = [types.get(t.dtype) for t in tensors]
+    except AttributeError:  # the gradient of a parameter that has none, as a rule
+        raise TypeError(f"gradients are tensors, not {type(next(t for t in tensors if not isinstance(t, Tensor))).__name__}") from None
     device = tensors[0].device
     index = tensors[0].get_device()
     if index < 0:
         raise TypeError("gradients must live on the GPU")
-    types = _types()
-    kinds = [types.get(t.dtype) for t in tensors]
     if None in kinds:
         raise TypeError(f"gradients are float32, bfloat16 or float16, not {tensors[kinds.index(None)].dtype}")
     places = list(map(Tensor.get_device, tensors))

@@ -4,7 +4,7 @@ in a run together, as they are used."""
 import pytest
 import torch
 
-from dense_fp32_matrix_row_amd import blockfp8, gradients, int8, lowp_training
+from dense_fp32_matrix_row_amd import blockfp8, gradients, int8, layernorm, lowp_training
 from tests import lowp_reference as low
 from tests import serving_reference as ref
 
@@ -152,3 +152,46 @@ def test_the_command_runs(capsys):
     lowp_training.main(["--steps", "3", "--norm", "--clip", "0.1", "--serve", "int8"])
     out = capsys.readouterr().out
     assert "loss" in out and "differ by 0.00e+00" in out
+
+
+def test_host_threads_call_at_once():
+    """Each thread on its own stream, with its own tensors: the results of the calls one after another."""
+    import threading
+
+    def work(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        x, dy = (torch.randn(300 + seed, 520, generator=g, device="cuda").bfloat16() for _ in range(2))
+        w = int8.quantize(torch.randn(264, 520, generator=g, device="cuda"))
+        scale, shift = (torch.randn(520, generator=g, device="cuda") for _ in range(2))
+        grads = [torch.randn(n, generator=g, device="cuda") for n in (seed + 1, 5000, 70000)] * (1 if seed % 2 else 30)
+
+        def calls():
+            y, stats = layernorm.layer_norm_forward(x, scale, shift)
+            norm, clipped = gradients.clip_grad_norm(grads, 1.0)
+            return [y, stats, *layernorm.layer_norm_backward(dy, x, stats, scale), int8.linear(y, w), int8.linear(y[:3], w),
+                    gradients.grad_norm(grads), norm, *clipped]
+        return calls
+
+    calls = [work(seed) for seed in range(4)]
+    expected = [c() for c in calls]
+    torch.cuda.synchronize()
+    results, failures = [None] * 4, []
+
+    def thread(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                results[i] = [calls[i]() for _ in range(8)]
+            stream.synchronize()
+        except Exception as e:  # raised where the test sees it
+            failures.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures
+    for want, runs in zip(expected, results):
+        for got in runs:
+            assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
