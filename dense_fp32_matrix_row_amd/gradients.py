@@ -105,7 +105,8 @@ def _layout(t, what):
     while sizes and sizes[-1][1] == ld * rows:
         rows *= sizes.pop()[0]
     if sizes or ld < cols:
-        raise ValueError(f"{what} of sizes {tuple(t.shape)} and strides {t.stride()} is not dense, nor rows of neighbours at one stride")
+        raise ValueError(f"{what} of sizes {tuple(t.shape)} and strides {t.stride()} is not dense, nor rows of neighbours "
+                         "at one stride")
     return rows, cols, ld
 
 
@@ -116,7 +117,8 @@ def _describe(tensors, outs):
     try:
         kinds = [types.get(t.dtype) for t in tensors]
     except AttributeError:  # the gradient of a parameter that has none, as a rule
-        raise TypeError(f"gradients are tensors, not {type(next(t for t in tensors if not isinstance(t, Tensor))).__name__}") from None
+        other = next(t for t in tensors if not isinstance(t, Tensor))
+        raise TypeError(f"gradients are tensors, not {type(other).__name__}") from None
     device = tensors[0].device
     index = tensors[0].get_device()
     if index < 0:

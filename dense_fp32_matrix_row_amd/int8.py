@@ -243,7 +243,7 @@ def _linear_bytes(T, I) -> int:
 def linear(x, w: Int8, bias=None, out=None, out_dtype=None):
     """x w^T (+ bias) of tokens x (T x I, rows may be strided) and a quantised weight w
     (O x I): gemm(quantize(x), w, bias), bit for bit, in one call.  The result has
-    x's type by default, or out's or out_dtype."""
+    x's type by default, or out's (which must not overlap what is read) or out_dtype."""
     import torch
     T, I, ldx = _matrix("x", x)
     x_type = _type("x", x.dtype)
