@@ -54,9 +54,9 @@ int hip_int8_quantize(int rows, int cols, const void *X, int x_type, int ldx, vo
  * floats, the bias added in the second multiplication's rounding, and the result
  * rounded to D's type.  Any code is allowed, -128 too.
  *   K: at most HIP_INT8_MAX_K.
- *   lda, ldb: multiples of 16 bytes, at most HIP_INT8_MAX_LD; A and B 16-byte
- *   aligned; a row is read up to the next multiple of 16 bytes (what lies past K
- *   has no influence).
+ *   lda, ldb: multiples of 16 bytes (best of 128, the cache's lines), at most
+ *   HIP_INT8_MAX_LD; A and B 16-byte aligned; a row is read up to the next multiple
+ *   of 16 bytes (what lies past K has no influence).
  *   bias: N numbers of bias_type side by side, or NULL for none.
  *   D: M x N of type d_type, row stride ldd; element alignment suffices.  It must
  *   not overlap anything that is read.

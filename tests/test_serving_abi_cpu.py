@@ -77,6 +77,7 @@ def test_linear_refusals(change, status):
 def test_linear_workspace_holds_codes_and_scales_of_all_but_few_tokens():
     assert int8.hip_int8_linear_workspace(40, 200) == 40 * (208 + 4) and int8.hip_int8_linear_workspace(0, 5) == 0
     assert int8.hip_int8_linear_workspace(2 ** 31 - 1, int8.MAX_K) == (2 ** 31 - 1) * (131072 + 4)
+    assert int8.hip_int8_linear_workspace(40, 513) == 40 * (640 + 4)
     for tokens, inputs in ((1, 1), (1, 16384), (16, 1024), (9, 1017), (5, 2048), (3, 4090)):
         assert int8.hip_int8_linear_workspace(tokens, inputs) == 0
     for tokens, inputs in ((1, 16385), (17, 8), (16, 1025), (9, 1025), (5, 2049), (3, 4097)):
