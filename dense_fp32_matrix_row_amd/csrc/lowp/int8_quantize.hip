@@ -30,12 +30,14 @@ void with_row_shape(int cols, const F& f) {
   else f(RowShape<512, 4>{});
 }
 
-// A row in the registers of its lanes: read once.  One MI355X, kernels alone: 16 x 1024
-// bf16 3.0 us, 8192 x 8192 41-43 us (4.7-4.9 TB/s, what a large copy reaches; with a
-// branch around the loads 46), float32 63 (5.3 TB/s), 65536 x 256 12.8, 4097 x 2049
-// float32 13; rows that no eight divides, 8192 x 8191, 55.  Blocks that walk the rows
-// with the next one's loads under way take no less (42-45, float32 65-69).
-template <bool EVEN, class S, class X>
+// A row in the registers of its lanes: read once.  The lane that reaches over the row's
+// end takes the last eight instead (WIDE), codes that its neighbour has too and writes
+// alike, so that no load has a branch around it, behind which the compiler would wait.
+// One MI355X, kernels alone: 16 x 1024 bf16 2.9 us, 8192 x 8192 42 us (4.8 TB/s, what a
+// large copy reaches; with branches 46), 8192 x 8191 42 (55), float32 63 (5.3 TB/s), 65536
+// x 256 12.4, 4097 x 2049 float32 9.9 (13).  Blocks that walk the rows with the next one's
+// loads under way take no less (42-45, float32 65-69).
+template <bool WIDE, class S, class X>
 __global__ __launch_bounds__(S::threads) void k_rows(const X* __restrict__ x, int64_t ldx, int8_t* __restrict__ q,
                                                      int64_t ldq, float* __restrict__ s, int rows, int cols) {
   __shared__ uint32_t meet[S::threads / 64][1];
@@ -49,14 +51,18 @@ __global__ __launch_bounds__(S::threads) void k_rows(const X* __restrict__ x, in
 #pragma unroll
     for (int c = 0; c < S::COUNT; ++c) {
       const int col = (c * S::LANES + lane) * 8;
-      v[c] = EVEN ? load_even8(x + row * ldx, col, cols) : load_row8(x + row * ldx, col, cols);
+      v[c] = WIDE ? load_last8(x + row * ldx, col, cols) : load_row8(x + row * ldx, col, cols);
     }
 #pragma unroll
     for (int c = 0; c < S::COUNT; ++c) top[0] = top8(top[0], v[c]);
     join_row<S>(top, meet, Max{});
     const Scale by = make_scale(top[0]);
 #pragma unroll
-    for (int c = 0; c < S::COUNT; ++c) store_row8(q + row * ldq, (c * S::LANES + lane) * 8, cols, codes8(v[c], by));
+    for (int c = 0; c < S::COUNT; ++c) {
+      const int col = (c * S::LANES + lane) * 8;
+      if constexpr (!WIDE) store_row8(q + row * ldq, col, cols, codes8(v[c], by));
+      else if (col < cols) store_pack(q + row * ldq + min(col, cols - 8), codes8(v[c], by));
+    }
     if (lane == 0) s[row] = by.s;
     if constexpr (S::waves > 1) __syncthreads();  // the next row writes the same LDS
   }
@@ -94,7 +100,7 @@ void launch_type(int rows, int cols, const void* x, int64_t ldx, int8_t* q, int6
     using S = decltype(shape);
     const int64_t steps = ceil_div(rows, S::rows), cap = kMaxWorkItems / S::threads;
     const dim3 grid(static_cast<unsigned>(steps < cap ? steps : cap));
-    const auto kernel = cols % 8 == 0 ? k_rows<true, S, X> : k_rows<false, S, X>;
+    const auto kernel = cols >= 8 ? k_rows<true, S, X> : k_rows<false, S, X>;
     hipLaunchKernelGGL(kernel, grid, dim3(S::threads), 0, stream, p, ldx, q, ldq, s, rows, cols);
   });
 }

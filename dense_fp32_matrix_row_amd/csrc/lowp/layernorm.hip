@@ -59,7 +59,7 @@ struct Share {
   __device__ __forceinline__ void load(const X* row, int lane, int cols) {
     if constexpr (EVEN) {
 #pragma unroll
-      for (int c = 0; c < S::COUNT; ++c) v[c] = load_even8(row, (c * S::LANES + lane) * 8, cols);
+      for (int c = 0; c < S::COUNT; ++c) v[c] = load_last8(row, (c * S::LANES + lane) * 8, cols);
 #pragma unroll
       for (int c = 0; c < S::COUNT; ++c)
         if ((c * S::LANES + lane) * 8 >= cols) v[c] = Pack<8, X>{};

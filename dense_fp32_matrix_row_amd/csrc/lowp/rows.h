@@ -31,10 +31,10 @@ __device__ __forceinline__ Pack<8, X> load_row8(const X* row, int col, int cols)
     if (col + i < cols) p.v[i] = row[col + i];
   return p;
 }
-// The same of a row of whole eights, without a branch around the load, behind which
-// the compiler would wait for it: past `cols` the row's last eight once more.
+// The same of a row of at least eight, without a branch around the load, behind which
+// the compiler would wait for it: where fewer than eight are left, the row's last eight.
 template <class X>
-__device__ __forceinline__ Pack<8, X> load_even8(const X* row, int col, int cols) {
+__device__ __forceinline__ Pack<8, X> load_last8(const X* row, int col, int cols) {
   return load_pack<8>(row + min(col, cols - 8));
 }
 // Those inside of eight neighbours of a row.
