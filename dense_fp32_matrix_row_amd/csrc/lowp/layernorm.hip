@@ -6,8 +6,8 @@
 //
 // One MI355X, kernels alone, forward and backward: 16 x 1024 bf16 3.2 and 2.8 us, 8192 x
 // 1024 8.4 and 17, 8192 x 4096 27 (4.9 TB/s) and 51 (3.9 TB/s, and 25 MB of parts written
-// and read), 8192 x 8192 56 and 96, 4096 x 16384 65 and 121, 65536 x 512 29 and 44; 4097 x
-// 2049 float32 15 and 29; 2048 x 32768, past what registers hold, 95 and 200.
+// and read), 8192 x 8192 56 and 93-96, 4096 x 16384 64 and 119, 65536 x 512 28 and 44; 4097 x
+// 2049 float32 14 and 29; 2048 x 32768, past what registers hold, 95 and 200.
 #include <algorithm>
 
 #include "../../../include/layernorm.h"
@@ -51,21 +51,41 @@ __device__ __forceinline__ void store_stats(float* stats, int64_t row, int64_t r
 // (x - mean) rstd: x - mean is exact where x is near the mean, and the rest small.
 __device__ __forceinline__ float normalised(float x, const Stats& s) { return ((x - s.mean) - s.rest) * s.rstd; }
 
+// Where chunk c of a lane lies: WIDE (load_last8), the row's last eight if it would reach
+// over its end.
+template <bool WIDE, class S>
+__device__ __forceinline__ int place(int c, int lane, int cols) {
+  const int col = (c * S::LANES + lane) * 8;
+  return WIDE ? min(col, cols - 8) : col;
+}
+
 // A lane's share of a row, zeros past its end.
 template <class S, class X>
 struct Share {
   Pack<8, X> v[S::COUNT];
-  template <bool EVEN = false>
   __device__ __forceinline__ void load(const X* row, int lane, int cols) {
-    if constexpr (EVEN) {
 #pragma unroll
-      for (int c = 0; c < S::COUNT; ++c) v[c] = load_last8(row, (c * S::LANES + lane) * 8, cols);
+    for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(row, (c * S::LANES + lane) * 8, cols);
+  }
+  // Without branches around the loads: of a row of whole eights; of any (at least eight),
+  // zeros also for those of its last eight that the lane before has.
+  __device__ __forceinline__ void load_even(const X* row, int lane, int cols) {
 #pragma unroll
-      for (int c = 0; c < S::COUNT; ++c)
-        if ((c * S::LANES + lane) * 8 >= cols) v[c] = Pack<8, X>{};
-    } else {
+    for (int c = 0; c < S::COUNT; ++c) v[c] = load_last8(row, (c * S::LANES + lane) * 8, cols);
 #pragma unroll
-      for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(row, (c * S::LANES + lane) * 8, cols);
+    for (int c = 0; c < S::COUNT; ++c)
+      if ((c * S::LANES + lane) * 8 >= cols) v[c] = Pack<8, X>{};
+  }
+  __device__ __forceinline__ void load_wide(const X* row, int lane, int cols) {
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) v[c] = load_last8(row, (c * S::LANES + lane) * 8, cols);
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) {
+      const int before = (c * S::LANES + lane) * 8 - (cols - 8);
+      if (before > 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < before) v[c].v[i] = X{};
     }
   }
   // Makes the compiler forget what it made of the elements so far, lest it keep them
@@ -89,7 +109,7 @@ struct Share {
 // off zero is much of its differences, so their own mean is taken beside their
 // squares': with d = x - mean, the mean is mean + avg d and the variance
 // avg d^2 - (avg d)^2.
-template <bool EVEN, class S, class X, class W>
+template <bool WIDE, class S, class X, class W>
 __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward(
     const X* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, X* y, int64_t ldy,
     float* __restrict__ stats, int rows, int cols) {
@@ -100,14 +120,17 @@ __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward
   float wv[S::COUNT][8], bv[S::COUNT][8];
 #pragma unroll
   for (int c = 0; c < S::COUNT; ++c) {
-    load_param(wv[c], w, 1.0f, (c * S::LANES + lane) * 8, cols);
-    load_param(bv[c], b, 0.0f, (c * S::LANES + lane) * 8, cols);
+    load_param(wv[c], w, 1.0f, place<WIDE, S>(c, lane, cols), cols);
+    load_param(bv[c], b, 0.0f, place<WIDE, S>(c, lane, cols), cols);
   }
   for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
     const int64_t row = step * S::rows + threadIdx.x / S::LANES;
     const bool live = S::rows == 1 || row < rows;
     Share<S, X> now{};
-    if (live) now.template load<EVEN>(x + row * ldx, lane, cols);
+    if (live) {
+      if constexpr (WIDE) now.load_wide(x + row * ldx, lane, cols);
+      else now.load(x + row * ldx, lane, cols);
+    }
     float sum[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < S::COUNT; ++c)
@@ -120,7 +143,8 @@ __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward
     for (int c = 0; c < S::COUNT; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float t = (c * S::LANES + lane) * 8 < cols - i ? to_float(now.v[c].v[i]) - s.mean : 0.0f;
+        const bool inside = WIDE ? i >= (c * S::LANES + lane) * 8 - (cols - 8) : (c * S::LANES + lane) * 8 < cols - i;
+        const float t = inside ? to_float(now.v[c].v[i]) - s.mean : 0.0f;
         d[0] += t;
         d[1] = fmaf(t, t, d[1]);
       }
@@ -135,7 +159,8 @@ __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward
         Pack<8, X> r;
 #pragma unroll
         for (int i = 0; i < 8; ++i) from_float(fmaf(normalised(to_float(now.v[c].v[i]), s), wv[c][i], bv[c][i]), r.v[i]);
-        store_row8(y + row * ldy, (c * S::LANES + lane) * 8, cols, r);
+        if constexpr (WIDE) store_last8(y + row * ldy, (c * S::LANES + lane) * 8, cols, r);
+        else store_row8(y + row * ldy, (c * S::LANES + lane) * 8, cols, r);
       }
       if (stats && lane == 0) store_stats(stats, row, rows, s);
     }
@@ -217,8 +242,13 @@ __global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 
   Stats s;
   const auto load = [&](int64_t step) {  // rows past the last repeat it
     const int64_t row = min(step * S::rows + threadIdx.x / S::LANES, int64_t(rows) - 1);
-    xv.template load<EVEN>(x + row * ldx, lane, cols);
-    gv.template load<EVEN>(dy + row * lddy, lane, cols);
+    if constexpr (EVEN) {
+      xv.load_even(x + row * ldx, lane, cols);
+      gv.load_even(dy + row * lddy, lane, cols);
+    } else {
+      xv.load(x + row * ldx, lane, cols);
+      gv.load(dy + row * lddy, lane, cols);
+    }
     s = load_stats(stats, row, rows);
   };
   load(blockIdx.x);
@@ -543,9 +573,11 @@ struct Backward {
   int count;
 };
 
-// Whether rows are loaded without branches: those of two chunks a lane (8192 x 8192 bf16
-// forward 61 -> 57 us, backward 103 -> 96; 4096 x 16384 72 -> 65, 125 -> 120), not those of
-// one (8192 x 4096 backward 51 -> 53, 65536 x 512 forward 29 -> 30).
+// Rows of two chunks a lane are loaded without branches (8192 x 8192 bf16 forward 61 ->
+// 57 us, backward 103 -> 96; 4096 x 16384 72 -> 65, 125 -> 120), in the forward pass ragged ones
+// too (8192 x 8191 79 -> 64; in the backward pass dropping what the lane before has costs
+// more: 8192 x 8192 122); rows of one chunk are not (8192 x 4096 backward 51 -> 53, 65536 x
+// 512 forward 29 -> 30).
 template <class S>
 bool even(int cols) { return S::COUNT == 2 && cols % 8 == 0; }
 
@@ -563,9 +595,8 @@ void launch(const Forward& a, hipStream_t stream) {
   with_forward_shape(a.cols, [&](auto shape) {
     using S = decltype(shape);
     const int64_t steps = ceil_div(a.rows, S::rows), cap = 256 * (S::COUNT == 2 && S::LANES <= 256 ? 1280 : 2048) / S::threads;
-    const auto kernel = even<S>(a.cols) ? k_forward<S::COUNT == 2, S, X, W> : k_forward<false, S, X, W>;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(steps < cap ? steps : cap)), dim3(S::threads), 0,
-                       stream, x, a.ldx, w, b, a.eps, y, a.ldy, a.stats, a.rows, a.cols);
+    const dim3 grid(static_cast<unsigned>(steps < cap ? steps : cap));
+    hipLaunchKernelGGL((k_forward<S::COUNT == 2, S, X, W>), grid, dim3(S::threads), 0, stream, x, a.ldx, w, b, a.eps, y, a.ldy, a.stats, a.rows, a.cols);
   });
 }
 

@@ -49,6 +49,19 @@ __device__ __forceinline__ void store_row8(X* row, int col, int cols, const Pack
   }
 }
 
+// Of eight that load_last8 takes, those that no lane before has.
+template <class X>
+__device__ __forceinline__ void store_last8(X* row, int col, int cols, const Pack<8, X>& p) {
+  const int before = col - (cols - 8);
+  if (before <= 0) {
+    store_pack(row + col, p);
+  } else {
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (i >= before) row[cols - 8 + i] = p.v[i];
+  }
+}
+
 // Another lane's value: the neighbour's, the next pair's, the other half of eight's
 // and of sixteen's.
 template <int CONTROL, class T>
