@@ -59,6 +59,15 @@ __device__ __forceinline__ int place(int c, int lane, int cols) {
   return WIDE ? min(col, cols - 8) : col;
 }
 
+// Adds g h to the backward pass's second sum; `inside`: of an element of the row.  Past its end
+// dy, and so g, is zero, but a zero's (x - mean) rstd may pass a float's range where the
+// row's own do not, and 0 inf is NaN.  (Not of halfs: no mean of theirs times an rstd does.)
+template <class X, class T>
+__device__ __forceinline__ void add_inside(T& sum, T g, T h, bool inside) {
+  const T v = fma(g, h, sum);
+  sum = std::is_same_v<X, _Float16> || inside ? v : sum;
+}
+
 // A lane's share of a row, zeros past its end.
 template <class S, class X>
 struct Share {
@@ -67,14 +76,18 @@ struct Share {
 #pragma unroll
     for (int c = 0; c < S::COUNT; ++c) v[c] = load_row8(row, (c * S::LANES + lane) * 8, cols);
   }
-  // Without branches around the loads: of a row of whole eights; of any (at least eight),
-  // zeros also for those of its last eight that the lane before has.
+  // Without branches around the loads: of a row of whole eights; the same with the row's last
+  // eight past its end; of any row (at least eight), zeros also for those of its last eight
+  // that the lane before has.
   __device__ __forceinline__ void load_even(const X* row, int lane, int cols) {
-#pragma unroll
-    for (int c = 0; c < S::COUNT; ++c) v[c] = load_last8(row, (c * S::LANES + lane) * 8, cols);
+    load_any(row, lane, cols);
 #pragma unroll
     for (int c = 0; c < S::COUNT; ++c)
       if ((c * S::LANES + lane) * 8 >= cols) v[c] = Pack<8, X>{};
+  }
+  __device__ __forceinline__ void load_any(const X* row, int lane, int cols) {
+#pragma unroll
+    for (int c = 0; c < S::COUNT; ++c) v[c] = load_last8(row, (c * S::LANES + lane) * 8, cols);
   }
   __device__ __forceinline__ void load_wide(const X* row, int lane, int cols) {
 #pragma unroll
@@ -243,7 +256,7 @@ __global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 
   const auto load = [&](int64_t step) {  // rows past the last repeat it
     const int64_t row = min(step * S::rows + threadIdx.x / S::LANES, int64_t(rows) - 1);
     if constexpr (EVEN) {
-      xv.load_even(x + row * ldx, lane, cols);
+      xv.load_any(x + row * ldx, lane, cols);
       gv.load_even(dy + row * lddy, lane, cols);
     } else {
       xv.load(x + row * ldx, lane, cols);
@@ -267,7 +280,7 @@ __global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 
           pw[c][i] = fmaf(t, h, pw[c][i]);
           pb[c][i] += t;
           sum[0] += g;
-          sum[1] = fmaf(g, h, sum[1]);
+          add_inside<X>(sum[1], g, h, EVEN || c < S::COUNT - 1 || (c * S::LANES + lane) * 8 < cols - i);
         }
       }
     }
@@ -351,7 +364,7 @@ __global__ __launch_bounds__(S::threads, S::COUNT == 1 && S::LANES <= 512 ? 6 : 
       for (int i = 0; i < 8; ++i) {
         const float g = to_float(gv.v[c].v[i]) * wv[c][i];
         sum[0] += g;
-        sum[1] = fmaf(g, normalised(to_float(xv.v[c].v[i]), s), sum[1]);
+        add_inside<X>(sum[1], g, normalised(to_float(xv.v[c].v[i]), s), c < S::COUNT - 1 || (c * S::LANES + lane) * 8 < cols - i);
       }
     }
     join_row<S>(sum, meet, Sum{});
@@ -447,7 +460,7 @@ __global__ __launch_bounds__(1024) void k_backward_long(const X* dy, int64_t ldd
       for (int i = 0; i < 8; ++i) {
         const float g = to_float(gv.v[i]) * wv[i];
         sum[0] += static_cast<double>(g);
-        sum[1] = fma(static_cast<double>(g), static_cast<double>(normalised(to_float(xv.v[i]), s)), sum[1]);
+        add_inside<X>(sum[1], static_cast<double>(g), static_cast<double>(normalised(to_float(xv.v[i]), s)), col < cols - i);
       }
     }
     join_row<S>(sum, meet[turn], Sum{});

@@ -269,3 +269,23 @@ def test_refusals_of_the_tensor_forms():
                 lambda: layernorm.layer_norm_backward(x, x, stats, w, dw=w[:3], db=w), lambda: layernorm.layer_norm(x[0])):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("rows", (4, 300))
+@pytest.mark.parametrize("cols", (5, 100, 512, 1001, 2000, 3001, 4098, 9000, 9001, 20001, 20002))
+@pytest.mark.parametrize("kind", ("f32", "bf16"))
+def test_large_constant_rows(kind, cols, rows):
+    """No differences, whatever the rows' size: h is 0, and the gradients are those of rows of zeros.  -mean rstd,
+    what a zero past the row's end would have for h, passes a float's range (2^110 by 10^6)."""
+    kind = TYPES[kind]
+    x = torch.full((rows, cols), 2.0 ** 110, dtype=kind)
+    x[1] = -2.0 ** 110
+    dy = ref.values(rows, cols, kind, 30)
+    w, b = params(cols, kind, 31)
+    zeros = ref.layer_norm(torch.zeros_like(x), w, b, 1e-12)
+    y, stats = layernorm.layer_norm_forward(x.cuda(), w.cuda(), b.cuda(), eps=1e-12)
+    assert torch.equal(y.cpu(), b.expand(rows, cols))
+    got = layernorm.layer_norm_backward(dy.cuda(), x.cuda(), stats, w.cuda())
+    tols = ref.backward_tolerance(zeros, dy, kind, rows)
+    for g, want, tol in zip(got, ref.layer_norm_backward(zeros, dy), tols):
+        ref.close(g, want, tol)
