@@ -122,11 +122,20 @@ struct Share {
 // off zero is much of its differences, so their own mean is taken beside their
 // squares': with d = x - mean, the mean is mean + avg d and the variance
 // avg d^2 - (avg d)^2.
-template <bool WIDE, class S, class X, class W>
+//
+// Where the squares' sum passes a float's range (rows of 10^18; equal values of 10^26, whose
+// mean is some steps off them; never halfs), the differences from the whole mean are squared
+// again, times 2^-80, behind a branch that is hardly taken (0.2 us of code to fetch; squares
+// of scaled differences throughout cost 2-6 %: 8192 x 4096 bf16 26.4 -> 28.1 us).  Where eps is
+// below kLeastEps (0 as a rule) and squares below a float's normal numbers would count, the
+// differences and their squares are summed in double.
+constexpr float kLeastEps = 0x1p-100f;
+template <bool WIDE, class D, class S, class X, class W>
 __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward(
     const X* x, int64_t ldx, const W* __restrict__ w, const W* __restrict__ b, float eps, X* y, int64_t ldy,
     float* __restrict__ stats, int rows, int cols) {
-  __shared__ float first[S::threads / 64][1], second[S::threads / 64][2];
+  __shared__ float first[S::threads / 64][1], third[S::threads / 64][1];
+  __shared__ D second[S::threads / 64][2];
   const int lane = threadIdx.x % S::LANES;
   const int64_t steps = ceil_div(rows, S::rows);
   const float n = static_cast<float>(cols);
@@ -151,7 +160,7 @@ __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward
       for (int i = 0; i < 8; ++i) sum[0] += to_float(now.v[c].v[i]);
     join_row<S>(sum, first, Sum{});
     Stats s{sum[0] / n, 0.0f, 0.0f};
-    float d[2] = {0.0f, 0.0f};
+    D d[2] = {0, 0};
 #pragma unroll
     for (int c = 0; c < S::COUNT; ++c)
 #pragma unroll
@@ -159,13 +168,42 @@ __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward
         const bool inside = WIDE ? i >= (c * S::LANES + lane) * 8 - (cols - 8) : (c * S::LANES + lane) * 8 < cols - i;
         const float t = inside ? to_float(now.v[c].v[i]) - s.mean : 0.0f;
         d[0] += t;
-        d[1] = fmaf(t, t, d[1]);
+        d[1] = fma(static_cast<D>(t), static_cast<D>(t), d[1]);
       }
     join_row<S>(d, second, Sum{});
     now.forget();
-    s.rest = d[0] / n;
-    s.rstd = 1.0f / sqrtf(fmaxf(d[1] / n - s.rest * s.rest, 0.0f) + eps);
-    if (!(fabsf(d[1]) < INFINITY)) s.rstd = __uint_as_float(0x7fc00000u);  // fmaxf takes no NaN over
+    if constexpr (sizeof(D) == 8) {
+      const double rest = d[0] / cols;
+      s.rest = static_cast<float>(rest);
+      s.rstd = static_cast<float>(1.0 / sqrt(fmax(d[1] / cols - rest * rest, 0.0) + static_cast<double>(eps)));
+    } else {
+      s.rest = d[0] / n;
+      s.rstd = 1.0f / sqrtf(fmaxf(d[1] / n - s.rest * s.rest, 0.0f) + eps);
+    }
+    const bool past = !(d[1] < static_cast<D>(INFINITY));
+    if constexpr (sizeof(D) == 8 || std::is_same_v<X, _Float16>) {
+      if (past) s.rstd = __uint_as_float(0x7fc00000u);  // fmax takes no NaN over
+    } else {
+      bool again = past;  // the same in all threads that meet
+      if constexpr (S::waves > 1 && S::rows > 1)
+#pragma unroll
+        for (int i = 0; i < S::threads / 64; ++i) again = again || !(second[i][1] < 0x1p126f);
+      if (__builtin_expect(again, 0)) {
+        float e[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < S::COUNT; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool inside = WIDE ? i >= (c * S::LANES + lane) * 8 - (cols - 8) : (c * S::LANES + lane) * 8 < cols - i;
+            const float t = inside ? ((to_float(now.v[c].v[i]) - s.mean) - s.rest) * 0x1p-80f : 0.0f;
+            e[0] = fmaf(t, t, e[0]);
+          }
+        join_row<S>(e, third, Sum{});
+        now.forget();
+        const float v = e[0] / n;  // 2^-160 of the variance
+        if (past) s.rstd = v < 0x1p-60f ? 1.0f / sqrtf(v * 0x1p80f * 0x1p80f + eps) : 0x1p-80f / sqrtf(v + eps * 0x1p-80f * 0x1p-80f);
+      }
+    }
     if (live) {
 #pragma unroll
       for (int c = 0; c < S::COUNT; ++c) {
@@ -609,7 +647,9 @@ void launch(const Forward& a, hipStream_t stream) {
     using S = decltype(shape);
     const int64_t steps = ceil_div(a.rows, S::rows), cap = 256 * (S::COUNT == 2 && S::LANES <= 256 ? 1280 : 2048) / S::threads;
     const dim3 grid(static_cast<unsigned>(steps < cap ? steps : cap));
-    hipLaunchKernelGGL((k_forward<S::COUNT == 2, S, X, W>), grid, dim3(S::threads), 0, stream, x, a.ldx, w, b, a.eps, y, a.ldy, a.stats, a.rows, a.cols);
+    const auto kernel = a.eps < kLeastEps ? k_forward<S::COUNT == 2, double, S, X, W> : k_forward<S::COUNT == 2, float, S, X, W>;
+    hipLaunchKernelGGL(kernel, grid, dim3(S::threads), 0, stream, x, a.ldx, w, b, a.eps, y, a.ldy, a.stats, a.rows,
+                       a.cols);
   });
 }
 

@@ -14,9 +14,11 @@
  *
  * Sums are float, or double for rows of more than HIP_LAYERNORM_ROW; the mean is kept
  * with what its rounding to float left over, so that a row far off zero keeps its
- * differences.  An infinity or NaN in a row of x, or a sum of the row or of its squared
- * differences past a float's range, makes that row of y and dx NaN, and dw.  A row
- * without differences has h 0 if eps > 0.
+ * differences, and the squared differences may be larger or smaller than a float holds.
+ * An infinity or NaN in a row of x, or a sum of the row or a difference past a float's range,
+ * makes that row of y and dx NaN, and dw.  A row without differences has h 0 if eps > 0.
+ * rstd is a float: infinite, with y and dx, where eps is 0 and the root of the squared
+ * differences' mean below 2^-128.
  *
  * Status codes: 0 enqueued; -i the i-th argument is invalid; > 0 the
  * hipError_t of a failed launch.  hip_layernorm_*_status_string name them.

@@ -289,3 +289,40 @@ def test_large_constant_rows(kind, cols, rows):
     tols = ref.backward_tolerance(zeros, dy, kind, rows)
     for g, want, tol in zip(got, ref.layer_norm_backward(zeros, dy), tols):
         ref.close(g, want, tol)
+
+
+@pytest.mark.parametrize("eps", (0.0, 1e-5))
+@pytest.mark.parametrize("power", (-120, -90, -75, -65, -55, 55, 62, 66, 100, 110))
+@pytest.mark.parametrize("cols", (3, 100, 200, 512, 700, 1500, 3000, 9001, 20001))
+def test_squares_past_a_floats_range(cols, power, eps):
+    """Differences whose squares, or the sums of these, a float cannot hold, or not with all its bits."""
+    g = torch.Generator().manual_seed(cols)
+    x, dy = torch.randn(5, cols, generator=g) * 2.0 ** power, torch.randn(5, cols, generator=g)
+    w, b = params(cols, torch.float32, 32)
+    check(x, dy, w, b, torch.float32, eps)
+
+
+@pytest.mark.parametrize("cols", (3, 100, 200, 512, 700, 1500, 3000, 9001, 20001))
+def test_large_constant_rows_whose_sum_is_rounded(cols):
+    """The mean is some steps off the values, whose squares pass a float's range; its remainder is these steps."""
+    for value in (1.1e10, 1.1e20, 1.1e27, 1.3e30, 1.7e33):
+        x, dy = torch.full((4, cols), value), ref.values(4, cols, torch.float32, 33)
+        w, b = params(cols, torch.float32, 34)
+        y, stats = layernorm.layer_norm_forward(x.cuda(), w.cuda(), b.cuda())
+        assert torch.equal(y.cpu(), b.expand(4, cols))
+        zeros = ref.layer_norm(torch.zeros_like(x), w, b, EPS)
+        got = layernorm.layer_norm_backward(dy.cuda(), x.cuda(), stats, w.cuda())
+        for v, want, tol in zip(got, ref.layer_norm_backward(zeros, dy), ref.backward_tolerance(zeros, dy, torch.float32, 4)):
+            ref.close(v, want, tol)
+
+
+@pytest.mark.parametrize("cols", (100, 200, 700, 1500, 3000, 9001))
+def test_rows_beside_such_a_row_stay_as_they_are(cols):
+    x = torch.randn(9, cols, generator=torch.Generator().manual_seed(35)).cuda()
+    want = layernorm.layer_norm_forward(x)
+    for at, factor in ((2, 2.0 ** 80), (5, 2.0 ** -80), (8, float("inf"))):
+        other = x.clone()
+        other[at] *= factor
+        got = layernorm.layer_norm_forward(other)
+        rest = torch.arange(9, device="cuda") != at
+        assert torch.equal(got[0][rest], want[0][rest]) and torch.equal(got[1][:, rest], want[1][:, rest])
