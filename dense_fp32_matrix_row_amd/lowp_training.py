@@ -112,8 +112,10 @@ class Network:
         return x
 
     def serve(self):
-        """The network with its weights as 8-bit integers, a scale for each output."""
-        return Served([int8.quantize(layer.master) for layer in self.layers], [(n.weight, n.bias) for n in self.norms])
+        """The network as it is now, with its weights as 8-bit integers, a scale for each output;
+        training that goes on leaves it as it is."""
+        return Served([int8.quantize(layer.master) for layer in self.layers],
+                      [(n.weight.clone(), n.bias.clone()) for n in self.norms])
 
 
 class Served:

@@ -195,3 +195,20 @@ def test_host_threads_call_at_once():
     for want, runs in zip(expected, results):
         for got in runs:
             assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("norm", (False, True))
+def test_a_served_network_stays_as_it_was_served(norm):
+    """Training that goes on changes neither the weights nor the norms' parameters of what is served."""
+    net = lowp_training.Network(96, 130, 33, seed=9, norm=norm)
+    if norm:
+        norms_with_parameters(net, 10)
+    served = net.serve()
+    x = torch.randn(7, 96, device="cuda").bfloat16()
+    want = served.infer(x)
+    for part in (*net.layers, *net.norms):
+        for gradient in ([part.gradient] if hasattr(part, "gradient") else [part.weight_gradient, part.bias_gradient]):
+            gradient.copy_(torch.randn(gradient.shape))
+        part.update(0.1)
+    assert torch.equal(served.infer(x), want)
+    assert not torch.equal(net.serve().infer(x), want)
