@@ -306,32 +306,61 @@ bool collect(Work& w, int count, const hip_gradient* tensors, bool clip) {
   return true;
 }
 
+// The sum of floor((a i + b) / m) over i < n, modulo 2^64.  Whole multiples of m in a and b
+// come out; what is left counts the points under a line, which as many columns of its
+// inverse hold.
+uint64_t sum_of_floors(uint64_t n, uint64_t m, uint64_t a, uint64_t b) {
+  const uint64_t pairs = n % 2 ? n * (n / 2) : n / 2 * (n - 1), whole = a / m * pairs + b / m * n;
+  const uint64_t top = a % m * n + b % m;
+  return top < m ? whole : whole + sum_of_floors(top / m, a % m, m, top % m);
+}
+
 // Whether what a clipping call writes overlaps anything else that it touches.
 struct Range {
-  uintptr_t from, to;  // bytes
-  uintptr_t row, ld;   // of a strided one
+  int64_t from, to;       // bytes
+  int64_t row, ld, rows;  // `rows` of `row` bytes, ld apart
   bool writes;
 };
+// How many of a's rows begin before `at`.
+int64_t rows_before(const Range& a, int64_t at) {
+  if (at <= a.from) return 0;
+  return std::min(a.rows, ceil_div(at - a.from, a.ld));
+}
 bool meet(const Range& a, const Range& b) {
   if (!(a.writes || b.writes) || a.to <= b.from || b.to <= a.from) return false;
-  if (a.ld == 0 || a.ld != b.ld) return true;
-  // two sets of columns of one matrix
-  const uintptr_t off = a.from <= b.from ? (b.from - a.from) % a.ld : (a.ld - (a.from - b.from) % a.ld) % a.ld;
-  return off < a.row || off + b.row > a.ld;
+  if (a.ld == b.ld) {  // two sets of columns of one matrix (a division instead of a dozen)
+    const int64_t off = a.from <= b.from ? (b.from - a.from) % a.ld : (a.ld - (a.from - b.from) % a.ld) % a.ld;
+    return off < a.row || off + b.row > a.ld;
+  }
+  const int64_t last = b.from + (b.rows - 1) * b.ld;  // b's last row
+  // a's rows that begin before b's first or within its last; and those between, which meet a
+  // row of b where its begin less b's, modulo b.ld, is less than b.row or more than b.ld - a.row
+  const int64_t first = rows_before(a, b.from), past = rows_before(a, last);
+  if (rows_before(a, b.from - a.row + 1) < first || past < rows_before(a, last + b.row)) return true;
+  if (first == past) return false;
+  const int64_t near = a.row + b.row - 1;  // as many of the b.ld places
+  if (near >= b.ld) return true;
+  const uint64_t n = past - first, at = a.from + first * a.ld - b.from + a.row - 1 + b.ld;
+  return sum_of_floors(n, b.ld, a.ld, at) != sum_of_floors(n, b.ld, a.ld, at - near);
 }
 bool overlaps(const Work& w, const float* norm) {
   std::vector<Range> ranges;
   ranges.reserve(2 * w.tensors.size() + 1);
   for (const Tensor& t : w.tensors) {
-    const uintptr_t size = t.type == HIP_GRADIENT_F32 ? 4 : 2, row = t.cols * size;
-    const auto add = [&](uintptr_t at, int64_t ld, bool writes) {
-      ranges.push_back(Range{at, at + (t.rows - 1) * ld * size + row, row, t.rows > 1 ? ld * size : 0, writes});
+    const int64_t size = t.type == HIP_GRADIENT_F32 ? 4 : 2, row = t.cols * size;
+    const auto add = [&](uintptr_t p, int64_t ld, bool writes) {
+      const int64_t at = static_cast<int64_t>(p), step = t.rows > 1 ? ld * size : row;
+      ranges.push_back(Range{at, at + (t.rows - 1) * step + row, row, step, t.rows, writes});
     };
     add(t.y, t.ldy, true);
     if (t.x != t.y || (t.rows > 1 && t.ldx != t.ldy)) add(t.x, t.ldx, false);
   }
-  if (norm) ranges.push_back(Range{reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, 4, 0, true});
-  std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+  if (norm) {
+    const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(norm));
+    ranges.push_back(Range{at, at + 4, 4, 4, 1, true});
+  }
+  const auto before = [](const Range& a, const Range& b) { return a.from < b.from; };
+  if (!std::is_sorted(ranges.begin(), ranges.end(), before)) std::sort(ranges.begin(), ranges.end(), before);
   std::vector<const Range*> open;  // those that reach past the present one's begin
   for (const Range& r : ranges) {
     size_t kept = 0;

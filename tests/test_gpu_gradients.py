@@ -233,3 +233,15 @@ def test_refusals_of_the_tensor_forms():
                 lambda: gradients.grad_norm([x[0].expand(4, 8)]), lambda: gradients.clip_by_norm([x], torch.ones(()), 1.0)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_disjoint_pieces_of_one_matrix_in_place():
+    """Strided pieces of other heights, strides and widths than their neighbours, none of them overlapping."""
+    base = torch.randn(40, 64, device="cuda")
+    want = base / (base.double().norm() + EPS).float()
+    pieces = [base[:, :4], base[0, 4:64], base[1:, 4:30], base[1::2, 30:50], base[2::2, 30:50], base[1:21, 50:64], base[21:, 50:64]]
+    assert sum(p.numel() for p in pieces) == base.numel()
+    _, out = gradients.clip_grad_norm(pieces, 1.0, out=pieces)
+    assert out is pieces and torch.allclose(base, want, rtol=1e-6, atol=0)
+    with pytest.raises(sgemm.SgemmError):
+        gradients.clip_grad_norm([base[1::2, 30:50], base[3:5, 49:60]], 1.0, out=[base[1::2, 30:50], base[3:5, 49:60]])

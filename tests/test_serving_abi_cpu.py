@@ -256,3 +256,70 @@ def test_clipping_refuses_no_tensors_and_bad_limits():
                  lambda: gradients.clip_by_norm([torch.ones(3)], torch.ones((), dtype=torch.float64), 1.0)):
         with pytest.raises(ValueError):
             call()
+
+
+def _places(t, address, ld):
+    """The bytes of a tensor of the array above."""
+    size = 4 if t["type"] == 0 else 2
+    return {address + r * ld * size + b for r in range(t["rows"]) for b in range(t["cols"] * size)}
+
+
+def _overlap(each, norm):
+    """Whether what a clipping call writes meets anything else that it touches, byte by byte."""
+    sets = [({norm + b for b in range(4)}, True)]
+    for t in each:
+        y = _places(t, t["y"], t["ldy"])
+        sets.append((y, True))
+        if t["x"] != t["y"] or (t["rows"] > 1 and t["ldx"] != t["ldy"]):  # the strides of one row are not read
+            sets.append((_places(t, t["x"], t["ldx"]), False))
+    return any(a & b for i, (a, wa) in enumerate(sets) for b, wb in sets[:i] if wa or wb)
+
+
+def _refused_as_overlapping(each, norm=0x4000):
+    """Without a device a call that is not refused gives the launch's error."""
+    status = clip_call(each, norm=norm)
+    assert status == -2 or status > 0
+    return status == -2
+
+
+without_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="addresses that nothing lies at, in calls that are not refused")
+
+
+@without_gpu
+def test_clip_refuses_what_overlaps_and_nothing_else():
+    import random
+    rng = random.Random(1)
+    found = [0, 0]
+    for trial in range(6000):
+        kind = rng.choice((0, 1))
+        size = 2 if kind else 4
+
+        def tensor():
+            rows, cols = rng.randint(1, 6), rng.randint(1, 9)
+            ldx = cols + rng.choice((0, 1, 3, 7, 16, rng.randint(0, 40)))
+            x = 0x10000 + size * rng.randint(0, 60)
+            t = dict(x=x, y=x, rows=rows, cols=cols, ldx=ldx, ldy=ldx, type=kind)
+            if rng.random() < 0.3:
+                t["y"], t["ldy"] = 0x10000 + size * rng.randint(0, 200), cols + rng.randint(0, 20)
+            return t
+        each = [tensor() for _ in range(rng.choice((2, 2, 2, 3)))]
+        norm = rng.choice((0x4000, 0x10000 + 4 * rng.randint(0, 60)))
+        want = _overlap(each, norm)
+        found[want] += 1
+        assert _refused_as_overlapping(each, norm) == want, str((each, norm))
+    assert min(found) > 500
+
+
+@without_gpu
+def test_clip_finds_overlaps_of_many_rows():
+    """Rows at two strides meet once in a million, or not at all."""
+    rows, one = 1 << 20, 0x100000000000
+    for lda, ldb, cols in ((1000, 1001, 1), (4099, 4111, 2), (64, 96, 16), (3000, 2000, 400), (1000, 1000, 300), (7, 1 << 20, 3)):
+        a = set(range(0, rows * lda, lda))
+        for shift in (0, 1, 5, 16, 17, 300, 499, 500, 700, 12345, 100003, 777777):
+            b = [shift + i * ldb for i in range(min(rows, 1 << 14))]
+            meets = any((at + d) in a for at in b for d in range(1 - cols, cols))
+            each = [dict(x=one, y=one, rows=rows, cols=cols, ldx=lda, ldy=lda, type=0),
+                    dict(x=one + 4 * shift, y=one + 4 * shift, rows=len(b), cols=cols, ldx=ldb, ldy=ldb, type=0)]
+            assert _refused_as_overlapping(each) == meets, (lda, ldb, cols, shift)
+            assert _refused_as_overlapping(each[::-1]) == meets
