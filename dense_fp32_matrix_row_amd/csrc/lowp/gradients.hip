@@ -343,7 +343,7 @@ bool meet(const Range& a, const Range& b) {
   const uint64_t n = past - first, at = a.from + first * a.ld - b.from + a.row - 1 + b.ld;
   return sum_of_floors(n, b.ld, a.ld, at) != sum_of_floors(n, b.ld, a.ld, at - near);
 }
-bool overlaps(const Work& w, const float* norm) {
+bool overlaps(const Work& w, const float* norm, bool writes_norm) {
   std::vector<Range> ranges;
   ranges.reserve(2 * w.tensors.size() + 1);
   for (const Tensor& t : w.tensors) {
@@ -357,7 +357,7 @@ bool overlaps(const Work& w, const float* norm) {
   }
   if (norm) {
     const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(norm));
-    ranges.push_back(Range{at, at + 4, 4, 4, 1, true});
+    ranges.push_back(Range{at, at + 4, 4, 4, 1, writes_norm});
   }
   const auto before = [](const Range& a, const Range& b) { return a.from < b.from; };
   if (!std::is_sorted(ranges.begin(), ranges.end(), before)) std::sort(ranges.begin(), ranges.end(), before);
@@ -423,7 +423,7 @@ bool off256(const void* p) { return reinterpret_cast<uintptr_t>(p) % 256 != 0; }
 
 // What the three calls share, their arguments' numbers being the same but the
 // norm's: 0, or a status.
-int begin(Work& w, int count, const hip_gradient* tensors, bool clip, const float* norm, void* workspace,
+int begin(Work& w, int count, const hip_gradient* tensors, bool clip, const float* norm, bool writes_norm, void* workspace,
           long long workspace_bytes, int workspace_at, hipStream_t stream) {
   if (bad_count(count)) return -1;
   if (count > 0 && tensors == nullptr) return -2;
@@ -432,7 +432,7 @@ int begin(Work& w, int count, const hip_gradient* tensors, bool clip, const floa
   if (workspace == nullptr || off256(workspace)) return -workspace_at;
   if (workspace_bytes < bytes_for(count)) return -(workspace_at + 1);
   if (!collect(w, count, tensors, clip)) return -2;
-  if (clip && overlaps(w, norm)) return -2;
+  if (clip && overlaps(w, norm, writes_norm)) return -2;
   if (static_cast<int>(w.slots.size()) > kInline) put_table(w, memory(workspace).table, stream);
   return 0;
 }
@@ -442,7 +442,7 @@ int clip(int count, const hip_gradient* tensors, double max_norm, double eps, fl
   if (!(max_norm >= 0.0)) return -3;
   if (!(eps >= 0.0) || eps == std::numeric_limits<double>::infinity()) return -4;
   Work w;
-  const int status = begin(w, count, tensors, true, given ? given : norm, workspace, workspace_bytes, 6, stream);
+  const int status = begin(w, count, tensors, true, given ? given : norm, !given, workspace, workspace_bytes, 6, stream);
   if (status != 0) return status;
   const Memory m = memory(workspace);
   if (!given) launch_norm(w, m, stream);
@@ -479,7 +479,7 @@ int hip_gradient_norm(int count, const hip_gradient* tensors, float* norm, void*
   return guarded([&] {
     if (norm == nullptr) return -3;
     Work w;
-    const int status = begin(w, count, tensors, false, nullptr, workspace, workspace_bytes, 4, stream);
+    const int status = begin(w, count, tensors, false, nullptr, false, workspace, workspace_bytes, 4, stream);
     if (status != 0) return status;
     const Memory m = memory(workspace);
     launch_norm(w, m, stream);

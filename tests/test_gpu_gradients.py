@@ -245,3 +245,12 @@ def test_disjoint_pieces_of_one_matrix_in_place():
     assert out is pieces and torch.allclose(base, want, rtol=1e-6, atol=0)
     with pytest.raises(sgemm.SgemmError):
         gradients.clip_grad_norm([base[1::2, 30:50], base[3:5, 49:60]], 1.0, out=[base[1::2, 30:50], base[3:5, 49:60]])
+
+
+def test_clipping_by_a_norm_that_is_a_gradient_too():
+    x = torch.tensor([3.0, 4.0], device="cuda")
+    norm = gradients.grad_norm([x])
+    out = gradients.clip_by_norm([x, norm], norm, 1.0, eps=0.0)
+    assert torch.allclose(out[0], x / 5) and out[1].item() == 1.0 and norm.item() == 5.0
+    with pytest.raises(sgemm.SgemmError):
+        gradients.clip_by_norm([x, norm], norm, 1.0, out=[x, norm])

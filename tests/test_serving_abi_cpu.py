@@ -323,3 +323,13 @@ def test_clip_finds_overlaps_of_many_rows():
                     dict(x=one + 4 * shift, y=one + 4 * shift, rows=len(b), cols=cols, ldx=ldb, ldy=ldb, type=0)]
             assert _refused_as_overlapping(each) == meets, (lda, ldb, cols, shift)
             assert _refused_as_overlapping(each[::-1]) == meets
+
+
+@without_gpu
+def test_clipping_by_a_norm_that_is_a_gradient_too():
+    """The norm that is given is read: new results of it are no overlap, a result written over it is."""
+    into = dict(x=0x10000, y=0x20000)
+    for norm, status in ((0x10000, None), (0x10000 + 396, None), (0x20000, -2), (0x20000 + 396, -2), (0x4000, None)):
+        got = clip_call([into], gradients.hip_gradient_clip_by, norm=norm)
+        assert got == status if status else got > 0
+        assert (clip_call([into], norm=norm) == -2) == (norm != 0x4000)
