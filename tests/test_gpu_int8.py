@@ -371,3 +371,28 @@ def test_out_counts_as_modified():
     int8.gemm(a, a, out=out)
     int8.linear(torch.randn(4, 64, device="cuda"), a, out=out)
     assert out._version == before + 2
+
+
+@pytest.mark.parametrize("cols,per_block", ((1, 16), (8, 16), (200, 8), (1025, 1)))
+def test_quantize_rows_of_a_blocks_second_turn(cols, per_block):
+    """A launch has at most 2^31 threads, 256 a block here: `per_block` rows of the shape that takes these widths
+    are a block's at a time, and the rows from per_block * 2^23 on a second turn's."""
+    first = per_block << 23
+    rows = first + 5
+    x = torch.zeros(rows, cols, device="cuda", dtype=torch.bfloat16)
+    g = torch.Generator().manual_seed(cols)
+    some = (torch.randn(40, cols, generator=g) * 3).bfloat16()
+    places = torch.cat([torch.arange(10), torch.arange(first // 2, first // 2 + 10), torch.arange(rows - 20, rows)])
+    x[places.cuda()] = some.cuda()
+    q = torch.full((rows, cols), 0x55, dtype=torch.int8, device="cuda")
+    s = torch.full((rows,), -1.0, device="cuda")
+    assert int8.hip_int8_quantize(rows, cols, x, int8.BF16, cols, q, cols, s) == 0
+    want, scales = ref.quantize(some)
+    ref.same(q[places.cuda()], want)
+    ref.same(s[places.cuda()], scales)
+    others = torch.ones(rows, dtype=torch.bool, device="cuda")
+    others[places.cuda()] = False
+    for at in range(0, rows, 1 << 24):  # rows of zeros
+        here = others[at:at + (1 << 24)]
+        assert not q[at:at + (1 << 24)][here].any()
+        assert (s[at:at + (1 << 24)][here] == torch.tensor(int8.AMAX_FLOOR / 127, dtype=torch.float32)).all()
