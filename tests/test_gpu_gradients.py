@@ -65,6 +65,36 @@ def test_many_tensors(count):
     check(tensors, 1.0)
 
 
+@pytest.mark.parametrize("count", (119, 120, 121, 239, 240, 241, 361))
+def test_as_many_tensors_as_a_launch_takes(count):
+    """A launch's arguments hold 120 of the table's slots, one a dense tensor: beside one, two and three launches' worth."""
+    check(some([(1 + (i * 37) % 300,) for i in range(count)], ("f32", "bf16"), seed=count), 1.0)
+
+
+@pytest.mark.parametrize("strided", (1, 2, 3))
+@pytest.mark.parametrize("count", (59, 60, 61, 79, 119, 120, 121, 300, 2100))
+def test_many_strided_tensors(count, strided):
+    """One of every `strided` tensors is of rows apart, which take two slots: also pairs of them that lie on both
+    sides of the 120th, and where a chunk's tensor is looked for in two rounds."""
+    g = torch.Generator().manual_seed(count)
+    tensors = []
+    for i in range(count):
+        rows, cols = 2 + i % 7, 1 + (i * 13) % 60
+        kind = (torch.float32, torch.bfloat16)[i % 2]
+        t = (torch.randn(rows, cols + 3, generator=g) * 4.0 ** (i % 5 - 2)).to(kind).cuda()
+        tensors.append(t[:, 1:1 + cols] if i % strided == 0 else t)
+    check(tensors, 1.0)
+
+
+@pytest.mark.parametrize("first", (0, 1))
+def test_strided_tensors_of_many_chunks_each(first):
+    """Chunks at the begin and the end of each, found in the table of a launch's arguments and in that in memory."""
+    for count in (3, 90):
+        wide = torch.randn(count, 40, 4200, device="cuda")
+        tensors = [w[:, 1:4200 - i % 3] for i, w in enumerate(wide)]
+        check(tensors[first:], 2.0)
+
+
 def test_more_tensors_than_two_rounds_find():
     """64^3 tensors and more: views of one buffer."""
     n = 64 ** 3 + 5
