@@ -13,6 +13,8 @@ namespace {
 
 using namespace int8;
 
+using Narrowest = RowShape<16, 1>;
+
 // Calls f with the shape that takes rows of `cols` (at most kRowWidth).  Lanes that
 // share a row in a wavefront need no barrier, and more rows in a block keep more
 // loads under way; longer rows take more lanes before more registers, up to 512 (8192 x
@@ -20,7 +22,7 @@ using namespace int8;
 // 1024 and two 49, with 512 and four 42).
 template <class F>
 void with_row_shape(int cols, const F& f) {
-  if (cols <= 128) f(RowShape<16, 1>{});
+  if (cols <= 128) f(Narrowest{});
   else if (cols <= 256) f(RowShape<32, 1>{});
   else if (cols <= 512) f(RowShape<64, 1>{});
   else if (cols <= 1024) f(RowShape<64, 2>{});
@@ -32,7 +34,8 @@ void with_row_shape(int cols, const F& f) {
 
 // A row in the registers of its lanes: read once.  The lane that reaches over the row's
 // end takes the last eight instead (WIDE), codes that its neighbour has too and writes
-// alike, so that no load has a branch around it, behind which the compiler would wait.
+// alike, so that no load has a branch around it, behind which the compiler would wait; a
+// row of fewer than eight, of the narrowest shape only, has none.
 // One MI355X, kernels alone: 16 x 1024 bf16 2.9 us, 8192 x 8192 42 us (4.8 TB/s, what a
 // large copy reaches; with branches 46), 8192 x 8191 42 (55), float32 63 (5.3 TB/s), 65536
 // x 256 12.4, 4097 x 2049 float32 9.9 (13).  Blocks that walk the rows with the next one's
@@ -96,13 +99,14 @@ void launch_type(int rows, int cols, const void* x, int64_t ldx, int8_t* q, int6
     hipLaunchKernelGGL((k_long<X>), grid, dim3(1024), 0, stream, p, ldx, q, ldq, s, rows, cols);
     return;
   }
-  with_row_shape(cols, [&](auto shape) {
+  const auto go = [&](auto shape, const auto& kernel) {
     using S = decltype(shape);
     const int64_t steps = ceil_div(rows, S::rows), cap = kMaxWorkItems / S::threads;
     const dim3 grid(static_cast<unsigned>(steps < cap ? steps : cap));
-    const auto kernel = cols >= 8 ? k_rows<true, S, X> : k_rows<false, S, X>;
     hipLaunchKernelGGL(kernel, grid, dim3(S::threads), 0, stream, p, ldx, q, ldq, s, rows, cols);
-  });
+  };
+  if (cols < 8) go(Narrowest{}, k_rows<false, Narrowest, X>);
+  else with_row_shape(cols, [&](auto shape) { go(shape, k_rows<true, decltype(shape), X>); });
 }
 
 }  // namespace

@@ -88,3 +88,11 @@ def test_the_gpu_tests_sizes_reach_every_tile():
     assert {p[0][:2] for p in shapes.INT8.values() if len(p) == 1} == set(shapes.INT8_TILES)
     edges = {"both" if q[4] else "right" if q[3] else "low" for p in shapes.INT8.values() for q in p[1:]}
     assert edges == {"both", "right", "low"}
+
+
+def test_the_quantiser_has_no_kernel_that_no_width_takes():
+    """Rows of fewer than eight columns have kernels of their own, of the narrowest shape alone, for three types."""
+    import re
+    with open(sgemm.LIBRARY, "rb") as f:
+        names = set(re.findall(rb"k_rowsILb0ENS_8RowShapeILi(\d+)ELi(\d+)ELi\d+EEE([a-zA-Z0-9_]*?)EEv", f.read()))
+    assert {(lanes, chunks) for lanes, chunks, _ in names} == {(b"16", b"1")} and len(names) == 3
