@@ -132,7 +132,7 @@ def _forward(x, weight, bias, eps, out, keep):
         y, ldy = torch.empty((rows, cols), dtype=x.dtype, device=device), max(cols, 1)
     else:
         y, ldy = out, _like("out", out, x)
-    stats = torch.empty((3, rows), dtype=torch.float32, device=device) if keep else None
+    stats = (torch.empty if cols else torch.zeros)((3, rows), dtype=torch.float32, device=device) if keep else None
     _call(device, load().hip_layernorm_forward, hip_layernorm_forward_status_string, rows, cols, kind, x.data_ptr(), ldx,
           w, b, w_type, eps, y.data_ptr(), ldy, stats.data_ptr() if keep else None)
     if out is not None:
@@ -149,7 +149,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None):
 
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None):
     """layer_norm(...), and the rows' statistics, which layer_norm_backward takes
-    (float32, 3 x T: the means, what their rounding left over, and 1 / the deviations)."""
+    (float32, 3 x T: the means, what their rounding left over, and 1 / the deviations;
+    zeros without columns)."""
     return _forward(x, weight, bias, eps, out, True)
 
 
@@ -187,8 +188,6 @@ def layer_norm_backward(dy, x, stats, weight=None, dw=None, db=None, out=None):
     add = any(given)
     if weight is not None and not add:
         dw, db = (torch.empty(cols, dtype=torch.float32, device=device) for _ in range(2))
-        if not cols:
-            return torch.empty_like(x), dw, db
     if out is None:
         dx, lddx = torch.empty((rows, cols), dtype=x.dtype, device=device), max(cols, 1)
     else:

@@ -326,3 +326,19 @@ def test_rows_beside_such_a_row_stay_as_they_are(cols):
         got = layernorm.layer_norm_forward(other)
         rest = torch.arange(9, device="cuda") != at
         assert torch.equal(got[0][rest], want[0][rest]) and torch.equal(got[1][:, rest], want[1][:, rest])
+
+
+def test_tokens_without_columns():
+    """Results go where they are asked for, and nothing that comes back is left as the memory was."""
+    flat, out = torch.empty(300, 0, device="cuda"), torch.empty(300, 0, device="cuda")
+    for _ in range(3):
+        torch.full((3, 300), float("nan"), device="cuda")  # freed: what the statistics' memory may hold
+        y, stats = layernorm.layer_norm_forward(flat, flat[0], flat[0], out=out)
+        assert y is out and (stats == 0).all()
+    dx, dw, db = layernorm.layer_norm_backward(flat, flat, stats, flat[0], out=out)
+    assert dx is out and dw.shape == db.shape == (0,)
+    with pytest.raises(ValueError):
+        layernorm.layer_norm_backward(flat, flat, stats, flat[0], out=flat[:4])
+    one, two = flat[0].clone(), flat[0].clone()
+    res = layernorm.layer_norm_backward(flat, flat, stats, flat[0], dw=one, db=two)
+    assert res[0].shape == (300, 0) and res[1] is one and res[2] is two
