@@ -4,7 +4,8 @@
 // Bound by memory: every element is read for the norm, and again, and written,
 // where it is scaled.  All tensors' elements are cut into chunks of one size, which
 // a grid of blocks walks, whatever the tensors' own sizes; a table says which
-// tensor a chunk lies in.  The norm's launch leaves a sum for each block, and each
+// tensor a chunk lies in.  (But rows shorter than a chunk, of strided tensors, are taken an
+// element at a time, with a division each: a fifth to a third of that rate.)  The norm's launch leaves a sum for each block, and each
 // block of the next launch adds them up for itself in the same order: no atomics,
 // no third launch.
 //
@@ -12,7 +13,9 @@
 // TB/s), scaled into others 629 us in all (a copy alone takes 441); 200 tensors, 64M
 // elements of mixed types, in place and within the limit, 51 us (205 MB at 5.4 TB/s, a
 // launch each for the table's two parts and 5 us to find that nothing is to be
-// written); 4 tensors of 1M floats 6.9 us, two launches.
+// written); 4 tensors with 1M floats in all 6.8 us, two launches.  Scaled in place: the 1
+// GiB in 48 tensors 642 us, the 200 tensors of bf16 72.  Strided and in place: 48 tensors of
+// 4096 rows of 4000 bf16, 4096 apart, 3.23 ms (norm 1.49; 1.1 TB/s), of floats 3.70 (1.61; 2.0).
 #include <algorithm>
 #include <limits>
 #include <vector>

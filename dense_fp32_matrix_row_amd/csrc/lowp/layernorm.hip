@@ -4,9 +4,9 @@
 // x and dy and writes dx, each once, against some ten vector instructions an
 // element; rows lie in registers (rows.h) from the sums to the results.
 //
-// One MI355X, kernels alone, forward and backward: 16 x 1024 bf16 3.2 and 2.8 us, 8192 x
-// 1024 8.4 and 17, 8192 x 4096 27 (4.9 TB/s) and 51 (3.9 TB/s, and 25 MB of parts written
-// and read), 8192 x 8192 56 and 93-96, 4096 x 16384 64 and 119, 65536 x 512 28 and 44; 4097 x
+// One MI355X, kernels alone, forward and backward: 16 x 1024 bf16 3.5 and 2.8 us, 8192 x
+// 1024 9.0 and 17, 8192 x 4096 27 (4.9 TB/s) and 51 (3.9 TB/s, and 25 MB of parts written
+// and read), 8192 x 8192 57 and 95, 4096 x 16384 65 and 121, 65536 x 512 28 and 45; 4097 x
 // 2049 float32 14 and 29; 2048 x 32768, past what registers hold, 95 and 200.
 #include <algorithm>
 

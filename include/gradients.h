@@ -9,7 +9,8 @@
  *     y = x * c,  c = 1 if norm + eps <= max_norm, else max_norm / (norm + eps)
  *
  * Squares are summed in double, in an order that depends on the sizes alone, and c
- * is worked out in double; it is rounded to float, and the product to y's type.
+ * is worked out in double; it is rounded to float, the product x c to float and then to
+ * y's type.
  * A NaN anywhere makes the norm and every y NaN (also for an infinite max_norm); an
  * infinity makes the norm infinite and, unless max_norm is infinite too, c 0: what is
  * finite becomes 0, what is not NaN.  The norm that is written is rounded to float (an
