@@ -188,7 +188,7 @@ __global__ __launch_bounds__(S::threads, S::LANES <= 256 ? 5 : 4) void k_forward
       if constexpr (S::waves > 1 && S::rows > 1)
 #pragma unroll
         for (int i = 0; i < S::threads / 64; ++i) again = again || !(second[i][1] < 0x1p126f);
-      if (__builtin_expect(again, 0)) {
+      if (__builtin_expect(__ballot(again) != 0, 0)) {
         float e[1] = {0.0f};
 #pragma unroll
         for (int c = 0; c < S::COUNT; ++c)
