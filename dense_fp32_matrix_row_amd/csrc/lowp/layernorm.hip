@@ -626,7 +626,7 @@ struct Backward {
 
 // Rows of two chunks a lane are loaded without branches (8192 x 8192 bf16 forward 61 ->
 // 57 us, backward 103 -> 96; 4096 x 16384 72 -> 65, 125 -> 120), in the forward pass ragged ones
-// too (8192 x 8191 79 -> 64; in the backward pass dropping what the lane before has costs
+// too (8192 x 8191 79 -> 65; in the backward pass dropping what the lane before has costs
 // more: 8192 x 8192 122); rows of one chunk are not (8192 x 4096 backward 51 -> 53, 65536 x
 // 512 forward 29 -> 30).
 template <class S>
